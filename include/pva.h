@@ -311,6 +311,145 @@ pva_status pva_attn_bwd(const void* q, const void* k, const void* v, const void*
                         const void* worklist_dev, void* plan_dev, void* dq, void* dk, void* dv,
                         int32_t grads_are_fp32, float softmax_scale, void* stream);
 
+/* ---- Positions and the key/value cache of a model in use.  The pages stop at
+ * training; these calls give a pack its positions (with the gradient) and carry
+ * a model trained on packs into decoding: prompts and tokens are appended to a
+ * paged cache, few new tokens attend to all that is cached, and cached rows
+ * come back as a contiguous pack where many new tokens attend through
+ * pva_attn_fwd.
+ *
+ * Token tensors are [tokens, heads, head_dim] with a token stride in elements,
+ * 0 for contiguous rows (heads * head_dim); heads and dims are contiguous, rows
+ * and pointers 16-byte aligned.  The strides let queries, keys and values stay
+ * in one projection's output.  head_dim is 64 or 128.
+ *
+ * A status word (DEVICE int32, set to 0 by its owner, or NULL) takes the first
+ * failure met on the device; pva_cache_status reads it:
+ *   300 a position without a page: outside the table's columns, or an entry
+ *       outside [0, num_pages)
+ *   301 lengths that do not fit: more new tokens than kv_lens counts, or
+ *       offsets that decrease or leave the tensor
+ *   303 a position outside the angle table (negative ones included)
+ * What such a token would have read or written is left out; the rest is done. */
+
+/* Angles: table DEVICE fp32 [max_pos, rot_dim / 2, 2], (cos, sin) of pair p at
+ * position t at [t][p]; rot_dim a multiple of 16, at most head_dim; 0: no
+ * rotation.  Pair p is the dims (p, p + rot_dim / 2), or (2p, 2p + 1) where
+ * interleaved = 1; dims from rot_dim on stay as they are. */
+typedef struct {
+    const float* table;
+    int32_t max_pos, rot_dim, interleaved;
+} pva_rope_desc;
+
+/* Rotation of a pack's queries and keys: (a, b) -> (a cos - b sin, b cos + a sin)
+ * for every pair; inverse = 1 turns back, which is the gradient of the rotation.
+ * fp32 products and sums, one rounding to the tensors' type.
+ *   q, k, q_out, k_out  DEVICE, all bf16 (is_fp32 = 0) or all fp32; in place
+ *                       (q_out = q with the same stride) is allowed; a tensor with
+ *                       0 heads may be NULL
+ *   positions_dev       DEVICE int32 [num_tokens], or NULL: the position inside the
+ *                       token's document of cu_seqlens_dev (int32 [num_docs + 1];
+ *                       rows of no document are left as they were), or, with that
+ *                       NULL too, the row's own number.  Not both. */
+pva_status pva_rope(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                    int32_t num_tokens, int32_t num_q_heads, int32_t num_kv_heads,
+                    int32_t head_dim, int32_t is_fp32, const pva_rope_desc* rope,
+                    const int32_t* cu_seqlens_dev, int32_t num_docs,
+                    const int32_t* positions_dev, int32_t inverse, void* q_out,
+                    int64_t q_out_stride, void* k_out, int64_t k_out_stride,
+                    int32_t* status_dev, void* stream);
+
+/* What a cache row holds. */
+typedef enum {
+    PVA_CACHE_BF16 = 0, /* head_dim bf16 values */
+    PVA_CACHE_INT4 = 1  /* head_dim codes of 4 bits; every 64 dims have a (scale, low)
+                           pair of bf16: value = low + code * scale */
+} pva_cache_kind;
+
+/* A paged cache; page_size a power of two, 16 to 1024.
+ *   k_pages, v_pages    DEVICE [num_pages, num_kv_heads, page_size, head_dim] bf16,
+ *                       or [.., head_dim / 2] bytes of codes
+ *   k_scales, v_scales  INT4: DEVICE [num_pages, num_kv_heads, page_size,
+ *                       head_dim / 64, 2] bf16
+ * Codes: eight dims share a 32-bit word, dim i of the eight at bit
+ * 4 * (i / 2) + 16 * (i % 2); dims 8o .. 8o + 7 are word
+ * (o % 8) * (head_dim / 64) + o / 8 of the row. */
+typedef struct {
+    int32_t kind; /* pva_cache_kind */
+    int32_t num_kv_heads, head_dim, page_size;
+    int64_t num_pages;
+    void *k_pages, *v_pages, *k_scales, *v_scales;
+} pva_cache_desc;
+
+/* The sequences of one call.  Sequence b has kv_lens[b] tokens in the cache, the
+ * call's new ones among them (the last ones); the token at position t of it is
+ * slot t % page_size of page page_table[b][t / page_size].  Sequences may share
+ * pages that are only read. */
+typedef struct {
+    int32_t num_seqs;
+    int32_t num_tokens;        /* rows of the tensors of new tokens; rows past the last
+                                  sequence's are left as they were */
+    int32_t max_pages;         /* columns of the page table */
+    int64_t table_stride;      /* entries from one sequence's row to the next */
+    const int32_t* page_table; /* DEVICE int32 */
+    const int32_t* kv_lens;    /* DEVICE int32 [num_seqs] */
+    const int32_t* cu_new;     /* DEVICE int32 [num_seqs + 1]: new tokens of sequence b are
+                                  rows cu_new[b] .. cu_new[b + 1]; NULL: row b alone */
+    int32_t* status;           /* status word or NULL */
+} pva_cache_batch;
+
+/* Append the new tokens' keys and values, keys (and queries) rotated to their
+ * positions kv_lens[b] - n_b + i.  fp32 arithmetic, rounded to bf16 as pva_rope
+ * does; an INT4 row is made from the bf16 row: low = min of the group, scale =
+ * bf16((max - min) / 15), code = round((x - low) / scale) to even, 0 to 15.  A
+ * group with an infinity or NaN is read back as NaN.
+ *   rope          or NULL: no rotation
+ *   k, v          DEVICE bf16 [num_tokens, num_kv_heads, head_dim]
+ *   q, q_out      DEVICE bf16 [num_tokens, num_q_heads, head_dim], both or neither
+ *                 (then num_q_heads = 0); in place allowed
+ *   k_out         DEVICE bf16 or NULL: the rotated keys once more, for pva_attn_fwd
+ * Two tokens of one call that name the same slot leave a mixture of both there. */
+pva_status pva_cache_append(const pva_cache_desc* cache, const pva_cache_batch* batch,
+                            const pva_rope_desc* rope, const void* k, int64_t k_stride,
+                            const void* v, int64_t v_stride, const void* q, int64_t q_stride,
+                            int32_t num_q_heads, void* q_out, int64_t q_out_stride, void* k_out,
+                            int64_t k_out_stride, void* stream);
+
+/* Cached rows as a contiguous pack, for pva_attn_fwd over a context that is
+ * already cached: row cu_new[b] + i is the token at position starts[b] + i
+ * (starts_dev DEVICE int32 [num_seqs], NULL: 0).  kv_lens is not used.
+ *   k_out, v_out  DEVICE bf16 [num_tokens, num_kv_heads, head_dim], contiguous */
+pva_status pva_cache_read(const pva_cache_desc* cache, const pva_cache_batch* batch,
+                          const int32_t* starts_dev, void* k_out, void* v_out, void* stream);
+
+/* Workspace of pva_cache_attn (HOST computation; 0 on invalid arguments).
+ * max_new: an upper bound of the new tokens of a sequence. */
+size_t pva_cache_attn_bytes(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
+                            int32_t head_dim, int32_t max_new);
+
+/* Attention of the new tokens over the cache: the token at position t sees the
+ * cached keys j <= t of its sequence, and with window > 0 only t - j < window
+ * (the masks of pva_attn_fwd).  Made for few new tokens a sequence (one, or some
+ * drafts); any number is right.
+ *   q          DEVICE bf16 [num_tokens, num_q_heads, head_dim], rotated as the keys are
+ *   out        DEVICE [num_tokens, num_q_heads, head_dim], bf16 or fp32
+ *   lse        DEVICE fp32 [num_q_heads, num_tokens], natural log: partials over
+ *              disjoint caches merge by pva_merge_partials
+ *   workspace  DEVICE, 256-byte aligned; its contents need not be kept between calls;
+ *              one call at a time
+ * Keys without a page are left out (status 300); a row that sees no key gives
+ * O = 0 and LSE = -inf. What slots past kv_lens hold does not matter.  A cached
+ * infinity or NaN that some of a sequence's new tokens see may reach the others.
+ * The result does not depend on timing.  softmax_scale <= 0 selects
+ * 1/sqrt(head_dim). */
+pva_status pva_cache_attn(const pva_cache_desc* cache, const pva_cache_batch* batch,
+                          const void* q, int64_t q_stride, int32_t num_q_heads, int32_t max_new,
+                          int32_t window, float softmax_scale, void* out, int32_t out_is_fp32,
+                          float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Read a status word (HOST code_out).  Synchronizes `stream`. */
+pva_status pva_cache_status(const int32_t* status_dev, int32_t* code_out, void* stream);
+
 /* ---- Sharding solvers for context parallelism ("03 · 长文负载均衡" §4.2-§4.4) ----
  * They plan how the query rows of a pack are split over cp ranks; the pieces
  * then run through pva_build_worklist / pva_attn_fwd (e.g. as AttnSlices). */

@@ -27,6 +27,8 @@ EXPORTS = ("pva_worklist_bytes", "pva_build_worklist", "pva_attn_fwd", "pva_attn
            "pva_striped_shard_len", "pva_striped_shard", "pva_wlb_choose",
            "pva_fit_tile_cost",
            "pva_bwd_plan_bytes", "pva_build_bwd_plan", "pva_attn_bwd",
+           "pva_rope", "pva_cache_append", "pva_cache_read", "pva_cache_attn_bytes",
+           "pva_cache_attn", "pva_cache_status",
            "pva_status_string", "pva_version")
 
 
@@ -51,6 +53,26 @@ class WorklistParams(ctypes.Structure):
                 ("num_ctas", ctypes.c_int32), ("refine_iters", ctypes.c_int32),
                 ("c_tile", ctypes.c_int64), ("dispatch", ctypes.c_int32),
                 ("pack_docs", ctypes.c_int32)]
+
+
+class RopeDesc(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("max_pos", ctypes.c_int32),
+                ("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32)]
+
+
+class CacheDesc(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("num_pages", ctypes.c_int64), ("k_pages", ctypes.c_void_p),
+                ("v_pages", ctypes.c_void_p), ("k_scales", ctypes.c_void_p),
+                ("v_scales", ctypes.c_void_p)]
+
+
+class CacheBatch(ctypes.Structure):
+    _fields_ = [("num_seqs", ctypes.c_int32), ("num_tokens", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32), ("table_stride", ctypes.c_int64),
+                ("page_table", ctypes.c_void_p), ("kv_lens", ctypes.c_void_p),
+                ("cu_new", ctypes.c_void_p), ("status", ctypes.c_void_p)]
 
 
 class PvaError(RuntimeError):
@@ -124,6 +146,22 @@ def lib() -> ctypes.CDLL:
         L.pva_attn_bwd.restype = ctypes.c_int
         L.pva_attn_bwd.argtypes = [P, P, P, P, P, P, P, i32, MP, WP, i32, P, P, P, P, P, i32,
                                    ctypes.c_float, P]
+        RP, CP, BP = (ctypes.POINTER(RopeDesc), ctypes.POINTER(CacheDesc),
+                      ctypes.POINTER(CacheBatch))
+        L.pva_rope.restype = ctypes.c_int
+        L.pva_rope.argtypes = [P, i64, P, i64, i32, i32, i32, i32, i32, RP, P, i32, P, i32, P,
+                               i64, P, i64, P, P]
+        L.pva_cache_append.restype = ctypes.c_int
+        L.pva_cache_append.argtypes = [CP, BP, RP, P, i64, P, i64, P, i64, i32, P, i64, P, i64, P]
+        L.pva_cache_read.restype = ctypes.c_int
+        L.pva_cache_read.argtypes = [CP, BP, P, P, P, P]
+        L.pva_cache_attn_bytes.restype = sz
+        L.pva_cache_attn_bytes.argtypes = [i32, i32, i32, i32, i32]
+        L.pva_cache_attn.restype = ctypes.c_int
+        L.pva_cache_attn.argtypes = [CP, BP, P, i64, i32, i32, i32, ctypes.c_float, P, i32, P, P,
+                                     sz, P]
+        L.pva_cache_status.restype = ctypes.c_int
+        L.pva_cache_status.argtypes = [P, ctypes.POINTER(i32), P]
         L.pva_debug_withhold_kv_load.restype = None
         L.pva_debug_withhold_kv_load.argtypes = [i32]
         L.pva_status_string.restype = ctypes.c_char_p

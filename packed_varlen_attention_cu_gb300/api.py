@@ -13,7 +13,7 @@ import numpy as np
 import torch
 
 from . import _lib
-from ._lib import MaskDesc, Slice, WorklistParams, check, lib
+from ._lib import CacheBatch, MaskDesc, RopeDesc, Slice, WorklistParams, check, lib
 from .workloads import (MASK_CAUSAL, MASK_SHARED_QUESTION, MASK_SLICES, MASK_SLIDING_WINDOW,
                         MASK_ZIGZAG_PAIR, MASK_ZIGZAG_STEP)
 
@@ -275,6 +275,230 @@ def attn_bwd(q, k, v, out, lse, dout, cu_seqlens: Optional[torch.Tensor], num_do
         ctypes.byref(mask), ctypes.byref(params), q.shape[-1], _ptr(worklist), _ptr(plan),
         _ptr(dq), _ptr(dk), _ptr(dv), 1 if dq.dtype == torch.float32 else 0,
         float(softmax_scale), _stream(stream)))
+
+
+# ------------------------------------------------------ positions and the key/value cache
+CACHE_BF16, CACHE_INT4 = 0, 1  # pva_cache_kind
+_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
+
+
+def _need(ok, what: str) -> None:
+    if not ok:
+        raise ValueError(what)
+
+
+def _rows3(t: torch.Tensor, name: str, dtype=_BF16) -> int:
+    """Token stride of a [tokens, heads, head_dim] tensor whose heads and dims are contiguous."""
+    _need(t.dim() == 3 and t.dtype == dtype and t.is_cuda, f"{name}: a {dtype} CUDA tensor [tokens, heads, head_dim]")
+    s, h, d = t.stride(), t.shape[1], t.shape[2]
+    _need((s[2] == 1 or d == 1) and (s[1] == d or h == 1), f"{name}: heads and dims must be contiguous")
+    _need(t.shape[0] <= 1 or s[0] >= h * d, f"{name}: token rows overlap")
+    return s[0] if t.shape[0] > 1 else 0
+
+
+def _ints(t: Optional[torch.Tensor], n: int, name: str) -> Optional[int]:
+    """Pointer of an int32 vector of at least n entries (None stays None)."""
+    if t is None:
+        return None
+    _need(t.dtype == _I32 and t.is_cuda and t.dim() == 1 and t.shape[0] >= n and
+          (t.shape[0] <= 1 or t.stride(0) == 1), f"{name}: a contiguous int32 CUDA tensor of at least {n} entries")
+    return t.data_ptr()
+
+
+def _here(stream, *tensors) -> int:
+    """Stream of a call whose tensors all live on the current device."""
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.device.index != dev:
+            raise ValueError(f"tensor on {t.device}, current device is cuda:{dev}")
+    return _stream(stream)
+
+
+def rope_table(max_pos: int, rot_dim: int, base: float = 10000.0, device="cuda",
+               inv_freq: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """(cos, sin) of position t and pair p, fp32 [max_pos, rot_dim / 2, 2]: angle
+    t * base^(-2 p / rot_dim), or t * inv_freq[p] (float64 [rot_dim / 2]); computed in 64 bits."""
+    if inv_freq is None:
+        inv_freq = float(base) ** (-torch.arange(0, rot_dim, 2, dtype=torch.float64) / rot_dim)
+    a = torch.arange(max_pos, dtype=torch.float64, device=device)[:, None] * \
+        inv_freq.to(device=device, dtype=torch.float64)
+    return torch.stack((a.cos(), a.sin()), -1).float()
+
+
+def _rope_desc(table: Optional[torch.Tensor], interleaved: bool) -> Optional[RopeDesc]:
+    if table is None:
+        return None
+    _need(table.dtype == _F32 and table.is_cuda and table.dim() == 3 and table.shape[2] == 2 and
+          table.is_contiguous(), "table: fp32 CUDA tensor [max_pos, rot_dim / 2, 2]")
+    return RopeDesc(table.data_ptr(), table.shape[0], 2 * table.shape[1], 1 if interleaved else 0)
+
+
+def rope(q: Optional[torch.Tensor], k: Optional[torch.Tensor], table: torch.Tensor,
+         q_out: Optional[torch.Tensor], k_out: Optional[torch.Tensor],
+         cu_seqlens: Optional[torch.Tensor] = None, positions: Optional[torch.Tensor] = None,
+         interleaved: bool = False, inverse: bool = False,
+         status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Rotate a pack's queries and keys ([tokens, heads, head_dim], bf16 or fp32) by
+    their positions: inside the documents of cu_seqlens, or `positions` (int32
+    [tokens], e.g. of a zigzag shard).  inverse: turn back (the gradient).
+    q or k may be None; q_out is q (in place) is allowed."""
+    x = q if q is not None else k
+    _need(x is not None and (q is None) == (q_out is None) and (k is None) == (k_out is None),
+          "rope: queries or keys, each with its output")
+    _need(x.dtype in (_BF16, _F32), "rope: bf16 or fp32")
+    _need(cu_seqlens is None or positions is None, "rope: cu_seqlens or positions, not both")
+    t, _, d = x.shape
+    for y, o in ((q, q_out), (k, k_out)):
+        _need(y is None or (y.shape == o.shape and y.shape[0] == t and y.shape[2] == d),
+              "rope: shapes differ")
+    qs, ks, qo, ko = (0 if y is None else _rows3(y, "rope", x.dtype) for y in (q, k, q_out, k_out))
+    st = _here(stream, q, k, q_out, k_out, table, cu_seqlens, positions, status)
+    check("pva_rope", lib().pva_rope(
+        _ptr(q), qs, _ptr(k), ks, t, 0 if q is None else q.shape[1],
+        0 if k is None else k.shape[1], d, 1 if x.dtype == _F32 else 0,
+        _rope_desc(table, interleaved), _ints(cu_seqlens, 1, "cu_seqlens"),
+        0 if cu_seqlens is None else cu_seqlens.shape[0] - 1, _ints(positions, t, "positions"),
+        1 if inverse else 0, _ptr(q_out), qo, _ptr(k_out), ko, _ints(status, 1, "status"), st))
+
+
+class KVCache:
+    """A paged key/value cache over tensors that the caller owns: bf16 rows
+    [num_pages, kv heads, page_size, head_dim], or 4-bit rows (uint8
+    [.., head_dim / 2]) with their scales (bf16 [.., head_dim / 64, 2])."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scales: Optional[torch.Tensor] = None,
+                 v_scales: Optional[torch.Tensor] = None):
+        int4 = k.dtype == torch.uint8
+        _need(k.dim() == 4 and k.shape == v.shape and k.dtype == v.dtype and
+              k.dtype in (_BF16, torch.uint8), "KVCache: k and v bf16 or uint8 [pages, heads, page_size, row]")
+        pages, heads, page, row = k.shape
+        self.kind, self.head_dim = (CACHE_INT4, 2 * row) if int4 else (CACHE_BF16, row)
+        self.num_pages, self.num_kv_heads, self.page_size = pages, heads, page
+        _need((k_scales is not None and v_scales is not None) if int4 else
+              (k_scales is None and v_scales is None), "KVCache: scales go with 4-bit rows")
+        for s in (k_scales, v_scales) if int4 else ():
+            _need(s.dtype == _BF16 and tuple(s.shape) == (pages, heads, page, self.head_dim // 64, 2),
+                  "KVCache: scales bf16 [pages, heads, page_size, head_dim / 64, 2]")
+        self.k, self.v, self.k_scales, self.v_scales = k, v, k_scales, v_scales
+        for t in (k, v, k_scales, v_scales):
+            _need(t is None or (t.is_cuda and t.is_contiguous() and t.device == k.device),
+                  "KVCache: contiguous CUDA tensors of one device")
+        self.device = k.device
+        self.desc = _lib.CacheDesc(self.kind, heads, self.head_dim, page, pages, _ptr(k), _ptr(v),
+                                   _ptr(k_scales), _ptr(v_scales))
+
+    @classmethod
+    def alloc(cls, num_pages: int, num_kv_heads: int, head_dim: int, page_size: int = 64,
+              kind: int = CACHE_BF16, device="cuda") -> "KVCache":
+        shape = (num_pages, num_kv_heads, page_size)
+        if kind == CACHE_BF16:
+            return cls(*(torch.zeros(shape + (head_dim,), dtype=_BF16, device=device) for _ in "kv"))
+        return cls(*(torch.zeros(shape + (head_dim // 2,), dtype=torch.uint8, device=device) for _ in "kv"),
+                   *(torch.zeros(shape + (head_dim // 64, 2), dtype=_BF16, device=device) for _ in "kv"))
+
+
+def _cache_batch(page_table, num_tokens: int, kv_lens, cu_new, status) -> CacheBatch:
+    _need(page_table.dtype == _I32 and page_table.is_cuda and page_table.dim() == 2 and
+          (page_table.shape[1] <= 1 or page_table.stride(1) == 1),
+          "page_table: int32 CUDA tensor [sequences, pages] with contiguous rows")
+    n, width = page_table.shape
+    return CacheBatch(n, num_tokens, width, page_table.stride(0) if n > 1 else width,
+                      page_table.data_ptr(), _ints(kv_lens, n, "kv_lens"),
+                      _ints(cu_new, n + 1, "cu_new"), _ints(status, 1, "status"))
+
+
+def cache_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, page_table: torch.Tensor,
+                 kv_lens: torch.Tensor, cu_new: Optional[torch.Tensor] = None,
+                 table: Optional[torch.Tensor] = None, q: Optional[torch.Tensor] = None,
+                 q_out: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None,
+                 interleaved: bool = False, status: Optional[torch.Tensor] = None,
+                 stream=None) -> None:
+    """Append the new tokens' keys and values ([tokens, kv heads, head_dim] bf16) to
+    the cache.  Sequence b owns rows cu_new[b] .. cu_new[b + 1] (None: row b) and
+    kv_lens[b] counts its tokens with the new ones; page_table [sequences, pages].
+    With an angle table the keys are rotated on the way (k_out: a copy of them for
+    attn_fwd), and the queries q into q_out."""
+    t, h, d = k.shape
+    _need(k.shape == v.shape and h == cache.num_kv_heads and d == cache.head_dim,
+          "cache_append: k and v [tokens, kv heads, head_dim] of the cache")
+    _need((q is None) == (q_out is None), "cache_append: q goes with q_out")
+    _need(q is None or (q.shape == q_out.shape and q.shape[0] == t and q.shape[2] == d),
+          "cache_append: q and q_out [tokens, heads, head_dim]")
+    _need(k_out is None or k_out.shape == k.shape, "cache_append: k_out has k's shape")
+    ks, vs = _rows3(k, "k"), _rows3(v, "v")
+    qs, qo, ko = (0 if x is None else _rows3(x, "q, q_out, k_out") for x in (q, q_out, k_out))
+    b = _cache_batch(page_table, t, kv_lens, cu_new, status)
+    st = _here(stream, cache.k, k, v, page_table, kv_lens, cu_new, table, q, q_out, k_out, status)
+    check("pva_cache_append", lib().pva_cache_append(
+        cache.desc, b, _rope_desc(table, interleaved), _ptr(k), ks, _ptr(v), vs, _ptr(q), qs,
+        0 if q is None else q.shape[1], _ptr(q_out), qo, _ptr(k_out), ko, st))
+
+
+def cache_read(cache: KVCache, page_table: torch.Tensor, cu_out: torch.Tensor,
+               k_out: torch.Tensor, v_out: torch.Tensor, starts: Optional[torch.Tensor] = None,
+               status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Cached rows as a contiguous pack: rows cu_out[b] .. cu_out[b + 1] of k_out and
+    v_out (bf16 [tokens, kv heads, head_dim]) are the tokens of sequence b from
+    position starts[b] (None: 0) on.  Other rows are left as they were."""
+    t = k_out.shape[0]
+    for x in (k_out, v_out):
+        _need(x.dtype == _BF16 and x.is_cuda and x.is_contiguous() and
+              tuple(x.shape) == (t, cache.num_kv_heads, cache.head_dim),
+              "cache_read: outputs contiguous bf16 [tokens, kv heads, head_dim]")
+    b = _cache_batch(page_table, t, None, cu_out, status)
+    st = _here(stream, cache.k, page_table, cu_out, k_out, v_out, starts, status)
+    check("pva_cache_read", lib().pva_cache_read(
+        cache.desc, b, _ints(starts, b.num_seqs, "starts"), _ptr(k_out), _ptr(v_out), st))
+
+
+def cache_attn_bytes(num_seqs: int, num_q_heads: int, num_kv_heads: int, head_dim: int,
+                     max_new: int = 1) -> int:
+    n = lib().pva_cache_attn_bytes(num_seqs, num_q_heads, num_kv_heads, head_dim, max_new)
+    if n == 0:
+        raise _lib.PvaError("pva_cache_attn_bytes", 1)
+    return int(n)
+
+
+def alloc_cache_workspace(num_seqs: int, num_q_heads: int, num_kv_heads: int, head_dim: int,
+                          max_new: int = 1, device="cuda") -> torch.Tensor:
+    """Workspace of cache_attn for up to num_seqs sequences; one call at a time uses it."""
+    return torch.empty(cache_attn_bytes(num_seqs, num_q_heads, num_kv_heads, head_dim, max_new),
+                       dtype=torch.uint8, device=device)
+
+
+def cache_attn(cache: KVCache, q: torch.Tensor, page_table: torch.Tensor, kv_lens: torch.Tensor,
+               out: torch.Tensor, lse: torch.Tensor, workspace: torch.Tensor,
+               cu_new: Optional[torch.Tensor] = None, max_new: int = 1, window: int = 0,
+               softmax_scale: float = 0.0, status: Optional[torch.Tensor] = None,
+               stream=None) -> None:
+    """Attention of the new tokens' queries ([tokens, heads, head_dim] bf16, rotated)
+    over their sequences' cached keys: token i of sequence b's n new ones stands at
+    position kv_lens[b] - n + i and sees the keys up to it (window > 0: the last
+    `window` of them).  out bf16 or fp32 like q, lse fp32 [heads, tokens]; max_new:
+    an upper bound of n."""
+    t, h, d = q.shape
+    _need(d == cache.head_dim, "cache_attn: head_dim differs from the cache's")
+    _need(out.shape == q.shape and out.is_contiguous() and out.is_cuda and
+          out.dtype in (_BF16, _F32), "cache_attn: out contiguous bf16 or fp32 of q's shape")
+    _need(lse.dtype == _F32 and lse.is_cuda and lse.is_contiguous() and
+          tuple(lse.shape) == (h, t), "cache_attn: lse contiguous fp32 [heads, tokens]")
+    _need(workspace.is_cuda and workspace.is_contiguous(), "cache_attn: a contiguous CUDA workspace")
+    qs = _rows3(q, "q")
+    b = _cache_batch(page_table, t, kv_lens, cu_new, status)
+    st = _here(stream, cache.k, q, page_table, kv_lens, out, lse, workspace, cu_new, status)
+    check("pva_cache_attn", lib().pva_cache_attn(
+        cache.desc, b, q.data_ptr(), qs, h, max_new, window, softmax_scale, out.data_ptr(),
+        1 if out.dtype == _F32 else 0, lse.data_ptr(), workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), st))
+
+
+def cache_status(status: torch.Tensor, stream=None) -> int:
+    """The first failure met on the device by the calls that were given this status word
+    (int32, 0 before them): 0, or a code of pva.h.  Synchronizes the stream."""
+    code = ctypes.c_int32(0)
+    check("pva_cache_status", lib().pva_cache_status(
+        _ints(status, 1, "status"), ctypes.byref(code), _here(stream, status)))
+    return int(code.value)
 
 
 # ------------------------------------------------------ sharding solvers

@@ -1,0 +1,582 @@
+// rope.cu -- rotation of queries and keys by their positions, alone (a pack and
+// its gradient) and on the way into the paged cache; and the way back, cached
+// rows as a contiguous pack.
+//
+// A pair (a, b) of a head's dims at position t turns by the angle w_p t of its
+// pair index p:  (a cos - b sin, b cos + a sin).  The turn is orthogonal, so
+// the gradient goes back through the same kernel with the sign of sin changed.
+// The angles come as a table of (cos, sin) in fp32: far positions need 64 bits
+// for w_p t, which the caller spends once.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "../../include/pva.h"
+#include "cache.cuh"
+
+namespace pva {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+enum { kNoCache = -1 };
+
+struct RotArgs {
+    const void *q, *k, *v;
+    void *q_out, *k_out;
+    int64_t q_stride, k_stride, v_stride, q_out_stride, k_out_stride;
+    const float* table;  // [max_pos][rot / 2][2], or null: no rotation
+    const int32_t* positions;
+    void *k_pages, *v_pages, *k_scales, *v_scales;
+    SeqView s;  // cu: documents (rotation alone) or new tokens (append)
+    int32_t max_pos, rot, inter, inverse;
+    int32_t hq, hkv, nslots;
+};
+
+__device__ __forceinline__ float min_nan(float a, float b) {
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+// Eight consecutive dims of a row.
+template <bool F32>
+struct Octet;
+template <>
+struct Octet<false> {
+    uint4 r;
+    __device__ __forceinline__ void load(const void* row, int o) {
+        r = __ldcs(reinterpret_cast<const uint4*>(row) + o);
+    }
+    __device__ __forceinline__ void store(void* row, int o) const {
+        reinterpret_cast<uint4*>(row)[o] = r;
+    }
+    __device__ __forceinline__ void get(float* x) const {
+        const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x[2 * i] = __uint_as_float(w[i] << 16);
+            x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
+    }
+    __device__ __forceinline__ void set(const float* x) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const __nv_bfloat162 p = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+            w[i] = *reinterpret_cast<const uint32_t*>(&p);
+        }
+        r = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+};
+template <>
+struct Octet<true> {
+    float4 a, b;
+    __device__ __forceinline__ void load(const void* row, int o) {
+        a = __ldcs(reinterpret_cast<const float4*>(row) + 2 * o);
+        b = __ldcs(reinterpret_cast<const float4*>(row) + 2 * o + 1);
+    }
+    __device__ __forceinline__ void store(void* row, int o) const {
+        reinterpret_cast<float4*>(row)[2 * o] = a;
+        reinterpret_cast<float4*>(row)[2 * o + 1] = b;
+    }
+    __device__ __forceinline__ void get(float* x) const {
+        x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+        x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+    }
+    __device__ __forceinline__ void set(const float* x) {
+        a = make_float4(x[0], x[1], x[2], x[3]);
+        b = make_float4(x[4], x[5], x[6], x[7]);
+    }
+};
+
+// Products and sums are rounded one by one (no contraction), as the formula
+// writes them: a 4-bit code then depends on the formula's own values alone.
+__device__ __forceinline__ void turn(float& a, float& b, float c, float s) {
+    const float x = __fsub_rn(__fmul_rn(a, c), __fmul_rn(b, s));
+    b = __fadd_rn(__fmul_rn(b, c), __fmul_rn(a, s));
+    a = x;
+}
+
+// Codes of eight values of a group with (low, inv): one 32-bit word.
+__device__ __forceinline__ uint32_t encode(const float* x, float low, float inv) {
+    uint32_t w = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float c = fminf(fmaxf(rintf(__fmul_rn(__fsub_rn(x[i], low), inv)), 0.f), 15.f);
+        w |= (uint32_t)c << (4 * (i / 2) + 16 * (i % 2));
+    }
+    return w;
+}
+
+// One warp takes kUnroll passes of a token; a pass is 32 lanes = 32 / (D / 16)
+// heads, a lane holds the two octets of its head that turn against each other
+// (half-split pairs p and p + rot / 2: octets j and j + rot / 16; interleaved
+// pairs: octets 2j and 2j + 1), so a rotation needs no shuffle and the lane's
+// 16 angles serve all its heads.  The heads of q, k and v form one list of
+// slots, whatever their counts.
+template <int D, bool F32, int KIND>
+__global__ void __launch_bounds__(kThreads) rotate_kernel(const RotArgs a) {
+    constexpr int kLph = D / 16;         // lanes a head
+    constexpr int kHpw = 32 / kLph;      // heads a pass
+    constexpr int kUnroll = F32 ? 2 : 4;
+    constexpr int kElem = F32 ? 4 : 2;
+    const int lane = threadIdx.x & 31;
+    const int j = lane % kLph, sub = lane / kLph;
+    int oa, ob;
+    bool rotated;
+    if (a.inter || j >= a.rot / 16) {
+        // interleaved pairs, or dims past the rotated ones
+        oa = a.inter ? 2 * j : a.rot / 8 + 2 * (j - a.rot / 16);
+        ob = oa + 1;
+        rotated = 16 * j < a.rot;
+    } else {
+        oa = j;
+        ob = j + a.rot / 16;
+        rotated = true;
+    }
+    const int slot0 = blockIdx.y * kUnroll * kHpw + sub;
+    const int64_t stride = (int64_t)gridDim.x * kWarps;
+    for (int64_t tt = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5); tt < a.s.num_tokens;
+         tt += stride) {
+        const int32_t t = (int32_t)tt;
+        int32_t b = -1, pos = t;
+        if (KIND != kNoCache) {
+            int32_t n = 1, i = 0;
+            if (a.s.cu) {
+                b = find_seq(a.s.cu, a.s.num_seqs, t);
+                if (b < 0) continue;
+                i = t - a.s.cu[b];
+                n = a.s.cu[b + 1] - a.s.cu[b];
+            } else {
+                b = t;
+                if (b >= a.s.num_seqs) continue;
+            }
+            pos = (int32_t)max((int64_t)a.s.kv_lens[b] - n + i, (int64_t)-1);
+        } else if (a.positions) {
+            pos = a.positions[t];
+        } else if (a.s.cu) {
+            b = find_seq(a.s.cu, a.s.num_seqs, t);
+            if (b < 0) continue;
+            pos = t - a.s.cu[b];
+        }
+        if (pos < 0 || (a.rot > 0 && pos >= a.max_pos)) {
+            if (lane == 0)
+                raise_status(a.s.status, KIND != kNoCache && pos < 0 ? kErrLength : kErrPosition);
+            continue;
+        }
+        Octet<F32> xa[kUnroll], xb[kUnroll];
+        const void* row[kUnroll];
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            const int slot = slot0 + u * kHpw;
+            row[u] = nullptr;
+            if (slot < a.hq)
+                row[u] = (const char*)a.q + (t * a.q_stride + (int64_t)slot * D) * kElem;
+            else if (slot < a.hq + a.hkv)
+                row[u] = (const char*)a.k + (t * a.k_stride + (int64_t)(slot - a.hq) * D) * kElem;
+            else if (KIND != kNoCache && slot < a.nslots)
+                row[u] = (const char*)a.v +
+                         (t * a.v_stride + (int64_t)(slot - a.hq - a.hkv) * D) * kElem;
+            if (row[u]) {
+                xa[u].load(row[u], oa);
+                xb[u].load(row[u], ob);
+            }
+        }
+        float c[8], s[8];
+        if (rotated) {
+            const float4* cs =
+                reinterpret_cast<const float4*>(a.table + ((int64_t)pos * (a.rot / 2) + 8 * j) * 2);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float4 f = __ldg(cs + i);
+                c[2 * i] = f.x;
+                s[2 * i] = a.inverse ? -f.y : f.y;
+                c[2 * i + 1] = f.z;
+                s[2 * i + 1] = a.inverse ? -f.w : f.w;
+            }
+        }
+        int64_t page = -1;
+        int32_t slot_in_page = 0;
+        if (KIND != kNoCache) {
+            page = page_of(a.s, b, pos);
+            slot_in_page = pos & ((1 << a.s.page_shift) - 1);
+            if (page < 0 && lane == 0) raise_status(a.s.status, kErrPage);
+        }
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            const int slot = slot0 + u * kHpw;
+            const bool live = row[u] != nullptr;
+            const bool is_q = slot < a.hq, is_k = !is_q && slot < a.hq + a.hkv;
+            if (live && rotated && (is_q || is_k)) {
+                float x[16];
+                xa[u].get(x);
+                xb[u].get(x + 8);
+                if (a.inter) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) turn(x[2 * i], x[2 * i + 1], c[i], s[i]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) turn(x[i], x[8 + i], c[i], s[i]);
+                }
+                xa[u].set(x);
+                xb[u].set(x + 8);
+            }
+            if (live && is_q) {
+                void* o = (char*)a.q_out + (t * a.q_out_stride + (int64_t)slot * D) * kElem;
+                xa[u].store(o, oa);
+                xb[u].store(o, ob);
+            }
+            if (live && is_k && a.k_out) {
+                void* o =
+                    (char*)a.k_out + (t * a.k_out_stride + (int64_t)(slot - a.hq) * D) * kElem;
+                xa[u].store(o, oa);
+                xb[u].store(o, ob);
+            }
+            if (KIND != kNoCache) {
+                const bool put = live && !is_q && page >= 0;
+                const int h = is_k ? slot - a.hq : slot - a.hq - a.hkv;
+                const int64_t at =
+                    ((page * a.hkv + h) << a.s.page_shift) + slot_in_page;  // cached row
+                if (KIND == PVA_CACHE_BF16) {
+                    if (put) {
+                        char* o = (char*)(is_k ? a.k_pages : a.v_pages) + at * D * 2;
+                        xa[u].store(o, oa);
+                        xb[u].store(o, ob);
+                    }
+                } else if (__any_sync(0xffffffffu, live && !is_q)) {
+                    // lowest and highest value of each group, over the head's lanes
+                    constexpr int kG = D / 64;
+                    float x[16], lo[kG], hi[kG];
+                    if (live) {
+                        xa[u].get(x);
+                        xb[u].get(x + 8);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) x[i] = 0.f;
+                    }
+                    float la = x[0], ha = x[0], lb = x[8], hb = x[8];
+#pragma unroll
+                    for (int i = 1; i < 8; ++i) {
+                        la = min_nan(la, x[i]);
+                        ha = max_nan(ha, x[i]);
+                        lb = min_nan(lb, x[8 + i]);
+                        hb = max_nan(hb, x[8 + i]);
+                    }
+                    const int ga = oa / 8, gb = ob / 8;
+#pragma unroll
+                    for (int g = 0; g < kG; ++g) {
+                        lo[g] = INFINITY;
+                        hi[g] = -INFINITY;
+                        if (ga == g) {
+                            lo[g] = min_nan(lo[g], la);
+                            hi[g] = max_nan(hi[g], ha);
+                        }
+                        if (gb == g) {
+                            lo[g] = min_nan(lo[g], lb);
+                            hi[g] = max_nan(hi[g], hb);
+                        }
+#pragma unroll
+                        for (int o = 1; o < kLph; o <<= 1) {
+                            lo[g] = min_nan(lo[g], __shfl_xor_sync(0xffffffffu, lo[g], o));
+                            hi[g] = max_nan(hi[g], __shfl_xor_sync(0xffffffffu, hi[g], o));
+                        }
+                    }
+                    // The scale is kept in bf16 and the codes are taken against the kept one;
+                    // low is one of the bf16 values, so it is kept exactly.
+                    float inv[kG];
+                    uint32_t pair[kG];
+#pragma unroll
+                    for (int g = 0; g < kG; ++g) {
+                        const __nv_bfloat16 sc =
+                            __float2bfloat16_rn(__fmul_rn(__fsub_rn(hi[g], lo[g]), 1.f / 15.f));
+                        const float f = __bfloat162float(sc);
+                        inv[g] = f == 0.f ? 0.f : __frcp_rn(f);
+                        pair[g] = (uint32_t)__bfloat16_as_ushort(sc) |
+                                  (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(lo[g])) << 16;
+                    }
+                    if (put) {
+                        uint32_t* o = (uint32_t*)(is_k ? a.k_pages : a.v_pages) + at * (D / 8);
+                        uint32_t* so = (uint32_t*)(is_k ? a.k_scales : a.v_scales) + at * kG;
+                        o[word_of_octet<D>(oa)] =
+                            encode(x, kG == 2 && ga ? lo[kG - 1] : lo[0],
+                                   kG == 2 && ga ? inv[kG - 1] : inv[0]);
+                        o[word_of_octet<D>(ob)] =
+                            encode(x + 8, kG == 2 && gb ? lo[kG - 1] : lo[0],
+                                   kG == 2 && gb ? inv[kG - 1] : inv[0]);
+                        if (j == 0) {
+#pragma unroll
+                            for (int g = 0; g < kG; ++g) so[g] = pair[g];
+                        }
+                    }
+                }
+            }
+        }
+    }
+}
+
+// ------------------------------------------------------------------ read
+struct ReadArgs {
+    const void *k_pages, *v_pages, *k_scales, *v_scales;
+    void *k_out, *v_out;  // [rows, hkv, D] bf16
+    const int32_t* starts;
+    SeqView s;
+    int32_t hkv;
+};
+
+// One warp takes kUnroll passes of a row; a lane gives one octet of a head.
+template <int D, int KIND>
+__global__ void __launch_bounds__(kThreads) read_kernel(const ReadArgs a) {
+    constexpr int kLph = D / 8, kHpw = 32 / kLph, kUnroll = 4;
+    const int lane = threadIdx.x & 31;
+    const int o = lane % kLph;
+    const int slot0 = blockIdx.y * kUnroll * kHpw + lane / kLph;
+    const int64_t stride = (int64_t)gridDim.x * kWarps;
+    for (int64_t tt = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5); tt < a.s.num_tokens;
+         tt += stride) {
+        const int32_t t = (int32_t)tt;
+        int32_t b = t, i = 0;
+        if (a.s.cu) {
+            b = find_seq(a.s.cu, a.s.num_seqs, t);
+            if (b >= 0) i = t - a.s.cu[b];
+        }
+        if (b < 0 || b >= a.s.num_seqs) continue;
+        const int64_t pos = (a.starts ? a.starts[b] : 0) + (int64_t)i;
+        const int64_t page = pos > INT32_MAX ? -1 : page_of(a.s, b, (int32_t)pos);
+        if (page < 0) {
+            if (lane == 0) raise_status(a.s.status, kErrPage);
+            continue;
+        }
+        const int32_t in_page = (int32_t)pos & ((1 << a.s.page_shift) - 1);
+        uint4 x[kUnroll];
+        uint32_t sc[kUnroll];
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            const int slot = slot0 + u * kHpw;
+            const bool is_k = slot < a.hkv;
+            const int h = is_k ? slot : slot - a.hkv;
+            if (h >= a.hkv) continue;
+            const int64_t at = ((page * a.hkv + h) << a.s.page_shift) + in_page;
+            if (KIND == PVA_CACHE_BF16) {
+                x[u] = __ldcs((const uint4*)(is_k ? a.k_pages : a.v_pages) + at * kLph + o);
+            } else {
+                x[u].x = __ldcs((const uint32_t*)(is_k ? a.k_pages : a.v_pages) + at * (D / 8) +
+                                word_of_octet<D>(o));
+                sc[u] = __ldcs((const uint32_t*)(is_k ? a.k_scales : a.v_scales) + at * (D / 64) +
+                               o / 8);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            const int slot = slot0 + u * kHpw;
+            const bool is_k = slot < a.hkv;
+            const int h = is_k ? slot : slot - a.hkv;
+            if (h >= a.hkv) continue;
+            if (KIND == PVA_CACHE_INT4) {
+                const float scale = __uint_as_float(sc[u] << 16);
+                const float low = __uint_as_float(sc[u] & 0xffff0000u);
+                float f[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    f[e] = __fadd_rn(low, __fmul_rn((float)((x[u].x >> (4 * (e / 2) + 16 * (e % 2))) & 15u), scale));
+                Octet<false> y;
+                y.set(f);
+                x[u] = y.r;
+            }
+            ((uint4*)(is_k ? a.k_out : a.v_out))[((int64_t)t * a.hkv + h) * kLph + o] = x[u];
+        }
+    }
+}
+
+// CTAs along the tokens: enough for every SM to hold eight, then a stride.
+int grid_x(int64_t tokens, int grid_y) {
+    int dev = 0, sms = 148;
+    if (cudaGetDevice(&dev) == cudaSuccess)
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    const int64_t blocks = (tokens + kWarps - 1) / kWarps;
+    const int64_t cap = ((int64_t)sms * 64 + grid_y - 1) / grid_y;
+    return (int)(blocks < cap ? (blocks > 0 ? blocks : 1) : cap);
+}
+
+template <int D, bool F32, int KIND>
+pva_status launch_rotate(const RotArgs& a, cudaStream_t st) {
+    constexpr int per = (F32 ? 2 : 4) * (32 / (D / 16));
+    const int gy = (a.nslots + per - 1) / per;
+    if (gy > 65535) return PVA_ERR_UNSUPPORTED;
+    rotate_kernel<D, F32, KIND><<<dim3(grid_x(a.s.num_tokens, gy), gy), kThreads, 0, st>>>(a);
+    return cudaGetLastError() == cudaSuccess ? PVA_OK : PVA_ERR_CUDA;
+}
+
+template <int D, int KIND>
+pva_status launch_read(const ReadArgs& a, cudaStream_t st) {
+    constexpr int per = 4 * (32 / (D / 8));
+    const int gy = (2 * a.hkv + per - 1) / per;
+    if (gy > 65535) return PVA_ERR_UNSUPPORTED;
+    read_kernel<D, KIND><<<dim3(grid_x(a.s.num_tokens, gy), gy), kThreads, 0, st>>>(a);
+    return cudaGetLastError() == cudaSuccess ? PVA_OK : PVA_ERR_CUDA;
+}
+
+// The angle table: rot_dim 0 (or no descriptor) means no rotation.
+pva_status check_rope(const pva_rope_desc* r, int32_t head_dim) {
+    if (!r) return PVA_OK;
+    if (r->rot_dim < 0 || r->rot_dim > head_dim || r->max_pos < 0 ||
+        (r->interleaved != 0 && r->interleaved != 1))
+        return PVA_ERR_INVALID_ARG;
+    if (r->rot_dim % 16 != 0) return PVA_ERR_UNSUPPORTED;
+    if (r->rot_dim > 0 && r->max_pos > 0 && (!r->table || !aligned16(r->table)))
+        return PVA_ERR_INVALID_ARG;
+    return PVA_OK;
+}
+
+void set_rope(RotArgs* a, const pva_rope_desc* r) {
+    a->rot = r ? r->rot_dim : 0;
+    a->table = r ? r->table : nullptr;
+    a->max_pos = r ? r->max_pos : 0;
+    a->inter = r ? r->interleaved : 0;
+}
+
+}  // namespace
+}  // namespace pva
+
+using namespace pva;
+
+extern "C" pva_status pva_rope(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                               int32_t num_tokens, int32_t num_q_heads, int32_t num_kv_heads,
+                               int32_t head_dim, int32_t is_fp32, const pva_rope_desc* rope,
+                               const int32_t* cu_seqlens_dev, int32_t num_docs,
+                               const int32_t* positions_dev, int32_t inverse, void* q_out,
+                               int64_t q_out_stride, void* k_out, int64_t k_out_stride,
+                               int32_t* status_dev, void* stream) {
+    if (num_tokens < 0 || num_q_heads < 0 || num_kv_heads < 0 || num_docs < 0 || !rope ||
+        (is_fp32 != 0 && is_fp32 != 1) || (inverse != 0 && inverse != 1))
+        return PVA_ERR_INVALID_ARG;
+    if (head_dim != 64 && head_dim != 128) return PVA_ERR_UNSUPPORTED;
+    const pva_status rs = check_rope(rope, head_dim);
+    if (rs != PVA_OK) return rs;
+    if (cu_seqlens_dev && positions_dev) return PVA_ERR_INVALID_ARG;
+    if (!aligned4(cu_seqlens_dev) || !aligned4(positions_dev) || !aligned4(status_dev))
+        return PVA_ERR_INVALID_ARG;
+    const int eb = is_fp32 ? 4 : 2;
+    RotArgs a = {};
+    a.q_stride = row_stride(q_stride, num_q_heads, head_dim, eb);
+    a.k_stride = row_stride(k_stride, num_kv_heads, head_dim, eb);
+    a.q_out_stride = row_stride(q_out_stride, num_q_heads, head_dim, eb);
+    a.k_out_stride = row_stride(k_out_stride, num_kv_heads, head_dim, eb);
+    if (a.q_stride < 0 || a.k_stride < 0 || a.q_out_stride < 0 || a.k_out_stride < 0)
+        return PVA_ERR_INVALID_ARG;
+    if (num_tokens == 0 || num_q_heads + num_kv_heads == 0) return PVA_OK;
+    if ((num_q_heads > 0 && (!q || !q_out)) || (num_kv_heads > 0 && (!k || !k_out)) ||
+        !aligned16(q) || !aligned16(k) || !aligned16(q_out) || !aligned16(k_out))
+        return PVA_ERR_INVALID_ARG;
+    a.q = q;
+    a.k = k;
+    a.q_out = q_out;
+    a.k_out = k_out;
+    a.positions = positions_dev;
+    a.inverse = inverse;
+    a.hq = num_q_heads;
+    a.hkv = num_kv_heads;
+    a.nslots = num_q_heads + num_kv_heads;
+    set_rope(&a, rope);
+    a.s.cu = cu_seqlens_dev;
+    a.s.num_seqs = num_docs;
+    a.s.num_tokens = num_tokens;
+    a.s.status = status_dev;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (head_dim == 128)
+        return is_fp32 ? launch_rotate<128, true, kNoCache>(a, st)
+                       : launch_rotate<128, false, kNoCache>(a, st);
+    return is_fp32 ? launch_rotate<64, true, kNoCache>(a, st)
+                   : launch_rotate<64, false, kNoCache>(a, st);
+}
+
+extern "C" pva_status pva_cache_append(const pva_cache_desc* cache, const pva_cache_batch* batch,
+                                       const pva_rope_desc* rope, const void* k, int64_t k_stride,
+                                       const void* v, int64_t v_stride, const void* q,
+                                       int64_t q_stride, int32_t num_q_heads, void* q_out,
+                                       int64_t q_out_stride, void* k_out, int64_t k_out_stride,
+                                       void* stream) {
+    pva_status st = check_cache(cache);
+    if (st == PVA_OK) st = check_batch(batch, true);
+    if (st == PVA_OK) st = check_rope(rope, cache->head_dim);
+    if (st != PVA_OK) return st;
+    const int32_t d = cache->head_dim, hkv = cache->num_kv_heads;
+    if (num_q_heads < 0 || (num_q_heads > 0) != (q != nullptr) || (q == nullptr) != (q_out == nullptr))
+        return PVA_ERR_INVALID_ARG;
+    RotArgs a = {};
+    a.q_stride = row_stride(q_stride, num_q_heads, d, 2);
+    a.k_stride = row_stride(k_stride, hkv, d, 2);
+    a.v_stride = row_stride(v_stride, hkv, d, 2);
+    a.q_out_stride = row_stride(q_out_stride, num_q_heads, d, 2);
+    a.k_out_stride = row_stride(k_out_stride, hkv, d, 2);
+    if (a.q_stride < 0 || a.k_stride < 0 || a.v_stride < 0 || a.q_out_stride < 0 ||
+        a.k_out_stride < 0)
+        return PVA_ERR_INVALID_ARG;
+    if (batch->num_tokens == 0 || batch->num_seqs == 0) return PVA_OK;
+    if (!k || !v || !aligned16(k) || !aligned16(v) || !aligned16(q) || !aligned16(q_out) ||
+        !aligned16(k_out))
+        return PVA_ERR_INVALID_ARG;
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.q_out = q_out;
+    a.k_out = k_out;
+    a.k_pages = cache->k_pages;
+    a.v_pages = cache->v_pages;
+    a.k_scales = cache->k_scales;
+    a.v_scales = cache->v_scales;
+    a.hq = num_q_heads;
+    a.hkv = hkv;
+    a.nslots = num_q_heads + 2 * hkv;
+    set_rope(&a, rope);
+    a.s = seq_view(cache, batch);
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (cache->kind == PVA_CACHE_BF16)
+        return d == 128 ? launch_rotate<128, false, PVA_CACHE_BF16>(a, s)
+                        : launch_rotate<64, false, PVA_CACHE_BF16>(a, s);
+    return d == 128 ? launch_rotate<128, false, PVA_CACHE_INT4>(a, s)
+                    : launch_rotate<64, false, PVA_CACHE_INT4>(a, s);
+}
+
+extern "C" pva_status pva_cache_read(const pva_cache_desc* cache, const pva_cache_batch* batch,
+                                     const int32_t* starts_dev, void* k_out, void* v_out,
+                                     void* stream) {
+    pva_status st = check_cache(cache);
+    if (st == PVA_OK) st = check_batch(batch, false);
+    if (st != PVA_OK) return st;
+    if (!aligned4(starts_dev)) return PVA_ERR_INVALID_ARG;
+    if (batch->num_tokens == 0 || batch->num_seqs == 0) return PVA_OK;
+    if (!k_out || !v_out || !aligned16(k_out) || !aligned16(v_out)) return PVA_ERR_INVALID_ARG;
+    ReadArgs a = {};
+    a.k_pages = cache->k_pages;
+    a.v_pages = cache->v_pages;
+    a.k_scales = cache->k_scales;
+    a.v_scales = cache->v_scales;
+    a.k_out = k_out;
+    a.v_out = v_out;
+    a.starts = starts_dev;
+    a.s = seq_view(cache, batch);
+    a.hkv = cache->num_kv_heads;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (cache->kind == PVA_CACHE_BF16)
+        return cache->head_dim == 128 ? launch_read<128, PVA_CACHE_BF16>(a, s)
+                                      : launch_read<64, PVA_CACHE_BF16>(a, s);
+    return cache->head_dim == 128 ? launch_read<128, PVA_CACHE_INT4>(a, s)
+                                  : launch_read<64, PVA_CACHE_INT4>(a, s);
+}
+
+extern "C" pva_status pva_cache_status(const int32_t* status_dev, int32_t* code_out,
+                                       void* stream) {
+    if (!status_dev || !code_out || !aligned4(status_dev)) return PVA_ERR_INVALID_ARG;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (cudaMemcpyAsync(code_out, status_dev, sizeof(int32_t), cudaMemcpyDeviceToHost, st) !=
+            cudaSuccess ||
+        cudaStreamSynchronize(st) != cudaSuccess)
+        return PVA_ERR_CUDA;
+    return PVA_OK;
+}
