@@ -1,4 +1,25 @@
 // cache_attn.cu -- attention of new tokens over the paged cache.
+//
+// For every new token (row) of a sequence, over the keys j it may see,
+//   s_j = scale q.k_j,  O = sum_j e^(s_j) v_j / sum_j e^(s_j),  LSE = ln sum_j e^(s_j).
+// A row and its head's group share one kv head, so a key and value row is read
+// once for group * new tokens rows: a few multiply-adds a byte, bounded by HBM.
+//
+// The products run transposed on m16n8k16 tiles, S^T = K Q^T and O^T = V^T P^T:
+// keys (or dims) fill the 16 rows of a tile, query rows its 8 columns, so a
+// decoding step of up to 8 rows a kv head (one token, groups up to 8) wastes no
+// half of every product, of the softmax and of the registers on absent rows; 16
+// and 32 rows take 2 and 4 column tiles on the same K and V fragments.
+// (tcgen05 tiles start at 64 rows of D and take their operands from shared memory,
+// where 4-bit rows would have to be written back expanded.)
+//
+// Each warp streams its own tiles of keys through a private ring of cp.async
+// stages: no barrier inside a context, running maximum and sum in registers.
+// The warps of a CTA take turns over the blocks of one (sequence, kv head, row
+// block) item and join at its end in shared memory.  All items together form one
+// line of units, a unit being a block of keys or an item's fixed cost, cut into
+// equal pieces over the CTAs; an item cut by a piece's end leaves partial sums in
+// the workspace, and a second, dependent kernel joins them in a fixed order.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -9,86 +30,931 @@
 namespace pva {
 namespace {
 
+constexpr int kMaxCtas = 512;   // pieces the workspace has room for
+constexpr int kFixedUnits = 1;  // an item's fixed cost, in blocks of keys
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+// The running maximum moves only when a tile exceeds it by 2^8: weights stay below
+// 2^8, sums far inside fp32's range, and the accumulators are rescaled rarely.
+constexpr float kSlack = 8.f;
+
 struct AttnArgs {
-    const void* q;
-    const void *k_pages, *v_pages, *k_scales, *v_scales;
+    const __nv_bfloat16* q;
+    const uint8_t *k_pages, *v_pages;
+    const uint8_t *k_scales, *v_scales;
     void* out;
     float* lse;
+    int64_t* ws_cum;    // [num_seqs]: first unit of each sequence
+    int64_t* ws_per;    // units of a piece
+    float* ws_o;        // [2 * kMaxCtas][R][D]: sums of cut items, not normalised
+    float2* ws_ml;      // [2 * kMaxCtas][R]: their (maximum in base 2, sum)
     int64_t q_stride;
     SeqView s;
-    int32_t hq, hkv, window, out_fp32;
-    float scale;
+    int32_t hq, hkv, group, window, out_fp32;
+    float scale2;  // softmax scale * log2(e)
 };
 
-// One CTA for a query row and head; its warps take every fourth key.
-template <int D, int KIND>
-__global__ void __launch_bounds__(128) simple_kernel(const AttnArgs a) {
-    constexpr int kE = D / 32;
-    __shared__ float sm_m[4], sm_l[4], sm_o[4][D];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int32_t t = blockIdx.x, h = blockIdx.y, kvh = h / (a.hq / a.hkv);
-    int32_t b = t, n = 1, i = 0;
-    if (a.s.cu && t == 0 && h == 0)
-        for (int32_t x = threadIdx.x; x < a.s.num_seqs; x += 128)
-            if (a.s.cu[x] < 0 || a.s.cu[x + 1] < a.s.cu[x] || a.s.cu[x + 1] > a.s.num_tokens)
-                raise_status(a.s.status, kErrLength);
+// Shape of a variant: warps a CTA, keys a step, ring stages, columns of the join buffer.
+template <int D, int KIND, int NT>
+struct Shape {
+    static constexpr bool kInt4 = KIND == PVA_CACHE_INT4;
+    static constexpr int kWarps = kInt4 && NT == 1 ? 8 : 4;
+    static constexpr int kKeys = D == 128 ? 16 : 32;
+    static constexpr int kStages = kInt4 ? 4 : 3;
+    static constexpr int kCtas = 2;  // resident on an SM
+    static constexpr int R = 8 * NT;
+    static constexpr int kThreads = 32 * kWarps;
+    static constexpr int kBlock = kWarps * kKeys;  // keys of a unit
+    static constexpr int kRowBytes = kInt4 ? D / 2 : 2 * D;
+    static constexpr int kGroups = D / 64;
+    static constexpr int kScaleBytes = kInt4 ? 4 * kGroups : 0;
+    static constexpr int kStageBytes = kKeys * 2 * (kRowBytes + kScaleBytes);
+    static constexpr int kTiles = D / 16;  // 16-dim tiles of O^T
+    // 16-dim tiles that the warps' sums are joined by at a time: what is left of the
+    // shared memory beside the ring
+    static constexpr int kJoinTiles = kInt4 ? (kWarps * R >= 128 ? 2 : 4) : 4 / NT;
+    static constexpr int kJoinDims = 16 * (kJoinTiles < kTiles ? kJoinTiles : kTiles);
+    static constexpr int kJoinPitch = kJoinDims + 4;
+    static constexpr int kRing = kWarps * kStages * kStageBytes;
+    static constexpr int kMeta = kWarps * kStages * 48;
+    static constexpr int kJoin = kWarps * R * (kJoinPitch + 2) * 4;
+    static constexpr int kSmem = kRing + kMeta + kJoin;
+};
+
+__device__ __forceinline__ uint32_t smem_addr(const void* p) {
+    return (uint32_t)__cvta_generic_to_shared(p);
+}
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, int bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void ldsm(uint32_t* r, uint32_t a) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(a)
+                 : "memory");
+}
+__device__ __forceinline__ void ldsm_t(uint32_t* r, uint32_t a) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(a)
+                 : "memory");
+}
+__device__ __forceinline__ void mma(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+    return r;
+}
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&p);
+}
+__device__ __forceinline__ float ex2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float lo_f(uint32_t x) { return __uint_as_float(x << 16); }
+__device__ __forceinline__ float hi_f(uint32_t x) { return __uint_as_float(x & 0xffff0000u); }
+// The codes at bits 4p and 16 + 4p as a pair of bf16 128 + code: 0x4300 is 128, whose
+// last mantissa bit counts 1.
+__device__ __forceinline__ uint32_t codes(uint32_t w, int p) {
+    return ((w >> (4 * p)) & 0x000f000fu) | 0x43004300u;
+}
+
+// ---------------------------------------------------------------- the line of units
+struct SeqInfo {
+    int32_t row0, n;      // rows of the new tokens
+    int32_t pos0;         // position of the first of them
+    int32_t klo, khi;     // keys any of them may see
+    int32_t nrb;          // row blocks
+    int32_t blo, nb;      // first block of keys, number of blocks
+};
+
+template <int R, int BLOCK>
+__device__ __forceinline__ SeqInfo seq_info(const AttnArgs& a, int32_t b, bool tell) {
+    SeqInfo s;
+    s.row0 = b;
+    s.n = 1;
+    bool bad = false;
     if (a.s.cu) {
-        b = find_seq(a.s.cu, a.s.num_seqs, t);
-        if (b < 0) return;
-        n = a.s.cu[b + 1] - a.s.cu[b];
-        i = t - a.s.cu[b];
+        s.row0 = __ldg(a.s.cu + b);
+        const int32_t end = __ldg(a.s.cu + b + 1);
+        bad = s.row0 < 0 || end < s.row0 || end > a.s.num_tokens;
+        s.n = bad ? 0 : end - s.row0;
     }
-    if (b >= a.s.num_seqs) return;
-    const int32_t pos = (int32_t)max((int64_t)a.s.kv_lens[b] - n + i, (int64_t)-1);
-    if (threadIdx.x == 0 && a.s.kv_lens[b] < n) raise_status(a.s.status, kErrLength);
-    const int32_t first = a.window > 0 && pos >= a.window ? pos - a.window + 1 : 0;
-    const __nv_bfloat16* q = (const __nv_bfloat16*)a.q + t * a.q_stride + (int64_t)h * D;
-    auto element = [&](const void* pages, const void* scales, int64_t at, int d) {
-        if (KIND == PVA_CACHE_BF16) return __bfloat162float(((const __nv_bfloat16*)pages)[at * D + d]);
-        const uint32_t w = ((const uint32_t*)pages)[at * (D / 8) + word_of_octet<D>(d / 8)];
-        const uint32_t sc = ((const uint32_t*)scales)[at * (D / 64) + d / 64];
-        const float code = (float)(w >> (4 * (d % 8 / 2) + 16 * (d % 2)) & 15u);
-        return __uint_as_float(sc & 0xffff0000u) + code * __uint_as_float(sc << 16);
+    const int32_t kv = __ldg(a.s.kv_lens + b);
+    const int64_t room = (int64_t)a.s.max_pages << a.s.page_shift;
+    if (tell) {
+        if (bad || kv < s.n) raise_status(a.s.status, kErrLength);
+        if (s.n > 0 && kv > room) raise_status(a.s.status, kErrPage);
+    }
+    const int32_t kvp = max(kv, 0);
+    s.pos0 = kvp - s.n;
+    s.khi = (int32_t)min((int64_t)kvp, min(room, (int64_t)INT32_MAX - 2 * BLOCK));
+    s.klo = a.window > 0 ? (int32_t)max((int64_t)s.pos0 - a.window + 1, (int64_t)0) : 0;
+    s.nrb = (int32_t)(((int64_t)s.n * a.group + R - 1) / R);
+    s.blo = s.klo / BLOCK;
+    s.nb = max((s.khi + BLOCK - 1) / BLOCK - s.blo, 0);
+    return s;
+}
+__device__ __forceinline__ int64_t units_of(const AttnArgs& a, const SeqInfo& s) {
+    return (int64_t)a.hkv * s.nrb * (kFixedUnits + s.nb);
+}
+
+enum { kFirst = 1, kLast = 2, kEmpty = 4, kWhole = 8 };
+
+// What a ring stage holds, as its consumer needs it.
+struct Meta {
+    int32_t key0, flags, vlo, vhi;   // keys vlo .. vhi of the tile are there
+    int32_t row0, rows, pos0, missing;  // first token, group * n, bit x: no page for keys 16x ..
+    int32_t rb, kvh, slot, n;
+};
+
+template <int D, int KIND, int NT>
+__global__ void __launch_bounds__(Shape<D, KIND, NT>::kThreads, Shape<D, KIND, NT>::kCtas)
+    attn_kernel(const AttnArgs a) {
+    using Sh = Shape<D, KIND, NT>;
+    constexpr int R = Sh::R, W = Sh::kWarps, KS = Sh::kKeys, S = Sh::kStages, SUB = KS / 16;
+    constexpr int G = Sh::kGroups, T = Sh::kTiles, BLOCK = Sh::kBlock, ROWB = Sh::kRowBytes;
+    constexpr bool INT4 = Sh::kInt4;
+    extern __shared__ __align__(128) uint8_t smem[];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int g = lane >> 2, c = lane & 3;
+    uint8_t* ring = smem + warp * S * Sh::kStageBytes;
+    Meta* meta = reinterpret_cast<Meta*>(smem + Sh::kRing) + warp * S;
+    uint8_t* tail = smem + Sh::kRing + Sh::kMeta;
+    float* join_o = reinterpret_cast<float*>(tail);             // [W][R][kJoinPitch]
+    float* join_m = join_o + W * R * Sh::kJoinPitch;            // [W][R]
+    float* join_l = join_m + W * R;                             // [W][R]
+
+    // ---- plan: this CTA's piece [u0, u1) of the line and the sequence it starts in.
+    // Every thread sums a run of sequences; a scan over the threads gives each run's
+    // first unit.
+    int32_t b, it;       // sequence, item inside it
+    int64_t u0, u1, ub;  // ub: first unit of sequence b
+    {
+        const int32_t ns = a.s.num_seqs, per_thread = (ns + Sh::kThreads - 1) / Sh::kThreads;
+        const int32_t s0 = min((int64_t)tid * per_thread, (int64_t)ns), s1 = min(s0 + per_thread, ns);
+        int64_t sum = 0;
+        for (int32_t x = s0; x < s1; ++x)
+            sum += units_of(a, seq_info<R, BLOCK>(a, x, blockIdx.x == 0));
+        int64_t inc = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += y;
+        }
+        __shared__ int64_t wsum[W];
+        __shared__ int32_t found_b;
+        __shared__ int64_t found_u;
+        if (lane == 31) wsum[warp] = inc;
+        __syncthreads();
+        int64_t before = 0, total = 0;
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+            before += w < warp ? wsum[w] : 0;
+            total += wsum[w];
+        }
+        inc += before;
+        int64_t per = (total + gridDim.x - 1) / gridDim.x;
+        per = max(per, (int64_t)kFixedUnits + 1);
+        u0 = per * blockIdx.x;
+        u1 = min(u0 + per, total);
+        if (blockIdx.x == 0) {  // for the join
+            if (tid == 0) *a.ws_per = per;
+            int64_t u = inc - sum;
+            for (int32_t x = s0; x < s1; ++x) {
+                a.ws_cum[x] = u;
+                u += units_of(a, seq_info<R, BLOCK>(a, x, false));
+            }
+        }
+        if (u0 >= total) return;
+        if (u0 >= inc - sum && u0 < inc) {
+            int64_t u = inc - sum;
+            for (int32_t x = s0; x < s1; ++x) {
+                const int64_t len = units_of(a, seq_info<R, BLOCK>(a, x, false));
+                if (u0 < u + len) {
+                    found_b = x;
+                    found_u = u;
+                    break;
+                }
+                u += len;
+            }
+        }
+        __syncthreads();
+        b = found_b;
+        ub = found_u;
+    }
+
+    // ---- cursor over this warp's steps
+    SeqInfo sq = seq_info<R, BLOCK>(a, b, false);
+    int32_t len = kFixedUnits + sq.nb;
+    it = (int32_t)((u0 - ub) / len);
+    int32_t rb = it / a.hkv, kvh = it - rb * a.hkv;
+    int64_t ui = ub + (int64_t)it * len;  // first unit of the item
+    int32_t t = 0, tend = 0;              // blocks left of the item for this warp (absolute)
+    int32_t rlo, rhi;                     // keys that the row block may see
+    int32_t slot = 0, next_key = 0, next_flags = 0;
+    int32_t page[SUB];
+    bool more = true;   // a step is pending
+    bool fresh = true;  // the cursor stands before its first item
+
+    // The item at the cursor: false where this piece has no block of it.
+    auto open_item = [&]() -> bool {
+        const int32_t i0 = (int32_t)((int64_t)rb * R / a.group);
+        const int32_t i1 = (int32_t)min(((int64_t)rb * R + R - 1) / a.group, (int64_t)sq.n - 1);
+        rlo = a.window > 0 ? (int32_t)max((int64_t)sq.pos0 + i0 - a.window + 1, (int64_t)0) : 0;
+        rhi = min(sq.pos0 + i1 + 1, sq.khi);
+        if (sq.nb == 0) {
+            t = tend = 0;
+            next_flags = kFirst | kLast | kEmpty | kWhole;
+            return u0 <= ui;
+        }
+        const int64_t first = ui + kFixedUnits, last = ui + len;
+        const int32_t t0 = (int32_t)max(u0 - first, (int64_t)0);
+        const int32_t t1 = (int32_t)(min(u1, last) - first);
+        if (t1 <= t0) return false;
+        next_flags = kFirst | (t0 == 0 && t1 == sq.nb ? kWhole : 0);
+        slot = 2 * blockIdx.x + (t0 == 0 ? 1 : 0);
+        // of blocks blo + t0 .. blo + t1, those whose keys of this warp the rows may see
+        const int32_t off = warp * KS;
+        t = max(sq.blo + t0, rlo - off - KS + 1 <= 0 ? 0 : (rlo - off - KS + BLOCK) / BLOCK);
+        tend = min(sq.blo + t1, rhi <= off ? 0 : (rhi - off + BLOCK - 1) / BLOCK);
+        if (t >= tend) next_flags |= kLast | kEmpty;
+        return true;
     };
-    float m = -INFINITY, l = 0.f, o[kE] = {};
-    for (int32_t j = first + warp; j <= pos; j += 4) {
-        const int64_t page = page_of(a.s, b, j);
-        if (page < 0) {
-            if (lane == 0) raise_status(a.s.status, kErrPage);
-            continue;
+    auto next = [&]() {
+        if (t < tend) {
+            next_flags &= ~kFirst;
+        } else {
+            for (;;) {
+                if (!fresh) {
+                    ui += len;
+                    if (++kvh == a.hkv) {
+                        kvh = 0;
+                        if (++rb == sq.nrb) {
+                            rb = 0;
+                            do {
+                                if (++b >= a.s.num_seqs) {
+                                    more = false;
+                                    return;
+                                }
+                                sq = seq_info<R, BLOCK>(a, b, false);
+                            } while (sq.nrb == 0);
+                            len = kFixedUnits + sq.nb;
+                        }
+                    }
+                }
+                fresh = false;
+                if (ui >= u1) {
+                    more = false;
+                    return;
+                }
+                if (open_item()) break;
+            }
         }
-        const int64_t at = ((page * a.hkv + kvh) << a.s.page_shift) + (j & ((1 << a.s.page_shift) - 1));
-        float s = 0.f;
-        for (int e = 0; e < kE; ++e)
-            s += __bfloat162float(q[e * 32 + lane]) * element(a.k_pages, a.k_scales, at, e * 32 + lane);
-        for (int x = 16; x; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-        s *= a.scale;
-        const float mn = fmaxf(m, s);
-        const float old = m == -INFINITY ? 0.f : expf(m - mn), p = s == -INFINITY ? 0.f : expf(s - mn);
-        l = l * old + p;
-        for (int e = 0; e < kE; ++e)
-            o[e] = o[e] * old + p * element(a.v_pages, a.v_scales, at, e * 32 + lane);
-        m = mn;
-    }
-    sm_m[warp] = m;
-    sm_l[warp] = l;
-    for (int e = 0; e < kE; ++e) sm_o[warp][e * 32 + lane] = o[e];
-    __syncthreads();
-    if (threadIdx.x < D) {
-        float mx = -INFINITY, lt = 0.f, ot = 0.f;
-        for (int w = 0; w < 4; ++w) mx = fmaxf(mx, sm_m[w]);
-        for (int w = 0; w < 4; ++w) {
-            const float f = sm_m[w] == -INFINITY ? 0.f : expf(sm_m[w] - mx);
-            lt += f * sm_l[w];
-            ot += f * sm_o[w][threadIdx.x];
+        if (!(next_flags & kEmpty)) {
+            next_key = t * BLOCK + warp * KS;
+            if (++t >= tend) next_flags |= kLast;
+#pragma unroll
+            for (int x = 0; x < SUB; ++x) {
+                const int32_t i = (next_key + 16 * x) >> a.s.page_shift;
+                page[x] = i < a.s.max_pages
+                              ? __ldg(a.s.page_table + b * a.s.table_stride + i)
+                              : -1;
+            }
         }
-        const float r = lt > 0.f ? ot / lt : 0.f;
-        const int64_t at = ((int64_t)t * a.hq + h) * D + threadIdx.x;
-        if (a.out_fp32) ((float*)a.out)[at] = r;
-        else ((__nv_bfloat16*)a.out)[at] = __float2bfloat16_rn(r);
-        if (threadIdx.x == 0)
-            a.lse[(int64_t)h * a.s.num_tokens + t] = lt > 0.f ? mx + logf(lt) : -INFINITY;
+    };
+    // Copies of the pending step into a stage, and the next step.
+    auto issue = [&](int stage) {
+        uint8_t* dst = ring + stage * Sh::kStageBytes;
+        const uint32_t kd = smem_addr(dst);
+        int32_t missing = 0;
+        if (!(next_flags & kEmpty)) {
+            const int32_t vlo = max(next_key, rlo), vhi = min(next_key + KS, rhi);
+#pragma unroll
+            for (int x = 0; x < SUB; ++x) {
+                const int32_t key = next_key + 16 * x;
+                const bool there = page[x] >= 0 && page[x] < a.s.num_pages;
+                if (!there) {
+                    missing |= 1 << x;
+                    if (lane == 0 && key < vhi && key + 16 > vlo) raise_status(a.s.status, kErrPage);
+                }
+                const int64_t row =
+                    there ? (((int64_t)page[x] * a.hkv + kvh) << a.s.page_shift) +
+                                (key & ((1 << a.s.page_shift) - 1))
+                          : 0;
+                if (!INT4) {
+                    // rows outside the valid keys are filled with zeros: a weight of 0 must not
+                    // meet a NaN
+                    constexpr int CPR = ROWB / 16, PER = 16 * CPR / 32;
+#pragma unroll
+                    for (int i = 0; i < PER; ++i) {
+                        const int r = (i * 32 + lane) / CPR, ch = (i * 32 + lane) % CPR;
+                        const bool ok = there && key + r >= vlo && key + r < vhi;
+                        const int64_t off = ok ? (row + r) * ROWB + ch * 16 : 0;
+                        const uint32_t to = (16 * x + r) * ROWB + ((ch ^ (r & 7)) << 4);
+                        cp16(kd + to, a.k_pages + off, ok ? 16 : 0);
+                        cp16(kd + KS * ROWB + to, a.v_pages + off, ok ? 16 : 0);
+                    }
+                } else if (there) {
+                    constexpr int CPR = ROWB / 16, PER = 16 * CPR / 32;
+#pragma unroll
+                    for (int i = 0; i < PER; ++i) {
+                        const int idx = i * 32 + lane;
+                        // V: 16-byte chunks of a 128-byte line change places with the line's
+                        // number, so that the rows a warp reads at once lie in other banks
+                        const int line = idx >> 3, sw = (idx & 7) ^ (D == 128 ? 2 * (line & 3) : 2 * (line & 1));
+                        cp16(kd + x * 16 * ROWB + idx * 16, a.k_pages + row * ROWB + idx * 16, 16);
+                        cp16(kd + (KS + 16 * x) * ROWB + (line * 8 + sw) * 16,
+                             a.v_pages + row * ROWB + idx * 16, 16);
+                    }
+                    constexpr int SC = 16 * Sh::kScaleBytes / 16;  // chunks of 16 keys' scales
+                    if (lane < 2 * SC) {
+                        const int v = lane >= SC, i = lane - v * SC;
+                        cp16(kd + 2 * KS * ROWB + (v * KS + 16 * x) * Sh::kScaleBytes + i * 16,
+                             (v ? a.v_scales : a.k_scales) + row * Sh::kScaleBytes + i * 16, 16);
+                    }
+                }
+            }
+            if (lane == 0) {
+                Meta& m = meta[stage];
+                *reinterpret_cast<int4*>(&m.key0) = make_int4(next_key, next_flags, vlo, vhi);
+                *reinterpret_cast<int4*>(&m.row0) = make_int4(sq.row0, sq.n * a.group, sq.pos0, missing);
+                *reinterpret_cast<int4*>(&m.rb) = make_int4(rb, kvh, slot, sq.n);
+            }
+        } else if (lane == 0) {
+            Meta& m = meta[stage];
+            *reinterpret_cast<int4*>(&m.key0) = make_int4(0, next_flags, 0, 0);
+            *reinterpret_cast<int4*>(&m.row0) = make_int4(sq.row0, sq.n * a.group, sq.pos0, 0);
+            *reinterpret_cast<int4*>(&m.rb) = make_int4(rb, kvh, slot, sq.n);
+        }
+        next();
+    };
+
+    next();
+    int issued = 0;
+#pragma unroll
+    for (int i = 0; i < S - 1; ++i) {
+        if (more) {
+            issue(i);
+            ++issued;
+        }
+        cp_commit();
     }
+
+    // ---- state of the item in hand
+    float o[NT][T][4], m_run[NT][2], l_run[NT][2];
+    float vs[INT4 ? G : 1][NT][4];     // 4 bits: sums of the scaled weights
+    float zs[INT4 ? G : 1][NT][2];     // 4 bits: sums of weight * low
+    float qs[INT4 ? G : 1][NT][2];     // 4 bits: sums of the query's dims of a group
+    uint32_t qf[NT][D / 16][2];
+    int32_t pos[NT][2];
+    int32_t full_lo = 0, full_hi = 0;  // keys that every row sees
+
+    for (int step = 0, stage = 0; step < issued; ++step, stage = stage + 1 == S ? 0 : stage + 1) {
+        cp_wait<S - 2>();
+        __syncwarp();  // every lane's copies are in, and the stage before this one is read
+        if (more) {
+            issue(stage == 0 ? S - 1 : stage - 1);
+            ++issued;
+        }
+        cp_commit();
+        const uint8_t* buf = ring + stage * Sh::kStageBytes;
+        const Meta& mt = meta[stage];
+        const int32_t flags = mt.flags;
+        if (flags & kFirst) {
+            const int32_t row0 = mt.row0, rows = mt.rows, pos0 = mt.pos0, r0 = mt.rb * R;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+                for (int i = 0; i < T; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[nt][i][e] = 0.f;
+                m_run[nt][0] = m_run[nt][1] = -INFINITY;
+                l_run[nt][0] = l_run[nt][1] = 0.f;
+                const int32_t r = r0 + 8 * nt + g;
+                const int32_t tok = r / a.group;
+                const __nv_bfloat16* q = a.q + (int64_t)(row0 + tok) * a.q_stride +
+                                         (int64_t)(mt.kvh * a.group + r - tok * a.group) * D;
+                const bool live = r < rows;
+                if (!INT4) {
+#pragma unroll
+                    for (int ks = 0; ks < D / 16; ++ks)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+                            qf[nt][ks][e] =
+                                live ? __ldg(reinterpret_cast<const uint32_t*>(q + 16 * ks + 8 * e + 2 * c)) : 0u;
+                } else {
+                    // the dims in the order in which the codes of a row come out of their words
+#pragma unroll
+                    for (int gr = 0; gr < G; ++gr) {
+                        float sum = 0.f;
+#pragma unroll
+                        for (int oc = 0; oc < 2; ++oc) {
+                            const uint4 x = live ? __ldg(reinterpret_cast<const uint4*>(q + 64 * gr + 16 * c + 8 * oc))
+                                                 : make_uint4(0, 0, 0, 0);
+                            qf[nt][4 * gr + 2 * oc][0] = x.x;
+                            qf[nt][4 * gr + 2 * oc][1] = x.y;
+                            qf[nt][4 * gr + 2 * oc + 1][0] = x.z;
+                            qf[nt][4 * gr + 2 * oc + 1][1] = x.w;
+                            sum += ((lo_f(x.x) + hi_f(x.x)) + (lo_f(x.y) + hi_f(x.y))) +
+                                   ((lo_f(x.z) + hi_f(x.z)) + (lo_f(x.w) + hi_f(x.w)));
+                        }
+                        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+                        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+                        qs[gr][nt][0] = __shfl_sync(0xffffffffu, sum, 8 * c);
+                        qs[gr][nt][1] = __shfl_sync(0xffffffffu, sum, 8 * c + 4);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) vs[gr][nt][e] = 0.f;
+                        zs[gr][nt][0] = zs[gr][nt][1] = 0.f;
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    pos[nt][e] = pos0 + min(r0 + 8 * nt + 2 * c + e, rows - 1) / a.group;
+            }
+            full_hi = pos0 + r0 / a.group;
+            full_lo = a.window > 0
+                          ? (int32_t)max((int64_t)pos0 + min(r0 + R - 1, rows - 1) / a.group - a.window + 1,
+                                         (int64_t)0)
+                          : 0;
+        }
+        if (!(flags & kEmpty)) {
+            const int32_t key0 = mt.key0, vlo = mt.vlo, vhi = mt.vhi, missing = mt.missing;
+            const bool partial = key0 < max(full_lo, vlo) || key0 + KS > min(full_hi + 1, vhi) || missing;
+            const uint32_t kb = smem_addr(buf), vb = kb + KS * ROWB;
+            float s[SUB][NT][4];
+            // ---- S^T
+#pragma unroll
+            for (int x = 0; x < SUB; ++x) {
+                if (!INT4) {
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) s[x][nt][e] = 0.f;
+#pragma unroll
+                    for (int ks = 0; ks < D / 16; ++ks) {
+                        uint32_t f[4];
+                        const int r = lane & 15, ch = 2 * ks + (lane >> 4);
+                        ldsm(f, kb + (16 * x + r) * ROWB + ((ch ^ (r & 7)) << 4));
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) mma(s[x][nt], f, qf[nt][ks][0], qf[nt][ks][1]);
+                    }
+                } else {
+                    uint32_t w[2][2 * G], sc[2][G];
+                    const uint8_t* kr = buf + (16 * x + g) * ROWB + c * (ROWB / 4);
+                    const uint8_t* sr = buf + 2 * KS * ROWB + (16 * x + g) * Sh::kScaleBytes;
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        if (D == 128) {
+                            const uint4 v = *reinterpret_cast<const uint4*>(kr + 8 * y * ROWB);
+                            w[y][0] = v.x;
+                            w[y][1] = v.y;
+                            w[y][2 * G - 2] = v.z;
+                            w[y][2 * G - 1] = v.w;
+                            const uint2 z = *reinterpret_cast<const uint2*>(sr + 8 * y * Sh::kScaleBytes);
+                            sc[y][0] = z.x;
+                            sc[y][G - 1] = z.y;
+                        } else {
+                            const uint2 v = *reinterpret_cast<const uint2*>(kr + 8 * y * ROWB);
+                            w[y][0] = v.x;
+                            w[y][1] = v.y;
+                            sc[y][0] = *reinterpret_cast<const uint32_t*>(sr + 8 * y * Sh::kScaleBytes);
+                        }
+                    }
+                    float acc[G][NT][4];
+#pragma unroll
+                    for (int gr = 0; gr < G; ++gr) {
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) acc[gr][nt][e] = 0.f;
+#pragma unroll
+                        for (int oc = 0; oc < 2; ++oc)
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                const uint32_t w0 = w[0][G * oc + gr], w1 = w[1][G * oc + gr];
+                                const uint32_t f[4] = {codes(w0, 2 * h), codes(w1, 2 * h),
+                                                       codes(w0, 2 * h + 1), codes(w1, 2 * h + 1)};
+#pragma unroll
+                                for (int nt = 0; nt < NT; ++nt)
+                                    mma(acc[gr][nt], f, qf[nt][4 * gr + 2 * oc + h][0],
+                                        qf[nt][4 * gr + 2 * oc + h][1]);
+                            }
+                    }
+                    // s = sum over groups of scale * (q . codes) + low * (sum of q); the products hold
+                    // q . (128 + code)
+#pragma unroll
+                    for (int y = 0; y < 2; ++y)
+#pragma unroll
+                        for (int gr = 0; gr < G; ++gr) {
+                            const float scl = lo_f(sc[y][gr]);
+                            const float off = fmaf(-128.f, scl, hi_f(sc[y][gr]));
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                                for (int e = 0; e < 2; ++e) {
+                                    const float before = gr == 0 ? 0.f : s[x][nt][2 * y + e];
+                                    s[x][nt][2 * y + e] = fmaf(
+                                        scl, acc[gr][nt][2 * y + e], fmaf(off, qs[gr][nt][e], before));
+                                }
+                        }
+                }
+            }
+            // ---- base 2, masks, maximum over the tile
+            float mx[NT][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mx[nt][0] = mx[nt][1] = -INFINITY;
+#pragma unroll
+            for (int x = 0; x < SUB; ++x)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        float v = s[x][nt][e] * a.scale2;
+                        if (partial) {
+                            const int32_t j = key0 + 16 * x + g + 8 * (e >> 1), p = pos[nt][e & 1];
+                            const bool ok = j >= vlo && j < vhi && j <= p && !(missing >> x & 1) &&
+                                            (a.window <= 0 || p - j < a.window);
+                            v = ok ? v : -INFINITY;
+                        }
+                        s[x][nt][e] = v;
+                        mx[nt][e & 1] = fmaxf(mx[nt][e & 1], v);
+                    }
+            bool up = false;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                    for (int d = 4; d < 32; d <<= 1)
+                        mx[nt][e] = fmaxf(mx[nt][e], __shfl_xor_sync(0xffffffffu, mx[nt][e], d));
+                    up |= mx[nt][e] > m_run[nt][e] + kSlack;
+                }
+            if (__any_sync(0xffffffffu, up)) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float mn = fmaxf(m_run[nt][e], mx[nt][e]);
+                        const float f = m_run[nt][e] == -INFINITY ? 0.f : ex2(m_run[nt][e] - mn);
+                        m_run[nt][e] = mn;
+                        l_run[nt][e] *= f;
+#pragma unroll
+                        for (int i = 0; i < T; ++i) {
+                            o[nt][i][e] *= f;
+                            o[nt][i][2 + e] *= f;
+                        }
+                        if (INT4) {
+#pragma unroll
+                            for (int gr = 0; gr < G; ++gr) {
+                                vs[gr][nt][e] *= f;
+                                zs[gr][nt][e] *= f;
+                            }
+                        }
+                    }
+            }
+            // ---- weights and O^T
+#pragma unroll
+            for (int x = 0; x < SUB; ++x) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float base = m_run[nt][e & 1] == -INFINITY ? 0.f : m_run[nt][e & 1];
+                        s[x][nt][e] = ex2(s[x][nt][e] - base);
+                        l_run[nt][e & 1] += s[x][nt][e];
+                    }
+                if (!INT4) {
+                    // the weights meet bf16 values in a bf16 product: one rounding of 2^-9
+                    uint32_t p[NT][2];
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        p[nt][0] = transpose8(pack2(s[x][nt][0], s[x][nt][1]));
+                        p[nt][1] = transpose8(pack2(s[x][nt][2], s[x][nt][3]));
+                    }
+#pragma unroll
+                    for (int i = 0; i < T; ++i) {
+                        uint32_t f[4];
+                        const int r = (lane & 7) + ((lane >> 4) << 3), ch = 2 * i + ((lane >> 3) & 1);
+                        ldsm_t(f, vb + (16 * x + r) * ROWB + ((ch ^ (r & 7)) << 4));
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) mma(o[nt][i], f, p[nt][0], p[nt][1]);
+                    }
+                } else {
+                    // weight * scale meets the codes, rounded to bf16 once; weight * low stays in fp32
+                    uint32_t sc[2][G], p[G][NT][2];
+                    const uint8_t* sr =
+                        buf + 2 * KS * ROWB + (KS + 16 * x + g) * Sh::kScaleBytes;
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        if (D == 128) {
+                            const uint2 z = *reinterpret_cast<const uint2*>(sr + 8 * y * Sh::kScaleBytes);
+                            sc[y][0] = z.x;
+                            sc[y][G - 1] = z.y;
+                        } else {
+                            sc[y][0] = *reinterpret_cast<const uint32_t*>(sr + 8 * y * Sh::kScaleBytes);
+                        }
+                        if (partial) {  // a slot of no token may hold anything: its weight is 0
+                            const int32_t j = key0 + 16 * x + g + 8 * y;
+                            if (j < vlo || j >= vhi || (missing >> x & 1)) {
+#pragma unroll
+                                for (int gr = 0; gr < G; ++gr) sc[y][gr] = 0;
+                            }
+                        }
+                    }
+#pragma unroll
+                    for (int gr = 0; gr < G; ++gr)
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+                            for (int y = 0; y < 2; ++y) {
+                                const float scl = lo_f(sc[y][gr]), low = hi_f(sc[y][gr]);
+                                p[gr][nt][y] = transpose8(
+                                    pack2(s[x][nt][2 * y] * scl, s[x][nt][2 * y + 1] * scl));
+                                zs[gr][nt][0] = fmaf(s[x][nt][2 * y], low, zs[gr][nt][0]);
+                                zs[gr][nt][1] = fmaf(s[x][nt][2 * y + 1], low, zs[gr][nt][1]);
+                            }
+                            const uint32_t ones[4] = {0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u};
+                            mma(vs[gr][nt], ones, p[gr][nt][0], p[gr][nt][1]);
+                        }
+                    uint32_t w[4][G];  // keys 2c, 2c + 1, 2c + 8, 2c + 9
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                        const int r = 16 * x + 2 * c + (y & 1) + 8 * (y >> 1);
+                        if (D == 128) {
+                            const int line = r >> 1, at = ((r & 1) * 4 + (g >> 1)) ^ (2 * (line & 3));
+                            const uint2 z = *reinterpret_cast<const uint2*>(
+                                buf + KS * ROWB + line * 128 + at * 16 + (g & 1) * 8);
+                            w[y][0] = z.x;
+                            w[y][G - 1] = z.y;
+                        } else {
+                            const int line = r >> 2, at = ((r & 3) * 2 + (g >> 2)) ^ (2 * (line & 1));
+                            w[y][0] = *reinterpret_cast<const uint32_t*>(
+                                buf + KS * ROWB + line * 128 + at * 16 + (g & 3) * 4);
+                        }
+                    }
+#pragma unroll
+                    for (int gr = 0; gr < G; ++gr) {
+                        const uint32_t a0 = __byte_perm(w[0][gr], w[1][gr], 0x5410);
+                        const uint32_t a1 = __byte_perm(w[0][gr], w[1][gr], 0x7632);
+                        const uint32_t a2 = __byte_perm(w[2][gr], w[3][gr], 0x5410);
+                        const uint32_t a3 = __byte_perm(w[2][gr], w[3][gr], 0x7632);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const uint32_t f[4] = {codes(a0, i), codes(a1, i), codes(a2, i), codes(a3, i)};
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+                                mma(o[nt][4 * gr + i], f, p[gr][nt][0], p[gr][nt][1]);
+                        }
+                    }
+                }
+            }
+        }
+        // ---- the item's end: the warps' sums are joined
+        if (flags & kLast) {
+            const int32_t r0 = mt.rb * R;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                    for (int d = 4; d < 32; d <<= 1) {
+                        l_run[nt][e] += __shfl_xor_sync(0xffffffffu, l_run[nt][e], d);
+                        if (INT4) {
+#pragma unroll
+                            for (int gr = 0; gr < G; ++gr)
+                                zs[gr][nt][e] += __shfl_xor_sync(0xffffffffu, zs[gr][nt][e], d);
+                        }
+                    }
+                    if (INT4) {
+#pragma unroll
+                        for (int i = 0; i < T; ++i) {
+                            const float add = fmaf(-128.f, vs[INT4 ? i / 4 : 0][nt][e], zs[INT4 ? i / 4 : 0][nt][e]);
+                            o[nt][i][e] += add;
+                            o[nt][i][2 + e] += add;
+                        }
+                    }
+                }
+            constexpr int JT = Sh::kJoinDims / 16, JD = Sh::kJoinDims, JP = Sh::kJoinPitch;
+#pragma unroll
+            for (int t0 = 0; t0 < T; t0 += JT) {
+                __syncthreads();  // the buffer's last readers are done
+                if (t0 == 0 && g == 0) {
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            join_m[warp * R + 8 * nt + 2 * c + e] = m_run[nt][e];
+                            join_l[warp * R + 8 * nt + 2 * c + e] = l_run[nt][e];
+                        }
+                }
+#pragma unroll
+                for (int i = 0; i < JT; ++i)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            // tile i holds dims 16i + g, 16i + g + 8, or with 4 bits dims
+                            // 8g + 2i, 8g + 2i + 1 of its group
+                            const int at = INT4 ? g * 2 * (JT < 4 ? JT : 4) + 2 * (i % 4) + (e >> 1) + (i / 4) * 64
+                                                : 16 * i + g + 8 * (e >> 1);
+                            join_o[(warp * R + 8 * nt + 2 * c + (e & 1)) * JP + at] = o[nt][t0 + i][e];
+                        }
+                __syncthreads();
+                for (int idx = tid; idx < R * (JD / 4); idx += Sh::kThreads) {
+                    const int r = idx / (JD / 4), d4 = idx % (JD / 4) * 4;
+                    if (r0 + r >= mt.rows) continue;
+                    float mm = -INFINITY;
+#pragma unroll
+                    for (int w = 0; w < W; ++w) mm = fmaxf(mm, join_m[w * R + r]);
+                    float l = 0.f;
+                    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                    for (int w = 0; w < W; ++w) {
+                        const float mw = join_m[w * R + r];
+                        const float f = mw == -INFINITY ? 0.f : ex2(mw - mm);
+                        const float4 v = *reinterpret_cast<const float4*>(join_o + (w * R + r) * JP + d4);
+                        l = fmaf(f, join_l[w * R + r], l);
+                        sum.x = fmaf(f, v.x, sum.x);
+                        sum.y = fmaf(f, v.y, sum.y);
+                        sum.z = fmaf(f, v.z, sum.z);
+                        sum.w = fmaf(f, v.w, sum.w);
+                    }
+                    // first of the four dims
+                    int dim;
+                    if (!INT4 || JT >= 4) dim = 16 * t0 + d4;
+                    else dim = 64 * (t0 / 4) + 8 * (d4 / (2 * JT)) + 2 * (t0 % 4) + d4 % (2 * JT);
+                    if (mt.flags & kWhole) {
+                        const int32_t tok = (r0 + r) / a.group;
+                        const int32_t h = mt.kvh * a.group + (r0 + r) - tok * a.group;
+                        const int64_t at = ((int64_t)(mt.row0 + tok) * a.hq + h) * D + dim;
+                        const float inv = l != 0.f ? 1.f / l : 0.f;
+                        if (l == 0.f) sum = make_float4(0.f, 0.f, 0.f, 0.f);
+                        if (a.out_fp32) {
+                            *reinterpret_cast<float4*>((float*)a.out + at) =
+                                make_float4(sum.x * inv, sum.y * inv, sum.z * inv, sum.w * inv);
+                        } else {
+                            *reinterpret_cast<uint2*>((__nv_bfloat16*)a.out + at) =
+                                make_uint2(pack2(sum.x * inv, sum.y * inv), pack2(sum.z * inv, sum.w * inv));
+                        }
+                        if (t0 == 0 && d4 == 0)
+                            a.lse[(int64_t)h * a.s.num_tokens + mt.row0 + tok] =
+                                l != 0.f ? fmaf(mm, kLn2, logf(l)) : -INFINITY;
+                    } else {
+                        const int64_t at = (int64_t)mt.slot * R + r;
+                        *reinterpret_cast<float4*>(a.ws_o + at * D + dim) = sum;
+                        if (t0 == 0 && d4 == 0) a.ws_ml[at] = make_float2(mm, l);
+                    }
+                }
+            }
+        }
+    }
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// Joins the partial sums of every item that was cut, in the order of the pieces.
+// One warp a row where there are many rows, a CTA's four warps where there are few.
+template <int D, int KIND, int NT, bool WIDE>
+__global__ void __launch_bounds__(128) join_kernel(const AttnArgs a) {
+    using Sh = Shape<D, KIND, NT>;
+    constexpr int R = Sh::R, E = D / 32, WS = WIDE ? 4 : 1;
+    __shared__ float sm_o[WIDE ? 4 : 1][D], sm_m[4], sm_l[4];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int64_t row = WIDE ? blockIdx.x : (int64_t)blockIdx.x * 4 + warp;
+    const int32_t t = (int32_t)(row / a.hq), h = (int32_t)(row - (int64_t)t * a.hq);
+    if (t >= a.s.num_tokens) return;
+    int32_t b = t;
+    if (a.s.cu) b = find_seq(a.s.cu, a.s.num_seqs, t);
+    if (b < 0 || b >= a.s.num_seqs) return;
+    const SeqInfo s = seq_info<R, Sh::kBlock>(a, b, false);
+    if (s.nb == 0 || t - s.row0 >= s.n) return;
+    const int32_t kvh = h / a.group;
+    const int64_t rr = (int64_t)(t - s.row0) * a.group + h - kvh * a.group;
+    const int32_t rb = (int32_t)(rr / R), r = (int32_t)(rr - (int64_t)rb * R);
+    const int64_t per = *a.ws_per, first = a.ws_cum[b] + ((int64_t)rb * a.hkv + kvh) * (kFixedUnits + s.nb);
+    const int32_t cf = (int32_t)((first + kFixedUnits) / per);
+    const int32_t cl = (int32_t)((first + kFixedUnits + s.nb - 1) / per);
+    if (cf == cl) return;  // one piece holds it all
+    const int32_t n = cl - cf + 1;
+    auto at = [&](int k) { return (int64_t)(k == 0 ? 2 * cf + 1 : 2 * (cf + k)) * R + r; };
+    float mm = -INFINITY;
+    for (int k = lane; k < n; k += 32) mm = fmaxf(mm, a.ws_ml[at(k)].x);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
+    float l = 0.f, acc[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = 0.f;
+#pragma unroll 4
+    for (int k = WIDE ? warp : 0; k < n; k += WS) {
+        const float2 ml = a.ws_ml[at(k)];
+        const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - mm);
+        const float* src = a.ws_o + at(k) * D + lane * E;
+        l = fmaf(f, ml.y, l);
+        if (E == 4) {
+            const float4 v = *reinterpret_cast<const float4*>(src);
+            acc[0] = fmaf(f, v.x, acc[0]);
+            acc[1] = fmaf(f, v.y, acc[1]);
+            acc[E - 2] = fmaf(f, v.z, acc[E - 2]);
+            acc[E - 1] = fmaf(f, v.w, acc[E - 1]);
+        } else {
+            const float2 v = *reinterpret_cast<const float2*>(src);
+            acc[0] = fmaf(f, v.x, acc[0]);
+            acc[1] = fmaf(f, v.y, acc[1]);
+        }
+    }
+    if (WIDE) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) sm_o[WIDE ? warp : 0][lane * E + e] = acc[e];
+        if (lane == 0) sm_l[warp] = l;
+        __syncthreads();
+        if (warp > 0) return;
+        l = 0.f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = 0.f;
+#pragma unroll
+        for (int w = 0; w < WS; ++w) {
+            l += sm_l[w];
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[e] += sm_o[WIDE ? w : 0][lane * E + e];
+        }
+    }
+    (void)sm_m;
+    const float inv = l != 0.f ? 1.f / l : 0.f;
+    const int64_t to = ((int64_t)t * a.hq + h) * D + lane * E;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = l != 0.f ? acc[e] * inv : 0.f;
+    if (a.out_fp32) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) ((float*)a.out)[to + e] = acc[e];
+    } else {
+#pragma unroll
+        for (int e = 0; e < E; e += 2)
+            *reinterpret_cast<uint32_t*>((__nv_bfloat16*)a.out + to + e) = pack2(acc[e], acc[e + 1]);
+    }
+    if (lane == 0) a.lse[(int64_t)h * a.s.num_tokens + t] = l != 0.f ? fmaf(mm, kLn2, logf(l)) : -INFINITY;
+}
+
+// Column tiles for `rows` query rows a kv head (group * new tokens of a sequence).
+int tiles_of(int64_t rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : 4; }
+
+size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
+
+template <int D, int KIND, int NT>
+pva_status launch(AttnArgs a, uint8_t* ws, cudaStream_t st) {
+    using Sh = Shape<D, KIND, NT>;
+    static_assert(Sh::kSmem <= 113 * 1024, "two CTAs share an SM");
+    a.ws_per = reinterpret_cast<int64_t*>(ws);
+    a.ws_cum = reinterpret_cast<int64_t*>(ws + 256);
+    ws += 256 + up256((size_t)a.s.num_seqs * 8);
+    a.ws_ml = reinterpret_cast<float2*>(ws);
+    a.ws_o = reinterpret_cast<float*>(ws + (size_t)2 * kMaxCtas * Sh::R * 8);
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        return PVA_ERR_CUDA;
+    const int ctas = sms * Sh::kCtas < kMaxCtas ? sms * Sh::kCtas : kMaxCtas;
+    if (cudaFuncSetAttribute(attn_kernel<D, KIND, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             Sh::kSmem) != cudaSuccess)
+        return PVA_ERR_CUDA;
+    attn_kernel<D, KIND, NT><<<ctas, Sh::kThreads, Sh::kSmem, st>>>(a);
+    if (cudaGetLastError() != cudaSuccess) return PVA_ERR_CUDA;
+    const int64_t rows = (int64_t)a.s.num_tokens * a.hq;
+    const bool wide = rows <= 2048;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(wide ? rows : (rows + 3) / 4));
+    cfg.blockDim = dim3(128);
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    const cudaError_t e = wide ? cudaLaunchKernelEx(&cfg, join_kernel<D, KIND, NT, true>, a)
+                               : cudaLaunchKernelEx(&cfg, join_kernel<D, KIND, NT, false>, a);
+    return e == cudaSuccess ? PVA_OK : PVA_ERR_CUDA;
+}
+
+template <int D, int KIND>
+pva_status launch_tiles(int nt, const AttnArgs& a, uint8_t* ws, cudaStream_t st) {
+    return nt == 1 ? launch<D, KIND, 1>(a, ws, st)
+           : nt == 2 ? launch<D, KIND, 2>(a, ws, st)
+                     : launch<D, KIND, 4>(a, ws, st);
 }
 
 }  // namespace
@@ -101,7 +967,9 @@ extern "C" size_t pva_cache_attn_bytes(int32_t num_seqs, int32_t num_q_heads, in
     if (num_seqs < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || num_q_heads % num_kv_heads != 0 ||
         (head_dim != 64 && head_dim != 128) || max_new < 1)
         return 0;
-    return 256;
+    const int64_t rows = (int64_t)(num_q_heads / num_kv_heads) * max_new;
+    const size_t r = 8 * (size_t)tiles_of(rows);
+    return 256 + up256((size_t)num_seqs * 8) + (size_t)2 * kMaxCtas * r * (8 + 4 * (size_t)head_dim);
 }
 
 extern "C" pva_status pva_cache_attn(const pva_cache_desc* cache, const pva_cache_batch* batch,
@@ -126,27 +994,28 @@ extern "C" pva_status pva_cache_attn(const pva_cache_desc* cache, const pva_cach
     if (workspace_bytes < pva_cache_attn_bytes(batch->num_seqs, num_q_heads, cache->num_kv_heads, d,
                                                max_new))
         return PVA_ERR_BUFFER_TOO_SMALL;
-    a.q = q;
-    a.k_pages = cache->k_pages;
-    a.v_pages = cache->v_pages;
-    a.k_scales = cache->k_scales;
-    a.v_scales = cache->v_scales;
+    if (batch->num_tokens > INT32_MAX / num_q_heads) return PVA_ERR_UNSUPPORTED;
+    a.q = reinterpret_cast<const __nv_bfloat16*>(q);
+    a.k_pages = reinterpret_cast<const uint8_t*>(cache->k_pages);
+    a.v_pages = reinterpret_cast<const uint8_t*>(cache->v_pages);
+    a.k_scales = reinterpret_cast<const uint8_t*>(cache->k_scales);
+    a.v_scales = reinterpret_cast<const uint8_t*>(cache->v_scales);
     a.out = out;
     a.lse = lse;
     a.s = seq_view(cache, batch);
     a.hq = num_q_heads;
     a.hkv = cache->num_kv_heads;
+    a.group = num_q_heads / cache->num_kv_heads;
     a.window = window;
     a.out_fp32 = out_is_fp32;
-    a.scale = softmax_scale > 0.f ? softmax_scale : rsqrtf((float)d);
+    a.scale2 = (softmax_scale > 0.f ? softmax_scale : 1.f / sqrtf((float)d)) * kLog2e;
+    // Without offsets every sequence has one row, whatever bound was given.
+    const int nt = tiles_of((int64_t)a.group * max_new);
+    uint8_t* ws = reinterpret_cast<uint8_t*>(workspace);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const dim3 grid(batch->num_tokens, num_q_heads);
-    if (cache->kind == PVA_CACHE_BF16) {
-        if (d == 128) simple_kernel<128, PVA_CACHE_BF16><<<grid, 128, 0, s>>>(a);
-        else simple_kernel<64, PVA_CACHE_BF16><<<grid, 128, 0, s>>>(a);
-    } else {
-        if (d == 128) simple_kernel<128, PVA_CACHE_INT4><<<grid, 128, 0, s>>>(a);
-        else simple_kernel<64, PVA_CACHE_INT4><<<grid, 128, 0, s>>>(a);
-    }
-    return cudaGetLastError() == cudaSuccess ? PVA_OK : PVA_ERR_CUDA;
+    if (cache->kind == PVA_CACHE_BF16)
+        return d == 128 ? launch_tiles<128, PVA_CACHE_BF16>(nt, a, ws, s)
+                        : launch_tiles<64, PVA_CACHE_BF16>(nt, a, ws, s);
+    return d == 128 ? launch_tiles<128, PVA_CACHE_INT4>(nt, a, ws, s)
+                    : launch_tiles<64, PVA_CACHE_INT4>(nt, a, ws, s);
 }
