@@ -51,17 +51,19 @@ struct AttnArgs {
     int64_t q_stride;
     SeqView s;
     int32_t hq, hkv, group, window, out_fp32;
-    float scale2;  // softmax scale * log2(e)
+    uint32_t page_bytes;  // codes or values of a page, one of K and V
+    float c;      // softmax scale * log2(e), times 2^69 with 4 bits (see low_codes)
+    float slack;  // kSlack / c
 };
 
 // Shape of a variant: warps a CTA, keys a step, ring stages, columns of the join buffer.
 template <int D, int KIND, int NT>
 struct Shape {
     static constexpr bool kInt4 = KIND == PVA_CACHE_INT4;
-    static constexpr int kWarps = kInt4 && NT == 1 ? 8 : 4;
-    static constexpr int kKeys = D == 128 ? 16 : 32;
-    static constexpr int kStages = kInt4 ? 4 : 3;
-    static constexpr int kCtas = 2;  // resident on an SM
+    static constexpr int kWarps = 4;
+    static constexpr int kKeys = (kInt4 ? 32 : 16) * (128 / D);
+    static constexpr int kStages = 3;
+    static constexpr int kCtas = kInt4 && NT == 1 ? 3 : 2;  // resident on an SM
     static constexpr int R = 8 * NT;
     static constexpr int kThreads = 32 * kWarps;
     static constexpr int kBlock = kWarps * kKeys;  // keys of a unit
@@ -72,7 +74,7 @@ struct Shape {
     static constexpr int kTiles = D / 16;  // 16-dim tiles of O^T
     // 16-dim tiles that the warps' sums are joined by at a time: what is left of the
     // shared memory beside the ring
-    static constexpr int kJoinTiles = kInt4 ? (kWarps * R >= 128 ? 2 : 4) : 4 / NT;
+    static constexpr int kJoinTiles = kInt4 ? (NT == 4 ? 2 : 4) : 4 / NT;
     static constexpr int kJoinDims = 16 * (kJoinTiles < kTiles ? kJoinTiles : kTiles);
     static constexpr int kJoinPitch = kJoinDims + 4;
     static constexpr int kRing = kWarps * kStages * kStageBytes;
@@ -112,6 +114,14 @@ __device__ __forceinline__ void mma(float* c, const uint32_t* a, uint32_t b0, ui
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+// The first product of a sum.
+__device__ __forceinline__ void mma0(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     uint32_t r;
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
@@ -128,11 +138,17 @@ __device__ __forceinline__ float ex2(float x) {
 }
 __device__ __forceinline__ float lo_f(uint32_t x) { return __uint_as_float(x << 16); }
 __device__ __forceinline__ float hi_f(uint32_t x) { return __uint_as_float(x & 0xffff0000u); }
-// The codes at bits 4p and 16 + 4p as a pair of bf16 128 + code: 0x4300 is 128, whose
-// last mantissa bit counts 1.
-__device__ __forceinline__ uint32_t codes(uint32_t w, int p) {
-    return ((w >> (4 * p)) & 0x000f000fu) | 0x43004300u;
-}
+// 4-bit codes as bf16 without arithmetic: a bf16 whose sign and upper seven exponent
+// bits are 0 is its low eight bits as a whole number, times 2^-133 (subnormals and the
+// first binade lie on one line).  So a mask alone makes code * 2^-133 of bits 0 .. 3 of
+// each half and 16 * code * 2^-133 of bits 4 .. 7; the products, which are exact in
+// fp32, stay in range because the other operand carries 2^64.
+__device__ __forceinline__ uint32_t low_codes(uint32_t w) { return w & 0x000f000fu; }
+__device__ __forceinline__ uint32_t high_codes(uint32_t w) { return w & 0x00f000f0u; }
+__device__ __forceinline__ uint32_t both_codes(uint32_t w) { return w & 0x00ff00ffu; }
+__device__ __forceinline__ uint32_t upper_bytes(uint32_t w) { return __byte_perm(w, 0, 0x4341); }
+constexpr float kUp64 = 18446744073709551616.f;           // 2^64
+constexpr float kUp69 = 590295810358705651712.f;          // 2^69 = 2^133 / 2^64
 
 // ---------------------------------------------------------------- the line of units
 struct SeqInfo {
@@ -174,13 +190,14 @@ __device__ __forceinline__ int64_t units_of(const AttnArgs& a, const SeqInfo& s)
     return (int64_t)a.hkv * s.nrb * (kFixedUnits + s.nb);
 }
 
-enum { kFirst = 1, kLast = 2, kEmpty = 4, kWhole = 8 };
+enum { kFirst = 1, kLast = 2, kEmpty = 4, kWhole = 8, kMissing = 16 };  // kMissing << x: no page for keys 16x ..
 
 // What a ring stage holds, as its consumer needs it.
 struct Meta {
-    int32_t key0, flags, vlo, vhi;   // keys vlo .. vhi of the tile are there
-    int32_t row0, rows, pos0, missing;  // first token, group * n, bit x: no page for keys 16x ..
-    int32_t rb, kvh, slot, n;
+    int32_t key0, flags, vlo, vhi;  // keys vlo .. vhi of the tile are there
+    // of an item's first and last step only:
+    int32_t row0, rows, pos0, rb;   // first token, group * new tokens, first position, row block
+    int32_t kvh, slot, pad[2];
 };
 
 template <int D, int KIND, int NT>
@@ -353,54 +370,64 @@ __global__ void __launch_bounds__(Shape<D, KIND, NT>::kThreads, Shape<D, KIND, N
                     missing |= 1 << x;
                     if (lane == 0 && key < vhi && key + 16 > vlo) raise_status(a.s.status, kErrPage);
                 }
-                const int64_t row =
-                    there ? (((int64_t)page[x] * a.hkv + kvh) << a.s.page_shift) +
-                                (key & ((1 << a.s.page_shift) - 1))
-                          : 0;
+                const uint32_t in_page =
+                    (((uint32_t)kvh << a.s.page_shift) + (key & ((1 << a.s.page_shift) - 1))) * ROWB;
+                const uint64_t off = (uint64_t)(uint32_t)page[x] * a.page_bytes + in_page;
+                constexpr int CPR = ROWB / 16, PER = 16 * CPR / 32;  // 16-byte chunks: a row's, a lane's
                 if (!INT4) {
-                    // rows outside the valid keys are filled with zeros: a weight of 0 must not
-                    // meet a NaN
-                    constexpr int CPR = ROWB / 16, PER = 16 * CPR / 32;
+                    const uint8_t* ks = a.k_pages + off + lane * 16;
+                    const uint8_t* vs16 = a.v_pages + off + lane * 16;
+                    const int r0 = lane / CPR, ch = lane % CPR;
+                    if (there && key >= vlo && key + 16 <= vhi) {
 #pragma unroll
-                    for (int i = 0; i < PER; ++i) {
-                        const int r = (i * 32 + lane) / CPR, ch = (i * 32 + lane) % CPR;
-                        const bool ok = there && key + r >= vlo && key + r < vhi;
-                        const int64_t off = ok ? (row + r) * ROWB + ch * 16 : 0;
-                        const uint32_t to = (16 * x + r) * ROWB + ((ch ^ (r & 7)) << 4);
-                        cp16(kd + to, a.k_pages + off, ok ? 16 : 0);
-                        cp16(kd + KS * ROWB + to, a.v_pages + off, ok ? 16 : 0);
+                        for (int i = 0; i < PER; ++i) {
+                            const int r = i * (32 / CPR) + r0;
+                            const uint32_t to = (16 * x + r) * ROWB + ((ch ^ (r & 7)) << 4);
+                            cp16(kd + to, ks + i * 512, 16);
+                            cp16(kd + KS * ROWB + to, vs16 + i * 512, 16);
+                        }
+                    } else {
+                        // rows outside the valid keys are filled with zeros: a weight of 0 must not
+                        // meet a NaN
+#pragma unroll
+                        for (int i = 0; i < PER; ++i) {
+                            const int r = i * (32 / CPR) + r0;
+                            const bool ok = there && key + r >= vlo && key + r < vhi;
+                            const uint32_t to = (16 * x + r) * ROWB + ((ch ^ (r & 7)) << 4);
+                            cp16(kd + to, ok ? ks + i * 512 : a.k_pages, ok ? 16 : 0);
+                            cp16(kd + KS * ROWB + to, ok ? vs16 + i * 512 : a.v_pages, ok ? 16 : 0);
+                        }
                     }
                 } else if (there) {
-                    constexpr int CPR = ROWB / 16, PER = 16 * CPR / 32;
+                    // V: 16-byte chunks of a 128-byte line change places with the line's number, so
+                    // that the rows a warp reads at once lie in other banks
+                    const int sw = (lane & 7) ^ (2 * ((lane >> 3) & (D == 128 ? 3 : 1)));
+                    const uint32_t kt = kd + 16 * x * ROWB + lane * 16;
+                    const uint32_t vt = kd + (KS + 16 * x) * ROWB + ((lane & 24) + sw) * 16;
 #pragma unroll
                     for (int i = 0; i < PER; ++i) {
-                        const int idx = i * 32 + lane;
-                        // V: 16-byte chunks of a 128-byte line change places with the line's
-                        // number, so that the rows a warp reads at once lie in other banks
-                        const int line = idx >> 3, sw = (idx & 7) ^ (D == 128 ? 2 * (line & 3) : 2 * (line & 1));
-                        cp16(kd + x * 16 * ROWB + idx * 16, a.k_pages + row * ROWB + idx * 16, 16);
-                        cp16(kd + (KS + 16 * x) * ROWB + (line * 8 + sw) * 16,
-                             a.v_pages + row * ROWB + idx * 16, 16);
+                        cp16(kt + i * 512, a.k_pages + off + lane * 16 + i * 512, 16);
+                        cp16(vt + i * 512, a.v_pages + off + lane * 16 + i * 512, 16);
                     }
-                    constexpr int SC = 16 * Sh::kScaleBytes / 16;  // chunks of 16 keys' scales
+                    constexpr int SC = Sh::kScaleBytes;  // chunks of 16 keys' scales, an eighth of the codes
                     if (lane < 2 * SC) {
-                        const int v = lane >= SC, i = lane - v * SC;
-                        cp16(kd + 2 * KS * ROWB + (v * KS + 16 * x) * Sh::kScaleBytes + i * 16,
-                             (v ? a.v_scales : a.k_scales) + row * Sh::kScaleBytes + i * 16, 16);
+                        const bool v = lane >= SC;
+                        const int i = v ? lane - SC : lane;
+                        cp16(kd + 2 * KS * ROWB + ((v ? KS : 0) + 16 * x) * Sh::kScaleBytes + i * 16,
+                             (v ? a.v_scales : a.k_scales) + (off >> 3) + i * 16, 16);
                     }
                 }
             }
-            if (lane == 0) {
-                Meta& m = meta[stage];
-                *reinterpret_cast<int4*>(&m.key0) = make_int4(next_key, next_flags, vlo, vhi);
-                *reinterpret_cast<int4*>(&m.row0) = make_int4(sq.row0, sq.n * a.group, sq.pos0, missing);
-                *reinterpret_cast<int4*>(&m.rb) = make_int4(rb, kvh, slot, sq.n);
-            }
+            if (lane == 0)
+                *reinterpret_cast<int4*>(&meta[stage].key0) =
+                    make_int4(next_key, next_flags | missing * kMissing, vlo, vhi);
         } else if (lane == 0) {
+            *reinterpret_cast<int4*>(&meta[stage].key0) = make_int4(0, next_flags, 0, 0);
+        }
+        if (lane == 0 && (next_flags & (kFirst | kLast))) {
             Meta& m = meta[stage];
-            *reinterpret_cast<int4*>(&m.key0) = make_int4(0, next_flags, 0, 0);
-            *reinterpret_cast<int4*>(&m.row0) = make_int4(sq.row0, sq.n * a.group, sq.pos0, 0);
-            *reinterpret_cast<int4*>(&m.rb) = make_int4(rb, kvh, slot, sq.n);
+            *reinterpret_cast<int4*>(&m.row0) = make_int4(sq.row0, sq.n * a.group, sq.pos0, rb);
+            *reinterpret_cast<int2*>(&m.kvh) = make_int2(kvh, slot);
         }
         next();
     };
@@ -417,8 +444,9 @@ __global__ void __launch_bounds__(Shape<D, KIND, NT>::kThreads, Shape<D, KIND, N
     }
 
     // ---- state of the item in hand
-    float o[NT][T][4], m_run[NT][2], l_run[NT][2];
-    float vs[INT4 ? G : 1][NT][4];     // 4 bits: sums of the scaled weights
+    // Scores stay as the products leave them; weights are 2^(c s + shift), shift = -c m
+    // (4 bits: + 64).
+    float o[NT][T][4], m_run[NT][2], shift[NT][2], l_run[NT][2];
     float zs[INT4 ? G : 1][NT][2];     // 4 bits: sums of weight * low
     float qs[INT4 ? G : 1][NT][2];     // 4 bits: sums of the query's dims of a group
     uint32_t qf[NT][D / 16][2];
@@ -445,6 +473,7 @@ __global__ void __launch_bounds__(Shape<D, KIND, NT>::kThreads, Shape<D, KIND, N
 #pragma unroll
                     for (int e = 0; e < 4; ++e) o[nt][i][e] = 0.f;
                 m_run[nt][0] = m_run[nt][1] = -INFINITY;
+                shift[nt][0] = shift[nt][1] = 0.f;
                 l_run[nt][0] = l_run[nt][1] = 0.f;
                 const int32_t r = r0 + 8 * nt + g;
                 const int32_t tok = r / a.group;
@@ -467,19 +496,19 @@ __global__ void __launch_bounds__(Shape<D, KIND, NT>::kThreads, Shape<D, KIND, N
                         for (int oc = 0; oc < 2; ++oc) {
                             const uint4 x = live ? __ldg(reinterpret_cast<const uint4*>(q + 64 * gr + 16 * c + 8 * oc))
                                                  : make_uint4(0, 0, 0, 0);
-                            qf[nt][4 * gr + 2 * oc][0] = x.x;
-                            qf[nt][4 * gr + 2 * oc][1] = x.y;
-                            qf[nt][4 * gr + 2 * oc + 1][0] = x.z;
-                            qf[nt][4 * gr + 2 * oc + 1][1] = x.w;
+                            constexpr float kUp60 = kUp64 / 16.f;  // meets 16 * code
+                            qf[nt][4 * gr + 2 * oc][0] = pack2(lo_f(x.x) * kUp64, hi_f(x.x) * kUp64);
+                            qf[nt][4 * gr + 2 * oc][1] = pack2(lo_f(x.y) * kUp60, hi_f(x.y) * kUp60);
+                            qf[nt][4 * gr + 2 * oc + 1][0] = pack2(lo_f(x.z) * kUp64, hi_f(x.z) * kUp64);
+                            qf[nt][4 * gr + 2 * oc + 1][1] = pack2(lo_f(x.w) * kUp60, hi_f(x.w) * kUp60);
                             sum += ((lo_f(x.x) + hi_f(x.x)) + (lo_f(x.y) + hi_f(x.y))) +
                                    ((lo_f(x.z) + hi_f(x.z)) + (lo_f(x.w) + hi_f(x.w)));
                         }
                         sum += __shfl_xor_sync(0xffffffffu, sum, 1);
                         sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+                        sum *= 1.f / kUp69;
                         qs[gr][nt][0] = __shfl_sync(0xffffffffu, sum, 8 * c);
                         qs[gr][nt][1] = __shfl_sync(0xffffffffu, sum, 8 * c + 4);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) vs[gr][nt][e] = 0.f;
                         zs[gr][nt][0] = zs[gr][nt][1] = 0.f;
                     }
                 }
@@ -494,7 +523,7 @@ __global__ void __launch_bounds__(Shape<D, KIND, NT>::kThreads, Shape<D, KIND, N
                           : 0;
         }
         if (!(flags & kEmpty)) {
-            const int32_t key0 = mt.key0, vlo = mt.vlo, vhi = mt.vhi, missing = mt.missing;
+            const int32_t key0 = mt.key0, vlo = mt.vlo, vhi = mt.vhi, missing = flags / kMissing;
             const bool partial = key0 < max(full_lo, vlo) || key0 + KS > min(full_hi + 1, vhi) || missing;
             const uint32_t kb = smem_addr(buf), vb = kb + KS * ROWB;
             float s[SUB][NT][4];
@@ -503,16 +532,15 @@ __global__ void __launch_bounds__(Shape<D, KIND, NT>::kThreads, Shape<D, KIND, N
             for (int x = 0; x < SUB; ++x) {
                 if (!INT4) {
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) s[x][nt][e] = 0.f;
-#pragma unroll
                     for (int ks = 0; ks < D / 16; ++ks) {
                         uint32_t f[4];
                         const int r = lane & 15, ch = 2 * ks + (lane >> 4);
                         ldsm(f, kb + (16 * x + r) * ROWB + ((ch ^ (r & 7)) << 4));
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) mma(s[x][nt], f, qf[nt][ks][0], qf[nt][ks][1]);
+                        for (int nt = 0; nt < NT; ++nt) {
+                            if (ks == 0) mma0(s[x][nt], f, qf[nt][ks][0], qf[nt][ks][1]);
+                            else mma(s[x][nt], f, qf[nt][ks][0], qf[nt][ks][1]);
+                        }
                     }
                 } else {
                     uint32_t w[2][2 * G], sc[2][G];
@@ -540,79 +568,75 @@ __global__ void __launch_bounds__(Shape<D, KIND, NT>::kThreads, Shape<D, KIND, N
 #pragma unroll
                     for (int gr = 0; gr < G; ++gr) {
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) acc[gr][nt][e] = 0.f;
-#pragma unroll
                         for (int oc = 0; oc < 2; ++oc)
 #pragma unroll
                             for (int h = 0; h < 2; ++h) {
-                                const uint32_t w0 = w[0][G * oc + gr], w1 = w[1][G * oc + gr];
-                                const uint32_t f[4] = {codes(w0, 2 * h), codes(w1, 2 * h),
-                                                       codes(w0, 2 * h + 1), codes(w1, 2 * h + 1)};
+                                const uint32_t w0 = w[0][G * oc + gr] >> (8 * h), w1 = w[1][G * oc + gr] >> (8 * h);
+                                const uint32_t f[4] = {low_codes(w0), low_codes(w1), high_codes(w0),
+                                                       high_codes(w1)};
 #pragma unroll
-                                for (int nt = 0; nt < NT; ++nt)
-                                    mma(acc[gr][nt], f, qf[nt][4 * gr + 2 * oc + h][0],
-                                        qf[nt][4 * gr + 2 * oc + h][1]);
+                                for (int nt = 0; nt < NT; ++nt) {
+                                    const uint32_t* q2 = qf[nt][4 * gr + 2 * oc + h];
+                                    if (oc == 0 && h == 0) mma0(acc[gr][nt], f, q2[0], q2[1]);
+                                    else mma(acc[gr][nt], f, q2[0], q2[1]);
+                                }
                             }
                     }
-                    // s = sum over groups of scale * (q . codes) + low * (sum of q); the products hold
-                    // q . (128 + code)
+                    // s = sum over groups of scale * (q . codes) + low * (sum of q)
 #pragma unroll
                     for (int y = 0; y < 2; ++y)
 #pragma unroll
                         for (int gr = 0; gr < G; ++gr) {
-                            const float scl = lo_f(sc[y][gr]);
-                            const float off = fmaf(-128.f, scl, hi_f(sc[y][gr]));
+                            const float scl = lo_f(sc[y][gr]), low = hi_f(sc[y][gr]);
 #pragma unroll
                             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                                 for (int e = 0; e < 2; ++e) {
-                                    const float before = gr == 0 ? 0.f : s[x][nt][2 * y + e];
-                                    s[x][nt][2 * y + e] = fmaf(
-                                        scl, acc[gr][nt][2 * y + e], fmaf(off, qs[gr][nt][e], before));
+                                    const float z = gr == 0 ? low * qs[gr][nt][e]
+                                                            : fmaf(low, qs[gr][nt][e], s[x][nt][2 * y + e]);
+                                    s[x][nt][2 * y + e] = fmaf(scl, acc[gr][nt][2 * y + e], z);
                                 }
                         }
                 }
             }
-            // ---- base 2, masks, maximum over the tile
-            float mx[NT][2];
+            // ---- masks; has a score left the range of the running maximum?
+            if (partial) {
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mx[nt][0] = mx[nt][1] = -INFINITY;
+                for (int x = 0; x < SUB; ++x)
 #pragma unroll
-            for (int x = 0; x < SUB; ++x)
+                    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        float v = s[x][nt][e] * a.scale2;
-                        if (partial) {
+                        for (int e = 0; e < 4; ++e) {
                             const int32_t j = key0 + 16 * x + g + 8 * (e >> 1), p = pos[nt][e & 1];
                             const bool ok = j >= vlo && j < vhi && j <= p && !(missing >> x & 1) &&
                                             (a.window <= 0 || p - j < a.window);
-                            v = ok ? v : -INFINITY;
+                            s[x][nt][e] = ok ? s[x][nt][e] : -INFINITY;
                         }
-                        s[x][nt][e] = v;
-                        mx[nt][e & 1] = fmaxf(mx[nt][e & 1], v);
-                    }
+            }
             bool up = false;
+            float mx[NT][2];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
+                    mx[nt][e] = fmaxf(s[0][nt][e], s[0][nt][2 + e]);
 #pragma unroll
-                    for (int d = 4; d < 32; d <<= 1)
-                        mx[nt][e] = fmaxf(mx[nt][e], __shfl_xor_sync(0xffffffffu, mx[nt][e], d));
-                    up |= mx[nt][e] > m_run[nt][e] + kSlack;
+                    for (int x = 1; x < SUB; ++x)
+                        mx[nt][e] = fmaxf(mx[nt][e], fmaxf(s[x][nt][e], s[x][nt][2 + e]));
+                    up |= mx[nt][e] > m_run[nt][e] + a.slack;
                 }
             if (__any_sync(0xffffffffu, up)) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                        for (int d = 4; d < 32; d <<= 1)
+                            mx[nt][e] = fmaxf(mx[nt][e], __shfl_xor_sync(0xffffffffu, mx[nt][e], d));
                         const float mn = fmaxf(m_run[nt][e], mx[nt][e]);
-                        const float f = m_run[nt][e] == -INFINITY ? 0.f : ex2(m_run[nt][e] - mn);
+                        const float f = m_run[nt][e] == -INFINITY ? 0.f : ex2((m_run[nt][e] - mn) * a.c);
                         m_run[nt][e] = mn;
+                        shift[nt][e] = mn == -INFINITY ? 0.f : (INT4 ? 64.f : 0.f) - mn * a.c;
                         l_run[nt][e] *= f;
 #pragma unroll
                         for (int i = 0; i < T; ++i) {
@@ -621,10 +645,7 @@ __global__ void __launch_bounds__(Shape<D, KIND, NT>::kThreads, Shape<D, KIND, N
                         }
                         if (INT4) {
 #pragma unroll
-                            for (int gr = 0; gr < G; ++gr) {
-                                vs[gr][nt][e] *= f;
-                                zs[gr][nt][e] *= f;
-                            }
+                            for (int gr = 0; gr < G; ++gr) zs[gr][nt][e] *= f;
                         }
                     }
             }
@@ -635,8 +656,7 @@ __global__ void __launch_bounds__(Shape<D, KIND, NT>::kThreads, Shape<D, KIND, N
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const float base = m_run[nt][e & 1] == -INFINITY ? 0.f : m_run[nt][e & 1];
-                        s[x][nt][e] = ex2(s[x][nt][e] - base);
+                        s[x][nt][e] = ex2(fmaf(s[x][nt][e], a.c, shift[nt][e & 1]));
                         l_run[nt][e & 1] += s[x][nt][e];
                     }
                 if (!INT4) {
@@ -689,8 +709,6 @@ __global__ void __launch_bounds__(Shape<D, KIND, NT>::kThreads, Shape<D, KIND, N
                                 zs[gr][nt][0] = fmaf(s[x][nt][2 * y], low, zs[gr][nt][0]);
                                 zs[gr][nt][1] = fmaf(s[x][nt][2 * y + 1], low, zs[gr][nt][1]);
                             }
-                            const uint32_t ones[4] = {0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u};
-                            mma(vs[gr][nt], ones, p[gr][nt][0], p[gr][nt][1]);
                         }
                     uint32_t w[4][G];  // keys 2c, 2c + 1, 2c + 8, 2c + 9
 #pragma unroll
@@ -710,16 +728,27 @@ __global__ void __launch_bounds__(Shape<D, KIND, NT>::kThreads, Shape<D, KIND, N
                     }
 #pragma unroll
                     for (int gr = 0; gr < G; ++gr) {
-                        const uint32_t a0 = __byte_perm(w[0][gr], w[1][gr], 0x5410);
-                        const uint32_t a1 = __byte_perm(w[0][gr], w[1][gr], 0x7632);
-                        const uint32_t a2 = __byte_perm(w[2][gr], w[3][gr], 0x5410);
-                        const uint32_t a3 = __byte_perm(w[2][gr], w[3][gr], 0x7632);
+                        // the even dims of two keys in one word, and the odd ones; halves e hold
+                        // keys 2c (+8) and 2c + 1 (+8)
+                        const uint32_t v[4] = {__byte_perm(w[0][gr], w[1][gr], 0x5410),
+                                               __byte_perm(w[0][gr], w[1][gr], 0x7632),
+                                               __byte_perm(w[2][gr], w[3][gr], 0x5410),
+                                               __byte_perm(w[2][gr], w[3][gr], 0x7632)};
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const uint32_t f[4] = {codes(a0, i), codes(a1, i), codes(a2, i), codes(a3, i)};
+                        for (int h = 0; h < 2; ++h) {
+                            // tile 2h: the lower code of a byte; tile 2h + 1: the whole byte, from which
+                            // the lower code is taken off again at the item's end
+                            uint32_t f[4], lo[4];
 #pragma unroll
-                            for (int nt = 0; nt < NT; ++nt)
-                                mma(o[nt][4 * gr + i], f, p[gr][nt][0], p[gr][nt][1]);
+                            for (int y = 0; y < 4; ++y) {
+                                f[y] = h == 0 ? both_codes(v[y]) : upper_bytes(v[y]);
+                                lo[y] = low_codes(f[y]);
+                            }
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt) {
+                                mma(o[nt][4 * gr + 2 * h], lo, p[gr][nt][0], p[gr][nt][1]);
+                                mma(o[nt][4 * gr + 2 * h + 1], f, p[gr][nt][0], p[gr][nt][1]);
+                            }
                         }
                     }
                 }
@@ -741,12 +770,18 @@ __global__ void __launch_bounds__(Shape<D, KIND, NT>::kThreads, Shape<D, KIND, N
                                 zs[gr][nt][e] += __shfl_xor_sync(0xffffffffu, zs[gr][nt][e], d);
                         }
                     }
+                    // sums in plain units, the maximum in base 2
+                    m_run[nt][e] *= a.c;
                     if (INT4) {
+                        l_run[nt][e] *= 1.f / kUp64;
 #pragma unroll
-                        for (int i = 0; i < T; ++i) {
-                            const float add = fmaf(-128.f, vs[INT4 ? i / 4 : 0][nt][e], zs[INT4 ? i / 4 : 0][nt][e]);
-                            o[nt][i][e] += add;
-                            o[nt][i][2 + e] += add;
+                        for (int i = 0; i < T; i += 2) {
+                            const float z = zs[INT4 ? i / 4 : 0][nt][e] * (1.f / kUp64);
+#pragma unroll
+                            for (int y = e; y < 4; y += 2) {
+                                o[nt][i + 1][y] = fmaf(o[nt][i + 1][y] - o[nt][i][y], kUp69 / 16.f, z);
+                                o[nt][i][y] = fmaf(o[nt][i][y], kUp69, z);
+                            }
                         }
                     }
                 }
@@ -918,7 +953,7 @@ size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 template <int D, int KIND, int NT>
 pva_status launch(AttnArgs a, uint8_t* ws, cudaStream_t st) {
     using Sh = Shape<D, KIND, NT>;
-    static_assert(Sh::kSmem <= 113 * 1024, "two CTAs share an SM");
+    static_assert((Sh::kSmem + 1280) * Sh::kCtas <= 228 * 1024, "the CTAs share an SM");
     a.ws_per = reinterpret_cast<int64_t*>(ws);
     a.ws_cum = reinterpret_cast<int64_t*>(ws + 256);
     ws += 256 + up256((size_t)a.s.num_seqs * 8);
@@ -1008,7 +1043,16 @@ extern "C" pva_status pva_cache_attn(const pva_cache_desc* cache, const pva_cach
     a.group = num_q_heads / cache->num_kv_heads;
     a.window = window;
     a.out_fp32 = out_is_fp32;
-    a.scale2 = (softmax_scale > 0.f ? softmax_scale : 1.f / sqrtf((float)d)) * kLog2e;
+    a.c = (softmax_scale > 0.f ? softmax_scale : 1.f / sqrtf((float)d)) * kLog2e;
+    a.slack = kSlack / a.c;
+    if (cache->kind == PVA_CACHE_INT4) {
+        a.c *= kUp69;
+        a.slack *= 1.f / kUp69;
+    }
+    const int64_t page_bytes =
+        (int64_t)cache->num_kv_heads * cache->page_size * (cache->kind == PVA_CACHE_INT4 ? d / 2 : 2 * d);
+    if (page_bytes > INT32_MAX) return PVA_ERR_UNSUPPORTED;
+    a.page_bytes = (uint32_t)page_bytes;
     // Without offsets every sequence has one row, whatever bound was given.
     const int nt = tiles_of((int64_t)a.group * max_new);
     uint8_t* ws = reinterpret_cast<uint8_t*>(workspace);
