@@ -51,7 +51,7 @@ struct AttnArgs {
     int64_t q_stride;
     SeqView s;
     int32_t hq, hkv, group, window, out_fp32;
-    uint32_t page_bytes;  // codes or values of a page, one of K and V
+    uint32_t num_pages, page_bytes;  // page_bytes: codes or values of a page, one of K and V
     float c;      // softmax scale * log2(e), times 2^69 with 4 bits (see low_codes)
     float slack;  // kSlack / c
 };
@@ -190,13 +190,14 @@ __device__ __forceinline__ int64_t units_of(const AttnArgs& a, const SeqInfo& s)
     return (int64_t)a.hkv * s.nrb * (kFixedUnits + s.nb);
 }
 
-enum { kFirst = 1, kLast = 2, kEmpty = 4, kWhole = 8, kMissing = 16 };  // kMissing << x: no page for keys 16x ..
+// Steps: first and last of an item, nothing to read, the item is all this piece's, some
+// key of the tile is not for every row.
+enum { kFirst = 1, kLast = 2, kEmpty = 4, kWhole = 8, kPartial = 16 };
 
-// What a ring stage holds, as its consumer needs it.
+// What a step's consumer needs beside its flags: written for first, last and partial steps.
 struct Meta {
-    int32_t key0, flags, vlo, vhi;  // keys vlo .. vhi of the tile are there
-    // of an item's first and last step only:
-    int32_t row0, rows, pos0, rb;   // first token, group * new tokens, first position, row block
+    int32_t key0, vlo, vhi, missing;  // partial: keys vlo .. vhi are there, bit x: no page for keys 16x ..
+    int32_t row0, rows, pos0, rb;     // first token, group * new tokens, first position, row block
     int32_t kvh, slot, pad[2];
 };
 
@@ -277,15 +278,19 @@ __global__ void __launch_bounds__(Shape<D, KIND, NT>::kThreads, Shape<D, KIND, N
     }
 
     // ---- cursor over this warp's steps
+    const int32_t own = warp * KS;      // this warp's keys inside a block
+    const bool one_page = (1 << a.s.page_shift) >= KS;
     SeqInfo sq = seq_info<R, BLOCK>(a, b, false);
+    const int32_t* pages = a.s.page_table + b * a.s.table_stride;
     int32_t len = kFixedUnits + sq.nb;
     it = (int32_t)((u0 - ub) / len);
     int32_t rb = it / a.hkv, kvh = it - rb * a.hkv;
     int64_t ui = ub + (int64_t)it * len;  // first unit of the item
-    int32_t t = 0, tend = 0;              // blocks left of the item for this warp (absolute)
-    int32_t rlo, rhi;                     // keys that the row block may see
-    int32_t slot = 0, next_key = 0, next_flags = 0;
-    int32_t page[SUB];
+    int32_t key = 0, kend = 0;            // the pending step's first key; where the item's steps end
+    int32_t rlo = 0, rhi = 0;             // keys that some row of the block may see
+    int32_t alo = 0, ahi = 0;             // keys that every row of it sees
+    int32_t slot = 0, flags_next = 0;
+    uint32_t page[SUB];
     bool more = true;   // a step is pending
     bool fresh = true;  // the cursor stands before its first item
 
@@ -293,30 +298,36 @@ __global__ void __launch_bounds__(Shape<D, KIND, NT>::kThreads, Shape<D, KIND, N
     auto open_item = [&]() -> bool {
         const int32_t i0 = (int32_t)((int64_t)rb * R / a.group);
         const int32_t i1 = (int32_t)min(((int64_t)rb * R + R - 1) / a.group, (int64_t)sq.n - 1);
-        rlo = a.window > 0 ? (int32_t)max((int64_t)sq.pos0 + i0 - a.window + 1, (int64_t)0) : 0;
+        rlo = alo = 0;
+        if (a.window > 0) {
+            rlo = (int32_t)max((int64_t)sq.pos0 + i0 - a.window + 1, (int64_t)0);
+            alo = (int32_t)max((int64_t)sq.pos0 + i1 - a.window + 1, (int64_t)0);
+        }
         rhi = min(sq.pos0 + i1 + 1, sq.khi);
+        ahi = min(sq.pos0 + i0 + 1, sq.khi);
         if (sq.nb == 0) {
-            t = tend = 0;
-            next_flags = kFirst | kLast | kEmpty | kWhole;
+            key = kend = 0;
+            flags_next = kFirst | kLast | kEmpty | kWhole;
             return u0 <= ui;
         }
         const int64_t first = ui + kFixedUnits, last = ui + len;
         const int32_t t0 = (int32_t)max(u0 - first, (int64_t)0);
         const int32_t t1 = (int32_t)(min(u1, last) - first);
         if (t1 <= t0) return false;
-        next_flags = kFirst | (t0 == 0 && t1 == sq.nb ? kWhole : 0);
+        flags_next = kFirst | (t0 == 0 && t1 == sq.nb ? kWhole : 0);
         slot = 2 * blockIdx.x + (t0 == 0 ? 1 : 0);
         // of blocks blo + t0 .. blo + t1, those whose keys of this warp the rows may see
-        const int32_t off = warp * KS;
-        t = max(sq.blo + t0, rlo - off - KS + 1 <= 0 ? 0 : (rlo - off - KS + BLOCK) / BLOCK);
-        tend = min(sq.blo + t1, rhi <= off ? 0 : (rhi - off + BLOCK - 1) / BLOCK);
-        if (t >= tend) next_flags |= kLast | kEmpty;
+        const int32_t ta = max(sq.blo + t0, rlo - own < KS ? 0 : (rlo - own - KS + BLOCK) / BLOCK);
+        const int32_t tb = min(sq.blo + t1, rhi <= own ? 0 : (rhi - own + BLOCK - 1) / BLOCK);
+        key = ta * BLOCK + own;
+        kend = tb * BLOCK + own;
+        if (ta >= tb) flags_next |= kLast | kEmpty;
         return true;
     };
     auto next = [&]() {
-        if (t < tend) {
-            next_flags &= ~kFirst;
-        } else {
+        key += BLOCK;
+        flags_next &= kWhole;
+        if (key >= kend) {
             for (;;) {
                 if (!fresh) {
                     ui += len;
@@ -332,6 +343,7 @@ __global__ void __launch_bounds__(Shape<D, KIND, NT>::kThreads, Shape<D, KIND, N
                                 sq = seq_info<R, BLOCK>(a, b, false);
                             } while (sq.nrb == 0);
                             len = kFixedUnits + sq.nb;
+                            pages = a.s.page_table + b * a.s.table_stride;
                         }
                     }
                 }
@@ -342,102 +354,112 @@ __global__ void __launch_bounds__(Shape<D, KIND, NT>::kThreads, Shape<D, KIND, N
                 }
                 if (open_item()) break;
             }
+            if (flags_next & kEmpty) return;
         }
-        if (!(next_flags & kEmpty)) {
-            next_key = t * BLOCK + warp * KS;
-            if (++t >= tend) next_flags |= kLast;
+        if (key + BLOCK >= kend) flags_next |= kLast;
+        if (key < alo || key + KS > ahi) flags_next |= kPartial;
+        const int32_t i = key >> a.s.page_shift;  // below max_pages: key < rhi
+        page[0] = (uint32_t)__ldg(pages + i);
+        if (!one_page) {
 #pragma unroll
-            for (int x = 0; x < SUB; ++x) {
-                const int32_t i = (next_key + 16 * x) >> a.s.page_shift;
-                page[x] = i < a.s.max_pages
-                              ? __ldg(a.s.page_table + b * a.s.table_stride + i)
-                              : -1;
+            for (int x = 1; x < SUB; ++x) {
+                const int32_t y = (key + 16 * x) >> a.s.page_shift;
+                page[x] = y < a.s.max_pages ? (uint32_t)__ldg(pages + y) : ~0u;
             }
         }
     };
-    // Copies of the pending step into a stage, and the next step.
-    auto issue = [&](int stage) {
-        uint8_t* dst = ring + stage * Sh::kStageBytes;
-        const uint32_t kd = smem_addr(dst);
-        int32_t missing = 0;
-        if (!(next_flags & kEmpty)) {
-            const int32_t vlo = max(next_key, rlo), vhi = min(next_key + KS, rhi);
+    // 16 keys at byte `off` of K and V into a stage; [vlo, vhi): rows of them that are there.
+    auto copy16 = [&](uint32_t kd, int x, uint64_t off, int vlo, int vhi) {
+        constexpr int CPR = ROWB / 16, PER = 16 * CPR / 32;  // 16-byte chunks: a row's, a lane's
+        const uint8_t* ks = a.k_pages + off + lane * 16;
+        const uint8_t* vs = a.v_pages + off + lane * 16;
+        if (!INT4) {
+            const int r0 = lane / CPR, ch = lane % CPR;
 #pragma unroll
-            for (int x = 0; x < SUB; ++x) {
-                const int32_t key = next_key + 16 * x;
-                const bool there = page[x] >= 0 && page[x] < a.s.num_pages;
-                if (!there) {
-                    missing |= 1 << x;
-                    if (lane == 0 && key < vhi && key + 16 > vlo) raise_status(a.s.status, kErrPage);
-                }
-                const uint32_t in_page =
-                    (((uint32_t)kvh << a.s.page_shift) + (key & ((1 << a.s.page_shift) - 1))) * ROWB;
-                const uint64_t off = (uint64_t)(uint32_t)page[x] * a.page_bytes + in_page;
-                constexpr int CPR = ROWB / 16, PER = 16 * CPR / 32;  // 16-byte chunks: a row's, a lane's
-                if (!INT4) {
-                    const uint8_t* ks = a.k_pages + off + lane * 16;
-                    const uint8_t* vs16 = a.v_pages + off + lane * 16;
-                    const int r0 = lane / CPR, ch = lane % CPR;
-                    if (there && key >= vlo && key + 16 <= vhi) {
+            for (int i = 0; i < PER; ++i) {
+                const int r = i * (32 / CPR) + r0;
+                const uint32_t to = (16 * x + r) * ROWB + ((ch ^ (r & 7)) << 4);
+                // rows that are not there are filled with zeros: a weight of 0 must not meet a NaN
+                const bool ok = r >= vlo && r < vhi;
+                cp16(kd + to, ok ? ks + i * 512 : a.k_pages, ok ? 16 : 0);
+                cp16(kd + KS * ROWB + to, ok ? vs + i * 512 : a.v_pages, ok ? 16 : 0);
+            }
+        } else {
+            // V: 16-byte chunks of a 128-byte line change places with the line's number, so that
+            // the rows a warp reads at once lie in other banks
+            const int sw = (lane & 7) ^ (2 * ((lane >> 3) & (D == 128 ? 3 : 1)));
+            const uint32_t kt = kd + 16 * x * ROWB + lane * 16;
+            const uint32_t vt = kd + (KS + 16 * x) * ROWB + ((lane & 24) + sw) * 16;
 #pragma unroll
-                        for (int i = 0; i < PER; ++i) {
-                            const int r = i * (32 / CPR) + r0;
-                            const uint32_t to = (16 * x + r) * ROWB + ((ch ^ (r & 7)) << 4);
-                            cp16(kd + to, ks + i * 512, 16);
-                            cp16(kd + KS * ROWB + to, vs16 + i * 512, 16);
-                        }
+            for (int i = 0; i < PER; ++i) {
+                cp16(kt + i * 512, ks + i * 512, 16);
+                cp16(vt + i * 512, vs + i * 512, 16);
+            }
+            constexpr int SC = Sh::kScaleBytes;  // chunks of 16 keys' scales, an eighth of the codes
+            if (lane < 2 * SC) {
+                const bool v = lane >= SC;
+                const int i = v ? lane - SC : lane;
+                cp16(kd + 2 * KS * ROWB + ((v ? KS : 0) + 16 * x) * Sh::kScaleBytes + i * 16,
+                     (v ? a.v_scales : a.k_scales) + (off >> 3) + i * 16, 16);
+            }
+        }
+    };
+    // Copies of the pending step into a stage, and the next step.  Returns the step's flags.
+    auto issue = [&](int stage) -> int32_t {
+        const uint32_t kd = smem_addr(ring + stage * Sh::kStageBytes);
+        int32_t flags = flags_next, missing = 0;
+        if (!(flags & kEmpty)) {
+            const uint32_t mask = (1u << a.s.page_shift) - 1;
+            const uint32_t head = (uint32_t)kvh << a.s.page_shift;
+            bool there = page[0] < a.num_pages;
+            if (!one_page) {
+#pragma unroll
+                for (int x = 1; x < SUB; ++x) there &= page[x] < a.num_pages;
+            }
+            if (there && !(flags & kPartial)) {
+                const uint64_t off = (uint64_t)page[0] * a.page_bytes + (head + (key & mask)) * ROWB;
+                copy16(kd, 0, off, 0, 16);
+#pragma unroll
+                for (int x = 1; x < SUB; ++x)
+                    copy16(kd, x,
+                           one_page ? off + 16 * x * ROWB
+                                    : (uint64_t)page[x] * a.page_bytes + (head + ((key + 16 * x) & mask)) * ROWB,
+                           0, 16);
+            } else {
+                flags |= kPartial;
+#pragma unroll
+                for (int x = 0; x < SUB; ++x) {
+                    const int32_t k = key + 16 * x;
+                    const uint32_t p = one_page ? page[0] : page[x];
+                    const int lo = max(rlo - k, 0), hi = min(rhi - k, 16);
+                    if (p < a.num_pages) {
+                        copy16(kd, x, (uint64_t)p * a.page_bytes + (head + (k & mask)) * ROWB, lo, hi);
                     } else {
-                        // rows outside the valid keys are filled with zeros: a weight of 0 must not
-                        // meet a NaN
-#pragma unroll
-                        for (int i = 0; i < PER; ++i) {
-                            const int r = i * (32 / CPR) + r0;
-                            const bool ok = there && key + r >= vlo && key + r < vhi;
-                            const uint32_t to = (16 * x + r) * ROWB + ((ch ^ (r & 7)) << 4);
-                            cp16(kd + to, ok ? ks + i * 512 : a.k_pages, ok ? 16 : 0);
-                            cp16(kd + KS * ROWB + to, ok ? vs16 + i * 512 : a.v_pages, ok ? 16 : 0);
-                        }
-                    }
-                } else if (there) {
-                    // V: 16-byte chunks of a 128-byte line change places with the line's number, so
-                    // that the rows a warp reads at once lie in other banks
-                    const int sw = (lane & 7) ^ (2 * ((lane >> 3) & (D == 128 ? 3 : 1)));
-                    const uint32_t kt = kd + 16 * x * ROWB + lane * 16;
-                    const uint32_t vt = kd + (KS + 16 * x) * ROWB + ((lane & 24) + sw) * 16;
-#pragma unroll
-                    for (int i = 0; i < PER; ++i) {
-                        cp16(kt + i * 512, a.k_pages + off + lane * 16 + i * 512, 16);
-                        cp16(vt + i * 512, a.v_pages + off + lane * 16 + i * 512, 16);
-                    }
-                    constexpr int SC = Sh::kScaleBytes;  // chunks of 16 keys' scales, an eighth of the codes
-                    if (lane < 2 * SC) {
-                        const bool v = lane >= SC;
-                        const int i = v ? lane - SC : lane;
-                        cp16(kd + 2 * KS * ROWB + ((v ? KS : 0) + 16 * x) * Sh::kScaleBytes + i * 16,
-                             (v ? a.v_scales : a.k_scales) + (off >> 3) + i * 16, 16);
+                        missing |= 1 << x;
+                        if (!INT4) copy16(kd, x, 0, 0, 0);
+                        if (lane == 0 && lo < hi) raise_status(a.s.status, kErrPage);
                     }
                 }
             }
-            if (lane == 0)
-                *reinterpret_cast<int4*>(&meta[stage].key0) =
-                    make_int4(next_key, next_flags | missing * kMissing, vlo, vhi);
-        } else if (lane == 0) {
-            *reinterpret_cast<int4*>(&meta[stage].key0) = make_int4(0, next_flags, 0, 0);
         }
-        if (lane == 0 && (next_flags & (kFirst | kLast))) {
+        if (lane == 0 && (flags & (kFirst | kLast | kPartial))) {
             Meta& m = meta[stage];
+            *reinterpret_cast<int4*>(&m.key0) = make_int4(key, rlo, rhi, missing);
             *reinterpret_cast<int4*>(&m.row0) = make_int4(sq.row0, sq.n * a.group, sq.pos0, rb);
             *reinterpret_cast<int2*>(&m.kvh) = make_int2(kvh, slot);
         }
         next();
+        return flags;
     };
 
     next();
     int issued = 0;
+    int32_t queue[S];  // flags of the steps in flight
 #pragma unroll
     for (int i = 0; i < S - 1; ++i) {
+        queue[i] = 0;
         if (more) {
-            issue(i);
+            queue[i] = issue(i);
             ++issued;
         }
         cp_commit();
@@ -448,22 +470,24 @@ __global__ void __launch_bounds__(Shape<D, KIND, NT>::kThreads, Shape<D, KIND, N
     // (4 bits: + 64).
     float o[NT][T][4], m_run[NT][2], shift[NT][2], l_run[NT][2];
     float zs[INT4 ? G : 1][NT][2];     // 4 bits: sums of weight * low
-    float qs[INT4 ? G : 1][NT][2];     // 4 bits: sums of the query's dims of a group
+    uint32_t qs[NT];                   // 4 bits: sums of the query's dims of a group
     uint32_t qf[NT][D / 16][2];
     int32_t pos[NT][2];
-    int32_t full_lo = 0, full_hi = 0;  // keys that every row sees
 
     for (int step = 0, stage = 0; step < issued; ++step, stage = stage + 1 == S ? 0 : stage + 1) {
         cp_wait<S - 2>();
         __syncwarp();  // every lane's copies are in, and the stage before this one is read
+        const int32_t flags = queue[0];
+        queue[S - 1] = 0;
         if (more) {
-            issue(stage == 0 ? S - 1 : stage - 1);
+            queue[S - 1] = issue(stage == 0 ? S - 1 : stage - 1);
             ++issued;
         }
         cp_commit();
+#pragma unroll
+        for (int i = 0; i < S - 1; ++i) queue[i] = queue[i + 1];
         const uint8_t* buf = ring + stage * Sh::kStageBytes;
         const Meta& mt = meta[stage];
-        const int32_t flags = mt.flags;
         if (flags & kFirst) {
             const int32_t row0 = mt.row0, rows = mt.rows, pos0 = mt.pos0, r0 = mt.rb * R;
 #pragma unroll
@@ -488,6 +512,7 @@ __global__ void __launch_bounds__(Shape<D, KIND, NT>::kThreads, Shape<D, KIND, N
                             qf[nt][ks][e] =
                                 live ? __ldg(reinterpret_cast<const uint32_t*>(q + 16 * ks + 8 * e + 2 * c)) : 0u;
                 } else {
+                    qs[nt] = 0;
                     // the dims in the order in which the codes of a row come out of their words
 #pragma unroll
                     for (int gr = 0; gr < G; ++gr) {
@@ -507,8 +532,13 @@ __global__ void __launch_bounds__(Shape<D, KIND, NT>::kThreads, Shape<D, KIND, N
                         sum += __shfl_xor_sync(0xffffffffu, sum, 1);
                         sum += __shfl_xor_sync(0xffffffffu, sum, 2);
                         sum *= 1.f / kUp69;
-                        qs[gr][nt][0] = __shfl_sync(0xffffffffu, sum, 8 * c);
-                        qs[gr][nt][1] = __shfl_sync(0xffffffffu, sum, 8 * c + 4);
+                        // in three bf16 parts that add up to fp32's bits, one for each of c = 0, 1, 2
+#pragma unroll
+                        for (int i = 0; i < 3; ++i) {
+                            const float part = __bfloat162float(__float2bfloat16_rn(sum));
+                            if (c == i) qs[nt] |= (__float_as_uint(part) >> 16) << (16 * gr);
+                            sum -= part;
+                        }
                         zs[gr][nt][0] = zs[gr][nt][1] = 0.f;
                     }
                 }
@@ -516,15 +546,17 @@ __global__ void __launch_bounds__(Shape<D, KIND, NT>::kThreads, Shape<D, KIND, N
                 for (int e = 0; e < 2; ++e)
                     pos[nt][e] = pos0 + min(r0 + 8 * nt + 2 * c + e, rows - 1) / a.group;
             }
-            full_hi = pos0 + r0 / a.group;
-            full_lo = a.window > 0
-                          ? (int32_t)max((int64_t)pos0 + min(r0 + R - 1, rows - 1) / a.group - a.window + 1,
-                                         (int64_t)0)
-                          : 0;
         }
         if (!(flags & kEmpty)) {
-            const int32_t key0 = mt.key0, vlo = mt.vlo, vhi = mt.vhi, missing = flags / kMissing;
-            const bool partial = key0 < max(full_lo, vlo) || key0 + KS > min(full_hi + 1, vhi) || missing;
+            const bool partial = flags & kPartial;
+            int32_t key0 = 0, vlo = 0, vhi = 0, missing = 0;
+            if (partial) {
+                const int4 m = *reinterpret_cast<const int4*>(&mt.key0);
+                key0 = m.x;
+                vlo = m.y;
+                vhi = m.z;
+                missing = m.w;
+            }
             const uint32_t kb = smem_addr(buf), vb = kb + KS * ROWB;
             float s[SUB][NT][4];
             // ---- S^T
@@ -582,20 +614,23 @@ __global__ void __launch_bounds__(Shape<D, KIND, NT>::kThreads, Shape<D, KIND, N
                                 }
                             }
                     }
-                    // s = sum over groups of scale * (q . codes) + low * (sum of q)
+                    // s = sum over groups of scale * (q . codes) + low * (sum of q); the second by one
+                    // more product, of the lows of a key with the parts of the sums
+                    const uint32_t lows[4] = {G == 2 ? __byte_perm(sc[0][0], sc[0][G - 1], 0x7632) : sc[0][0] >> 16,
+                                              G == 2 ? __byte_perm(sc[1][0], sc[1][G - 1], 0x7632) : sc[1][0] >> 16,
+                                              0u, 0u};
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) mma0(s[x][nt], lows, qs[nt], 0u);
 #pragma unroll
                     for (int y = 0; y < 2; ++y)
 #pragma unroll
                         for (int gr = 0; gr < G; ++gr) {
-                            const float scl = lo_f(sc[y][gr]), low = hi_f(sc[y][gr]);
+                            const float scl = lo_f(sc[y][gr]);
 #pragma unroll
                             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                                for (int e = 0; e < 2; ++e) {
-                                    const float z = gr == 0 ? low * qs[gr][nt][e]
-                                                            : fmaf(low, qs[gr][nt][e], s[x][nt][2 * y + e]);
-                                    s[x][nt][2 * y + e] = fmaf(scl, acc[gr][nt][2 * y + e], z);
-                                }
+                                for (int e = 0; e < 2; ++e)
+                                    s[x][nt][2 * y + e] = fmaf(scl, acc[gr][nt][2 * y + e], s[x][nt][2 * y + e]);
                         }
                 }
             }
@@ -834,7 +869,7 @@ __global__ void __launch_bounds__(Shape<D, KIND, NT>::kThreads, Shape<D, KIND, N
                     int dim;
                     if (!INT4 || JT >= 4) dim = 16 * t0 + d4;
                     else dim = 64 * (t0 / 4) + 8 * (d4 / (2 * JT)) + 2 * (t0 % 4) + d4 % (2 * JT);
-                    if (mt.flags & kWhole) {
+                    if (flags & kWhole) {
                         const int32_t tok = (r0 + r) / a.group;
                         const int32_t h = mt.kvh * a.group + (r0 + r) - tok * a.group;
                         const int64_t at = ((int64_t)(mt.row0 + tok) * a.hq + h) * D + dim;
@@ -1031,8 +1066,9 @@ extern "C" pva_status pva_cache_attn(const pva_cache_desc* cache, const pva_cach
         return PVA_ERR_BUFFER_TOO_SMALL;
     if (batch->num_tokens > INT32_MAX / num_q_heads) return PVA_ERR_UNSUPPORTED;
     a.q = reinterpret_cast<const __nv_bfloat16*>(q);
-    a.k_pages = reinterpret_cast<const uint8_t*>(cache->k_pages);
-    a.v_pages = reinterpret_cast<const uint8_t*>(cache->v_pages);
+    // (a copy of no bytes still names an address)
+    a.k_pages = reinterpret_cast<const uint8_t*>(cache->num_pages > 0 ? cache->k_pages : q);
+    a.v_pages = reinterpret_cast<const uint8_t*>(cache->num_pages > 0 ? cache->v_pages : q);
     a.k_scales = reinterpret_cast<const uint8_t*>(cache->k_scales);
     a.v_scales = reinterpret_cast<const uint8_t*>(cache->v_scales);
     a.out = out;
@@ -1053,6 +1089,7 @@ extern "C" pva_status pva_cache_attn(const pva_cache_desc* cache, const pva_cach
         (int64_t)cache->num_kv_heads * cache->page_size * (cache->kind == PVA_CACHE_INT4 ? d / 2 : 2 * d);
     if (page_bytes > INT32_MAX) return PVA_ERR_UNSUPPORTED;
     a.page_bytes = (uint32_t)page_bytes;
+    a.num_pages = (uint32_t)cache->num_pages;
     // Without offsets every sequence has one row, whatever bound was given.
     const int nt = tiles_of((int64_t)a.group * max_new);
     uint8_t* ws = reinterpret_cast<uint8_t*>(workspace);
