@@ -57,14 +57,15 @@ struct AttnArgs {
 };
 
 // Shape of a variant: warps a CTA, keys a step, ring stages, columns of the join buffer.
-template <int D, int KIND, int NT>
+template <int D, int KIND, int NT, bool H>
 struct Shape {
     static constexpr bool kInt4 = KIND == PVA_CACHE_INT4;
     static constexpr int kWarps = 4;
-    static constexpr int kKeys = (kInt4 ? 32 : 16) * (128 / D);
-    static constexpr int kStages = 3;
-    static constexpr int kCtas = kInt4 && NT == 1 ? 3 : 2;  // resident on an SM
-    static constexpr int R = 8 * NT;
+    static constexpr int kKeys = kInt4 ? (NT == 1 ? 64 : 32 * (128 / D)) : 16 * (128 / D);
+    static constexpr int kStages = kInt4 && NT == 1 ? 2 : 3;
+    static constexpr int kCtas = 2;          // resident on an SM
+    static constexpr int kCols = 8 * NT;     // columns of S^T
+    static constexpr int R = H ? 4 : kCols;  // rows of an item
     static constexpr int kThreads = 32 * kWarps;
     static constexpr int kBlock = kWarps * kKeys;  // keys of a unit
     static constexpr int kRowBytes = kInt4 ? D / 2 : 2 * D;
@@ -79,7 +80,7 @@ struct Shape {
     static constexpr int kJoinPitch = kJoinDims + 4;
     static constexpr int kRing = kWarps * kStages * kStageBytes;
     static constexpr int kMeta = kWarps * kStages * 48;
-    static constexpr int kJoin = kWarps * R * (kJoinPitch + 2) * 4;
+    static constexpr int kJoin = kWarps * kCols * (kJoinPitch + 2) * 4;
     static constexpr int kSmem = kRing + kMeta + kJoin;
 };
 
@@ -201,11 +202,13 @@ struct Meta {
     int32_t kvh, slot, pad[2];
 };
 
-template <int D, int KIND, int NT>
-__global__ void __launch_bounds__(Shape<D, KIND, NT>::kThreads, Shape<D, KIND, NT>::kCtas)
+template <int D, int KIND, int NT, bool H>
+__global__ void __launch_bounds__(Shape<D, KIND, NT, H>::kThreads, Shape<D, KIND, NT, H>::kCtas)
     attn_kernel(const AttnArgs a) {
-    using Sh = Shape<D, KIND, NT>;
+    using Sh = Shape<D, KIND, NT, H>;
     constexpr int R = Sh::R, W = Sh::kWarps, KS = Sh::kKeys, S = Sh::kStages, SUB = KS / 16;
+    constexpr int HN = H ? 2 : 1, ST = SUB / HN;  // tiles of keys that share the columns, sets of scores
+    constexpr int C = Sh::kCols;
     constexpr int G = Sh::kGroups, T = Sh::kTiles, BLOCK = Sh::kBlock, ROWB = Sh::kRowBytes;
     constexpr bool INT4 = Sh::kInt4;
     extern __shared__ __align__(128) uint8_t smem[];
@@ -214,9 +217,9 @@ __global__ void __launch_bounds__(Shape<D, KIND, NT>::kThreads, Shape<D, KIND, N
     uint8_t* ring = smem + warp * S * Sh::kStageBytes;
     Meta* meta = reinterpret_cast<Meta*>(smem + Sh::kRing) + warp * S;
     uint8_t* tail = smem + Sh::kRing + Sh::kMeta;
-    float* join_o = reinterpret_cast<float*>(tail);             // [W][R][kJoinPitch]
-    float* join_m = join_o + W * R * Sh::kJoinPitch;            // [W][R]
-    float* join_l = join_m + W * R;                             // [W][R]
+    float* join_o = reinterpret_cast<float*>(tail);             // [W][C][kJoinPitch]
+    float* join_m = join_o + W * C * Sh::kJoinPitch;            // [W][C]
+    float* join_l = join_m + W * C;                             // [W][C]
 
     // ---- plan: this CTA's piece [u0, u1) of the line and the sequence it starts in.
     // Every thread sums a run of sequences; a scan over the threads gives each run's
@@ -470,9 +473,32 @@ __global__ void __launch_bounds__(Shape<D, KIND, NT>::kThreads, Shape<D, KIND, N
     // (4 bits: + 64).
     float o[NT][T][4], m_run[NT][2], shift[NT][2], l_run[NT][2];
     float zs[INT4 ? G : 1][NT][2];     // 4 bits: sums of weight * low
-    uint32_t qs[NT];                   // 4 bits: sums of the query's dims of a group
-    uint32_t qf[NT][D / 16][2];
+    uint32_t qs[HN][NT];                 // 4 bits: sums of the query's dims of a group
+    uint32_t qf[HN][NT][D / 16][2];
     int32_t pos[NT][2];
+
+    // (scale, low) of a tile's keys g and g + 8
+    auto scales = [&](uint32_t (&sc)[2][G], const uint8_t* at) {
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+            if (D == 128) {
+                const uint2 z = *reinterpret_cast<const uint2*>(at + 8 * y * Sh::kScaleBytes);
+                sc[y][0] = z.x;
+                sc[y][G - 1] = z.y;
+            } else {
+                sc[y][0] = *reinterpret_cast<const uint32_t*>(at + 8 * y * Sh::kScaleBytes);
+            }
+        }
+    };
+
+    // a slot of no token may hold anything: nothing of it goes into a product
+    auto no_token = [&](uint32_t (&sc)[2][G], int32_t j, int32_t vlo, int32_t vhi, bool missing) {
+#pragma unroll
+        for (int y = 0; y < 2; ++y)
+#pragma unroll
+            for (int gr = 0; gr < G; ++gr)
+                sc[y][gr] = missing || j + 8 * y < vlo || j + 8 * y >= vhi ? 0u : sc[y][gr];
+    };
 
     for (int step = 0, stage = 0; step < issued; ++step, stage = stage + 1 == S ? 0 : stage + 1) {
         cp_wait<S - 2>();
@@ -499,7 +525,7 @@ __global__ void __launch_bounds__(Shape<D, KIND, NT>::kThreads, Shape<D, KIND, N
                 m_run[nt][0] = m_run[nt][1] = -INFINITY;
                 shift[nt][0] = shift[nt][1] = 0.f;
                 l_run[nt][0] = l_run[nt][1] = 0.f;
-                const int32_t r = r0 + 8 * nt + g;
+                const int32_t r = r0 + (H ? g & 3 : 8 * nt + g);
                 const int32_t tok = r / a.group;
                 const __nv_bfloat16* q = a.q + (int64_t)(row0 + tok) * a.q_stride +
                                          (int64_t)(mt.kvh * a.group + r - tok * a.group) * D;
@@ -509,23 +535,29 @@ __global__ void __launch_bounds__(Shape<D, KIND, NT>::kThreads, Shape<D, KIND, N
                     for (int ks = 0; ks < D / 16; ++ks)
 #pragma unroll
                         for (int e = 0; e < 2; ++e)
-                            qf[nt][ks][e] =
+                            qf[0][nt][ks][e] =
                                 live ? __ldg(reinterpret_cast<const uint32_t*>(q + 16 * ks + 8 * e + 2 * c)) : 0u;
                 } else {
-                    qs[nt] = 0;
+#pragma unroll
+                    for (int hh = 0; hh < HN; ++hh) qs[hh][nt] = 0;
                     // the dims in the order in which the codes of a row come out of their words
 #pragma unroll
                     for (int gr = 0; gr < G; ++gr) {
                         float sum = 0.f;
 #pragma unroll
                         for (int oc = 0; oc < 2; ++oc) {
+                            constexpr float kUp60 = kUp64 / 16.f;  // meets 16 * code
                             const uint4 x = live ? __ldg(reinterpret_cast<const uint4*>(q + 64 * gr + 16 * c + 8 * oc))
                                                  : make_uint4(0, 0, 0, 0);
-                            constexpr float kUp60 = kUp64 / 16.f;  // meets 16 * code
-                            qf[nt][4 * gr + 2 * oc][0] = pack2(lo_f(x.x) * kUp64, hi_f(x.x) * kUp64);
-                            qf[nt][4 * gr + 2 * oc][1] = pack2(lo_f(x.y) * kUp60, hi_f(x.y) * kUp60);
-                            qf[nt][4 * gr + 2 * oc + 1][0] = pack2(lo_f(x.z) * kUp64, hi_f(x.z) * kUp64);
-                            qf[nt][4 * gr + 2 * oc + 1][1] = pack2(lo_f(x.w) * kUp60, hi_f(x.w) * kUp60);
+                            const uint32_t y[4] = {pack2(lo_f(x.x) * kUp64, hi_f(x.x) * kUp64),
+                                                   pack2(lo_f(x.y) * kUp60, hi_f(x.y) * kUp60),
+                                                   pack2(lo_f(x.z) * kUp64, hi_f(x.z) * kUp64),
+                                                   pack2(lo_f(x.w) * kUp60, hi_f(x.w) * kUp60)};
+#pragma unroll
+                            for (int hh = 0; hh < HN; ++hh)
+#pragma unroll
+                                for (int i = 0; i < 4; ++i)
+                                    qf[hh][nt][4 * gr + 2 * oc + i / 2][i % 2] = !H || (g >> 2) == hh ? y[i] : 0u;
                             sum += ((lo_f(x.x) + hi_f(x.x)) + (lo_f(x.y) + hi_f(x.y))) +
                                    ((lo_f(x.z) + hi_f(x.z)) + (lo_f(x.w) + hi_f(x.w)));
                         }
@@ -536,7 +568,10 @@ __global__ void __launch_bounds__(Shape<D, KIND, NT>::kThreads, Shape<D, KIND, N
 #pragma unroll
                         for (int i = 0; i < 3; ++i) {
                             const float part = __bfloat162float(__float2bfloat16_rn(sum));
-                            if (c == i) qs[nt] |= (__float_as_uint(part) >> 16) << (16 * gr);
+#pragma unroll
+                            for (int hh = 0; hh < HN; ++hh)
+                                if (c == i && (!H || (g >> 2) == hh))
+                                    qs[hh][nt] |= (__float_as_uint(part) >> 16) << (16 * gr);
                             sum -= part;
                         }
                         zs[gr][nt][0] = zs[gr][nt][1] = 0.f;
@@ -544,7 +579,7 @@ __global__ void __launch_bounds__(Shape<D, KIND, NT>::kThreads, Shape<D, KIND, N
                 }
 #pragma unroll
                 for (int e = 0; e < 2; ++e)
-                    pos[nt][e] = pos0 + min(r0 + 8 * nt + 2 * c + e, rows - 1) / a.group;
+                    pos[nt][e] = pos0 + min(r0 + (H ? (2 * c + e) & 3 : 8 * nt + 2 * c + e), rows - 1) / a.group;
             }
         }
         if (!(flags & kEmpty)) {
@@ -558,94 +593,115 @@ __global__ void __launch_bounds__(Shape<D, KIND, NT>::kThreads, Shape<D, KIND, N
                 missing = m.w;
             }
             const uint32_t kb = smem_addr(buf), vb = kb + KS * ROWB;
-            float s[SUB][NT][4];
+            // Set z of scores: tile z of 16 keys; with H tile 2z in columns 0 .. 3 and tile 2z + 1 in
+            // columns 4 .. 7, so that up to four rows leave no column of the softmax empty.  This
+            // lane's columns belong to tile HN * z + mine.
+            float s[ST][NT][4];
+            uint32_t own_sc[INT4 ? ST : 1][2][G];
+            const int mine = H ? c >> 1 : 0;
             // ---- S^T
 #pragma unroll
-            for (int x = 0; x < SUB; ++x) {
+            for (int z = 0; z < ST; ++z) {
                 if (!INT4) {
 #pragma unroll
                     for (int ks = 0; ks < D / 16; ++ks) {
                         uint32_t f[4];
                         const int r = lane & 15, ch = 2 * ks + (lane >> 4);
-                        ldsm(f, kb + (16 * x + r) * ROWB + ((ch ^ (r & 7)) << 4));
+                        ldsm(f, kb + (16 * z + r) * ROWB + ((ch ^ (r & 7)) << 4));
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
-                            if (ks == 0) mma0(s[x][nt], f, qf[nt][ks][0], qf[nt][ks][1]);
-                            else mma(s[x][nt], f, qf[nt][ks][0], qf[nt][ks][1]);
+                            if (ks == 0) mma0(s[z][nt], f, qf[0][nt][ks][0], qf[0][nt][ks][1]);
+                            else mma(s[z][nt], f, qf[0][nt][ks][0], qf[0][nt][ks][1]);
                         }
                     }
                 } else {
-                    uint32_t w[2][2 * G], sc[2][G];
-                    const uint8_t* kr = buf + (16 * x + g) * ROWB + c * (ROWB / 4);
-                    const uint8_t* sr = buf + 2 * KS * ROWB + (16 * x + g) * Sh::kScaleBytes;
-#pragma unroll
-                    for (int y = 0; y < 2; ++y) {
-                        if (D == 128) {
-                            const uint4 v = *reinterpret_cast<const uint4*>(kr + 8 * y * ROWB);
-                            w[y][0] = v.x;
-                            w[y][1] = v.y;
-                            w[y][2 * G - 2] = v.z;
-                            w[y][2 * G - 1] = v.w;
-                            const uint2 z = *reinterpret_cast<const uint2*>(sr + 8 * y * Sh::kScaleBytes);
-                            sc[y][0] = z.x;
-                            sc[y][G - 1] = z.y;
-                        } else {
-                            const uint2 v = *reinterpret_cast<const uint2*>(kr + 8 * y * ROWB);
-                            w[y][0] = v.x;
-                            w[y][1] = v.y;
-                            sc[y][0] = *reinterpret_cast<const uint32_t*>(sr + 8 * y * Sh::kScaleBytes);
-                        }
-                    }
                     float acc[G][NT][4];
 #pragma unroll
-                    for (int gr = 0; gr < G; ++gr) {
+                    for (int hh = 0; hh < HN; ++hh) {
+                        const int x = HN * z + hh;
+                        uint32_t w[2][2 * G], sc[2][G];
+                        const uint8_t* kr = buf + (16 * x + g) * ROWB + c * (ROWB / 4);
 #pragma unroll
-                        for (int oc = 0; oc < 2; ++oc)
-#pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                const uint32_t w0 = w[0][G * oc + gr] >> (8 * h), w1 = w[1][G * oc + gr] >> (8 * h);
-                                const uint32_t f[4] = {low_codes(w0), low_codes(w1), high_codes(w0),
-                                                       high_codes(w1)};
-#pragma unroll
-                                for (int nt = 0; nt < NT; ++nt) {
-                                    const uint32_t* q2 = qf[nt][4 * gr + 2 * oc + h];
-                                    if (oc == 0 && h == 0) mma0(acc[gr][nt], f, q2[0], q2[1]);
-                                    else mma(acc[gr][nt], f, q2[0], q2[1]);
-                                }
+                        for (int y = 0; y < 2; ++y) {
+                            if (D == 128) {
+                                const uint4 v = *reinterpret_cast<const uint4*>(kr + 8 * y * ROWB);
+                                w[y][0] = v.x;
+                                w[y][1] = v.y;
+                                w[y][2 * G - 2] = v.z;
+                                w[y][2 * G - 1] = v.w;
+                            } else {
+                                const uint2 v = *reinterpret_cast<const uint2*>(kr + 8 * y * ROWB);
+                                w[y][0] = v.x;
+                                w[y][1] = v.y;
                             }
-                    }
-                    // s = sum over groups of scale * (q . codes) + low * (sum of q); the second by one
-                    // more product, of the lows of a key with the parts of the sums
-                    const uint32_t lows[4] = {G == 2 ? __byte_perm(sc[0][0], sc[0][G - 1], 0x7632) : sc[0][0] >> 16,
-                                              G == 2 ? __byte_perm(sc[1][0], sc[1][G - 1], 0x7632) : sc[1][0] >> 16,
-                                              0u, 0u};
+                        }
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) mma0(s[x][nt], lows, qs[nt], 0u);
+                        for (int gr = 0; gr < G; ++gr)
+#pragma unroll
+                            for (int oc = 0; oc < 2; ++oc)
+#pragma unroll
+                                for (int h = 0; h < 2; ++h) {
+                                    const uint32_t w0 = w[0][G * oc + gr] >> (8 * h), w1 = w[1][G * oc + gr] >> (8 * h);
+                                    const uint32_t f[4] = {low_codes(w0), low_codes(w1), high_codes(w0),
+                                                           high_codes(w1)};
+#pragma unroll
+                                    for (int nt = 0; nt < NT; ++nt) {
+                                        const uint32_t* q2 = qf[hh][nt][4 * gr + 2 * oc + h];
+                                        if (hh == 0 && oc == 0 && h == 0) mma0(acc[gr][nt], f, q2[0], q2[1]);
+                                        else mma(acc[gr][nt], f, q2[0], q2[1]);
+                                    }
+                                }
+                        // s = sum over groups of scale * (q . codes) + low * (sum of q); the second by
+                        // one more product, of the lows of a key with the parts of the sums
+                        scales(sc, buf + 2 * KS * ROWB + (16 * x + g) * Sh::kScaleBytes);
+                        if (partial) no_token(sc, key0 + 16 * x + g, vlo, vhi, missing >> x & 1);
+                        const uint32_t lows[4] = {G == 2 ? __byte_perm(sc[0][0], sc[0][G - 1], 0x7632) : sc[0][0] >> 16,
+                                                  G == 2 ? __byte_perm(sc[1][0], sc[1][G - 1], 0x7632) : sc[1][0] >> 16,
+                                                  0u, 0u};
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            if (hh == 0) mma0(s[z][nt], lows, qs[hh][nt], 0u);
+                            else mma(s[z][nt], lows, qs[hh][nt], 0u);
+                        }
+                        if (H && hh == 0) {
+                            own_sc[z][0][0] = sc[0][0];
+                            own_sc[z][0][G - 1] = sc[0][G - 1];
+                            own_sc[z][1][0] = sc[1][0];
+                            own_sc[z][1][G - 1] = sc[1][G - 1];
+                        } else {
+#pragma unroll
+                            for (int y = 0; y < 2; ++y)
+#pragma unroll
+                                for (int gr = 0; gr < G; ++gr)
+                                    own_sc[z][y][gr] = !H || mine ? sc[y][gr] : own_sc[z][y][gr];
+                        }
+                    }
 #pragma unroll
                     for (int y = 0; y < 2; ++y)
 #pragma unroll
                         for (int gr = 0; gr < G; ++gr) {
-                            const float scl = lo_f(sc[y][gr]);
+                            const float scl = lo_f(own_sc[z][y][gr]);
 #pragma unroll
                             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                                 for (int e = 0; e < 2; ++e)
-                                    s[x][nt][2 * y + e] = fmaf(scl, acc[gr][nt][2 * y + e], s[x][nt][2 * y + e]);
+                                    s[z][nt][2 * y + e] = fmaf(scl, acc[gr][nt][2 * y + e], s[z][nt][2 * y + e]);
                         }
                 }
             }
             // ---- masks; has a score left the range of the running maximum?
             if (partial) {
 #pragma unroll
-                for (int x = 0; x < SUB; ++x)
+                for (int z = 0; z < ST; ++z)
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
+                            const int x = HN * z + mine;
                             const int32_t j = key0 + 16 * x + g + 8 * (e >> 1), p = pos[nt][e & 1];
                             const bool ok = j >= vlo && j < vhi && j <= p && !(missing >> x & 1) &&
                                             (a.window <= 0 || p - j < a.window);
-                            s[x][nt][e] = ok ? s[x][nt][e] : -INFINITY;
+                            s[z][nt][e] = ok ? s[z][nt][e] : -INFINITY;
                         }
             }
             bool up = false;
@@ -656,8 +712,8 @@ __global__ void __launch_bounds__(Shape<D, KIND, NT>::kThreads, Shape<D, KIND, N
                 for (int e = 0; e < 2; ++e) {
                     mx[nt][e] = fmaxf(s[0][nt][e], s[0][nt][2 + e]);
 #pragma unroll
-                    for (int x = 1; x < SUB; ++x)
-                        mx[nt][e] = fmaxf(mx[nt][e], fmaxf(s[x][nt][e], s[x][nt][2 + e]));
+                    for (int z = 1; z < ST; ++z)
+                        mx[nt][e] = fmaxf(mx[nt][e], fmaxf(s[z][nt][e], s[z][nt][2 + e]));
                     up |= mx[nt][e] > m_run[nt][e] + a.slack;
                 }
             if (__any_sync(0xffffffffu, up)) {
@@ -686,109 +742,102 @@ __global__ void __launch_bounds__(Shape<D, KIND, NT>::kThreads, Shape<D, KIND, N
             }
             // ---- weights and O^T
 #pragma unroll
-            for (int x = 0; x < SUB; ++x) {
+            for (int z = 0; z < ST; ++z) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        s[x][nt][e] = ex2(fmaf(s[x][nt][e], a.c, shift[nt][e & 1]));
-                        l_run[nt][e & 1] += s[x][nt][e];
+                        s[z][nt][e] = ex2(fmaf(s[z][nt][e], a.c, shift[nt][e & 1]));
+                        l_run[nt][e & 1] += s[z][nt][e];
                     }
                 if (!INT4) {
-                    // the weights meet bf16 values in a bf16 product: one rounding of 2^-9
+                    // the weights meet bf16 values in a bf16 product: one rounding, 2^-8 of a weight
                     uint32_t p[NT][2];
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
-                        p[nt][0] = transpose8(pack2(s[x][nt][0], s[x][nt][1]));
-                        p[nt][1] = transpose8(pack2(s[x][nt][2], s[x][nt][3]));
+                        p[nt][0] = transpose8(pack2(s[z][nt][0], s[z][nt][1]));
+                        p[nt][1] = transpose8(pack2(s[z][nt][2], s[z][nt][3]));
                     }
 #pragma unroll
                     for (int i = 0; i < T; ++i) {
                         uint32_t f[4];
                         const int r = (lane & 7) + ((lane >> 4) << 3), ch = 2 * i + ((lane >> 3) & 1);
-                        ldsm_t(f, vb + (16 * x + r) * ROWB + ((ch ^ (r & 7)) << 4));
+                        ldsm_t(f, vb + (16 * z + r) * ROWB + ((ch ^ (r & 7)) << 4));
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) mma(o[nt][i], f, p[nt][0], p[nt][1]);
                     }
                 } else {
                     // weight * scale meets the codes, rounded to bf16 once; weight * low stays in fp32
                     uint32_t sc[2][G], p[G][NT][2];
-                    const uint8_t* sr =
-                        buf + 2 * KS * ROWB + (KS + 16 * x + g) * Sh::kScaleBytes;
-#pragma unroll
-                    for (int y = 0; y < 2; ++y) {
-                        if (D == 128) {
-                            const uint2 z = *reinterpret_cast<const uint2*>(sr + 8 * y * Sh::kScaleBytes);
-                            sc[y][0] = z.x;
-                            sc[y][G - 1] = z.y;
-                        } else {
-                            sc[y][0] = *reinterpret_cast<const uint32_t*>(sr + 8 * y * Sh::kScaleBytes);
-                        }
-                        if (partial) {  // a slot of no token may hold anything: its weight is 0
-                            const int32_t j = key0 + 16 * x + g + 8 * y;
-                            if (j < vlo || j >= vhi || (missing >> x & 1)) {
-#pragma unroll
-                                for (int gr = 0; gr < G; ++gr) sc[y][gr] = 0;
-                            }
-                        }
-                    }
+                    const int own_x = HN * z + mine;
+                    scales(sc, buf + 2 * KS * ROWB + (KS + 16 * own_x + g) * Sh::kScaleBytes);
+                    if (partial) no_token(sc, key0 + 16 * own_x + g, vlo, vhi, missing >> own_x & 1);
 #pragma unroll
                     for (int gr = 0; gr < G; ++gr)
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) {
+                        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                             for (int y = 0; y < 2; ++y) {
                                 const float scl = lo_f(sc[y][gr]), low = hi_f(sc[y][gr]);
                                 p[gr][nt][y] = transpose8(
-                                    pack2(s[x][nt][2 * y] * scl, s[x][nt][2 * y + 1] * scl));
-                                zs[gr][nt][0] = fmaf(s[x][nt][2 * y], low, zs[gr][nt][0]);
-                                zs[gr][nt][1] = fmaf(s[x][nt][2 * y + 1], low, zs[gr][nt][1]);
-                            }
-                        }
-                    uint32_t w[4][G];  // keys 2c, 2c + 1, 2c + 8, 2c + 9
-#pragma unroll
-                    for (int y = 0; y < 4; ++y) {
-                        const int r = 16 * x + 2 * c + (y & 1) + 8 * (y >> 1);
-                        if (D == 128) {
-                            const int line = r >> 1, at = ((r & 1) * 4 + (g >> 1)) ^ (2 * (line & 3));
-                            const uint2 z = *reinterpret_cast<const uint2*>(
-                                buf + KS * ROWB + line * 128 + at * 16 + (g & 1) * 8);
-                            w[y][0] = z.x;
-                            w[y][G - 1] = z.y;
-                        } else {
-                            const int line = r >> 2, at = ((r & 3) * 2 + (g >> 2)) ^ (2 * (line & 1));
-                            w[y][0] = *reinterpret_cast<const uint32_t*>(
-                                buf + KS * ROWB + line * 128 + at * 16 + (g & 3) * 4);
-                        }
-                    }
-#pragma unroll
-                    for (int gr = 0; gr < G; ++gr) {
-                        // the even dims of two keys in one word, and the odd ones; halves e hold
-                        // keys 2c (+8) and 2c + 1 (+8)
-                        const uint32_t v[4] = {__byte_perm(w[0][gr], w[1][gr], 0x5410),
-                                               __byte_perm(w[0][gr], w[1][gr], 0x7632),
-                                               __byte_perm(w[2][gr], w[3][gr], 0x5410),
-                                               __byte_perm(w[2][gr], w[3][gr], 0x7632)};
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            // tile 2h: the lower code of a byte; tile 2h + 1: the whole byte, from which
-                            // the lower code is taken off again at the item's end
-                            uint32_t f[4], lo[4];
-#pragma unroll
-                            for (int y = 0; y < 4; ++y) {
-                                f[y] = h == 0 ? both_codes(v[y]) : upper_bytes(v[y]);
-                                lo[y] = low_codes(f[y]);
+                                    pack2(s[z][nt][2 * y] * scl, s[z][nt][2 * y + 1] * scl));
+                                zs[gr][nt][0] = fmaf(s[z][nt][2 * y], low, zs[gr][nt][0]);
+                                zs[gr][nt][1] = fmaf(s[z][nt][2 * y + 1], low, zs[gr][nt][1]);
                             }
 #pragma unroll
-                            for (int nt = 0; nt < NT; ++nt) {
-                                mma(o[nt][4 * gr + 2 * h], lo, p[gr][nt][0], p[gr][nt][1]);
-                                mma(o[nt][4 * gr + 2 * h + 1], f, p[gr][nt][0], p[gr][nt][1]);
+                    for (int hh = 0; hh < HN; ++hh) {
+                        const int x = HN * z + hh;
+                        uint32_t w[4][G];  // keys 2c, 2c + 1, 2c + 8, 2c + 9
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) {
+                            const int r = 16 * x + 2 * c + (y & 1) + 8 * (y >> 1);
+                            if (D == 128) {
+                                const int line = r >> 1, at = ((r & 1) * 4 + (g >> 1)) ^ (2 * (line & 3));
+                                const uint2 v = *reinterpret_cast<const uint2*>(
+                                    buf + KS * ROWB + line * 128 + at * 16 + (g & 1) * 8);
+                                w[y][0] = v.x;
+                                w[y][G - 1] = v.y;
+                            } else {
+                                const int line = r >> 2, at = ((r & 3) * 2 + (g >> 2)) ^ (2 * (line & 1));
+                                w[y][0] = *reinterpret_cast<const uint32_t*>(
+                                    buf + KS * ROWB + line * 128 + at * 16 + (g & 3) * 4);
+                            }
+                        }
+#pragma unroll
+                        for (int gr = 0; gr < G; ++gr) {
+                            // the even dims of two keys in one word, and the odd ones
+                            const uint32_t v[4] = {__byte_perm(w[0][gr], w[1][gr], 0x5410),
+                                                   __byte_perm(w[0][gr], w[1][gr], 0x7632),
+                                                   __byte_perm(w[2][gr], w[3][gr], 0x5410),
+                                                   __byte_perm(w[2][gr], w[3][gr], 0x7632)};
+                            uint32_t b[NT][2];  // with H: the columns of this tile
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                                for (int y = 0; y < 2; ++y)
+                                    b[nt][y] = !H || (g >> 2) == hh ? p[gr][nt][y] : 0u;
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                // tile 2h: the lower code of a byte; tile 2h + 1: the whole byte, from
+                                // which the lower code is taken off again at the item's end
+                                uint32_t f[4], lo[4];
+#pragma unroll
+                                for (int y = 0; y < 4; ++y) {
+                                    f[y] = h == 0 ? both_codes(v[y]) : upper_bytes(v[y]);
+                                    lo[y] = low_codes(f[y]);
+                                }
+#pragma unroll
+                                for (int nt = 0; nt < NT; ++nt) {
+                                    mma(o[nt][4 * gr + 2 * h], lo, b[nt][0], b[nt][1]);
+                                    mma(o[nt][4 * gr + 2 * h + 1], f, b[nt][0], b[nt][1]);
+                                }
                             }
                         }
                     }
                 }
             }
         }
+
         // ---- the item's end: the warps' sums are joined
         if (flags & kLast) {
             const int32_t r0 = mt.rb * R;
@@ -829,8 +878,8 @@ __global__ void __launch_bounds__(Shape<D, KIND, NT>::kThreads, Shape<D, KIND, N
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
-                            join_m[warp * R + 8 * nt + 2 * c + e] = m_run[nt][e];
-                            join_l[warp * R + 8 * nt + 2 * c + e] = l_run[nt][e];
+                            join_m[warp * C + 8 * nt + 2 * c + e] = m_run[nt][e];
+                            join_l[warp * C + 8 * nt + 2 * c + e] = l_run[nt][e];
                         }
                 }
 #pragma unroll
@@ -843,7 +892,7 @@ __global__ void __launch_bounds__(Shape<D, KIND, NT>::kThreads, Shape<D, KIND, N
                             // 8g + 2i, 8g + 2i + 1 of its group
                             const int at = INT4 ? g * 2 * (JT < 4 ? JT : 4) + 2 * (i % 4) + (e >> 1) + (i / 4) * 64
                                                 : 16 * i + g + 8 * (e >> 1);
-                            join_o[(warp * R + 8 * nt + 2 * c + (e & 1)) * JP + at] = o[nt][t0 + i][e];
+                            join_o[(warp * C + 8 * nt + 2 * c + (e & 1)) * JP + at] = o[nt][t0 + i][e];
                         }
                 __syncthreads();
                 for (int idx = tid; idx < R * (JD / 4); idx += Sh::kThreads) {
@@ -851,15 +900,15 @@ __global__ void __launch_bounds__(Shape<D, KIND, NT>::kThreads, Shape<D, KIND, N
                     if (r0 + r >= mt.rows) continue;
                     float mm = -INFINITY;
 #pragma unroll
-                    for (int w = 0; w < W; ++w) mm = fmaxf(mm, join_m[w * R + r]);
+                    for (int w = 0; w < W * HN; ++w) mm = fmaxf(mm, join_m[w * (C / HN) + r]);
                     float l = 0.f;
                     float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-                    for (int w = 0; w < W; ++w) {
-                        const float mw = join_m[w * R + r];
+                    for (int w = 0; w < W * HN; ++w) {  // with H two sets of columns a warp
+                        const float mw = join_m[w * (C / HN) + r];
                         const float f = mw == -INFINITY ? 0.f : ex2(mw - mm);
-                        const float4 v = *reinterpret_cast<const float4*>(join_o + (w * R + r) * JP + d4);
-                        l = fmaf(f, join_l[w * R + r], l);
+                        const float4 v = *reinterpret_cast<const float4*>(join_o + (w * (C / HN) + r) * JP + d4);
+                        l = fmaf(f, join_l[w * (C / HN) + r], l);
                         sum.x = fmaf(f, v.x, sum.x);
                         sum.y = fmaf(f, v.y, sum.y);
                         sum.z = fmaf(f, v.z, sum.z);
@@ -899,9 +948,9 @@ __global__ void __launch_bounds__(Shape<D, KIND, NT>::kThreads, Shape<D, KIND, N
 
 // Joins the partial sums of every item that was cut, in the order of the pieces.
 // One warp a row where there are many rows, a CTA's four warps where there are few.
-template <int D, int KIND, int NT, bool WIDE>
+template <int D, int KIND, int NT, bool H, bool WIDE>
 __global__ void __launch_bounds__(128) join_kernel(const AttnArgs a) {
-    using Sh = Shape<D, KIND, NT>;
+    using Sh = Shape<D, KIND, NT, H>;
     constexpr int R = Sh::R, E = D / 32, WS = WIDE ? 4 : 1;
     __shared__ float sm_o[WIDE ? 4 : 1][D], sm_m[4], sm_l[4];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -985,9 +1034,9 @@ int tiles_of(int64_t rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : 4; }
 
 size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 
-template <int D, int KIND, int NT>
+template <int D, int KIND, int NT, bool H>
 pva_status launch(AttnArgs a, uint8_t* ws, cudaStream_t st) {
-    using Sh = Shape<D, KIND, NT>;
+    using Sh = Shape<D, KIND, NT, H>;
     static_assert((Sh::kSmem + 1280) * Sh::kCtas <= 228 * 1024, "the CTAs share an SM");
     a.ws_per = reinterpret_cast<int64_t*>(ws);
     a.ws_cum = reinterpret_cast<int64_t*>(ws + 256);
@@ -999,10 +1048,10 @@ pva_status launch(AttnArgs a, uint8_t* ws, cudaStream_t st) {
         cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
         return PVA_ERR_CUDA;
     const int ctas = sms * Sh::kCtas < kMaxCtas ? sms * Sh::kCtas : kMaxCtas;
-    if (cudaFuncSetAttribute(attn_kernel<D, KIND, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    if (cudaFuncSetAttribute(attn_kernel<D, KIND, NT, H>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              Sh::kSmem) != cudaSuccess)
         return PVA_ERR_CUDA;
-    attn_kernel<D, KIND, NT><<<ctas, Sh::kThreads, Sh::kSmem, st>>>(a);
+    attn_kernel<D, KIND, NT, H><<<ctas, Sh::kThreads, Sh::kSmem, st>>>(a);
     if (cudaGetLastError() != cudaSuccess) return PVA_ERR_CUDA;
     const int64_t rows = (int64_t)a.s.num_tokens * a.hq;
     const bool wide = rows <= 2048;
@@ -1015,16 +1064,18 @@ pva_status launch(AttnArgs a, uint8_t* ws, cudaStream_t st) {
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    const cudaError_t e = wide ? cudaLaunchKernelEx(&cfg, join_kernel<D, KIND, NT, true>, a)
-                               : cudaLaunchKernelEx(&cfg, join_kernel<D, KIND, NT, false>, a);
+    const cudaError_t e = wide ? cudaLaunchKernelEx(&cfg, join_kernel<D, KIND, NT, H, true>, a)
+                               : cudaLaunchKernelEx(&cfg, join_kernel<D, KIND, NT, H, false>, a);
     return e == cudaSuccess ? PVA_OK : PVA_ERR_CUDA;
 }
 
 template <int D, int KIND>
-pva_status launch_tiles(int nt, const AttnArgs& a, uint8_t* ws, cudaStream_t st) {
-    return nt == 1 ? launch<D, KIND, 1>(a, ws, st)
-           : nt == 2 ? launch<D, KIND, 2>(a, ws, st)
-                     : launch<D, KIND, 4>(a, ws, st);
+pva_status launch_rows(int64_t rows, const AttnArgs& a, uint8_t* ws, cudaStream_t st) {
+    if (KIND == PVA_CACHE_INT4 && rows <= 4) return launch<D, KIND, 1, KIND == PVA_CACHE_INT4>(a, ws, st);
+    const int nt = tiles_of(rows);
+    return nt == 1   ? launch<D, KIND, 1, false>(a, ws, st)
+           : nt == 2 ? launch<D, KIND, 2, false>(a, ws, st)
+                     : launch<D, KIND, 4, false>(a, ws, st);
 }
 
 }  // namespace
@@ -1091,12 +1142,12 @@ extern "C" pva_status pva_cache_attn(const pva_cache_desc* cache, const pva_cach
     a.page_bytes = (uint32_t)page_bytes;
     a.num_pages = (uint32_t)cache->num_pages;
     // Without offsets every sequence has one row, whatever bound was given.
-    const int nt = tiles_of((int64_t)a.group * max_new);
+    const int64_t rows = (int64_t)a.group * (batch->cu_new ? max_new : 1);
     uint8_t* ws = reinterpret_cast<uint8_t*>(workspace);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (cache->kind == PVA_CACHE_BF16)
-        return d == 128 ? launch_tiles<128, PVA_CACHE_BF16>(nt, a, ws, s)
-                        : launch_tiles<64, PVA_CACHE_BF16>(nt, a, ws, s);
-    return d == 128 ? launch_tiles<128, PVA_CACHE_INT4>(nt, a, ws, s)
-                    : launch_tiles<64, PVA_CACHE_INT4>(nt, a, ws, s);
+        return d == 128 ? launch_rows<128, PVA_CACHE_BF16>(rows, a, ws, s)
+                        : launch_rows<64, PVA_CACHE_BF16>(rows, a, ws, s);
+    return d == 128 ? launch_rows<128, PVA_CACHE_INT4>(rows, a, ws, s)
+                    : launch_rows<64, PVA_CACHE_INT4>(rows, a, ws, s);
 }
