@@ -63,7 +63,7 @@ struct Shape {
     static constexpr int kWarps = 4;
     static constexpr int kKeys = kInt4 ? (NT == 1 ? 64 : 32 * (128 / D)) : 16 * (128 / D);
     static constexpr int kStages = kInt4 && NT == 1 ? 2 : 3;
-    static constexpr int kCtas = 2;          // resident on an SM
+    static constexpr int kCtas = kInt4 && NT == 1 ? 3 : 2;  // resident on an SM
     static constexpr int kCols = 8 * NT;     // columns of S^T
     static constexpr int R = H ? 4 : kCols;  // rows of an item
     static constexpr int kThreads = 32 * kWarps;
@@ -73,14 +73,13 @@ struct Shape {
     static constexpr int kScaleBytes = kInt4 ? 4 * kGroups : 0;
     static constexpr int kStageBytes = kKeys * 2 * (kRowBytes + kScaleBytes);
     static constexpr int kTiles = D / 16;  // 16-dim tiles of O^T
-    // 16-dim tiles that the warps' sums are joined by at a time: what is left of the
-    // shared memory beside the ring
-    static constexpr int kJoinTiles = kInt4 ? (NT == 4 ? 2 : 4) : 4 / NT;
-    static constexpr int kJoinDims = 16 * (kJoinTiles < kTiles ? kJoinTiles : kTiles);
+    // Dims that the warps' sums are joined by at a time, in the stage that each has just read.
+    static constexpr int kJoinDims = NT == 1 ? D : NT == 2 ? 64 : 32;
     static constexpr int kJoinPitch = kJoinDims + 4;
+    static_assert(kCols * kJoinPitch * 4 <= kStageBytes, "the sums fit a stage");
     static constexpr int kRing = kWarps * kStages * kStageBytes;
     static constexpr int kMeta = kWarps * kStages * 48;
-    static constexpr int kJoin = kWarps * kCols * (kJoinPitch + 2) * 4;
+    static constexpr int kJoin = kWarps * (2 * kCols + 4) * 4;
     static constexpr int kSmem = kRing + kMeta + kJoin;
 };
 
@@ -216,11 +215,9 @@ __global__ void __launch_bounds__(Shape<D, KIND, NT, H>::kThreads, Shape<D, KIND
     const int g = lane >> 2, c = lane & 3;
     uint8_t* ring = smem + warp * S * Sh::kStageBytes;
     Meta* meta = reinterpret_cast<Meta*>(smem + Sh::kRing) + warp * S;
-    uint8_t* tail = smem + Sh::kRing + Sh::kMeta;
-    float* join_o = reinterpret_cast<float*>(tail);             // [W][C][kJoinPitch]
-    float* join_m = join_o + W * C * Sh::kJoinPitch;            // [W][C]
-    float* join_l = join_m + W * C;                             // [W][C]
-
+    float* join_m = reinterpret_cast<float*>(smem + Sh::kRing + Sh::kMeta);  // [W][C]
+    float* join_l = join_m + W * C;                                          // [W][C]
+    int* join_at = reinterpret_cast<int*>(join_l + W * C);                   // [W]: stage of the sums
     // ---- plan: this CTA's piece [u0, u1) of the line and the sequence it starts in.
     // Every thread sums a run of sequences; a scan over the threads gives each run's
     // first unit.
@@ -872,7 +869,10 @@ __global__ void __launch_bounds__(Shape<D, KIND, NT, H>::kThreads, Shape<D, KIND
             constexpr int JT = Sh::kJoinDims / 16, JD = Sh::kJoinDims, JP = Sh::kJoinPitch;
 #pragma unroll
             for (int t0 = 0; t0 < T; t0 += JT) {
-                __syncthreads();  // the buffer's last readers are done
+                if (t0 > 0) __syncthreads();  // the last dims are read
+                if (t0 == 0 && lane == 0) join_at[warp] = (warp * S + stage) * Sh::kStageBytes;
+                float* join_o = reinterpret_cast<float*>(ring + stage * Sh::kStageBytes);  // [C][JP]
+                __syncwarp();  // the stage is read
                 if (t0 == 0 && g == 0) {
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
@@ -892,7 +892,7 @@ __global__ void __launch_bounds__(Shape<D, KIND, NT, H>::kThreads, Shape<D, KIND
                             // 8g + 2i, 8g + 2i + 1 of its group
                             const int at = INT4 ? g * 2 * (JT < 4 ? JT : 4) + 2 * (i % 4) + (e >> 1) + (i / 4) * 64
                                                 : 16 * i + g + 8 * (e >> 1);
-                            join_o[(warp * C + 8 * nt + 2 * c + (e & 1)) * JP + at] = o[nt][t0 + i][e];
+                            join_o[(8 * nt + 2 * c + (e & 1)) * JP + at] = o[nt][t0 + i][e];
                         }
                 __syncthreads();
                 for (int idx = tid; idx < R * (JD / 4); idx += Sh::kThreads) {
@@ -907,7 +907,8 @@ __global__ void __launch_bounds__(Shape<D, KIND, NT, H>::kThreads, Shape<D, KIND
                     for (int w = 0; w < W * HN; ++w) {  // with H two sets of columns a warp
                         const float mw = join_m[w * (C / HN) + r];
                         const float f = mw == -INFINITY ? 0.f : ex2(mw - mm);
-                        const float4 v = *reinterpret_cast<const float4*>(join_o + (w * (C / HN) + r) * JP + d4);
+                        const float4 v = *reinterpret_cast<const float4*>(
+                            smem + join_at[w / HN] + (((w % HN) * (C / HN) + r) * JP + d4) * 4);
                         l = fmaf(f, join_l[w * (C / HN) + r], l);
                         sum.x = fmaf(f, v.x, sum.x);
                         sum.y = fmaf(f, v.y, sum.y);
@@ -941,6 +942,7 @@ __global__ void __launch_bounds__(Shape<D, KIND, NT, H>::kThreads, Shape<D, KIND
                     }
                 }
             }
+            __syncthreads();  // the sums are read: the stages may be filled again
         }
     }
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
