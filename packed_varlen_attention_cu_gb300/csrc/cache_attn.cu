@@ -190,6 +190,11 @@ __device__ __forceinline__ int64_t units_of(const AttnArgs& a, const SeqInfo& s)
     return (int64_t)a.hkv * s.nrb * (kFixedUnits + s.nb);
 }
 
+template <int N>
+struct Const {
+    static constexpr int value = N;
+};
+
 // Steps: first and last of an item, nothing to read, the item is all this piece's, some
 // key of the tile is not for every row.
 enum { kFirst = 1, kLast = 2, kEmpty = 4, kWhole = 8, kPartial = 16 };
@@ -368,19 +373,21 @@ __global__ void __launch_bounds__(Shape<D, KIND, NT, H>::kThreads, Shape<D, KIND
             }
         }
     };
-    // 16 keys at byte `off` of K and V into a stage; [vlo, vhi): rows of them that are there.
-    auto copy16 = [&](uint32_t kd, int x, uint64_t off, int vlo, int vhi) {
-        constexpr int CPR = ROWB / 16, PER = 16 * CPR / 32;  // 16-byte chunks: a row's, a lane's
+    // N * 16 keys from byte `off` of a page's K and V on, into tile x of a stage;
+    // [vlo, vhi): rows of the first 16 that are there.
+    auto copy = [&](auto tiles, uint32_t kd, int x, uint64_t off, int vlo, int vhi) {
+        constexpr int N = decltype(tiles)::value;
+        constexpr int CPR = ROWB / 16, PER = CPR / 2;  // 16-byte chunks: a row's, a lane's of 16 keys
         const uint8_t* ks = a.k_pages + off + lane * 16;
         const uint8_t* vs = a.v_pages + off + lane * 16;
         if (!INT4) {
             const int r0 = lane / CPR, ch = lane % CPR;
 #pragma unroll
-            for (int i = 0; i < PER; ++i) {
+            for (int i = 0; i < N * PER; ++i) {
                 const int r = i * (32 / CPR) + r0;
                 const uint32_t to = (16 * x + r) * ROWB + ((ch ^ (r & 7)) << 4);
                 // rows that are not there are filled with zeros: a weight of 0 must not meet a NaN
-                const bool ok = r >= vlo && r < vhi;
+                const bool ok = N > 1 || (r >= vlo && r < vhi);
                 cp16(kd + to, ok ? ks + i * 512 : a.k_pages, ok ? 16 : 0);
                 cp16(kd + KS * ROWB + to, ok ? vs + i * 512 : a.v_pages, ok ? 16 : 0);
             }
@@ -391,16 +398,19 @@ __global__ void __launch_bounds__(Shape<D, KIND, NT, H>::kThreads, Shape<D, KIND
             const uint32_t kt = kd + 16 * x * ROWB + lane * 16;
             const uint32_t vt = kd + (KS + 16 * x) * ROWB + ((lane & 24) + sw) * 16;
 #pragma unroll
-            for (int i = 0; i < PER; ++i) {
+            for (int i = 0; i < N * PER; ++i) {
                 cp16(kt + i * 512, ks + i * 512, 16);
                 cp16(vt + i * 512, vs + i * 512, 16);
             }
-            constexpr int SC = Sh::kScaleBytes;  // chunks of 16 keys' scales, an eighth of the codes
-            if (lane < 2 * SC) {
-                const bool v = lane >= SC;
-                const int i = v ? lane - SC : lane;
-                cp16(kd + 2 * KS * ROWB + ((v ? KS : 0) + 16 * x) * Sh::kScaleBytes + i * 16,
-                     (v ? a.v_scales : a.k_scales) + (off >> 3) + i * 16, 16);
+            // scales, an eighth of the codes: of 16 keys (16 * N) kScaleBytes chunks, K's then V's
+            constexpr int SC = Sh::kScaleBytes * N, HALF = SC < 16 ? SC : 16;
+            const bool v = lane >= HALF;
+            const int i0 = v ? lane - HALF : lane;
+            const uint8_t* ss = (v ? a.v_scales : a.k_scales) + (off >> 3) + i0 * 16;
+            const uint32_t st = kd + 2 * KS * ROWB + ((v ? KS : 0) + 16 * x) * Sh::kScaleBytes + i0 * 16;
+            if (lane < 2 * HALF) {
+#pragma unroll
+                for (int i = 0; i < SC; i += HALF) cp16(st + i * 16, ss + i * 16, 16);
             }
         }
     };
@@ -417,14 +427,15 @@ __global__ void __launch_bounds__(Shape<D, KIND, NT, H>::kThreads, Shape<D, KIND
                 for (int x = 1; x < SUB; ++x) there &= page[x] < a.num_pages;
             }
             if (there && !(flags & kPartial)) {
-                const uint64_t off = (uint64_t)page[0] * a.page_bytes + (head + (key & mask)) * ROWB;
-                copy16(kd, 0, off, 0, 16);
+                if (one_page) {
+                    copy(Const<SUB>(), kd, 0,
+                         (uint64_t)page[0] * a.page_bytes + (head + (key & mask)) * ROWB, 0, 16);
+                } else {
 #pragma unroll
-                for (int x = 1; x < SUB; ++x)
-                    copy16(kd, x,
-                           one_page ? off + 16 * x * ROWB
-                                    : (uint64_t)page[x] * a.page_bytes + (head + ((key + 16 * x) & mask)) * ROWB,
-                           0, 16);
+                    for (int x = 0; x < SUB; ++x)
+                        copy(Const<1>(), kd, x,
+                             (uint64_t)page[x] * a.page_bytes + (head + ((key + 16 * x) & mask)) * ROWB, 0, 16);
+                }
             } else {
                 flags |= kPartial;
 #pragma unroll
@@ -433,10 +444,10 @@ __global__ void __launch_bounds__(Shape<D, KIND, NT, H>::kThreads, Shape<D, KIND
                     const uint32_t p = one_page ? page[0] : page[x];
                     const int lo = max(rlo - k, 0), hi = min(rhi - k, 16);
                     if (p < a.num_pages) {
-                        copy16(kd, x, (uint64_t)p * a.page_bytes + (head + (k & mask)) * ROWB, lo, hi);
+                        copy(Const<1>(), kd, x, (uint64_t)p * a.page_bytes + (head + (k & mask)) * ROWB, lo, hi);
                     } else {
                         missing |= 1 << x;
-                        if (!INT4) copy16(kd, x, 0, 0, 0);
+                        if (!INT4) copy(Const<1>(), kd, x, 0, 0, 0);
                         if (lane == 0 && lo < hi) raise_status(a.s.status, kErrPage);
                     }
                 }
