@@ -282,36 +282,53 @@ CACHE_BF16, CACHE_INT4 = 0, 1  # pva_cache_kind
 _BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
 
 
-def _need(ok, what: str) -> None:
-    if not ok:
-        raise ValueError(what)
+# A decoding step is a few microseconds of GPU work for each call, so the checks below
+# ask a tensor as few questions as they can and format a message only to raise it.
+def _device(t: torch.Tensor, name: str) -> int:
+    """The current device, which the call's first tensor must live on."""
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{name}: a CUDA tensor is needed")
+    if dev != torch._C._cuda_getDevice():
+        raise ValueError(f"{name}: tensor on cuda:{dev}, current device is cuda:{torch.cuda.current_device()}")
+    return dev
 
 
-def _rows3(t: torch.Tensor, name: str, dtype=_BF16) -> int:
+def _queue(stream, dev: int) -> int:
+    # (torch.cuda.current_stream(dev).cuda_stream without making a Stream object)
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
+
+
+def _rows3(t: torch.Tensor, name: str, dev: int, dtype=_BF16) -> int:
     """Token stride of a [tokens, heads, head_dim] tensor whose heads and dims are contiguous."""
-    _need(t.dim() == 3 and t.dtype == dtype and t.is_cuda, f"{name}: a {dtype} CUDA tensor [tokens, heads, head_dim]")
-    s, h, d = t.stride(), t.shape[1], t.shape[2]
-    _need((s[2] == 1 or d == 1) and (s[1] == d or h == 1), f"{name}: heads and dims must be contiguous")
-    _need(t.shape[0] <= 1 or s[0] >= h * d, f"{name}: token rows overlap")
-    return s[0] if t.shape[0] > 1 else 0
+    if t.dtype is not dtype or t.get_device() != dev or t.dim() != 3:
+        raise ValueError(f"{name}: a {dtype} tensor [tokens, heads, head_dim] on cuda:{dev} is needed")
+    if t.is_contiguous():
+        return 0
+    (n, h, d), (st, sh, sd) = t.shape, t.stride()
+    if (sd != 1 and d != 1) or (sh != d and h != 1) or (st < h * d and n > 1):
+        raise ValueError(f"{name}: heads and dims must be contiguous and rows must not overlap")
+    return st if n > 1 else 0
 
 
-def _ints(t: Optional[torch.Tensor], n: int, name: str) -> Optional[int]:
-    """Pointer of an int32 vector of at least n entries (None stays None)."""
-    if t is None:
-        return None
-    _need(t.dtype == _I32 and t.is_cuda and t.dim() == 1 and t.shape[0] >= n and
-          (t.shape[0] <= 1 or t.stride(0) == 1), f"{name}: a contiguous int32 CUDA tensor of at least {n} entries")
+def _whole(t: torch.Tensor, name: str, dev: int, shape, *dtypes) -> int:
+    if t.dtype not in dtypes or t.get_device() != dev or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name}: a contiguous tensor {list(shape)} of {dtypes} on cuda:{dev} is needed")
     return t.data_ptr()
 
 
-def _here(stream, *tensors) -> int:
-    """Stream of a call whose tensors all live on the current device."""
-    dev = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.device.index != dev:
-            raise ValueError(f"tensor on {t.device}, current device is cuda:{dev}")
-    return _stream(stream)
+def _ints(t: Optional[torch.Tensor], n: int, name: str, dev: int) -> Optional[int]:
+    """Pointer of a contiguous int32 vector of at least n entries (None stays None)."""
+    if t is None:
+        return None
+    if t.dtype is not _I32 or t.get_device() != dev or t.numel() < n or not t.is_contiguous():
+        raise ValueError(f"{name}: a contiguous int32 tensor of at least {n} entries on cuda:{dev} is needed")
+    return t.data_ptr()
+
+
+def _need(ok, what: str) -> None:
+    if not ok:
+        raise ValueError(what)
 
 
 def rope_table(max_pos: int, rot_dim: int, base: float = 10000.0, device="cuda",
@@ -325,12 +342,15 @@ def rope_table(max_pos: int, rot_dim: int, base: float = 10000.0, device="cuda",
     return torch.stack((a.cos(), a.sin()), -1).float()
 
 
-def _rope_desc(table: Optional[torch.Tensor], interleaved: bool) -> Optional[RopeDesc]:
+def _rope_desc(table: Optional[torch.Tensor], interleaved: bool, dev: int) -> Optional[RopeDesc]:
     if table is None:
         return None
-    _need(table.dtype == _F32 and table.is_cuda and table.dim() == 3 and table.shape[2] == 2 and
-          table.is_contiguous(), "table: fp32 CUDA tensor [max_pos, rot_dim / 2, 2]")
-    return RopeDesc(table.data_ptr(), table.shape[0], 2 * table.shape[1], 1 if interleaved else 0)
+    if table.dtype is not _F32 or table.get_device() != dev or table.dim() != 3 or not table.is_contiguous():
+        raise ValueError(f"table: a contiguous fp32 tensor [max_pos, rot_dim / 2, 2] on cuda:{dev} is needed")
+    n, pairs, two = table.shape
+    if two != 2:
+        raise ValueError("table: fp32 [max_pos, rot_dim / 2, 2]")
+    return RopeDesc(table.data_ptr(), n, 2 * pairs, 1 if interleaved else 0)
 
 
 def rope(q: Optional[torch.Tensor], k: Optional[torch.Tensor], table: torch.Tensor,
@@ -345,20 +365,26 @@ def rope(q: Optional[torch.Tensor], k: Optional[torch.Tensor], table: torch.Tens
     x = q if q is not None else k
     _need(x is not None and (q is None) == (q_out is None) and (k is None) == (k_out is None),
           "rope: queries or keys, each with its output")
-    _need(x.dtype in (_BF16, _F32), "rope: bf16 or fp32")
+    kind = x.dtype
+    _need(kind is _BF16 or kind is _F32, "rope: bf16 or fp32")
     _need(cu_seqlens is None or positions is None, "rope: cu_seqlens or positions, not both")
+    dev = _device(x, "rope")
+    _need(x.dim() == 3, "rope: [tokens, heads, head_dim]")
     t, _, d = x.shape
-    for y, o in ((q, q_out), (k, k_out)):
-        _need(y is None or (y.shape == o.shape and y.shape[0] == t and y.shape[2] == d),
-              "rope: shapes differ")
-    qs, ks, qo, ko = (0 if y is None else _rows3(y, "rope", x.dtype) for y in (q, k, q_out, k_out))
-    st = _here(stream, q, k, q_out, k_out, table, cu_seqlens, positions, status)
+    hq = hkv = qs = ks = qo = ko = 0
+    if q is not None:
+        qs, qo, hq = _rows3(q, "q", dev, kind), _rows3(q_out, "q_out", dev, kind), q.shape[1]
+        _need(q.shape == q_out.shape, "rope: q and q_out differ in shape")
+    if k is not None:
+        ks, ko, hkv = _rows3(k, "k", dev, kind), _rows3(k_out, "k_out", dev, kind), k.shape[1]
+        _need(k.shape == k_out.shape and k.shape[0] == t and k.shape[2] == d,
+              "rope: k and k_out [tokens, kv heads, head_dim]")
     check("pva_rope", lib().pva_rope(
-        _ptr(q), qs, _ptr(k), ks, t, 0 if q is None else q.shape[1],
-        0 if k is None else k.shape[1], d, 1 if x.dtype == _F32 else 0,
-        _rope_desc(table, interleaved), _ints(cu_seqlens, 1, "cu_seqlens"),
-        0 if cu_seqlens is None else cu_seqlens.shape[0] - 1, _ints(positions, t, "positions"),
-        1 if inverse else 0, _ptr(q_out), qo, _ptr(k_out), ko, _ints(status, 1, "status"), st))
+        _ptr(q), qs, _ptr(k), ks, t, hq, hkv, d, 1 if kind is _F32 else 0,
+        _rope_desc(table, interleaved, dev), _ints(cu_seqlens, 1, "cu_seqlens", dev),
+        0 if cu_seqlens is None else cu_seqlens.numel() - 1, _ints(positions, t, "positions", dev),
+        1 if inverse else 0, _ptr(q_out), qo, _ptr(k_out), ko, _ints(status, 1, "status", dev),
+        _queue(stream, dev)))
 
 
 class KVCache:
@@ -383,7 +409,7 @@ class KVCache:
         for t in (k, v, k_scales, v_scales):
             _need(t is None or (t.is_cuda and t.is_contiguous() and t.device == k.device),
                   "KVCache: contiguous CUDA tensors of one device")
-        self.device = k.device
+        self.device, self.index = k.device, k.get_device()
         self.desc = _lib.CacheDesc(self.kind, heads, self.head_dim, page, pages, _ptr(k), _ptr(v),
                                    _ptr(k_scales), _ptr(v_scales))
 
@@ -397,14 +423,22 @@ class KVCache:
                    *(torch.zeros(shape + (head_dim // 64, 2), dtype=_BF16, device=device) for _ in "kv"))
 
 
-def _cache_batch(page_table, num_tokens: int, kv_lens, cu_new, status) -> CacheBatch:
-    _need(page_table.dtype == _I32 and page_table.is_cuda and page_table.dim() == 2 and
-          (page_table.shape[1] <= 1 or page_table.stride(1) == 1),
-          "page_table: int32 CUDA tensor [sequences, pages] with contiguous rows")
+def _cache_batch(cache: KVCache, page_table, num_tokens: int, kv_lens, cu_new, status, dev: int) -> CacheBatch:
+    if page_table.dtype is not _I32 or page_table.get_device() != dev or page_table.dim() != 2:
+        raise ValueError(f"page_table: an int32 tensor [sequences, pages] on cuda:{dev} is needed")
+    if cache.index != dev:
+        raise ValueError(f"the cache is on cuda:{cache.index}, the call's tensors on cuda:{dev}")
     n, width = page_table.shape
-    return CacheBatch(n, num_tokens, width, page_table.stride(0) if n > 1 else width,
-                      page_table.data_ptr(), _ints(kv_lens, n, "kv_lens"),
-                      _ints(cu_new, n + 1, "cu_new"), _ints(status, 1, "status"))
+    stride = width
+    if not page_table.is_contiguous():
+        stride, one = page_table.stride()
+        _need(one == 1 or width <= 1, "page_table: rows must be contiguous")
+        if n <= 1:
+            stride = width
+        _need(stride >= width, "page_table: rows overlap")
+    return CacheBatch(n, num_tokens, width, stride, page_table.data_ptr(),
+                      _ints(kv_lens, n, "kv_lens", dev), _ints(cu_new, n + 1, "cu_new", dev),
+                      _ints(status, 1, "status", dev))
 
 
 def cache_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, page_table: torch.Tensor,
@@ -418,20 +452,24 @@ def cache_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, page_table: t
     kv_lens[b] counts its tokens with the new ones; page_table [sequences, pages].
     With an angle table the keys are rotated on the way (k_out: a copy of them for
     attn_fwd), and the queries q into q_out."""
-    t, h, d = k.shape
-    _need(k.shape == v.shape and h == cache.num_kv_heads and d == cache.head_dim,
-          "cache_append: k and v [tokens, kv heads, head_dim] of the cache")
+    dev = _device(k, "k")
+    ks, vs = _rows3(k, "k", dev), _rows3(v, "v", dev)
+    shape = k.shape
+    t, h, d = shape
+    if v.shape != shape or h != cache.num_kv_heads or d != cache.head_dim:
+        raise ValueError("cache_append: k and v [tokens, kv heads, head_dim] of the cache")
+    hq = qs = qo = ko = 0
     _need((q is None) == (q_out is None), "cache_append: q goes with q_out")
-    _need(q is None or (q.shape == q_out.shape and q.shape[0] == t and q.shape[2] == d),
-          "cache_append: q and q_out [tokens, heads, head_dim]")
-    _need(k_out is None or k_out.shape == k.shape, "cache_append: k_out has k's shape")
-    ks, vs = _rows3(k, "k"), _rows3(v, "v")
-    qs, qo, ko = (0 if x is None else _rows3(x, "q, q_out, k_out") for x in (q, q_out, k_out))
-    b = _cache_batch(page_table, t, kv_lens, cu_new, status)
-    st = _here(stream, cache.k, k, v, page_table, kv_lens, cu_new, table, q, q_out, k_out, status)
+    if q is not None:
+        qs, qo, hq = _rows3(q, "q", dev), _rows3(q_out, "q_out", dev), q.shape[1]
+        _need(q.shape == q_out.shape == (t, hq, d), "cache_append: q and q_out [tokens, heads, head_dim]")
+    if k_out is not None:
+        ko = _rows3(k_out, "k_out", dev)
+        _need(k_out.shape == shape, "cache_append: k_out has k's shape")
     check("pva_cache_append", lib().pva_cache_append(
-        cache.desc, b, _rope_desc(table, interleaved), _ptr(k), ks, _ptr(v), vs, _ptr(q), qs,
-        0 if q is None else q.shape[1], _ptr(q_out), qo, _ptr(k_out), ko, st))
+        cache.desc, _cache_batch(cache, page_table, t, kv_lens, cu_new, status, dev),
+        _rope_desc(table, interleaved, dev), k.data_ptr(), ks, v.data_ptr(), vs, _ptr(q), qs, hq,
+        _ptr(q_out), qo, _ptr(k_out), ko, _queue(stream, dev)))
 
 
 def cache_read(cache: KVCache, page_table: torch.Tensor, cu_out: torch.Tensor,
@@ -440,15 +478,15 @@ def cache_read(cache: KVCache, page_table: torch.Tensor, cu_out: torch.Tensor,
     """Cached rows as a contiguous pack: rows cu_out[b] .. cu_out[b + 1] of k_out and
     v_out (bf16 [tokens, kv heads, head_dim]) are the tokens of sequence b from
     position starts[b] (None: 0) on.  Other rows are left as they were."""
+    dev = _device(k_out, "k_out")
     t = k_out.shape[0]
-    for x in (k_out, v_out):
-        _need(x.dtype == _BF16 and x.is_cuda and x.is_contiguous() and
-              tuple(x.shape) == (t, cache.num_kv_heads, cache.head_dim),
-              "cache_read: outputs contiguous bf16 [tokens, kv heads, head_dim]")
-    b = _cache_batch(page_table, t, None, cu_out, status)
-    st = _here(stream, cache.k, page_table, cu_out, k_out, v_out, starts, status)
+    shape = (t, cache.num_kv_heads, cache.head_dim)
+    ko, vo = _whole(k_out, "k_out", dev, shape, _BF16), _whole(v_out, "v_out", dev, shape, _BF16)
+    _need(cu_out is not None, "cache_read: cu_out is needed")
+    b = _cache_batch(cache, page_table, t, None, cu_out, status, dev)
     check("pva_cache_read", lib().pva_cache_read(
-        cache.desc, b, _ints(starts, b.num_seqs, "starts"), _ptr(k_out), _ptr(v_out), st))
+        cache.desc, b, _ints(starts, page_table.shape[0], "starts", dev), ko, vo,
+        _queue(stream, dev)))
 
 
 def cache_attn_bytes(num_seqs: int, num_q_heads: int, num_kv_heads: int, head_dim: int,
@@ -476,28 +514,28 @@ def cache_attn(cache: KVCache, q: torch.Tensor, page_table: torch.Tensor, kv_len
     position kv_lens[b] - n + i and sees the keys up to it (window > 0: the last
     `window` of them).  out bf16 or fp32 like q, lse fp32 [heads, tokens]; max_new:
     an upper bound of n."""
-    t, h, d = q.shape
-    _need(d == cache.head_dim, "cache_attn: head_dim differs from the cache's")
-    _need(out.shape == q.shape and out.is_contiguous() and out.is_cuda and
-          out.dtype in (_BF16, _F32), "cache_attn: out contiguous bf16 or fp32 of q's shape")
-    _need(lse.dtype == _F32 and lse.is_cuda and lse.is_contiguous() and
-          tuple(lse.shape) == (h, t), "cache_attn: lse contiguous fp32 [heads, tokens]")
-    _need(workspace.is_cuda and workspace.is_contiguous(), "cache_attn: a contiguous CUDA workspace")
-    qs = _rows3(q, "q")
-    b = _cache_batch(page_table, t, kv_lens, cu_new, status)
-    st = _here(stream, cache.k, q, page_table, kv_lens, out, lse, workspace, cu_new, status)
+    dev = _device(q, "q")
+    qs = _rows3(q, "q", dev)
+    shape = q.shape
+    t, h, d = shape
+    if d != cache.head_dim:
+        raise ValueError("cache_attn: head_dim differs from the cache's")
+    o, l = _whole(out, "out", dev, shape, _BF16, _F32), _whole(lse, "lse", dev, (h, t), _F32)
+    if workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace: a contiguous tensor on cuda:{dev} is needed")
     check("pva_cache_attn", lib().pva_cache_attn(
-        cache.desc, b, q.data_ptr(), qs, h, max_new, window, softmax_scale, out.data_ptr(),
-        1 if out.dtype == _F32 else 0, lse.data_ptr(), workspace.data_ptr(),
-        workspace.numel() * workspace.element_size(), st))
+        cache.desc, _cache_batch(cache, page_table, t, kv_lens, cu_new, status, dev), q.data_ptr(),
+        qs, h, max_new, window, softmax_scale, o, 1 if out.dtype is _F32 else 0, l,
+        workspace.data_ptr(), workspace.nbytes, _queue(stream, dev)))
 
 
 def cache_status(status: torch.Tensor, stream=None) -> int:
     """The first failure met on the device by the calls that were given this status word
     (int32, 0 before them): 0, or a code of pva.h.  Synchronizes the stream."""
+    dev = _device(status, "status")
     code = ctypes.c_int32(0)
     check("pva_cache_status", lib().pva_cache_status(
-        _ints(status, 1, "status"), ctypes.byref(code), _here(stream, status)))
+        _ints(status, 1, "status", dev), ctypes.byref(code), _queue(stream, dev)))
     return int(code.value)
 
 
