@@ -170,23 +170,21 @@ __global__ void __launch_bounds__(kThreads) rotate_kernel(const RotArgs a) {
                 raise_status(a.s.status, KIND != kNoCache && pos < 0 ? kErrLength : kErrPosition);
             continue;
         }
+        // A lane without a head loads the token's first one again: a branch around the loads
+        // would make each wait for the one before it.
         Octet<F32> xa[kUnroll], xb[kUnroll];
-        const void* row[kUnroll];
+        const char* q_row = (const char*)a.q + t * a.q_stride * kElem;
+        const char* k_row = (const char*)a.k + t * a.k_stride * kElem;
+        const char* v_row = (const char*)a.v + t * a.v_stride * kElem;
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
             const int slot = slot0 + u * kHpw;
-            row[u] = nullptr;
-            if (slot < a.hq)
-                row[u] = (const char*)a.q + (t * a.q_stride + (int64_t)slot * D) * kElem;
-            else if (slot < a.hq + a.hkv)
-                row[u] = (const char*)a.k + (t * a.k_stride + (int64_t)(slot - a.hq) * D) * kElem;
-            else if (KIND != kNoCache && slot < a.nslots)
-                row[u] = (const char*)a.v +
-                         (t * a.v_stride + (int64_t)(slot - a.hq - a.hkv) * D) * kElem;
-            if (row[u]) {
-                xa[u].load(row[u], oa);
-                xb[u].load(row[u], ob);
-            }
+            const char* row = a.hq > 0 ? q_row : k_row;
+            if (slot < a.hq) row = q_row + slot * (D * kElem);
+            else if (slot < a.hq + a.hkv) row = k_row + (slot - a.hq) * (D * kElem);
+            else if (KIND != kNoCache && slot < a.nslots) row = v_row + (slot - a.hq - a.hkv) * (D * kElem);
+            xa[u].load(row, oa);
+            xb[u].load(row, ob);
         }
         float c[8], s[8];
         if (rotated) {
@@ -211,7 +209,7 @@ __global__ void __launch_bounds__(kThreads) rotate_kernel(const RotArgs a) {
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
             const int slot = slot0 + u * kHpw;
-            const bool live = row[u] != nullptr;
+            const bool live = slot < a.nslots;
             const bool is_q = slot < a.hq, is_k = !is_q && slot < a.hq + a.hkv;
             if (live && rotated && (is_q || is_k)) {
                 float x[16];
@@ -329,66 +327,109 @@ struct ReadArgs {
     int32_t hkv;
 };
 
-// One warp takes kUnroll passes of a row; a lane gives one octet of a head.
+// One warp takes `run` (at most 32) consecutive rows: lane i finds the page of row i, so
+// that the lookups of a run go on at once, then the warp passes over rows and heads,
+// kUnroll passes' loads in flight.  A lane holds 16 bytes of a bf16 row; of a 4-bit row
+// the word or two (one of each group) that become one or two octets.
 template <int D, int KIND>
-__global__ void __launch_bounds__(kThreads) read_kernel(const ReadArgs a) {
-    constexpr int kLph = D / 8, kHpw = 32 / kLph, kUnroll = 4;
+__global__ void __launch_bounds__(kThreads) read_kernel(const ReadArgs a, int32_t run) {
+    constexpr bool kInt4 = KIND == PVA_CACHE_INT4;
+    constexpr int kLph = kInt4 ? 8 : D / 8, kHpw = 32 / kLph, kUnroll = 4, kG = D / 64;
     const int lane = threadIdx.x & 31;
-    const int o = lane % kLph;
-    const int slot0 = blockIdx.y * kUnroll * kHpw + lane / kLph;
-    const int64_t stride = (int64_t)gridDim.x * kWarps;
-    for (int64_t tt = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5); tt < a.s.num_tokens;
-         tt += stride) {
-        const int32_t t = (int32_t)tt;
-        int32_t b = t, i = 0;
-        if (a.s.cu) {
-            b = find_seq(a.s.cu, a.s.num_seqs, t);
-            if (b >= 0) i = t - a.s.cu[b];
-        }
-        if (b < 0 || b >= a.s.num_seqs) continue;
-        const int64_t pos = (a.starts ? a.starts[b] : 0) + (int64_t)i;
-        const int64_t page = pos > INT32_MAX ? -1 : page_of(a.s, b, (int32_t)pos);
-        if (page < 0) {
-            if (lane == 0) raise_status(a.s.status, kErrPage);
-            continue;
-        }
-        const int32_t in_page = (int32_t)pos & ((1 << a.s.page_shift) - 1);
-        uint4 x[kUnroll];
-        uint32_t sc[kUnroll];
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            const int slot = slot0 + u * kHpw;
-            const bool is_k = slot < a.hkv;
-            const int h = is_k ? slot : slot - a.hkv;
-            if (h >= a.hkv) continue;
-            const int64_t at = ((page * a.hkv + h) << a.s.page_shift) + in_page;
-            if (KIND == PVA_CACHE_BF16) {
-                x[u] = __ldcs((const uint4*)(is_k ? a.k_pages : a.v_pages) + at * kLph + o);
-            } else {
-                x[u].x = __ldcs((const uint32_t*)(is_k ? a.k_pages : a.v_pages) + at * (D / 8) +
-                                word_of_octet<D>(o));
-                sc[u] = __ldcs((const uint32_t*)(is_k ? a.k_scales : a.v_scales) + at * (D / 64) +
-                               o / 8);
+    const int o = lane % kLph, sub = lane / kLph;
+    const int ppr = (2 * a.hkv + kHpw - 1) / kHpw;  // passes a row
+    // p / ppr for p below 32 * ppr + kUnroll as a product: exact while 33 ppr^2 < 2^20
+    const uint32_t inv = ((1u << 20) + ppr - 1) / ppr;
+    const int64_t runs = ((int64_t)a.s.num_tokens + run - 1) / run;
+    for (int64_t ri = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5); ri < runs;
+         ri += (int64_t)gridDim.x * kWarps) {
+        const int32_t t0 = (int32_t)(ri * run);
+        const int32_t rows = min(run, a.s.num_tokens - t0);
+        // the cached row (of head 0) that lane i's row is
+        int64_t at = -1;
+        {
+            const int32_t t = t0 + lane;
+            int32_t b = -1, i = 0;
+            if (a.s.cu) {
+                const int32_t b0 = find_seq(a.s.cu, a.s.num_seqs, t0);
+                if (lane < rows) {
+                    if (b0 >= 0 && t < __ldg(a.s.cu + b0 + 1)) {
+                        b = b0;
+                    } else {  // the run goes on into another sequence, or begins before the first
+                        int32_t lo = max(b0, 0), hi = a.s.num_seqs;
+                        while (hi - lo > 1) {
+                            const int32_t mid = lo + (hi - lo) / 2;
+                            if (__ldg(a.s.cu + mid) <= t) lo = mid;
+                            else hi = mid;
+                        }
+                        if (__ldg(a.s.cu + lo) <= t && t < __ldg(a.s.cu + lo + 1)) b = lo;
+                    }
+                    if (b >= 0) i = t - __ldg(a.s.cu + b);
+                }
+            } else if (lane < rows && t < a.s.num_seqs) {
+                b = t;
+            }
+            if (b >= 0) {
+                const int64_t pos = (a.starts ? __ldg(a.starts + b) : 0) + (int64_t)i;
+                const int64_t page = pos > INT32_MAX ? -1 : page_of(a.s, b, (int32_t)pos);
+                if (page < 0) raise_status(a.s.status, kErrPage);
+                else at = ((page * a.hkv) << a.s.page_shift) + (pos & ((1 << a.s.page_shift) - 1));
             }
         }
+        if (!__any_sync(0xffffffffu, at >= 0)) continue;  // (a cache may have no page at all)
+        for (int p0 = 0; p0 < rows * ppr; p0 += kUnroll) {
+            uint4 x[kUnroll];
+            uint2 sc[kUnroll];
+            bool live[kUnroll];
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            const int slot = slot0 + u * kHpw;
-            const bool is_k = slot < a.hkv;
-            const int h = is_k ? slot : slot - a.hkv;
-            if (h >= a.hkv) continue;
-            if (KIND == PVA_CACHE_INT4) {
-                const float scale = __uint_as_float(sc[u] << 16);
-                const float low = __uint_as_float(sc[u] & 0xffff0000u);
-                float f[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    f[e] = __fadd_rn(low, __fmul_rn((float)((x[u].x >> (4 * (e / 2) + 16 * (e % 2))) & 15u), scale));
-                Octet<false> y;
-                y.set(f);
-                x[u] = y.r;
+            for (int u = 0; u < kUnroll; ++u) {
+                const int r = (int)(((uint32_t)(p0 + u) * inv) >> 20), slot = (p0 + u - r * ppr) * kHpw + sub;
+                const int64_t row0 = __shfl_sync(0xffffffffu, at, r & 31);
+                const bool is_k = slot < a.hkv;
+                const int h = is_k ? slot : slot - a.hkv;
+                // (lanes without a row load the first one, so that no branch parts the loads)
+                live[u] = r < rows && h < a.hkv && row0 >= 0;
+                const int64_t row = live[u] ? row0 + ((int64_t)h << a.s.page_shift) : 0;
+                const void* pages = is_k ? a.k_pages : a.v_pages;
+                if (!kInt4) {
+                    x[u] = __ldcs((const uint4*)pages + row * kLph + o);
+                } else {
+                    const void* scales = is_k ? a.k_scales : a.v_scales;
+                    if (kG == 2) {
+                        const uint2 w = __ldcs((const uint2*)pages + row * 8 + o);
+                        x[u].x = w.x;
+                        x[u].y = w.y;
+                        sc[u] = __ldg((const uint2*)scales + row);
+                    } else {
+                        x[u].x = __ldcs((const uint32_t*)pages + row * 8 + o);
+                        sc[u].x = __ldg((const uint32_t*)scales + row);
+                    }
+                }
             }
-            ((uint4*)(is_k ? a.k_out : a.v_out))[((int64_t)t * a.hkv + h) * kLph + o] = x[u];
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u) {
+                if (!live[u]) continue;
+                const int r = (int)(((uint32_t)(p0 + u) * inv) >> 20), slot = (p0 + u - r * ppr) * kHpw + sub;
+                const bool is_k = slot < a.hkv;
+                const int h = is_k ? slot : slot - a.hkv;
+                uint4* out = (uint4*)(is_k ? a.k_out : a.v_out) + ((int64_t)(t0 + r) * a.hkv + h) * (D / 8);
+                if (!kInt4) {
+                    out[o] = x[u];
+                } else {
+#pragma unroll
+                    for (int g = 0; g < kG; ++g) {
+                        const uint32_t w = g == 0 ? x[u].x : x[u].y, s = g == 0 ? sc[u].x : sc[u].y;
+                        const float scale = __uint_as_float(s << 16), low = __uint_as_float(s & 0xffff0000u);
+                        float f[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            f[e] = __fadd_rn(low, __fmul_rn((float)((w >> (4 * (e / 2) + 16 * (e % 2))) & 15u), scale));
+                        Octet<false> y;
+                        y.set(f);
+                        out[8 * g + o] = y.r;
+                    }
+                }
+            }
         }
     }
 }
@@ -414,10 +455,17 @@ pva_status launch_rotate(const RotArgs& a, cudaStream_t st) {
 
 template <int D, int KIND>
 pva_status launch_read(const ReadArgs& a, cudaStream_t st) {
-    constexpr int per = 4 * (32 / (D / 8));
-    const int gy = (2 * a.hkv + per - 1) / per;
-    if (gy > 65535) return PVA_ERR_UNSUPPORTED;
-    read_kernel<D, KIND><<<dim3(grid_x(a.s.num_tokens, gy), gy), kThreads, 0, st>>>(a);
+    if ((2 * (int64_t)a.hkv * (KIND == PVA_CACHE_INT4 ? 8 : D / 8) + 31) / 32 > 176)
+        return PVA_ERR_UNSUPPORTED;  // the kernel's division (704 kv heads of 64 dims, 352 of 128)
+    // runs as long as leave every SM two CTAs of work
+    int dev = 0, sms = 148;
+    if (cudaGetDevice(&dev) == cudaSuccess)
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    int32_t run = 32;
+    while (run > 1 && (int64_t)a.s.num_tokens / run < (int64_t)sms * 2 * kWarps) run /= 2;
+    const int64_t blocks = (((int64_t)a.s.num_tokens + run - 1) / run + kWarps - 1) / kWarps;
+    const int64_t cap = (int64_t)sms * 64;
+    read_kernel<D, KIND><<<(int)(blocks < cap ? blocks : cap), kThreads, 0, st>>>(a, run);
     return cudaGetLastError() == cudaSuccess ? PVA_OK : PVA_ERR_CUDA;
 }
 
