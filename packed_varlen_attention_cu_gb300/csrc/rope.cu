@@ -20,6 +20,11 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 enum { kNoCache = -1 };
+// Passes whose loads a lane has in flight.
+template <bool F32, int KIND>
+struct Unroll {
+    static constexpr int value = F32 ? 4 : KIND == kNoCache ? 5 : 3;
+};
 
 struct RotArgs {
     const void *q, *k, *v;
@@ -44,54 +49,41 @@ __device__ __forceinline__ float max_nan(float a, float b) {
     return r;
 }
 
-// Eight consecutive dims of a row.
+// 16 bytes of a row: eight bf16 or four fp32 dims.
 template <bool F32>
-struct Octet;
-template <>
-struct Octet<false> {
+struct Vec {
+    static constexpr int kDims = F32 ? 4 : 8;
     uint4 r;
-    __device__ __forceinline__ void load(const void* row, int o) {
-        r = __ldcs(reinterpret_cast<const uint4*>(row) + o);
+    __device__ __forceinline__ void load(const void* row, int v) {
+        r = __ldcs(reinterpret_cast<const uint4*>(row) + v);
     }
-    __device__ __forceinline__ void store(void* row, int o) const {
-        reinterpret_cast<uint4*>(row)[o] = r;
+    __device__ __forceinline__ void store(void* row, int v) const {
+        reinterpret_cast<uint4*>(row)[v] = r;
     }
     __device__ __forceinline__ void get(float* x) const {
         const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            x[2 * i] = __uint_as_float(w[i] << 16);
-            x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+            if (F32) {
+                x[i] = __uint_as_float(w[i]);
+            } else {
+                x[2 * i] = __uint_as_float(w[i] << 16);
+                x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+            }
         }
     }
     __device__ __forceinline__ void set(const float* x) {
         uint32_t w[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const __nv_bfloat162 p = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-            w[i] = *reinterpret_cast<const uint32_t*>(&p);
+            if (F32) {
+                w[i] = __float_as_uint(x[i]);
+            } else {
+                const __nv_bfloat162 p = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+                w[i] = *reinterpret_cast<const uint32_t*>(&p);
+            }
         }
         r = make_uint4(w[0], w[1], w[2], w[3]);
-    }
-};
-template <>
-struct Octet<true> {
-    float4 a, b;
-    __device__ __forceinline__ void load(const void* row, int o) {
-        a = __ldcs(reinterpret_cast<const float4*>(row) + 2 * o);
-        b = __ldcs(reinterpret_cast<const float4*>(row) + 2 * o + 1);
-    }
-    __device__ __forceinline__ void store(void* row, int o) const {
-        reinterpret_cast<float4*>(row)[2 * o] = a;
-        reinterpret_cast<float4*>(row)[2 * o + 1] = b;
-    }
-    __device__ __forceinline__ void get(float* x) const {
-        x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-        x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-    }
-    __device__ __forceinline__ void set(const float* x) {
-        a = make_float4(x[0], x[1], x[2], x[3]);
-        b = make_float4(x[4], x[5], x[6], x[7]);
     }
 };
 
@@ -114,65 +106,63 @@ __device__ __forceinline__ uint32_t encode(const float* x, float low, float inv)
     return w;
 }
 
-// One warp takes kUnroll passes of a token; a pass is 32 lanes = 32 / (D / 16)
-// heads, a lane holds the two octets of its head that turn against each other
-// (half-split pairs p and p + rot / 2: octets j and j + rot / 16; interleaved
-// pairs: octets 2j and 2j + 1), so a rotation needs no shuffle and the lane's
-// 16 angles serve all its heads.  The heads of q, k and v form one list of
-// slots, whatever their counts.
+// Sequence (or document) of row t0 + lane, for a warp's run of `rows` rows; -1: none.
+__device__ __forceinline__ int32_t seq_of_lane(const SeqView& s, int32_t t0, int32_t rows) {
+    const int lane = threadIdx.x & 31;
+    const int32_t t = t0 + lane;
+    if (!s.cu) return lane < rows && t < s.num_seqs ? t : -1;
+    const int32_t b0 = find_seq(s.cu, s.num_seqs, t0);
+    if (lane >= rows) return -1;
+    if (b0 >= 0 && t < __ldg(s.cu + b0 + 1)) return b0;
+    // the run goes on into another sequence, or begins before the first
+    int32_t lo = max(b0, 0), hi = s.num_seqs;
+    while (hi - lo > 1) {
+        const int32_t mid = lo + (hi - lo) / 2;
+        if (__ldg(s.cu + mid) <= t) lo = mid;
+        else hi = mid;
+    }
+    return s.num_seqs > 0 && __ldg(s.cu + lo) <= t && t < __ldg(s.cu + lo + 1) ? lo : -1;
+}
+
+// One warp takes kUnroll passes of a token, whose loads go out before the token's place is
+// looked up; a pass is 32 / (D / 2 / dims) heads.  A lane holds two 16-byte vectors of its
+// head: with half-split pairs (p, p + rot / 2) those that turn against each other; with
+// interleaved pairs, which lie inside a vector, one of each half of the head.  So a
+// rotation needs no shuffle, a warp's accesses are whole lines, and a lane's angles serve
+// all its heads.  The heads of q, k and v form one list of slots, whatever their counts.
+// Bounded by HBM; three CTAs an SM (85 registers) measured best: 131072 tokens of 40 heads
+// of 128, bf16: 472 us without the bound, 415 us with it (96% of the copy rate), 454 us
+// with four.
 template <int D, bool F32, int KIND>
-__global__ void __launch_bounds__(kThreads) rotate_kernel(const RotArgs a) {
-    constexpr int kLph = D / 16;         // lanes a head
+__global__ void __launch_bounds__(kThreads, 3) rotate_kernel(const RotArgs a) {
+    constexpr int kV = Vec<F32>::kDims;
+    constexpr int kLph = D / (2 * kV);   // lanes a head
     constexpr int kHpw = 32 / kLph;      // heads a pass
-    constexpr int kUnroll = F32 ? 2 : 4;
+    constexpr int kUnroll = Unroll<F32, KIND>::value;
     constexpr int kElem = F32 ? 4 : 2;
     const int lane = threadIdx.x & 31;
     const int j = lane % kLph, sub = lane / kLph;
-    int oa, ob;
-    bool rotated;
-    if (a.inter || j >= a.rot / 16) {
-        // interleaved pairs, or dims past the rotated ones
-        oa = a.inter ? 2 * j : a.rot / 8 + 2 * (j - a.rot / 16);
-        ob = oa + 1;
-        rotated = 16 * j < a.rot;
-    } else {
+    const int pairs = a.rot / (2 * kV);  // vectors of the first half of the rotated dims
+    int oa, ob;           // the lane's vectors
+    bool rot_a, rot_b;    // are they rotated?
+    if (a.inter) {
         oa = j;
-        ob = j + a.rot / 16;
-        rotated = true;
+        ob = j + kLph;
+        rot_a = oa < 2 * pairs;
+        rot_b = ob < 2 * pairs;
+    } else {
+        rot_a = rot_b = j < pairs;
+        oa = rot_a ? j : j + pairs;
+        ob = rot_a ? j + pairs : j + kLph;
     }
     const int slot0 = blockIdx.y * kUnroll * kHpw + sub;
     const int64_t stride = (int64_t)gridDim.x * kWarps;
     for (int64_t tt = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5); tt < a.s.num_tokens;
          tt += stride) {
         const int32_t t = (int32_t)tt;
-        int32_t b = -1, pos = t;
-        if (KIND != kNoCache) {
-            int32_t n = 1, i = 0;
-            if (a.s.cu) {
-                b = find_seq(a.s.cu, a.s.num_seqs, t);
-                if (b < 0) continue;
-                i = t - a.s.cu[b];
-                n = a.s.cu[b + 1] - a.s.cu[b];
-            } else {
-                b = t;
-                if (b >= a.s.num_seqs) continue;
-            }
-            pos = (int32_t)max((int64_t)a.s.kv_lens[b] - n + i, (int64_t)-1);
-        } else if (a.positions) {
-            pos = a.positions[t];
-        } else if (a.s.cu) {
-            b = find_seq(a.s.cu, a.s.num_seqs, t);
-            if (b < 0) continue;
-            pos = t - a.s.cu[b];
-        }
-        if (pos < 0 || (a.rot > 0 && pos >= a.max_pos)) {
-            if (lane == 0)
-                raise_status(a.s.status, KIND != kNoCache && pos < 0 ? kErrLength : kErrPosition);
-            continue;
-        }
         // A lane without a head loads the token's first one again: a branch around the loads
         // would make each wait for the one before it.
-        Octet<F32> xa[kUnroll], xb[kUnroll];
+        Vec<F32> xa[kUnroll], xb[kUnroll];
         const char* q_row = (const char*)a.q + t * a.q_stride * kElem;
         const char* k_row = (const char*)a.k + t * a.k_stride * kElem;
         const char* v_row = (const char*)a.v + t * a.v_stride * kElem;
@@ -186,44 +176,77 @@ __global__ void __launch_bounds__(kThreads) rotate_kernel(const RotArgs a) {
             xa[u].load(row, oa);
             xb[u].load(row, ob);
         }
-        float c[8], s[8];
-        if (rotated) {
-            const float4* cs =
-                reinterpret_cast<const float4*>(a.table + ((int64_t)pos * (a.rot / 2) + 8 * j) * 2);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float4 f = __ldg(cs + i);
-                c[2 * i] = f.x;
-                s[2 * i] = a.inverse ? -f.y : f.y;
-                c[2 * i + 1] = f.z;
-                s[2 * i + 1] = a.inverse ? -f.w : f.w;
-            }
-        }
-        int64_t page = -1;
-        int32_t slot_in_page = 0;
+        // position of the token, and its cached row (of head 0; -1: it has no page)
+        int64_t p = t, row_at = -1;
         if (KIND != kNoCache) {
-            page = page_of(a.s, b, pos);
-            slot_in_page = pos & ((1 << a.s.page_shift) - 1);
-            if (page < 0 && lane == 0) raise_status(a.s.status, kErrPage);
+            int32_t b = t, first = t, n = 1;
+            if (a.s.cu) {
+                b = find_seq(a.s.cu, a.s.num_seqs, t);
+                if (b < 0) continue;
+                first = __ldg(a.s.cu + b);
+                n = __ldg(a.s.cu + b + 1) - first;
+            } else if (b >= a.s.num_seqs) {
+                continue;
+            }
+            p = (int64_t)__ldg(a.s.kv_lens + b) - n + (t - first);
+            const int64_t page = p < 0 ? -1 : page_of(a.s, b, (int32_t)p);
+            if (page >= 0) row_at = ((page * a.hkv) << a.s.page_shift) + (p & ((1 << a.s.page_shift) - 1));
+        } else if (a.positions) {
+            p = __ldg(a.positions + t);
+        } else if (a.s.cu) {
+            const int32_t b = find_seq(a.s.cu, a.s.num_seqs, t);
+            if (b < 0) continue;
+            p = t - __ldg(a.s.cu + b);
+        }
+        if (p < 0 || (a.rot > 0 && p >= a.max_pos)) {
+            if (lane == 0) raise_status(a.s.status, KIND != kNoCache && p < 0 ? kErrLength : kErrPosition);
+            continue;
+        }
+        if (KIND != kNoCache && row_at < 0 && lane == 0) raise_status(a.s.status, kErrPage);
+        const int32_t pos = (int32_t)p;
+        // angles: of pairs kV * j on, or of kV / 2 pairs of each vector
+        float c[kV], s[kV];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            if (h == 0 ? rot_a : rot_b) {
+                const int first = a.inter ? kV / 2 * (h == 0 ? oa : ob) : kV * j + kV / 2 * h;
+                const float4* cs =
+                    reinterpret_cast<const float4*>(a.table + ((int64_t)pos * (a.rot / 2) + first) * 2);
+#pragma unroll
+                for (int i = 0; i < kV / 4; ++i) {
+                    const float4 f = __ldg(cs + i);
+                    const int at = h * (kV / 2) + 2 * i;
+                    c[at] = f.x;
+                    s[at] = a.inverse ? -f.y : f.y;
+                    c[at + 1] = f.z;
+                    s[at + 1] = a.inverse ? -f.w : f.w;
+                }
+            } else {  // no turn
+#pragma unroll
+                for (int i = 0; i < kV / 2; ++i) {
+                    c[h * (kV / 2) + i] = 1.f;
+                    s[h * (kV / 2) + i] = 0.f;
+                }
+            }
         }
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
             const int slot = slot0 + u * kHpw;
             const bool live = slot < a.nslots;
             const bool is_q = slot < a.hq, is_k = !is_q && slot < a.hq + a.hkv;
-            if (live && rotated && (is_q || is_k)) {
-                float x[16];
+            if (live && (is_q || is_k) && (rot_a || rot_b)) {
+                float x[2 * kV];
                 xa[u].get(x);
-                xb[u].get(x + 8);
+                xb[u].get(x + kV);
                 if (a.inter) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) turn(x[2 * i], x[2 * i + 1], c[i], s[i]);
+                    for (int i = 0; i < kV; ++i) turn(x[2 * i], x[2 * i + 1], c[i], s[i]);
                 } else {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) turn(x[i], x[8 + i], c[i], s[i]);
+                    for (int i = 0; i < kV; ++i) turn(x[i], x[kV + i], c[i], s[i]);
                 }
-                xa[u].set(x);
-                xb[u].set(x + 8);
+                if (rot_a) xa[u].set(x);
+                if (rot_b) xb[u].set(x + kV);
             }
             if (live && is_q) {
                 void* o = (char*)a.q_out + (t * a.q_out_stride + (int64_t)slot * D) * kElem;
@@ -237,10 +260,9 @@ __global__ void __launch_bounds__(kThreads) rotate_kernel(const RotArgs a) {
                 xb[u].store(o, ob);
             }
             if (KIND != kNoCache) {
-                const bool put = live && !is_q && page >= 0;
+                const bool put = live && !is_q && row_at >= 0;
                 const int h = is_k ? slot - a.hq : slot - a.hq - a.hkv;
-                const int64_t at =
-                    ((page * a.hkv + h) << a.s.page_shift) + slot_in_page;  // cached row
+                const int64_t at = row_at + ((int64_t)h << a.s.page_shift);  // cached row
                 if (KIND == PVA_CACHE_BF16) {
                     if (put) {
                         char* o = (char*)(is_k ? a.k_pages : a.v_pages) + at * D * 2;
@@ -348,27 +370,8 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const ReadArgs a, int32_
         // the cached row (of head 0) that lane i's row is
         int64_t at = -1;
         {
-            const int32_t t = t0 + lane;
-            int32_t b = -1, i = 0;
-            if (a.s.cu) {
-                const int32_t b0 = find_seq(a.s.cu, a.s.num_seqs, t0);
-                if (lane < rows) {
-                    if (b0 >= 0 && t < __ldg(a.s.cu + b0 + 1)) {
-                        b = b0;
-                    } else {  // the run goes on into another sequence, or begins before the first
-                        int32_t lo = max(b0, 0), hi = a.s.num_seqs;
-                        while (hi - lo > 1) {
-                            const int32_t mid = lo + (hi - lo) / 2;
-                            if (__ldg(a.s.cu + mid) <= t) lo = mid;
-                            else hi = mid;
-                        }
-                        if (__ldg(a.s.cu + lo) <= t && t < __ldg(a.s.cu + lo + 1)) b = lo;
-                    }
-                    if (b >= 0) i = t - __ldg(a.s.cu + b);
-                }
-            } else if (lane < rows && t < a.s.num_seqs) {
-                b = t;
-            }
+            const int32_t t = t0 + lane, b = seq_of_lane(a.s, t0, rows);
+            const int32_t i = b >= 0 && a.s.cu ? t - __ldg(a.s.cu + b) : 0;
             if (b >= 0) {
                 const int64_t pos = (a.starts ? __ldg(a.starts + b) : 0) + (int64_t)i;
                 const int64_t page = pos > INT32_MAX ? -1 : page_of(a.s, b, (int32_t)pos);
@@ -424,7 +427,7 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const ReadArgs a, int32_
 #pragma unroll
                         for (int e = 0; e < 8; ++e)
                             f[e] = __fadd_rn(low, __fmul_rn((float)((w >> (4 * (e / 2) + 16 * (e % 2))) & 15u), scale));
-                        Octet<false> y;
+                        Vec<false> y;
                         y.set(f);
                         out[8 * g + o] = y.r;
                     }
@@ -434,22 +437,28 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const ReadArgs a, int32_
     }
 }
 
-// CTAs along the tokens: enough for every SM to hold eight, then a stride.
-int grid_x(int64_t tokens, int grid_y) {
+int sm_count() {
     int dev = 0, sms = 148;
     if (cudaGetDevice(&dev) == cudaSuccess)
         cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    const int64_t blocks = (tokens + kWarps - 1) / kWarps;
+    return sms;
+}
+
+// CTAs along the runs: up to 64 on an SM, then a stride.
+int grid_x(int64_t tokens, int32_t run, int grid_y, int sms) {
+    const int64_t blocks = ((tokens + run - 1) / run + kWarps - 1) / kWarps;
     const int64_t cap = ((int64_t)sms * 64 + grid_y - 1) / grid_y;
     return (int)(blocks < cap ? (blocks > 0 ? blocks : 1) : cap);
 }
 
 template <int D, bool F32, int KIND>
 pva_status launch_rotate(const RotArgs& a, cudaStream_t st) {
-    constexpr int per = (F32 ? 2 : 4) * (32 / (D / 16));
+    constexpr int per = Unroll<F32, KIND>::value * (32 / (D / (2 * Vec<F32>::kDims)));
     const int gy = (a.nslots + per - 1) / per;
     if (gy > 65535) return PVA_ERR_UNSUPPORTED;
-    rotate_kernel<D, F32, KIND><<<dim3(grid_x(a.s.num_tokens, gy), gy), kThreads, 0, st>>>(a);
+    const int sms = sm_count();
+    rotate_kernel<D, F32, KIND>
+        <<<dim3(grid_x(a.s.num_tokens, 1, gy, sms), gy), kThreads, 0, st>>>(a);
     return cudaGetLastError() == cudaSuccess ? PVA_OK : PVA_ERR_CUDA;
 }
 
@@ -457,15 +466,10 @@ template <int D, int KIND>
 pva_status launch_read(const ReadArgs& a, cudaStream_t st) {
     if ((2 * (int64_t)a.hkv * (KIND == PVA_CACHE_INT4 ? 8 : D / 8) + 31) / 32 > 176)
         return PVA_ERR_UNSUPPORTED;  // the kernel's division (704 kv heads of 64 dims, 352 of 128)
-    // runs as long as leave every SM two CTAs of work
-    int dev = 0, sms = 148;
-    if (cudaGetDevice(&dev) == cudaSuccess)
-        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    int32_t run = 32;
-    while (run > 1 && (int64_t)a.s.num_tokens / run < (int64_t)sms * 2 * kWarps) run /= 2;
-    const int64_t blocks = (((int64_t)a.s.num_tokens + run - 1) / run + kWarps - 1) / kWarps;
-    const int64_t cap = (int64_t)sms * 64;
-    read_kernel<D, KIND><<<(int)(blocks < cap ? blocks : cap), kThreads, 0, st>>>(a, run);
+    const int sms = sm_count();
+    int32_t run = 32;  // as many rows a warp as leave every SM two CTAs of work
+    while (run > 1 && a.s.num_tokens / run < sms * 2 * kWarps) run /= 2;
+    read_kernel<D, KIND><<<grid_x(a.s.num_tokens, run, 1, sms), kThreads, 0, st>>>(a, run);
     return cudaGetLastError() == cudaSuccess ? PVA_OK : PVA_ERR_CUDA;
 }
 
