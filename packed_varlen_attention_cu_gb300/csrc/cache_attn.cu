@@ -32,6 +32,7 @@ namespace {
 
 constexpr int kMaxCtas = 512;   // pieces the workspace has room for
 constexpr int kFixedUnits = 1;  // an item's fixed cost, in blocks of keys
+constexpr int64_t kSpreadRows = 1024;  // rows (tokens * heads) up to which the join spreads a row
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 // The running maximum moves only when a tile exceeds it by 2^8: weights stay below
@@ -186,6 +187,10 @@ __device__ __forceinline__ SeqInfo seq_info(const AttnArgs& a, int32_t b, bool t
     s.nb = max((s.khi + BLOCK - 1) / BLOCK - s.blo, 0);
     return s;
 }
+// x / y of whole numbers >= 0, by 32 bits where they fit.
+__device__ __forceinline__ int64_t quotient(int64_t x, int64_t y) {
+    return ((x | y) >> 32) == 0 ? (int64_t)((uint32_t)x / (uint32_t)y) : x / y;
+}
 __device__ __forceinline__ int64_t units_of(const AttnArgs& a, const SeqInfo& s) {
     return (int64_t)a.hkv * s.nrb * (kFixedUnits + s.nb);
 }
@@ -216,6 +221,8 @@ __global__ void __launch_bounds__(Shape<D, KIND, NT, H>::kThreads, Shape<D, KIND
     constexpr int G = Sh::kGroups, T = Sh::kTiles, BLOCK = Sh::kBlock, ROWB = Sh::kRowBytes;
     constexpr bool INT4 = Sh::kInt4;
     extern __shared__ __align__(128) uint8_t smem[];
+    // the join waits for the end of this grid; its launch need not
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, c = lane & 3;
     uint8_t* ring = smem + warp * S * Sh::kStageBytes;
@@ -252,7 +259,7 @@ __global__ void __launch_bounds__(Shape<D, KIND, NT, H>::kThreads, Shape<D, KIND
             total += wsum[w];
         }
         inc += before;
-        int64_t per = (total + gridDim.x - 1) / gridDim.x;
+        int64_t per = quotient(total + gridDim.x - 1, gridDim.x);
         per = max(per, (int64_t)kFixedUnits + 1);
         u0 = per * blockIdx.x;
         u1 = min(u0 + per, total);
@@ -288,7 +295,7 @@ __global__ void __launch_bounds__(Shape<D, KIND, NT, H>::kThreads, Shape<D, KIND
     SeqInfo sq = seq_info<R, BLOCK>(a, b, false);
     const int32_t* pages = a.s.page_table + b * a.s.table_stride;
     int32_t len = kFixedUnits + sq.nb;
-    it = (int32_t)((u0 - ub) / len);
+    it = (int32_t)quotient(u0 - ub, len);
     int32_t rb = it / a.hkv, kvh = it - rb * a.hkv;
     int64_t ui = ub + (int64_t)it * len;  // first unit of the item
     int32_t key = 0, kend = 0;            // the pending step's first key; where the item's steps end
@@ -509,8 +516,7 @@ __global__ void __launch_bounds__(Shape<D, KIND, NT, H>::kThreads, Shape<D, KIND
     };
 
     for (int step = 0, stage = 0; step < issued; ++step, stage = stage + 1 == S ? 0 : stage + 1) {
-        cp_wait<S - 2>();
-        __syncwarp();  // every lane's copies are in, and the stage before this one is read
+        __syncwarp();  // the stage before this one is read
         const int32_t flags = queue[0];
         queue[S - 1] = 0;
         if (more) {
@@ -590,6 +596,8 @@ __global__ void __launch_bounds__(Shape<D, KIND, NT, H>::kThreads, Shape<D, KIND
                     pos[nt][e] = pos0 + min(r0 + (H ? (2 * c + e) & 3 : 8 * nt + 2 * c + e), rows - 1) / a.group;
             }
         }
+        cp_wait<S - 1>();
+        __syncwarp();  // every lane's copies of this step are in
         if (!(flags & kEmpty)) {
             const bool partial = flags & kPartial;
             int32_t key0 = 0, vlo = 0, vhi = 0, missing = 0;
@@ -956,77 +964,100 @@ __global__ void __launch_bounds__(Shape<D, KIND, NT, H>::kThreads, Shape<D, KIND
             __syncthreads();  // the sums are read: the stages may be filled again
         }
     }
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
 // Joins the partial sums of every item that was cut, in the order of the pieces.
-// One warp a row where there are many rows, a CTA's four warps where there are few.
-template <int D, int KIND, int NT, bool H, bool WIDE>
-__global__ void __launch_bounds__(128) join_kernel(const AttnArgs a) {
+// What it costs is latency: one load for the piece, one for the sums.  So a row's
+// partials are spread over WARPS warps, four at a time in flight in each, and every warp
+// keeps its own maximum until the end.  (32 partials of a row of 128: 13 us with one warp,
+// 3 us with eight.)  Where rows are many, pieces are few and each warp takes a row.
+template <int D, int KIND, int NT, bool H, int WARPS>
+__global__ void __launch_bounds__(256) join_kernel(const AttnArgs a) {
     using Sh = Shape<D, KIND, NT, H>;
-    constexpr int R = Sh::R, E = D / 32, WS = WIDE ? 4 : 1;
-    __shared__ float sm_o[WIDE ? 4 : 1][D], sm_m[4], sm_l[4];
+    constexpr int R = Sh::R, E = D / 32;
+    __shared__ float sm_o[WARPS][D], sm_m[WARPS], sm_l[WARPS];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int64_t row = WIDE ? blockIdx.x : (int64_t)blockIdx.x * 4 + warp;
-    const int32_t t = (int32_t)(row / a.hq), h = (int32_t)(row - (int64_t)t * a.hq);
+    const int64_t row = WARPS > 1 ? blockIdx.x : (int64_t)blockIdx.x * 8 + warp;
+    const int32_t t = (int32_t)quotient(row, a.hq), h = (int32_t)(row - (int64_t)t * a.hq);
     if (t >= a.s.num_tokens) return;
     int32_t b = t;
     if (a.s.cu) b = find_seq(a.s.cu, a.s.num_seqs, t);
     if (b < 0 || b >= a.s.num_seqs) return;
     const SeqInfo s = seq_info<R, Sh::kBlock>(a, b, false);
     if (s.nb == 0 || t - s.row0 >= s.n) return;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int32_t kvh = h / a.group;
     const int64_t rr = (int64_t)(t - s.row0) * a.group + h - kvh * a.group;
     const int32_t rb = (int32_t)(rr / R), r = (int32_t)(rr - (int64_t)rb * R);
     const int64_t per = *a.ws_per, first = a.ws_cum[b] + ((int64_t)rb * a.hkv + kvh) * (kFixedUnits + s.nb);
-    const int32_t cf = (int32_t)((first + kFixedUnits) / per);
-    const int32_t cl = (int32_t)((first + kFixedUnits + s.nb - 1) / per);
+    const int32_t cf = (int32_t)quotient(first + kFixedUnits, per);
+    const int32_t cl = (int32_t)quotient(first + kFixedUnits + s.nb - 1, per);
     if (cf == cl) return;  // one piece holds it all
     const int32_t n = cl - cf + 1;
-    auto at = [&](int k) { return (int64_t)(k == 0 ? 2 * cf + 1 : 2 * (cf + k)) * R + r; };
-    float mm = -INFINITY;
-    for (int k = lane; k < n; k += 32) mm = fmaxf(mm, a.ws_ml[at(k)].x);
-#pragma unroll
-    for (int o = 16; o; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
-    float l = 0.f, acc[E];
+    float mm = -INFINITY, l = 0.f, acc[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] = 0.f;
-#pragma unroll 4
-    for (int k = WIDE ? warp : 0; k < n; k += WS) {
-        const float2 ml = a.ws_ml[at(k)];
-        const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - mm);
-        const float* src = a.ws_o + at(k) * D + lane * E;
-        l = fmaf(f, ml.y, l);
-        if (E == 4) {
-            const float4 v = *reinterpret_cast<const float4*>(src);
-            acc[0] = fmaf(f, v.x, acc[0]);
-            acc[1] = fmaf(f, v.y, acc[1]);
-            acc[E - 2] = fmaf(f, v.z, acc[E - 2]);
-            acc[E - 1] = fmaf(f, v.w, acc[E - 1]);
-        } else {
-            const float2 v = *reinterpret_cast<const float2*>(src);
-            acc[0] = fmaf(f, v.x, acc[0]);
-            acc[1] = fmaf(f, v.y, acc[1]);
-        }
-    }
-    if (WIDE) {
+    for (int k0 = WARPS > 1 ? warp : 0; k0 < n; k0 += 4 * WARPS) {
+        float2 ml[4];
+        float v[4][E];
 #pragma unroll
-        for (int e = 0; e < E; ++e) sm_o[WIDE ? warp : 0][lane * E + e] = acc[e];
-        if (lane == 0) sm_l[warp] = l;
+        for (int u = 0; u < 4; ++u) {  // (past the end the last one again, with weight 0)
+            const int k = min(k0 + u * WARPS, n - 1);
+            const int64_t at = (int64_t)(k == 0 ? 2 * cf + 1 : 2 * (cf + k)) * R + r;
+            ml[u] = a.ws_ml[at];
+            const float* src = a.ws_o + at * D + lane * E;
+            if (E == 4) {
+                const float4 f = *reinterpret_cast<const float4*>(src);
+                v[u][0] = f.x;
+                v[u][1] = f.y;
+                v[u][E - 2] = f.z;
+                v[u][E - 1] = f.w;
+            } else {
+                const float2 f = *reinterpret_cast<const float2*>(src);
+                v[u][0] = f.x;
+                v[u][1] = f.y;
+            }
+        }
+        float mn = mm;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) mn = fmaxf(mn, ml[u].x);
+        const float old = mm == -INFINITY ? 0.f : ex2(mm - mn);
+        l *= old;
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] *= old;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const float f = k0 + u * WARPS >= n || ml[u].x == -INFINITY ? 0.f : ex2(ml[u].x - mn);
+            // (a weight of 0 must not meet a NaN of sums that are not this row's)
+            l += f == 0.f ? 0.f : f * ml[u].y;
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[e] += f == 0.f ? 0.f : f * v[u][e];
+        }
+        mm = mn;
+    }
+    if (WARPS > 1) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) sm_o[warp][lane * E + e] = acc[e];
+        if (lane == 0) {
+            sm_m[warp] = mm;
+            sm_l[warp] = l;
+        }
         __syncthreads();
         if (warp > 0) return;
+        mm = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w) mm = fmaxf(mm, sm_m[w]);
         l = 0.f;
 #pragma unroll
         for (int e = 0; e < E; ++e) acc[e] = 0.f;
 #pragma unroll
-        for (int w = 0; w < WS; ++w) {
-            l += sm_l[w];
+        for (int w = 0; w < WARPS; ++w) {
+            const float f = sm_m[w] == -INFINITY ? 0.f : ex2(sm_m[w] - mm);
+            l = fmaf(f, sm_l[w], l);
 #pragma unroll
-            for (int e = 0; e < E; ++e) acc[e] += sm_o[WIDE ? w : 0][lane * E + e];
+            for (int e = 0; e < E; ++e) acc[e] = fmaf(f, sm_o[w][lane * E + e], acc[e]);
         }
     }
-    (void)sm_m;
     const float inv = l != 0.f ? 1.f / l : 0.f;
     const int64_t to = ((int64_t)t * a.hq + h) * D + lane * E;
 #pragma unroll
@@ -1067,18 +1098,18 @@ pva_status launch(AttnArgs a, uint8_t* ws, cudaStream_t st) {
     attn_kernel<D, KIND, NT, H><<<ctas, Sh::kThreads, Sh::kSmem, st>>>(a);
     if (cudaGetLastError() != cudaSuccess) return PVA_ERR_CUDA;
     const int64_t rows = (int64_t)a.s.num_tokens * a.hq;
-    const bool wide = rows <= 2048;
+    const bool spread = rows <= kSpreadRows;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(wide ? rows : (rows + 3) / 4));
-    cfg.blockDim = dim3(128);
+    cfg.gridDim = dim3((unsigned)(spread ? rows : (rows + 7) / 8));
+    cfg.blockDim = dim3(256);
     cfg.stream = st;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    const cudaError_t e = wide ? cudaLaunchKernelEx(&cfg, join_kernel<D, KIND, NT, H, true>, a)
-                               : cudaLaunchKernelEx(&cfg, join_kernel<D, KIND, NT, H, false>, a);
+    const cudaError_t e = spread ? cudaLaunchKernelEx(&cfg, join_kernel<D, KIND, NT, H, 8>, a)
+                                 : cudaLaunchKernelEx(&cfg, join_kernel<D, KIND, NT, H, 1>, a);
     return e == cudaSuccess ? PVA_OK : PVA_ERR_CUDA;
 }
 
