@@ -302,8 +302,9 @@ __global__ void __launch_bounds__(Shape<D, KIND, NT, H>::kThreads, Shape<D, KIND
     int32_t rlo = 0, rhi = 0;             // keys that some row of the block may see
     int32_t alo = 0, ahi = 0;             // keys that every row of it sees
     int32_t slot = 0, flags_next = 0;
-    uint32_t page[SUB];
-    bool more = true;   // a step is pending
+    uint32_t page = 0;     // lane x < SUB: of the pending step's keys 16x ..
+    bool more = true;      // the piece may have another step
+    bool pending = false;  // a step waits to be copied
     bool fresh = true;  // the cursor stands before its first item
 
     // The item at the cursor: false where this piece has no block of it.
@@ -337,6 +338,7 @@ __global__ void __launch_bounds__(Shape<D, KIND, NT, H>::kThreads, Shape<D, KIND
         return true;
     };
     auto next = [&]() {
+        pending = false;
         key += BLOCK;
         flags_next &= kWhole;
         if (key >= kend) {
@@ -349,7 +351,7 @@ __global__ void __launch_bounds__(Shape<D, KIND, NT, H>::kThreads, Shape<D, KIND
                             rb = 0;
                             do {
                                 if (++b >= a.s.num_seqs) {
-                                    more = false;
+                                    more = pending = false;
                                     return;
                                 }
                                 sq = seq_info<R, BLOCK>(a, b, false);
@@ -366,19 +368,13 @@ __global__ void __launch_bounds__(Shape<D, KIND, NT, H>::kThreads, Shape<D, KIND
                 }
                 if (open_item()) break;
             }
-            if (flags_next & kEmpty) return;
         }
+        pending = true;
+        if (key >= kend) return;  // an empty step
         if (key + BLOCK >= kend) flags_next |= kLast;
         if (key < alo || key + KS > ahi) flags_next |= kPartial;
-        const int32_t i = key >> a.s.page_shift;  // below max_pages: key < rhi
-        page[0] = (uint32_t)__ldg(pages + i);
-        if (!one_page) {
-#pragma unroll
-            for (int x = 1; x < SUB; ++x) {
-                const int32_t y = (key + 16 * x) >> a.s.page_shift;
-                page[x] = y < a.s.max_pages ? (uint32_t)__ldg(pages + y) : ~0u;
-            }
-        }
+        const int32_t i = (key + 16 * min(lane, SUB - 1)) >> a.s.page_shift;
+        page = lane < SUB && i < a.s.max_pages ? (uint32_t)__ldg(pages + i) : ~0u;
     };
     // N * 16 keys from byte `off` of a page's K and V on, into tile x of a stage;
     // [vlo, vhi): rows of the first 16 that are there.
@@ -421,42 +417,36 @@ __global__ void __launch_bounds__(Shape<D, KIND, NT, H>::kThreads, Shape<D, KIND
             }
         }
     };
-    // Copies of the pending step into a stage, and the next step.  Returns the step's flags.
+    // Copies of the pending step into a stage.  Returns the step's flags.
     auto issue = [&](int stage) -> int32_t {
         const uint32_t kd = smem_addr(ring + stage * Sh::kStageBytes);
         int32_t flags = flags_next, missing = 0;
         if (!(flags & kEmpty)) {
             const uint32_t mask = (1u << a.s.page_shift) - 1;
             const uint32_t head = (uint32_t)kvh << a.s.page_shift;
-            bool there = page[0] < a.num_pages;
-            if (!one_page) {
+            if (!__all_sync(0xffffffffu, lane >= SUB || page < a.num_pages)) flags |= kPartial;
+            if (one_page && !(flags & kPartial)) {
+                copy(Const<SUB>(), kd, 0,
+                     (uint64_t)__shfl_sync(0xffffffffu, page, 0) * a.page_bytes + (head + (key & mask)) * ROWB, 0, 16);
+            } else if (!(flags & kPartial)) {
 #pragma unroll
-                for (int x = 1; x < SUB; ++x) there &= page[x] < a.num_pages;
-            }
-            if (there && !(flags & kPartial)) {
-                if (one_page) {
-                    copy(Const<SUB>(), kd, 0,
-                         (uint64_t)page[0] * a.page_bytes + (head + (key & mask)) * ROWB, 0, 16);
-                } else {
-#pragma unroll
-                    for (int x = 0; x < SUB; ++x)
-                        copy(Const<1>(), kd, x,
-                             (uint64_t)page[x] * a.page_bytes + (head + ((key + 16 * x) & mask)) * ROWB, 0, 16);
-                }
+                for (int x = 0; x < SUB; ++x)
+                    copy(Const<1>(), kd, x,
+                         (uint64_t)__shfl_sync(0xffffffffu, page, x) * a.page_bytes +
+                             (head + ((key + 16 * x) & mask)) * ROWB, 0, 16);
             } else {
-                flags |= kPartial;
-#pragma unroll
+#pragma unroll 1
                 for (int x = 0; x < SUB; ++x) {
                     const int32_t k = key + 16 * x;
-                    const uint32_t p = one_page ? page[0] : page[x];
+                    const uint32_t p = __shfl_sync(0xffffffffu, page, x);
                     const int lo = max(rlo - k, 0), hi = min(rhi - k, 16);
-                    if (p < a.num_pages) {
-                        copy(Const<1>(), kd, x, (uint64_t)p * a.page_bytes + (head + (k & mask)) * ROWB, lo, hi);
-                    } else {
+                    const bool there = p < a.num_pages;
+                    const uint64_t off = (uint64_t)p * a.page_bytes + (head + (k & mask)) * ROWB;
+                    if (!there) {
                         missing |= 1 << x;
-                        if (!INT4) copy(Const<1>(), kd, x, 0, 0, 0);
                         if (lane == 0 && lo < hi) raise_status(a.s.status, kErrPage);
                     }
+                    if (!INT4 || there) copy(Const<1>(), kd, x, there ? off : 0, lo, there ? hi : 0);
                 }
             }
         }
@@ -466,22 +456,8 @@ __global__ void __launch_bounds__(Shape<D, KIND, NT, H>::kThreads, Shape<D, KIND
             *reinterpret_cast<int4*>(&m.row0) = make_int4(sq.row0, sq.n * a.group, sq.pos0, rb);
             *reinterpret_cast<int2*>(&m.kvh) = make_int2(kvh, slot);
         }
-        next();
         return flags;
     };
-
-    next();
-    int issued = 0;
-    int32_t queue[S];  // flags of the steps in flight
-#pragma unroll
-    for (int i = 0; i < S - 1; ++i) {
-        queue[i] = 0;
-        if (more) {
-            queue[i] = issue(i);
-            ++issued;
-        }
-        cp_commit();
-    }
 
     // ---- state of the item in hand
     // Scores stay as the products leave them; weights are 2^(c s + shift), shift = -c m
@@ -515,17 +491,27 @@ __global__ void __launch_bounds__(Shape<D, KIND, NT, H>::kThreads, Shape<D, KIND
                 sc[y][gr] = missing || j + 8 * y < vlo || j + 8 * y >= vhi ? 0u : sc[y][gr];
     };
 
-    for (int step = 0, stage = 0; step < issued; ++step, stage = stage + 1 == S ? 0 : stage + 1) {
+    // Each turn copies step `step + S - 1` (the first turn finds the first step only), then
+    // takes step `step`: one place for everything, since short contexts run through the code
+    // once and wait for its instructions.
+    int32_t queue[S];  // flags of the steps in flight
+#pragma unroll
+    for (int i = 0; i < S; ++i) queue[i] = 0;
+    int issued = 0;
+#pragma unroll 1
+    for (int step = -S, stage = 0;; ++step, stage = stage + 1 == S ? 0 : stage + 1) {
         __syncwarp();  // the stage before this one is read
-        const int32_t flags = queue[0];
-        queue[S - 1] = 0;
-        if (more) {
+#pragma unroll
+        for (int i = 0; i + 1 < S; ++i) queue[i] = queue[i + 1];
+        if (pending) {
             queue[S - 1] = issue(stage == 0 ? S - 1 : stage - 1);
             ++issued;
         }
         cp_commit();
-#pragma unroll
-        for (int i = 0; i < S - 1; ++i) queue[i] = queue[i + 1];
+        if (more) next();
+        if (step < 0) continue;
+        if (step >= issued) break;
+        const int32_t flags = queue[0];
         const uint8_t* buf = ring + stage * Sh::kStageBytes;
         const Meta& mt = meta[stage];
         if (flags & kFirst) {
