@@ -7,6 +7,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../../include/pva.h"
 
 namespace pva {
@@ -35,6 +37,46 @@ __device__ __forceinline__ int32_t find_seq(const int32_t* __restrict__ cu, int3
         hi = min(hi, lo + step);
     }
     return (n > 0 && __ldg(cu + lo) <= t && t < __ldg(cu + lo + 1)) ? lo : -1;
+}
+
+// Dependent launches.  Every kernel of these calls lets the next kernel of the stream be
+// launched at once and then waits for the end of the one before it, so that a chain of
+// short kernels (append, attention, join) pays for a launch once.  All its reads and
+// writes come after the wait, except of what was there before the kernel before it; no
+// thread block leaves without having waited, so that the end of a kernel is the end of
+// all before it.
+__device__ __forceinline__ void launch_next() {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void wait_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+template <typename... P, typename... A>
+inline cudaError_t launch_after(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st,
+                                const A&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+}
+
+constexpr int kMaxDevices = 64;
+
+// SMs of the current device (asked once for each), or 0.
+inline int sm_count() {
+    static std::atomic<int> known[kMaxDevices];
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return 0;
+    if (dev < kMaxDevices && (sms = known[dev].load(std::memory_order_relaxed)) > 0) return sms;
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+    if (dev < kMaxDevices) known[dev].store(sms, std::memory_order_relaxed);
+    return sms;
 }
 
 // The sequences of one call, as pva_cache_batch describes them.

@@ -221,8 +221,8 @@ __global__ void __launch_bounds__(Shape<D, KIND, NT, H>::kThreads, Shape<D, KIND
     constexpr int G = Sh::kGroups, T = Sh::kTiles, BLOCK = Sh::kBlock, ROWB = Sh::kRowBytes;
     constexpr bool INT4 = Sh::kInt4;
     extern __shared__ __align__(128) uint8_t smem[];
-    // the join waits for the end of this grid; its launch need not
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    launch_next();
+    wait_previous();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, c = lane & 3;
     uint8_t* ring = smem + warp * S * Sh::kStageBytes;
@@ -965,13 +965,15 @@ __global__ void __launch_bounds__(256) join_kernel(const AttnArgs a) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t row = WARPS > 1 ? blockIdx.x : (int64_t)blockIdx.x * 8 + warp;
     const int32_t t = (int32_t)quotient(row, a.hq), h = (int32_t)(row - (int64_t)t * a.hq);
-    if (t >= a.s.num_tokens) return;
+    launch_next();
+    // (the lengths were there before the attention began)
     int32_t b = t;
-    if (a.s.cu) b = find_seq(a.s.cu, a.s.num_seqs, t);
-    if (b < 0 || b >= a.s.num_seqs) return;
-    const SeqInfo s = seq_info<R, Sh::kBlock>(a, b, false);
-    if (s.nb == 0 || t - s.row0 >= s.n) return;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (a.s.cu && t < a.s.num_tokens) b = find_seq(a.s.cu, a.s.num_seqs, t);
+    const bool any = t < a.s.num_tokens && b >= 0 && b < a.s.num_seqs;
+    SeqInfo s = {};
+    if (any) s = seq_info<R, Sh::kBlock>(a, b, false);
+    wait_previous();
+    if (!any || s.nb == 0 || t - s.row0 >= s.n) return;
     const int32_t kvh = h / a.group;
     const int64_t rr = (int64_t)(t - s.row0) * a.group + h - kvh * a.group;
     const int32_t rb = (int32_t)(rr / R), r = (int32_t)(rr - (int64_t)rb * R);
@@ -1073,29 +1075,19 @@ pva_status launch(AttnArgs a, uint8_t* ws, cudaStream_t st) {
     ws += 256 + up256((size_t)a.s.num_seqs * 8);
     a.ws_ml = reinterpret_cast<float2*>(ws);
     a.ws_o = reinterpret_cast<float*>(ws + (size_t)2 * kMaxCtas * Sh::R * 8);
-    int dev = 0, sms = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-        return PVA_ERR_CUDA;
+    const int sms = sm_count();
+    if (sms <= 0) return PVA_ERR_CUDA;
     const int ctas = sms * Sh::kCtas < kMaxCtas ? sms * Sh::kCtas : kMaxCtas;
     if (cudaFuncSetAttribute(attn_kernel<D, KIND, NT, H>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              Sh::kSmem) != cudaSuccess)
         return PVA_ERR_CUDA;
-    attn_kernel<D, KIND, NT, H><<<ctas, Sh::kThreads, Sh::kSmem, st>>>(a);
-    if (cudaGetLastError() != cudaSuccess) return PVA_ERR_CUDA;
+    if (launch_after(attn_kernel<D, KIND, NT, H>, dim3(ctas), Sh::kThreads, Sh::kSmem, st, a) != cudaSuccess)
+        return PVA_ERR_CUDA;
     const int64_t rows = (int64_t)a.s.num_tokens * a.hq;
     const bool spread = rows <= kSpreadRows;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(spread ? rows : (rows + 7) / 8));
-    cfg.blockDim = dim3(256);
-    cfg.stream = st;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    const cudaError_t e = spread ? cudaLaunchKernelEx(&cfg, join_kernel<D, KIND, NT, H, 8>, a)
-                                 : cudaLaunchKernelEx(&cfg, join_kernel<D, KIND, NT, H, 1>, a);
+    const dim3 grid((unsigned)(spread ? rows : (rows + 7) / 8));
+    const cudaError_t e = spread ? launch_after(join_kernel<D, KIND, NT, H, 8>, grid, 256, 0, st, a)
+                                 : launch_after(join_kernel<D, KIND, NT, H, 1>, grid, 256, 0, st, a);
     return e == cudaSuccess ? PVA_OK : PVA_ERR_CUDA;
 }
 

@@ -140,6 +140,8 @@ __global__ void __launch_bounds__(kThreads, 3) rotate_kernel(const RotArgs a) {
     constexpr int kHpw = 32 / kLph;      // heads a pass
     constexpr int kUnroll = Unroll<F32, KIND>::value;
     constexpr int kElem = F32 ? 4 : 2;
+    launch_next();
+    wait_previous();
     const int lane = threadIdx.x & 31;
     const int j = lane % kLph, sub = lane / kLph;
     const int pairs = a.rot / (2 * kV);  // vectors of the first half of the rotated dims
@@ -357,6 +359,8 @@ template <int D, int KIND>
 __global__ void __launch_bounds__(kThreads) read_kernel(const ReadArgs a, int32_t run) {
     constexpr bool kInt4 = KIND == PVA_CACHE_INT4;
     constexpr int kLph = kInt4 ? 8 : D / 8, kHpw = 32 / kLph, kUnroll = 4, kG = D / 64;
+    launch_next();
+    wait_previous();
     const int lane = threadIdx.x & 31;
     const int o = lane % kLph, sub = lane / kLph;
     const int ppr = (2 * a.hkv + kHpw - 1) / kHpw;  // passes a row
@@ -437,13 +441,6 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const ReadArgs a, int32_
     }
 }
 
-int sm_count() {
-    int dev = 0, sms = 148;
-    if (cudaGetDevice(&dev) == cudaSuccess)
-        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    return sms;
-}
-
 // CTAs along the runs: up to 64 on an SM, then a stride.
 int grid_x(int64_t tokens, int32_t run, int grid_y, int sms) {
     const int64_t blocks = ((tokens + run - 1) / run + kWarps - 1) / kWarps;
@@ -457,9 +454,10 @@ pva_status launch_rotate(const RotArgs& a, cudaStream_t st) {
     const int gy = (a.nslots + per - 1) / per;
     if (gy > 65535) return PVA_ERR_UNSUPPORTED;
     const int sms = sm_count();
-    rotate_kernel<D, F32, KIND>
-        <<<dim3(grid_x(a.s.num_tokens, 1, gy, sms), gy), kThreads, 0, st>>>(a);
-    return cudaGetLastError() == cudaSuccess ? PVA_OK : PVA_ERR_CUDA;
+    if (sms <= 0) return PVA_ERR_CUDA;
+    const dim3 grid(grid_x(a.s.num_tokens, 1, gy, sms), gy);
+    return launch_after(rotate_kernel<D, F32, KIND>, grid, kThreads, 0, st, a) == cudaSuccess ? PVA_OK
+                                                                                              : PVA_ERR_CUDA;
 }
 
 template <int D, int KIND>
@@ -467,10 +465,12 @@ pva_status launch_read(const ReadArgs& a, cudaStream_t st) {
     if ((2 * (int64_t)a.hkv * (KIND == PVA_CACHE_INT4 ? 8 : D / 8) + 31) / 32 > 176)
         return PVA_ERR_UNSUPPORTED;  // the kernel's division (704 kv heads of 64 dims, 352 of 128)
     const int sms = sm_count();
+    if (sms <= 0) return PVA_ERR_CUDA;
     int32_t run = 32;  // as many rows a warp as leave every SM two CTAs of work
     while (run > 1 && a.s.num_tokens / run < sms * 2 * kWarps) run /= 2;
-    read_kernel<D, KIND><<<grid_x(a.s.num_tokens, run, 1, sms), kThreads, 0, st>>>(a, run);
-    return cudaGetLastError() == cudaSuccess ? PVA_OK : PVA_ERR_CUDA;
+    const dim3 grid(grid_x(a.s.num_tokens, run, 1, sms));
+    return launch_after(read_kernel<D, KIND>, grid, kThreads, 0, st, a, run) == cudaSuccess ? PVA_OK
+                                                                                            : PVA_ERR_CUDA;
 }
 
 // The angle table: rot_dim 0 (or no descriptor) means no rotation.
