@@ -20,7 +20,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 enum { kNoCache = -1 };
-// Passes whose loads a lane has in flight.
+// Passes whose loads a lane has in flight, where there is work for every SM.
 template <bool F32, int KIND>
 struct Unroll {
     static constexpr int value = F32 ? 4 : KIND == kNoCache ? 5 : 3;
@@ -133,12 +133,11 @@ __device__ __forceinline__ int32_t seq_of_lane(const SeqView& s, int32_t t0, int
 // Bounded by HBM; three CTAs an SM (85 registers) measured best: 131072 tokens of 40 heads
 // of 128, bf16: 472 us without the bound, 415 us with it (96% of the copy rate), 454 us
 // with four.
-template <int D, bool F32, int KIND>
+template <int D, bool F32, int KIND, int kUnroll>
 __global__ void __launch_bounds__(kThreads, 3) rotate_kernel(const RotArgs a) {
     constexpr int kV = Vec<F32>::kDims;
     constexpr int kLph = D / (2 * kV);   // lanes a head
     constexpr int kHpw = 32 / kLph;      // heads a pass
-    constexpr int kUnroll = Unroll<F32, KIND>::value;
     constexpr int kElem = F32 ? 4 : 2;
     launch_next();
     wait_previous();
@@ -448,16 +447,28 @@ int grid_x(int64_t tokens, int32_t run, int grid_y, int sms) {
     return (int)(blocks < cap ? (blocks > 0 ? blocks : 1) : cap);
 }
 
-template <int D, bool F32, int KIND>
-pva_status launch_rotate(const RotArgs& a, cudaStream_t st) {
-    constexpr int per = Unroll<F32, KIND>::value * (32 / (D / (2 * Vec<F32>::kDims)));
+template <int D, bool F32, int KIND, int kUnroll>
+pva_status launch_unrolled(const RotArgs& a, int sms, cudaStream_t st) {
+    constexpr int per = kUnroll * (32 / (D / (2 * Vec<F32>::kDims)));
     const int gy = (a.nslots + per - 1) / per;
     if (gy > 65535) return PVA_ERR_UNSUPPORTED;
+    const dim3 grid(grid_x(a.s.num_tokens, 1, gy, sms), gy);
+    return launch_after(rotate_kernel<D, F32, KIND, kUnroll>, grid, kThreads, 0, st, a) == cudaSuccess
+               ? PVA_OK
+               : PVA_ERR_CUDA;
+}
+
+// A few tokens take one pass a warp: what they cost is latency (96 tokens of 24 heads into
+// 4 bits: 5.7 us with three passes a warp, 3.6 us with one).
+template <int D, bool F32, int KIND>
+pva_status launch_rotate(const RotArgs& a, cudaStream_t st) {
     const int sms = sm_count();
     if (sms <= 0) return PVA_ERR_CUDA;
-    const dim3 grid(grid_x(a.s.num_tokens, 1, gy, sms), gy);
-    return launch_after(rotate_kernel<D, F32, KIND>, grid, kThreads, 0, st, a) == cudaSuccess ? PVA_OK
-                                                                                              : PVA_ERR_CUDA;
+    constexpr int per = 32 / (D / (2 * Vec<F32>::kDims));
+    const int64_t warps = (int64_t)a.s.num_tokens * ((a.nslots + per - 1) / per);
+    return warps <= (int64_t)sms * 3 * kWarps
+               ? launch_unrolled<D, F32, KIND, 1>(a, sms, st)
+               : launch_unrolled<D, F32, KIND, Unroll<F32, KIND>::value>(a, sms, st);
 }
 
 template <int D, int KIND>
