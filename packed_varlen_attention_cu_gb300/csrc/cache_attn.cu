@@ -31,7 +31,6 @@ namespace pva {
 namespace {
 
 constexpr int kMaxCtas = 512;   // pieces the workspace has room for
-constexpr int kFixedUnits = 1;  // an item's fixed cost, in blocks of keys
 constexpr int64_t kSpreadRows = 1024;  // rows (tokens * heads) up to which the join spreads a row
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -68,6 +67,10 @@ struct Shape {
     static constexpr int kCols = 8 * NT;     // columns of S^T
     static constexpr int R = H ? 4 : kCols;  // rows of an item
     static constexpr int kThreads = 32 * kWarps;
+    // An item's fixed cost (queries, join, results) in blocks of keys.  bf16: 256 contexts of
+    // 10 .. 1000 tokens 60.6 us at 1, 50.7 us at 3; 4 bits, whose block is four times as
+    // long: 2 is no better than 1, 0 is worse.
+    static constexpr int kFixed = kInt4 ? 1 : 3;
     static constexpr int kBlock = kWarps * kKeys;  // keys of a unit
     static constexpr int kRowBytes = kInt4 ? D / 2 : 2 * D;
     static constexpr int kGroups = D / 64;
@@ -75,7 +78,7 @@ struct Shape {
     static constexpr int kStageBytes = kKeys * 2 * (kRowBytes + kScaleBytes);
     static constexpr int kTiles = D / 16;  // 16-dim tiles of O^T
     // Dims that the warps' sums are joined by at a time, in the stage that each has just read.
-    static constexpr int kJoinDims = NT == 1 ? D : NT == 2 ? 64 : 32;
+    static constexpr int kJoinDims = NT == 1 ? D : 64;
     static constexpr int kJoinPitch = kJoinDims + 4;
     static_assert(kCols * kJoinPitch * 4 <= kStageBytes, "the sums fit a stage");
     static constexpr int kRing = kWarps * kStages * kStageBytes;
@@ -160,8 +163,9 @@ struct SeqInfo {
     int32_t blo, nb;      // first block of keys, number of blocks
 };
 
-template <int R, int BLOCK>
+template <class Sh>
 __device__ __forceinline__ SeqInfo seq_info(const AttnArgs& a, int32_t b, bool tell) {
+    constexpr int R = Sh::R, BLOCK = Sh::kBlock;
     SeqInfo s;
     s.row0 = b;
     s.n = 1;
@@ -191,8 +195,9 @@ __device__ __forceinline__ SeqInfo seq_info(const AttnArgs& a, int32_t b, bool t
 __device__ __forceinline__ int64_t quotient(int64_t x, int64_t y) {
     return ((x | y) >> 32) == 0 ? (int64_t)((uint32_t)x / (uint32_t)y) : x / y;
 }
+template <class Sh>
 __device__ __forceinline__ int64_t units_of(const AttnArgs& a, const SeqInfo& s) {
-    return (int64_t)a.hkv * s.nrb * (kFixedUnits + s.nb);
+    return (int64_t)a.hkv * s.nrb * (Sh::kFixed + s.nb);
 }
 
 template <int N>
@@ -240,7 +245,7 @@ __global__ void __launch_bounds__(Shape<D, KIND, NT, H>::kThreads, Shape<D, KIND
         const int32_t s0 = min((int64_t)tid * per_thread, (int64_t)ns), s1 = min(s0 + per_thread, ns);
         int64_t sum = 0;
         for (int32_t x = s0; x < s1; ++x)
-            sum += units_of(a, seq_info<R, BLOCK>(a, x, blockIdx.x == 0));
+            sum += units_of<Sh>(a, seq_info<Sh>(a, x, blockIdx.x == 0));
         int64_t inc = sum;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -260,7 +265,7 @@ __global__ void __launch_bounds__(Shape<D, KIND, NT, H>::kThreads, Shape<D, KIND
         }
         inc += before;
         int64_t per = quotient(total + gridDim.x - 1, gridDim.x);
-        per = max(per, (int64_t)kFixedUnits + 1);
+        per = max(per, (int64_t)2);
         u0 = per * blockIdx.x;
         u1 = min(u0 + per, total);
         if (blockIdx.x == 0) {  // for the join
@@ -268,14 +273,14 @@ __global__ void __launch_bounds__(Shape<D, KIND, NT, H>::kThreads, Shape<D, KIND
             int64_t u = inc - sum;
             for (int32_t x = s0; x < s1; ++x) {
                 a.ws_cum[x] = u;
-                u += units_of(a, seq_info<R, BLOCK>(a, x, false));
+                u += units_of<Sh>(a, seq_info<Sh>(a, x, false));
             }
         }
         if (u0 >= total) return;
         if (u0 >= inc - sum && u0 < inc) {
             int64_t u = inc - sum;
             for (int32_t x = s0; x < s1; ++x) {
-                const int64_t len = units_of(a, seq_info<R, BLOCK>(a, x, false));
+                const int64_t len = units_of<Sh>(a, seq_info<Sh>(a, x, false));
                 if (u0 < u + len) {
                     found_b = x;
                     found_u = u;
@@ -292,9 +297,9 @@ __global__ void __launch_bounds__(Shape<D, KIND, NT, H>::kThreads, Shape<D, KIND
     // ---- cursor over this warp's steps
     const int32_t own = warp * KS;      // this warp's keys inside a block
     const bool one_page = (1 << a.s.page_shift) >= KS;
-    SeqInfo sq = seq_info<R, BLOCK>(a, b, false);
+    SeqInfo sq = seq_info<Sh>(a, b, false);
     const int32_t* pages = a.s.page_table + b * a.s.table_stride;
-    int32_t len = kFixedUnits + sq.nb;
+    int32_t len = Sh::kFixed + sq.nb;
     it = (int32_t)quotient(u0 - ub, len);
     int32_t rb = it / a.hkv, kvh = it - rb * a.hkv;
     int64_t ui = ub + (int64_t)it * len;  // first unit of the item
@@ -323,7 +328,7 @@ __global__ void __launch_bounds__(Shape<D, KIND, NT, H>::kThreads, Shape<D, KIND
             flags_next = kFirst | kLast | kEmpty | kWhole;
             return u0 <= ui;
         }
-        const int64_t first = ui + kFixedUnits, last = ui + len;
+        const int64_t first = ui + Sh::kFixed, last = ui + len;
         const int32_t t0 = (int32_t)max(u0 - first, (int64_t)0);
         const int32_t t1 = (int32_t)(min(u1, last) - first);
         if (t1 <= t0) return false;
@@ -354,9 +359,9 @@ __global__ void __launch_bounds__(Shape<D, KIND, NT, H>::kThreads, Shape<D, KIND
                                     more = pending = false;
                                     return;
                                 }
-                                sq = seq_info<R, BLOCK>(a, b, false);
+                                sq = seq_info<Sh>(a, b, false);
                             } while (sq.nrb == 0);
-                            len = kFixedUnits + sq.nb;
+                            len = Sh::kFixed + sq.nb;
                             pages = a.s.page_table + b * a.s.table_stride;
                         }
                     }
@@ -971,15 +976,15 @@ __global__ void __launch_bounds__(256) join_kernel(const AttnArgs a) {
     if (a.s.cu && t < a.s.num_tokens) b = find_seq(a.s.cu, a.s.num_seqs, t);
     const bool any = t < a.s.num_tokens && b >= 0 && b < a.s.num_seqs;
     SeqInfo s = {};
-    if (any) s = seq_info<R, Sh::kBlock>(a, b, false);
+    if (any) s = seq_info<Sh>(a, b, false);
     wait_previous();
     if (!any || s.nb == 0 || t - s.row0 >= s.n) return;
     const int32_t kvh = h / a.group;
     const int64_t rr = (int64_t)(t - s.row0) * a.group + h - kvh * a.group;
     const int32_t rb = (int32_t)(rr / R), r = (int32_t)(rr - (int64_t)rb * R);
-    const int64_t per = *a.ws_per, first = a.ws_cum[b] + ((int64_t)rb * a.hkv + kvh) * (kFixedUnits + s.nb);
-    const int32_t cf = (int32_t)quotient(first + kFixedUnits, per);
-    const int32_t cl = (int32_t)quotient(first + kFixedUnits + s.nb - 1, per);
+    const int64_t per = *a.ws_per, first = a.ws_cum[b] + ((int64_t)rb * a.hkv + kvh) * (Sh::kFixed + s.nb);
+    const int32_t cf = (int32_t)quotient(first + Sh::kFixed, per);
+    const int32_t cl = (int32_t)quotient(first + Sh::kFixed + s.nb - 1, per);
     if (cf == cl) return;  // one piece holds it all
     const int32_t n = cl - cf + 1;
     float mm = -INFINITY, l = 0.f, acc[E];
@@ -1062,7 +1067,7 @@ __global__ void __launch_bounds__(256) join_kernel(const AttnArgs a) {
 }
 
 // Column tiles for `rows` query rows a kv head (group * new tokens of a sequence).
-int tiles_of(int64_t rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : 4; }
+int tiles_of(int64_t rows) { return rows <= 8 ? 1 : 2; }
 
 size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 
@@ -1094,10 +1099,7 @@ pva_status launch(AttnArgs a, uint8_t* ws, cudaStream_t st) {
 template <int D, int KIND>
 pva_status launch_rows(int64_t rows, const AttnArgs& a, uint8_t* ws, cudaStream_t st) {
     if (KIND == PVA_CACHE_INT4 && rows <= 4) return launch<D, KIND, 1, KIND == PVA_CACHE_INT4>(a, ws, st);
-    const int nt = tiles_of(rows);
-    return nt == 1   ? launch<D, KIND, 1, false>(a, ws, st)
-           : nt == 2 ? launch<D, KIND, 2, false>(a, ws, st)
-                     : launch<D, KIND, 4, false>(a, ws, st);
+    return tiles_of(rows) == 1 ? launch<D, KIND, 1, false>(a, ws, st) : launch<D, KIND, 2, false>(a, ws, st);
 }
 
 }  // namespace
