@@ -764,20 +764,29 @@ __global__ void __launch_bounds__(Shape<D, KIND, NT, H>::kThreads, Shape<D, KIND
                         l_run[nt][e & 1] += s[z][nt][e];
                     }
                 if (!INT4) {
-                    // the weights meet bf16 values in a bf16 product: one rounding, 2^-8 of a weight
-                    uint32_t p[NT][2];
+                    // the values are bf16, so the weights go in as the sum of two bf16 numbers: 16 of
+                    // their bits, and what the result loses is its own rounding.  (One bf16 number
+                    // alone adds as much again; the second product hides behind HBM.)
+                    uint32_t p[NT][2], q[NT][2];
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        p[nt][0] = transpose8(pack2(s[z][nt][0], s[z][nt][1]));
-                        p[nt][1] = transpose8(pack2(s[z][nt][2], s[z][nt][3]));
-                    }
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int y = 0; y < 2; ++y) {
+                            const float p0 = s[z][nt][2 * y], p1 = s[z][nt][2 * y + 1];
+                            const uint32_t hi = pack2(p0, p1);
+                            p[nt][y] = transpose8(hi);
+                            q[nt][y] = transpose8(pack2(p0 - lo_f(hi), p1 - hi_f(hi)));
+                        }
 #pragma unroll
                     for (int i = 0; i < T; ++i) {
                         uint32_t f[4];
                         const int r = (lane & 7) + ((lane >> 4) << 3), ch = 2 * i + ((lane >> 3) & 1);
                         ldsm_t(f, vb + (16 * z + r) * ROWB + ((ch ^ (r & 7)) << 4));
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) mma(o[nt][i], f, p[nt][0], p[nt][1]);
+                        for (int nt = 0; nt < NT; ++nt) {
+                            mma(o[nt][i], f, p[nt][0], p[nt][1]);
+                            mma(o[nt][i], f, q[nt][0], q[nt][1]);
+                        }
                     }
                 } else {
                     // v = middle + scale * (code - 7.5), middle = low + 7.5 scale.  weight * middle stays
