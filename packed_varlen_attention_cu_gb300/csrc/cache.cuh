@@ -41,10 +41,9 @@ __device__ __forceinline__ int32_t find_seq(const int32_t* __restrict__ cu, int3
 
 // Dependent launches.  Every kernel of these calls lets the next kernel of the stream be
 // launched at once and then waits for the end of the one before it, so that a chain of
-// short kernels (append, attention, join) pays for a launch once.  All its reads and
-// writes come after the wait, except of what was there before the kernel before it; no
-// thread block leaves without having waited, so that the end of a kernel is the end of
-// all before it.
+// short kernels (append, attention, join) pays for a launch once.  All reads and writes
+// come after the wait, and no thread block leaves without having waited, so that the end
+// of a kernel is the end of all before it.
 __device__ __forceinline__ void launch_next() {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }

@@ -8,8 +8,10 @@
 // The products run transposed on m16n8k16 tiles, S^T = K Q^T and O^T = V^T P^T:
 // keys (or dims) fill the 16 rows of a tile, query rows its 8 columns, so a
 // decoding step of up to 8 rows a kv head (one token, groups up to 8) wastes no
-// half of every product, of the softmax and of the registers on absent rows; 16
-// and 32 rows take 2 and 4 column tiles on the same K and V fragments.
+// half of every product, of the softmax and of the registers on absent rows.  More
+// rows take two column tiles on the same K and V fragments, 16 rows an item; four
+// column tiles spilled and were slower than reading K and V again from L2 (32 rows of
+// 128 dims, 64 contexts of 4000 .. 9001 keys: 567 us against 303 us).
 // (tcgen05 tiles start at 64 rows of D and take their operands from shared memory,
 // where 4-bit rows would have to be written back expanded.)
 //
@@ -52,7 +54,7 @@ struct AttnArgs {
     SeqView s;
     int32_t hq, hkv, group, window, out_fp32;
     uint32_t num_pages, page_bytes;  // page_bytes: codes or values of a page, one of K and V
-    float c;      // softmax scale * log2(e), times 2^69 with 4 bits (see low_codes)
+    float c;      // softmax scale * log2(e), times 2^69 with 4 bits (whose scores carry 2^-69)
     float slack;  // kSlack / c
 };
 
@@ -67,6 +69,11 @@ struct Shape {
     static constexpr int kCols = 8 * NT;     // columns of S^T
     static constexpr int R = H ? 4 : kCols;  // rows of an item
     static constexpr int kThreads = 32 * kWarps;
+    // Ring sizes: bf16 16 KB (128 dims) a step and warp in flight at 8 warps an SM keep HBM
+    // busy (98% of the copy rate on a batch of 64 contexts).  4 bits are bounded by issue slots
+    // and the integer pipe, not by HBM: 64 keys a step spread a step's fixed instructions (16
+    // keys: 143 us, 32: 91 us, 64: 84 us on 3 contexts of 131072), and twelve warps with two
+    // stages beat eight (84 -> 82 us).
     // An item's fixed cost (queries, join, results) in blocks of keys.  bf16: 256 contexts of
     // 10 .. 1000 tokens 60.6 us at 1, 50.7 us at 3; 4 bits, whose block is four times as
     // long: 2 is no better than 1, 0 is worse.
@@ -993,18 +1000,17 @@ __global__ void __launch_bounds__(256) join_kernel(const AttnArgs a) {
     using Sh = Shape<D, KIND, NT, H>;
     constexpr int R = Sh::R, E = D / 32;
     __shared__ float sm_o[WARPS][D], sm_m[WARPS], sm_l[WARPS];
+    launch_next();
+    wait_previous();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t row = WARPS > 1 ? blockIdx.x : (int64_t)blockIdx.x * 8 + warp;
     const int32_t t = (int32_t)quotient(row, a.hq), h = (int32_t)(row - (int64_t)t * a.hq);
-    launch_next();
-    // (the lengths were there before the attention began)
+    if (t >= a.s.num_tokens) return;
     int32_t b = t;
-    if (a.s.cu && t < a.s.num_tokens) b = find_seq(a.s.cu, a.s.num_seqs, t);
-    const bool any = t < a.s.num_tokens && b >= 0 && b < a.s.num_seqs;
-    SeqInfo s = {};
-    if (any) s = seq_info<Sh>(a, b, false);
-    wait_previous();
-    if (!any || s.nb == 0 || t - s.row0 >= s.n) return;
+    if (a.s.cu) b = find_seq(a.s.cu, a.s.num_seqs, t);
+    if (b < 0 || b >= a.s.num_seqs) return;
+    const SeqInfo s = seq_info<Sh>(a, b, false);
+    if (s.nb == 0 || t - s.row0 >= s.n) return;
     const int32_t kvh = h / a.group;
     const int64_t rr = (int64_t)(t - s.row0) * a.group + h - kvh * a.group;
     const int32_t rb = (int32_t)(rr / R), r = (int32_t)(rr - (int64_t)rb * R);
@@ -1153,7 +1159,7 @@ extern "C" pva_status pva_cache_attn(const pva_cache_desc* cache, const pva_cach
     if (st != PVA_OK) return st;
     const int32_t d = cache->head_dim;
     if (num_q_heads <= 0 || num_q_heads % cache->num_kv_heads != 0 || max_new < 1 || window < 0 ||
-        (out_is_fp32 != 0 && out_is_fp32 != 1) || !(softmax_scale == softmax_scale))
+        (out_is_fp32 != 0 && out_is_fp32 != 1) || !(softmax_scale - softmax_scale == 0.f))
         return PVA_ERR_INVALID_ARG;
     AttnArgs a = {};
     a.q_stride = row_stride(q_stride, num_q_heads, d, 2);

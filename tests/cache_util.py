@@ -75,7 +75,7 @@ class Problem:
     order, garbage (NaN) in every slot that belongs to no token."""
 
     def __init__(self, lens, news, hq, hkv, d, page, int4=False, seed=0, spare_rows=0, garbage=math.nan,
-                 spread=1.0, strided=False):
+                 spread=1.0, strided=False, v_spread=None):
         g = torch.Generator().manual_seed(seed)
         self.lens, self.news, self.hq, self.hkv, self.d, self.page, self.int4 = lens, news, hq, hkv, d, page, int4
         used = [-(-n // page) for n in lens]
@@ -95,7 +95,7 @@ class Problem:
         shape = (count, hkv, page)
         self.rows = {}
         for x in "kv":
-            rows = torch.randn(shape + (d,), generator=g).mul(spread).bfloat16()
+            rows = torch.randn(shape + (d,), generator=g).mul(spread if x == "k" or v_spread is None else v_spread).bfloat16()
             mine = torch.zeros((count, page), dtype=torch.bool)
             for b, n in enumerate(lens):
                 j = torch.arange(n)

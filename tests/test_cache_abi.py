@@ -121,7 +121,8 @@ def test_bad_read(L):
 
 def test_bad_attention(L):
     assert attn(L, hq=3) == attn(L, hq=0) == attn(L, new=0) == attn(L, window=-1) == attn(L, f32=2) == INVALID
-    assert attn(L, scale=float("nan")) == INVALID
+    assert attn(L, scale=float("nan")) == attn(L, scale=float("inf")) == INVALID
+    assert attn(L, c=cache(page_size=1024, head_dim=128, num_kv_heads=8192), hq=8192) == UNSUPPORTED  # 2 GB a page
     assert attn(L, q=None) == attn(L, out=None) == attn(L, lse=None) == attn(L, ws=None) == INVALID
     assert attn(L, q=A + 2) == attn(L, out=A + 8) == attn(L, lse=A + 2) == attn(L, ws=A + 16) == INVALID
     assert attn(L, qs=100) == attn(L, qs=260) == INVALID

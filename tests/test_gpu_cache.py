@@ -273,6 +273,77 @@ def test_scale_and_fp32_output():
     check_attention(p, a, la, p.attend())
 
 
+def test_fp32_output_keeps_the_weights():
+    """A bf16 cache's weights go into the products with 16 bits: each is off by 2^-17 of itself at
+    most, so an fp32 output is off by 2^-17 of the sum of |weight * value| and the scores' own error
+    (a score of these sizes: below 128 products of fp32, 2e-6 in all; the values are below 6)."""
+    p = Problem([400, 77, 3000], [1, 3, 1], 8, 2, 128, 16)
+    out, _ = attend(p, fp32=True)
+    o, _, _, _ = p.attend()
+    assert float((out.double().cpu() - o).abs().max()) <= (2 ** -17 + 2 * 4e-6) * 6
+
+
+@pytest.mark.parametrize("int4", [False, True])
+@pytest.mark.parametrize("v_spread", [1e-6, 1e6])
+@pytest.mark.parametrize("spread", [1e-4, 1.0, 30.0])
+def test_small_and_large_values(int4, v_spread, spread):
+    p = Problem([300, 17, 1], [1, 2, 1], 8, 2, 128, 16, int4, spread=spread, v_spread=v_spread)
+    if spread == 30.0:
+        p.q.mul_(1 / 30)
+    check_attention(p, *attend(p), p.attend())
+
+
+@pytest.mark.parametrize("int4", [False, True])
+def test_thousands_of_sequences(int4):
+    g = torch.Generator().manual_seed(3)
+    lens = torch.randint(0, 40, (2500,), generator=g).tolist()
+    news = [min(n, int(x)) for n, x in zip(lens, torch.randint(0, 3, (2500,), generator=g))]
+    p = Problem(lens, news, 2, 1, 64, 16, int4, spare_rows=1)
+    check_attention(p, *attend(p), p.attend())
+
+
+def test_a_cache_without_pages():
+    """Empty sequences need no page: an empty cache and a table without columns are fine."""
+    cache = api.KVCache(*(torch.zeros((0, 2, 16, 64), dtype=torch.bfloat16, device="cuda") for _ in "kv"))
+    q = torch.randn((3, 4, 64), device="cuda").bfloat16()
+    out, lse = torch.ones_like(q), torch.ones((4, 3), device="cuda")
+    ws, status = api.alloc_cache_workspace(3, 4, 2, 64), word()
+    table = torch.zeros((3, 0), dtype=torch.int32, device="cuda")
+    api.cache_attn(cache, q, table, i32([0, 0, 0]), out, lse, ws, cu_new=i32([0, 0, 0, 0]), status=status)
+    assert api.cache_status(status) == 0 and bool((out == 1).all()) and bool((lse == 1).all())
+    # tokens without a page: nothing to read, and told
+    api.cache_attn(cache, q, table, i32([5, 1, 3]), out, lse, ws, status=status)
+    assert api.cache_status(status) == 300 and bool((out == 0).all()) and bool(torch.isneginf(lse).all())
+    k = torch.zeros((3, 2, 64), dtype=torch.bfloat16, device="cuda")
+    status = word()
+    api.cache_append(cache, k, k, table, i32([5, 1, 3]), status=status)
+    assert api.cache_status(status) == 300
+    status = word()
+    api.cache_read(cache, table, i32([0, 1, 2, 3]), k, torch.empty_like(k), status=status)
+    assert api.cache_status(status) == 300
+
+
+@pytest.mark.parametrize("int4", [False, True])
+def test_lengths_written_just_before(int4):
+    """Kernels that change the lengths run right before each call, without a wait in between."""
+    lens = [37, 700, 5, 64]
+    p = Problem(lens, [1] * 4, 8, 2, 64, 16, int4)
+    cache, table, q = on_gpu(p), p.table.cuda(), p.q.contiguous().cuda()
+    dev = i32([0] * 4)
+    ws = api.alloc_cache_workspace(4, 8, 2, 64)
+    outs = []
+    for cut in (0, 1, 4, 0, 3):
+        dev.copy_(i32(lens))
+        dev.sub_(cut)
+        out, lse = torch.empty_like(q), torch.empty((8, 4), device="cuda")
+        api.cache_attn(cache, q, table, dev, out, lse, ws)
+        dev.zero_()
+        outs.append((cut, out, lse))
+    for cut, out, lse in outs:
+        p.lens = [n - cut for n in lens]
+        check_attention(p, out, lse, p.attend())
+
+
 def test_one_row_larger_than_all_others():
     """A running maximum that rises at the last key, and one that stands at the first."""
     for at in (0, 999, 500):
