@@ -425,14 +425,21 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const ReadArgs a, int32_
 #pragma unroll
                     for (int g = 0; g < kG; ++g) {
                         const uint32_t w = g == 0 ? x[u].x : x[u].y, s = g == 0 ? sc[u].x : sc[u].y;
-                        const float scale = __uint_as_float(s << 16), low = __uint_as_float(s & 0xffff0000u);
-                        float f[8];
+                        // low + code * scale by one fused operation on bf16 pairs: the product is
+                        // exact and the sum is rounded once.  128 + code is a mask and an OR.
+                        const uint32_t sw = __byte_perm(s, 0, 0x1010), lw = __byte_perm(s, 0, 0x3232);
+                        uint32_t y[4];
 #pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            f[e] = __fadd_rn(low, __fmul_rn((float)((w >> (4 * (e / 2) + 16 * (e % 2))) & 15u), scale));
-                        Vec<false> y;
-                        y.set(f);
-                        out[8 * g + o] = y.r;
+                        for (int p = 0; p < 4; ++p) {
+                            const uint32_t m = ((w >> (4 * p)) & 0x000f000fu) | 0x43004300u;
+                            const uint32_t k128 = 0x43004300u;
+                            const __nv_bfloat162 code = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&m),
+                                                                *reinterpret_cast<const __nv_bfloat162*>(&k128));
+                            const __nv_bfloat162 v = __hfma2(code, *reinterpret_cast<const __nv_bfloat162*>(&sw),
+                                                             *reinterpret_cast<const __nv_bfloat162*>(&lw));
+                            y[p] = *reinterpret_cast<const uint32_t*>(&v);
+                        }
+                        out[8 * g + o] = make_uint4(y[0], y[1], y[2], y[3]);
                     }
                 }
             }
