@@ -389,6 +389,34 @@ def test_missing_pages_are_left_out_and_told(int4):
     assert torch.equal(again[0], out) and torch.equal(again[1], lse)
 
 
+@pytest.mark.parametrize("int4", [False, True])
+def test_strided_page_table_and_shared_pages(int4):
+    """A table with rows further apart than they are long; two sequences over the same pages."""
+    p = Problem([100, 70, 100], [1, 1, 1], 8, 2, 64, 16, int4)
+    p.table[2] = p.table[0]
+    wide = torch.full((3, 40), 7777, dtype=torch.int32)
+    wide[:, 5:5 + p.table.shape[1]] = p.table
+    table = wide.cuda()[:, 5:5 + p.table.shape[1]]
+    check_attention(p, *attend(p, table=table), p.attend())
+    ko = torch.empty((270, 2, 64), dtype=torch.bfloat16, device="cuda")
+    api.cache_read(on_gpu(p), table, i32([0, 100, 170, 270]), ko, torch.empty_like(ko))
+    assert torch.equal(ko.cpu(), torch.cat([p.cached("k", b) for b in range(3)]).float().bfloat16())
+    with pytest.raises(ValueError):
+        attend(p, table=wide.cuda().t())
+
+
+def test_misaligned_tensors_are_refused():
+    p = Problem([20], [1], 4, 2, 64, 16)
+    odd = torch.zeros(4 * 64 + 1, dtype=torch.bfloat16, device="cuda")[1:].view(1, 4, 64)
+    with pytest.raises(PvaError):
+        attend(p, q=odd)
+    flat = torch.zeros((3, 4 * 64 + 4), dtype=torch.bfloat16, device="cuda")
+    rows = flat[:, :256].view(3, 4, 64)  # rows 8 bytes off every other time
+    out = torch.empty((3, 4, 64), dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(PvaError):
+        api.rope(rows, None, angles(3, 64).cuda(), out, None)
+
+
 def test_lengths_that_do_not_fit_are_told():
     p = Problem([40, 40], [2, 2], 4, 2, 64, 16)
     cache = on_gpu(p)
