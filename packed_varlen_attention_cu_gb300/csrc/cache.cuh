@@ -22,28 +22,32 @@ __device__ __forceinline__ void raise_status(int32_t* status, int code) {
     if (status) atomicCAS(status, 0, code);
 }
 
+// Lengths, offsets and pages may have been written by the kernel before, which may
+// still run when this one is launched (see launch_next): they are read after the wait,
+// and by ordinary loads, not through the read-only path.
+
 // Sequence b with cu[b] <= t < cu[b + 1], or -1; called by whole warps.  Each
 // round every lane probes one offset, so a batch of up to 1024 sequences takes
 // two rounds.  Whatever cu holds, the reads stay inside cu[0 .. n].
-__device__ __forceinline__ int32_t find_seq(const int32_t* __restrict__ cu, int32_t n, int32_t t) {
+__device__ __forceinline__ int32_t find_seq(const int32_t* cu, int32_t n, int32_t t) {
     const int lane = threadIdx.x & 31;
     int32_t lo = 0, hi = n;
     while (hi - lo > 1) {
         const int32_t step = (hi - lo + 31) / 32;
         const int64_t at = lo + (int64_t)lane * step;
-        const bool le = at < hi && __ldg(cu + at) <= t;
+        const bool le = at < hi && cu[at] <= t;
         const int c = __popc(__ballot_sync(0xffffffffu, le));
         lo += (c > 0 ? c - 1 : 0) * step;
         hi = min(hi, lo + step);
     }
-    return (n > 0 && __ldg(cu + lo) <= t && t < __ldg(cu + lo + 1)) ? lo : -1;
+    return (n > 0 && cu[lo] <= t && t < cu[lo + 1]) ? lo : -1;
 }
 
 // Dependent launches.  Every kernel of these calls lets the next kernel of the stream be
 // launched at once and then waits for the end of the one before it, so that a chain of
-// short kernels (append, attention, join) pays for a launch once.  All reads and writes
-// come after the wait, and no thread block leaves without having waited, so that the end
-// of a kernel is the end of all before it.
+// short kernels (append, attention, join) pays for a launch once.  All reads and
+// writes come after the wait, and no thread block leaves without having waited, so that the end of a
+// kernel is the end of all before it.
 __device__ __forceinline__ void launch_next() {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
@@ -93,7 +97,7 @@ struct SeqView {
 __device__ __forceinline__ int64_t page_of(const SeqView& s, int32_t b, int32_t pos) {
     const int32_t i = pos >> s.page_shift;
     if (pos < 0 || i >= s.max_pages) return -1;
-    const int32_t p = __ldg(s.page_table + b * s.table_stride + i);
+    const int32_t p = s.page_table[b * s.table_stride + i];
     return (p < 0 || p >= s.num_pages) ? -1 : p;
 }
 

@@ -178,12 +178,12 @@ __device__ __forceinline__ SeqInfo seq_info(const AttnArgs& a, int32_t b, bool t
     s.n = 1;
     bool bad = false;
     if (a.s.cu) {
-        s.row0 = __ldg(a.s.cu + b);
-        const int32_t end = __ldg(a.s.cu + b + 1);
+        s.row0 = a.s.cu[b];
+        const int32_t end = a.s.cu[b + 1];
         bad = s.row0 < 0 || end < s.row0 || end > a.s.num_tokens;
         s.n = bad ? 0 : end - s.row0;
     }
-    const int32_t kv = __ldg(a.s.kv_lens + b);
+    const int32_t kv = a.s.kv_lens[b];
     const int64_t room = (int64_t)a.s.max_pages << a.s.page_shift;
     if (tell) {
         if (bad || kv < s.n) raise_status(a.s.status, kErrLength);
@@ -386,7 +386,7 @@ __global__ void __launch_bounds__(Shape<D, KIND, NT, H>::kThreads, Shape<D, KIND
         if (key + BLOCK >= kend) flags_next |= kLast;
         if (key < alo || key + KS > ahi) flags_next |= kPartial;
         const int32_t i = (key + 16 * min(lane, SUB - 1)) >> a.s.page_shift;
-        page = lane < SUB && i < a.s.max_pages ? (uint32_t)__ldg(pages + i) : ~0u;
+        page = lane < SUB && i < a.s.max_pages ? (uint32_t)pages[i] : ~0u;
     };
     // N * 16 keys from byte `off` of a page's K and V on, into tile x of a stage;
     // [vlo, vhi): rows of the first 16 that are there.
@@ -549,7 +549,7 @@ __global__ void __launch_bounds__(Shape<D, KIND, NT, H>::kThreads, Shape<D, KIND
 #pragma unroll
                         for (int e = 0; e < 2; ++e)
                             qf[0][nt][ks][e] =
-                                live ? __ldg(reinterpret_cast<const uint32_t*>(q + 16 * ks + 8 * e + 2 * c)) : 0u;
+                                live ? *reinterpret_cast<const uint32_t*>(q + 16 * ks + 8 * e + 2 * c) : 0u;
                 } else {
 #pragma unroll
                     for (int hh = 0; hh < HN; ++hh) qs[hh][nt] = 0;
@@ -560,7 +560,7 @@ __global__ void __launch_bounds__(Shape<D, KIND, NT, H>::kThreads, Shape<D, KIND
 #pragma unroll
                         for (int oc = 0; oc < 2; ++oc) {
                             constexpr float kUp60 = kUp64 / 16.f;  // meets 16 * code
-                            const uint4 x = live ? __ldg(reinterpret_cast<const uint4*>(q + 64 * gr + 16 * c + 8 * oc))
+                            const uint4 x = live ? *reinterpret_cast<const uint4*>(q + 64 * gr + 16 * c + 8 * oc)
                                                  : make_uint4(0, 0, 0, 0);
                             const uint32_t y[4] = {pack2(lo_f(x.x) * kUp64, hi_f(x.x) * kUp64),
                                                    pack2(lo_f(x.y) * kUp60, hi_f(x.y) * kUp60),

@@ -113,15 +113,15 @@ __device__ __forceinline__ int32_t seq_of_lane(const SeqView& s, int32_t t0, int
     if (!s.cu) return lane < rows && t < s.num_seqs ? t : -1;
     const int32_t b0 = find_seq(s.cu, s.num_seqs, t0);
     if (lane >= rows) return -1;
-    if (b0 >= 0 && t < __ldg(s.cu + b0 + 1)) return b0;
+    if (b0 >= 0 && t < s.cu[b0 + 1]) return b0;
     // the run goes on into another sequence, or begins before the first
     int32_t lo = max(b0, 0), hi = s.num_seqs;
     while (hi - lo > 1) {
         const int32_t mid = lo + (hi - lo) / 2;
-        if (__ldg(s.cu + mid) <= t) lo = mid;
+        if (s.cu[mid] <= t) lo = mid;
         else hi = mid;
     }
-    return s.num_seqs > 0 && __ldg(s.cu + lo) <= t && t < __ldg(s.cu + lo + 1) ? lo : -1;
+    return s.num_seqs > 0 && s.cu[lo] <= t && t < s.cu[lo + 1] ? lo : -1;
 }
 
 // One warp takes kUnroll passes of a token, whose loads go out before the token's place is
@@ -184,20 +184,20 @@ __global__ void __launch_bounds__(kThreads, 3) rotate_kernel(const RotArgs a) {
             if (a.s.cu) {
                 b = find_seq(a.s.cu, a.s.num_seqs, t);
                 if (b < 0) continue;
-                first = __ldg(a.s.cu + b);
-                n = __ldg(a.s.cu + b + 1) - first;
+                first = a.s.cu[b];
+                n = a.s.cu[b + 1] - first;
             } else if (b >= a.s.num_seqs) {
                 continue;
             }
-            p = (int64_t)__ldg(a.s.kv_lens + b) - n + (t - first);
+            p = (int64_t)a.s.kv_lens[b] - n + (t - first);
             const int64_t page = p < 0 ? -1 : page_of(a.s, b, (int32_t)p);
             if (page >= 0) row_at = ((page * a.hkv) << a.s.page_shift) + (p & ((1 << a.s.page_shift) - 1));
         } else if (a.positions) {
-            p = __ldg(a.positions + t);
+            p = a.positions[t];
         } else if (a.s.cu) {
             const int32_t b = find_seq(a.s.cu, a.s.num_seqs, t);
             if (b < 0) continue;
-            p = t - __ldg(a.s.cu + b);
+            p = t - a.s.cu[b];
         }
         if (p < 0 || (a.rot > 0 && p >= a.max_pos)) {
             if (lane == 0) raise_status(a.s.status, KIND != kNoCache && p < 0 ? kErrLength : kErrPosition);
@@ -215,7 +215,7 @@ __global__ void __launch_bounds__(kThreads, 3) rotate_kernel(const RotArgs a) {
                     reinterpret_cast<const float4*>(a.table + ((int64_t)pos * (a.rot / 2) + first) * 2);
 #pragma unroll
                 for (int i = 0; i < kV / 4; ++i) {
-                    const float4 f = __ldg(cs + i);
+                    const float4 f = cs[i];
                     const int at = h * (kV / 2) + 2 * i;
                     c[at] = f.x;
                     s[at] = a.inverse ? -f.y : f.y;
@@ -374,9 +374,9 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const ReadArgs a, int32_
         int64_t at = -1;
         {
             const int32_t t = t0 + lane, b = seq_of_lane(a.s, t0, rows);
-            const int32_t i = b >= 0 && a.s.cu ? t - __ldg(a.s.cu + b) : 0;
+            const int32_t i = b >= 0 && a.s.cu ? t - a.s.cu[b] : 0;
             if (b >= 0) {
-                const int64_t pos = (a.starts ? __ldg(a.starts + b) : 0) + (int64_t)i;
+                const int64_t pos = (a.starts ? a.starts[b] : 0) + (int64_t)i;
                 const int64_t page = pos > INT32_MAX ? -1 : page_of(a.s, b, (int32_t)pos);
                 if (page < 0) raise_status(a.s.status, kErrPage);
                 else at = ((page * a.hkv) << a.s.page_shift) + (pos & ((1 << a.s.page_shift) - 1));
@@ -405,10 +405,10 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const ReadArgs a, int32_
                         const uint2 w = __ldcs((const uint2*)pages + row * 8 + o);
                         x[u].x = w.x;
                         x[u].y = w.y;
-                        sc[u] = __ldg((const uint2*)scales + row);
+                        sc[u] = ((const uint2*)scales)[row];
                     } else {
                         x[u].x = __ldcs((const uint32_t*)pages + row * 8 + o);
-                        sc[u].x = __ldg((const uint32_t*)scales + row);
+                        sc[u].x = ((const uint32_t*)scales)[row];
                     }
                 }
             }
