@@ -23,7 +23,7 @@ __device__ __forceinline__ void raise_status(int32_t* status, int code) {
 }
 
 // Lengths, offsets and pages may have been written by the kernel before, which may
-// still run when this one is launched (see launch_next): they are read after the wait,
+// still run when this one is launched (see wait_previous): they are read after the wait,
 // and by ordinary loads, not through the read-only path.
 
 // Sequence b with cu[b] <= t < cu[b + 1], or -1; called by whole warps.  Each
@@ -43,14 +43,12 @@ __device__ __forceinline__ int32_t find_seq(const int32_t* cu, int32_t n, int32_
     return (n > 0 && cu[lo] <= t && t < cu[lo + 1]) ? lo : -1;
 }
 
-// Dependent launches.  Every kernel of these calls lets the next kernel of the stream be
-// launched at once and then waits for the end of the one before it, so that a chain of
-// short kernels (append, attention, join) pays for a launch once.  All reads and
-// writes come after the wait, and no thread block leaves without having waited, so that the end of a
-// kernel is the end of all before it.
-__device__ __forceinline__ void launch_next() {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
+// Dependent launches.  A kernel of these calls may be launched while the kernel before
+// it in the stream runs out, and waits for its end: a chain of short kernels (append,
+// attention, join) pays less for its launches (0.3 to 1 us each; letting the next kernel
+// start any earlier than the last blocks' exit was no better and cost the long ones 1%).
+// All reads and writes come after the wait, and no thread block leaves without having
+// waited, so that the end of a kernel is the end of all before it.
 __device__ __forceinline__ void wait_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 template <typename... P, typename... A>

@@ -233,7 +233,6 @@ __global__ void __launch_bounds__(Shape<D, KIND, NT, H>::kThreads, Shape<D, KIND
     constexpr int G = Sh::kGroups, T = Sh::kTiles, BLOCK = Sh::kBlock, ROWB = Sh::kRowBytes;
     constexpr bool INT4 = Sh::kInt4;
     extern __shared__ __align__(128) uint8_t smem[];
-    launch_next();
     wait_previous();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, c = lane & 3;
@@ -1000,7 +999,6 @@ __global__ void __launch_bounds__(256) join_kernel(const AttnArgs a) {
     using Sh = Shape<D, KIND, NT, H>;
     constexpr int R = Sh::R, E = D / 32;
     __shared__ float sm_o[WARPS][D], sm_m[WARPS], sm_l[WARPS];
-    launch_next();
     wait_previous();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t row = WARPS > 1 ? blockIdx.x : (int64_t)blockIdx.x * 8 + warp;

@@ -139,7 +139,6 @@ __global__ void __launch_bounds__(kThreads, 3) rotate_kernel(const RotArgs a) {
     constexpr int kLph = D / (2 * kV);   // lanes a head
     constexpr int kHpw = 32 / kLph;      // heads a pass
     constexpr int kElem = F32 ? 4 : 2;
-    launch_next();
     wait_previous();
     const int lane = threadIdx.x & 31;
     const int j = lane % kLph, sub = lane / kLph;
@@ -358,7 +357,6 @@ template <int D, int KIND>
 __global__ void __launch_bounds__(kThreads) read_kernel(const ReadArgs a, int32_t run) {
     constexpr bool kInt4 = KIND == PVA_CACHE_INT4;
     constexpr int kLph = kInt4 ? 8 : D / 8, kHpw = 32 / kLph, kUnroll = 4, kG = D / 64;
-    launch_next();
     wait_previous();
     const int lane = threadIdx.x & 31;
     const int o = lane % kLph, sub = lane / kLph;
