@@ -437,8 +437,9 @@ def _cache_batch(cache: KVCache, page_table, num_tokens: int, kv_lens, cu_new, s
             stride = width
         _need(stride >= width, "page_table: rows overlap")
     return CacheBatch(n, num_tokens, width, stride, page_table.data_ptr(),
-                      _ints(kv_lens, n, "kv_lens", dev), _ints(cu_new, n + 1, "cu_new", dev),
-                      _ints(status, 1, "status", dev))
+                      None if kv_lens is None else _ints(kv_lens, n, "kv_lens", dev),
+                      None if cu_new is None else _ints(cu_new, n + 1, "cu_new", dev),
+                      None if status is None else _ints(status, 1, "status", dev))
 
 
 def cache_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, page_table: torch.Tensor,
@@ -459,17 +460,25 @@ def cache_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, page_table: t
     if v.shape != shape or h != cache.num_kv_heads or d != cache.head_dim:
         raise ValueError("cache_append: k and v [tokens, kv heads, head_dim] of the cache")
     hq = qs = qo = ko = 0
-    _need((q is None) == (q_out is None), "cache_append: q goes with q_out")
+    if (q is None) != (q_out is None):
+        raise ValueError("cache_append: q goes with q_out")
     if q is not None:
-        qs, qo, hq = _rows3(q, "q", dev), _rows3(q_out, "q_out", dev), q.shape[1]
-        _need(q.shape == q_out.shape == (t, hq, d), "cache_append: q and q_out [tokens, heads, head_dim]")
+        qs, qo = _rows3(q, "q", dev), _rows3(q_out, "q_out", dev)
+        q_shape = q.shape
+        hq = q_shape[1]
+        if q_shape != q_out.shape or q_shape[0] != t or q_shape[2] != d:
+            raise ValueError("cache_append: q and q_out [tokens, heads, head_dim]")
     if k_out is not None:
         ko = _rows3(k_out, "k_out", dev)
         _need(k_out.shape == shape, "cache_append: k_out has k's shape")
-    check("pva_cache_append", lib().pva_cache_append(
+    rc = (_lib._lib or lib()).pva_cache_append(
         cache.desc, _cache_batch(cache, page_table, t, kv_lens, cu_new, status, dev),
-        _rope_desc(table, interleaved, dev), k.data_ptr(), ks, v.data_ptr(), vs, _ptr(q), qs, hq,
-        _ptr(q_out), qo, _ptr(k_out), ko, _queue(stream, dev)))
+        None if table is None else _rope_desc(table, interleaved, dev), k.data_ptr(), ks,
+        v.data_ptr(), vs, None if q is None else q.data_ptr(), qs, hq,
+        None if q is None else q_out.data_ptr(), qo, None if k_out is None else k_out.data_ptr(), ko,
+        _queue(stream, dev))
+    if rc:
+        check("pva_cache_append", rc)
 
 
 def cache_read(cache: KVCache, page_table: torch.Tensor, cu_out: torch.Tensor,
@@ -523,10 +532,12 @@ def cache_attn(cache: KVCache, q: torch.Tensor, page_table: torch.Tensor, kv_len
     o, l = _whole(out, "out", dev, shape, _BF16, _F32), _whole(lse, "lse", dev, (h, t), _F32)
     if workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace: a contiguous tensor on cuda:{dev} is needed")
-    check("pva_cache_attn", lib().pva_cache_attn(
+    rc = (_lib._lib or lib()).pva_cache_attn(
         cache.desc, _cache_batch(cache, page_table, t, kv_lens, cu_new, status, dev), q.data_ptr(),
         qs, h, max_new, window, softmax_scale, o, 1 if out.dtype is _F32 else 0, l,
-        workspace.data_ptr(), workspace.nbytes, _queue(stream, dev)))
+        workspace.data_ptr(), workspace.nbytes, _queue(stream, dev))
+    if rc:
+        check("pva_cache_attn", rc)
 
 
 def cache_status(status: torch.Tensor, stream=None) -> int:
