@@ -138,8 +138,8 @@ class Problem:
             ok = (j <= pos) & (j > pos - window if window else j >= 0)
             ok = ok & (self.table[b, j[0] // self.page] >= 0)[None]
             qq = q[a:a + m].unflatten(1, (hkv, hq // hkv))
-            kk = torch.where(torch.isnan(k), torch.zeros_like(k), k)
-            vv = torch.where(torch.isnan(v), torch.zeros_like(v), v)
+            kk = torch.where(torch.isfinite(k), k, torch.zeros_like(k))  # slots of no token
+            vv = torch.where(torch.isfinite(v), v, torch.zeros_like(v))
             s = torch.einsum("mhgd,lhd->hgml", qq, kk) * scale
             mag = torch.einsum("mhgd,lhd->hgml", qq.abs(), kk.abs()) * scale
             s = s.masked_fill(~ok, -math.inf)
