@@ -9,9 +9,9 @@
 // keys (or dims) fill the 16 rows of a tile, query rows its 8 columns, so a
 // decoding step of up to 8 rows a kv head (one token, groups up to 8) wastes no
 // half of every product, of the softmax and of the registers on absent rows.  More
-// rows take two column tiles on the same K and V fragments, 16 rows an item; four
-// column tiles spilled and were slower than reading K and V again from L2 (32 rows of
-// 128 dims, 64 contexts of 4000 .. 9001 keys: 567 us against 303 us).
+// rows of a bf16 cache take two column tiles on the same K and V fragments, 16 rows an
+// item; four column tiles spilled and were slower than reading K and V again from L2
+// (32 rows of 128 dims, 64 contexts of 4000 .. 9001 keys: 567 us against 303 us).
 // (tcgen05 tiles start at 64 rows of D and take their operands from shared memory,
 // where 4-bit rows would have to be written back expanded.)
 //
@@ -63,9 +63,10 @@ template <int D, int KIND, int NT, bool H>
 struct Shape {
     static constexpr bool kInt4 = KIND == PVA_CACHE_INT4;
     static constexpr int kWarps = 4;
-    static constexpr int kKeys = kInt4 ? (NT == 1 ? 64 : 32 * (128 / D)) : 16 * (128 / D);
-    static constexpr int kStages = kInt4 && NT == 1 ? 2 : 3;
-    static constexpr int kCtas = kInt4 && NT == 1 ? 3 : 2;  // resident on an SM
+    static_assert(!kInt4 || NT == 1, "4 bits take one column tile");
+    static constexpr int kKeys = kInt4 ? 64 : 16 * (128 / D);
+    static constexpr int kStages = kInt4 ? 2 : 3;
+    static constexpr int kCtas = kInt4 ? 3 : 2;  // resident on an SM
     static constexpr int kCols = 8 * NT;     // columns of S^T
     static constexpr int R = H ? 4 : kCols;  // rows of an item
     static constexpr int kThreads = 32 * kWarps;
@@ -932,7 +933,7 @@ __global__ void __launch_bounds__(Shape<D, KIND, NT, H>::kThreads, Shape<D, KIND
                         for (int e = 0; e < 4; ++e) {
                             // tile i holds dims 16i + g, 16i + g + 8, or with 4 bits dims
                             // 8g + 2i, 8g + 2i + 1 of its group
-                            const int at = INT4 ? g * 2 * (JT < 4 ? JT : 4) + 2 * (i % 4) + (e >> 1) + (i / 4) * 64
+                            const int at = INT4 ? 64 * (i / 4) + 8 * g + 2 * (i % 4) + (e >> 1)
                                                 : 16 * i + g + 8 * (e >> 1);
                             join_o[(8 * nt + 2 * c + (e & 1)) * JP + at] = o[nt][t0 + i][e];
                         }
@@ -957,10 +958,7 @@ __global__ void __launch_bounds__(Shape<D, KIND, NT, H>::kThreads, Shape<D, KIND
                         sum.z = fmaf(f, v.z, sum.z);
                         sum.w = fmaf(f, v.w, sum.w);
                     }
-                    // first of the four dims
-                    int dim;
-                    if (!INT4 || JT >= 4) dim = 16 * t0 + d4;
-                    else dim = 64 * (t0 / 4) + 8 * (d4 / (2 * JT)) + 2 * (t0 % 4) + d4 % (2 * JT);
+                    const int dim = 16 * t0 + d4;  // first of four
                     if (flags & kWhole) {
                         const int32_t tok = (r0 + r) / a.group;
                         const int32_t h = mt.kvh * a.group + (r0 + r) - tok * a.group;
@@ -1096,9 +1094,6 @@ __global__ void __launch_bounds__(256) join_kernel(const AttnArgs a) {
     if (lane == 0) a.lse[(int64_t)h * a.s.num_tokens + t] = l != 0.f ? fmaf(mm, kLn2, logf(l)) : -INFINITY;
 }
 
-// Column tiles for `rows` query rows a kv head (group * new tokens of a sequence).
-int tiles_of(int64_t rows) { return rows <= 8 ? 1 : 2; }
-
 size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 template <int D, int KIND, int NT, bool H>
@@ -1126,10 +1121,16 @@ pva_status launch(AttnArgs a, uint8_t* ws, cudaStream_t st) {
     return e == cudaSuccess ? PVA_OK : PVA_ERR_CUDA;
 }
 
+// Variants by rows a kv head: 4 bits up to 4 rows two key tiles in the columns, else items of 8
+// rows (two column tiles of 16 rows were slower: 12 contexts to 49635 tokens, 12 rows: 52 us
+// against 37 us; 32 contexts to 16000, 32 rows: 85 against 83); bf16 up to 8 rows one column
+// tile, else items of 16 rows (4 contexts of 8192, 4 rows 31 us, 16 rows 33 us).
 template <int D, int KIND>
 pva_status launch_rows(int64_t rows, const AttnArgs& a, uint8_t* ws, cudaStream_t st) {
-    if (KIND == PVA_CACHE_INT4 && rows <= 4) return launch<D, KIND, 1, KIND == PVA_CACHE_INT4>(a, ws, st);
-    return tiles_of(rows) == 1 ? launch<D, KIND, 1, false>(a, ws, st) : launch<D, KIND, 2, false>(a, ws, st);
+    if constexpr (KIND == PVA_CACHE_INT4)
+        return rows <= 4 ? launch<D, KIND, 1, true>(a, ws, st) : launch<D, KIND, 1, false>(a, ws, st);
+    else
+        return rows <= 8 ? launch<D, KIND, 1, false>(a, ws, st) : launch<D, KIND, 2, false>(a, ws, st);
 }
 
 }  // namespace
@@ -1143,7 +1144,7 @@ extern "C" size_t pva_cache_attn_bytes(int32_t num_seqs, int32_t num_q_heads, in
         (head_dim != 64 && head_dim != 128) || max_new < 1)
         return 0;
     const int64_t rows = (int64_t)(num_q_heads / num_kv_heads) * max_new;
-    const size_t r = 8 * (size_t)tiles_of(rows);
+    const size_t r = rows <= 8 ? 8 : 16;
     return 256 + up256((size_t)num_seqs * 8) + (size_t)2 * kMaxCtas * r * (8 + 4 * (size_t)head_dim);
 }
 

