@@ -389,6 +389,34 @@ def test_missing_pages_are_left_out_and_told(int4):
     assert torch.equal(again[0], out) and torch.equal(again[1], lse)
 
 
+def test_long_sums_of_codes_have_no_bias():
+    """64 contexts of 131072 tokens, so that whole contexts are summed in one place, with equal
+    weights (queries of 0, weights exactly 1): the result is an average of random values, three
+    hundred times smaller than they are.  At most 64 products' sums stand between two corrections of
+    the codes' middle; each may lose a last bit (2^-23) of a sum that is below 15 scales a weight."""
+    d, hkv, page, ctx, batch = 128, 8, 64, 131072, 64
+    g = torch.Generator(device="cuda").manual_seed(1)
+    shape = (ctx // page, hkv, page)
+    cache = api.KVCache(*(torch.randint(0, 256, shape + (d // 2,), generator=g, dtype=torch.uint8, device="cuda") for _ in "kv"),
+                        *(torch.empty(shape + (d // 64, 2), dtype=torch.bfloat16, device="cuda") for _ in "kv"))
+    for s in (cache.k_scales, cache.v_scales):
+        s[..., 0] = torch.rand(shape + (2,), generator=g, device="cuda") * 0.2 + 0.3
+        s[..., 1] = -7.5 * s[..., 0].float()
+    table = torch.stack([torch.randperm(ctx // page, generator=g, device="cuda") for _ in range(batch)]).int()
+    q = torch.zeros((batch, 4 * hkv, d), dtype=torch.bfloat16, device="cuda")
+    out, lse = torch.empty((batch, 4 * hkv, d), device="cuda"), torch.empty((4 * hkv, batch), device="cuda")
+    ws = api.alloc_cache_workspace(batch, 4 * hkv, hkv, d)
+    api.cache_attn(cache, q, table, i32([ctx] * batch), out, lse, ws)
+    total = torch.zeros((hkv, d), dtype=torch.float64, device="cuda")
+    for h in range(hkv):
+        sc = cache.v_scales[:, h].double()
+        code = unpack(cache.v[:, h].cpu()).cuda().double().unflatten(-1, (2, 64))
+        total[h] = (sc[..., 1:] + code * sc[..., :1]).flatten(-2).sum((0, 1))
+    mean = (total / ctx).repeat_interleave(4, 0)
+    assert float((out.double() - mean).abs().max()) <= 64 * 2 ** -23 * 15 * 0.5 + 1e-6
+    assert float((lse.double() - math.log(ctx)).abs().max()) <= 1e-5
+
+
 @pytest.mark.parametrize("int4", [False, True])
 def test_strided_page_table_and_shared_pages(int4):
     """A table with rows further apart than they are long; two sequences over the same pages."""
