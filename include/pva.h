@@ -418,6 +418,7 @@ pva_status pva_cache_append(const pva_cache_desc* cache, const pva_cache_batch* 
 /* Cached rows as a contiguous pack, for pva_attn_fwd over a context that is
  * already cached: row cu_new[b] + i is the token at position starts[b] + i
  * (starts_dev DEVICE int32 [num_seqs], NULL: 0).  kv_lens is not used.
+ * Up to 176 kv heads (PVA_ERR_UNSUPPORTED from 353 on, or 177 of 128 bf16 dims).
  *   k_out, v_out  DEVICE bf16 [num_tokens, num_kv_heads, head_dim], contiguous */
 pva_status pva_cache_read(const pva_cache_desc* cache, const pva_cache_batch* batch,
                           const int32_t* starts_dev, void* k_out, void* v_out, void* stream);

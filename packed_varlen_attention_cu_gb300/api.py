@@ -416,6 +416,7 @@ class KVCache:
     @classmethod
     def alloc(cls, num_pages: int, num_kv_heads: int, head_dim: int, page_size: int = 64,
               kind: int = CACHE_BF16, device="cuda") -> "KVCache":
+        _need(kind in (CACHE_BF16, CACHE_INT4), "KVCache: kind is CACHE_BF16 or CACHE_INT4")
         shape = (num_pages, num_kv_heads, page_size)
         if kind == CACHE_BF16:
             return cls(*(torch.zeros(shape + (head_dim,), dtype=_BF16, device=device) for _ in "kv"))

@@ -482,7 +482,7 @@ pva_status launch_rotate(const RotArgs& a, cudaStream_t st) {
 template <int D, int KIND>
 pva_status launch_read(const ReadArgs& a, cudaStream_t st) {
     if ((2 * (int64_t)a.hkv * (KIND == PVA_CACHE_INT4 ? 8 : D / 8) + 31) / 32 > 176)
-        return PVA_ERR_UNSUPPORTED;  // the kernel's division (704 kv heads of 64 dims, 352 of 128)
+        return PVA_ERR_UNSUPPORTED;  // the kernel's division (352 kv heads, 176 of 128 bf16 dims)
     const int sms = sm_count();
     if (sms <= 0) return PVA_ERR_CUDA;
     int32_t run = 32;  // as many rows a warp as leave every SM two CTAs of work

@@ -117,6 +117,8 @@ def test_bad_read(L):
     assert L.pva_cache_read(cache(), batch(), None, None, A, None) == INVALID
     assert L.pva_cache_read(cache(), batch(), None, A, A + 8, None) == INVALID
     assert L.pva_cache_read(cache(), batch(), A + 1, A, A, None) == INVALID
+    assert L.pva_cache_read(cache(num_kv_heads=353), batch(), None, A, A, None) == UNSUPPORTED
+    assert L.pva_cache_read(cache(num_kv_heads=177, head_dim=128), batch(), None, A, A, None) == UNSUPPORTED
 
 
 def test_bad_attention(L):
@@ -159,6 +161,8 @@ def test_binding_refuses_host_tensors_and_wrong_shapes():
         api.KVCache(k.float(), k.float())
     with pytest.raises(ValueError, match="scales"):
         api.KVCache(k.view(torch.uint8), k.view(torch.uint8))
+    with pytest.raises(ValueError, match="kind"):
+        api.KVCache.alloc(4, 2, 64, kind=2, device="cpu")
     x = torch.zeros(3, 2, 64, dtype=torch.bfloat16)
     table = api.rope_table(8, 64, device="cpu")
     with pytest.raises(ValueError):
