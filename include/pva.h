@@ -394,7 +394,9 @@ typedef struct {
     const int32_t* page_table; /* DEVICE int32 */
     const int32_t* kv_lens;    /* DEVICE int32 [num_seqs] */
     const int32_t* cu_new;     /* DEVICE int32 [num_seqs + 1]: new tokens of sequence b are
-                                  rows cu_new[b] .. cu_new[b + 1]; NULL: row b alone */
+                                  rows cu_new[b] .. cu_new[b + 1]; NULL: row b alone, or
+                                  none where kv_lens[b] = 0 (a padded batch): nothing is
+                                  appended or rotated, and its attention is empty */
     int32_t* status;           /* status word or NULL */
 } pva_cache_batch;
 

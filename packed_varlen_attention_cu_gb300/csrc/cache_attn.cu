@@ -187,7 +187,8 @@ __device__ __forceinline__ SeqInfo seq_info(const AttnArgs& a, int32_t b, bool t
     const int32_t kv = a.s.kv_lens[b];
     const int64_t room = (int64_t)a.s.max_pages << a.s.page_shift;
     if (tell) {
-        if (bad || kv < s.n) raise_status(a.s.status, kErrLength);
+        // (without offsets a length of 0 is a row of no sequence: a padded batch)
+        if (bad || (kv < s.n && (a.s.cu || kv != 0))) raise_status(a.s.status, kErrLength);
         if (s.n > 0 && kv > room) raise_status(a.s.status, kErrPage);
     }
     const int32_t kvp = max(kv, 0);

@@ -185,8 +185,8 @@ __global__ void __launch_bounds__(kThreads, 3) rotate_kernel(const RotArgs a) {
                 if (b < 0) continue;
                 first = a.s.cu[b];
                 n = a.s.cu[b + 1] - first;
-            } else if (b >= a.s.num_seqs) {
-                continue;
+            } else if (b >= a.s.num_seqs || a.s.kv_lens[b] == 0) {
+                continue;  // (a length of 0: a padded batch)
             }
             p = (int64_t)a.s.kv_lens[b] - n + (t - first);
             const int64_t page = p < 0 ? -1 : page_of(a.s, b, (int32_t)p);

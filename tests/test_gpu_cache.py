@@ -389,6 +389,32 @@ def test_missing_pages_are_left_out_and_told(int4):
     assert torch.equal(again[0], out) and torch.equal(again[1], lse)
 
 
+@pytest.mark.parametrize("int4", [False, True])
+def test_padded_batch(int4):
+    """Rows of no sequence (length 0, no pages) in a batch of single tokens: no failure, nothing
+    appended or rotated for them, empty results; the others as without them."""
+    lens = [33, 0, 7, 0, 0, 100]
+    p = Problem(lens, [int(n > 0) for n in lens], 8, 2, 64, 16, int4)
+    cache, status = on_gpu(p), word()
+    t = len(lens)
+    q, k = (torch.randn((t, h, 64), device="cuda").bfloat16() for h in (8, 2))
+    qo = torch.full_like(q, 7.0)
+    table = torch.full((t, 7), -1, dtype=torch.int32)
+    table[:, :p.table.shape[1]] = p.table
+    held = [x.clone() for x in (cache.k, cache.v)]
+    api.cache_append(cache, k, k, table.cuda(), i32(lens), table=angles(100, 64).cuda(), q=q, q_out=qo, status=status)
+    out, lse = torch.full_like(q, 7.0), torch.full((8, t), 7.0, device="cuda")
+    api.cache_attn(cache, qo, table.cuda(), i32(lens), out, lse, api.alloc_cache_workspace(t, 8, 2, 64), status=status)
+    assert api.cache_status(status) == 0
+    none = torch.tensor([n == 0 for n in lens], device="cuda")
+    assert bool((qo[none] == 7).all()) and bool((qo[~none] != 7).any(-1).all())
+    assert bool((out[none] == 0).all()) and bool(torch.isneginf(lse[:, none]).all())
+    assert bool(torch.isfinite(out).all()) and bool(torch.isfinite(lse[:, ~none]).all())
+    changed = [(a.view(torch.uint8) != b.view(torch.uint8)).flatten(1).any(1).sum().item()
+               for a, b in zip((cache.k, cache.v), held)]  # by their bits: slots of no token are NaN
+    assert max(changed) <= 3
+
+
 def test_long_sums_of_codes_have_no_bias():
     """64 contexts of 131072 tokens, so that whole contexts are summed in one place, with equal
     weights (queries of 0, weights exactly 1): the result is an average of random values, three
