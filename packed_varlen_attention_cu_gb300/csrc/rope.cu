@@ -467,16 +467,19 @@ pva_status launch_unrolled(const RotArgs& a, int sms, cudaStream_t st) {
 }
 
 // A few tokens take one pass a warp: what they cost is latency (96 tokens of 24 heads into
-// 4 bits: 5.7 us with three passes a warp, 3.6 us with one).
+// 4 bits: 5.7 us with three passes a warp, 3.6 us with one).  Many take no more passes a warp
+// than their heads fill (bf16, interleaved: 32768 tokens of 16 heads of 64, two passes: 34.9 us
+// with five, 31.4 us with two; 20383 of 8 heads, one pass: 18.0 and 13.8 us).
 template <int D, bool F32, int KIND>
 pva_status launch_rotate(const RotArgs& a, cudaStream_t st) {
     const int sms = sm_count();
     if (sms <= 0) return PVA_ERR_CUDA;
     constexpr int per = 32 / (D / (2 * Vec<F32>::kDims));
-    const int64_t warps = (int64_t)a.s.num_tokens * ((a.nslots + per - 1) / per);
-    return warps <= (int64_t)sms * 3 * kWarps
-               ? launch_unrolled<D, F32, KIND, 1>(a, sms, st)
-               : launch_unrolled<D, F32, KIND, Unroll<F32, KIND>::value>(a, sms, st);
+    const int passes = (a.nslots + per - 1) / per;
+    if (passes <= 1 || (int64_t)a.s.num_tokens * passes <= (int64_t)sms * 3 * kWarps)
+        return launch_unrolled<D, F32, KIND, 1>(a, sms, st);
+    if (passes == 2) return launch_unrolled<D, F32, KIND, 2>(a, sms, st);
+    return launch_unrolled<D, F32, KIND, Unroll<F32, KIND>::value>(a, sms, st);
 }
 
 template <int D, int KIND>

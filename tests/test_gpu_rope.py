@@ -64,6 +64,29 @@ def test_heads_and_row_numbers(hq, hkv, t):
             close(o, *rotate(x, table, torch.arange(t), False), torch.bfloat16)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("hq,hkv", [(3, 1), (4, 4), (5, 4), (9, 4), (12, 4)])  # 1 to 4 passes of heads
+@pytest.mark.parametrize("d", [64, 128])
+def test_many_tokens_of_few_heads(dtype, hq, hkv, d):
+    t = 9001
+    g = torch.Generator().manual_seed(hq)
+    q, k = (torch.randn((t, h, d), generator=g).to(dtype) for h in (hq, hkv))
+    table = angles(t, d)
+    qd, kd = q.cuda(), k.cuda()
+    api.rope(qd, kd, table.cuda(), qd, kd)
+    for x, o in ((q, qd), (k, kd)):
+        close(o, *rotate(x, table, torch.arange(t), False), dtype)
+    # the same rows into a cache: bit for bit the rotated ones
+    if dtype == torch.bfloat16:
+        pages = torch.arange((t + 63) // 64, dtype=torch.int32, device="cuda").view(1, -1)
+        cache = api.KVCache.alloc(num_pages=pages.numel(), num_kv_heads=hkv, head_dim=d, page_size=64)
+        ends, qo = torch.tensor([0, t], dtype=torch.int32, device="cuda"), torch.empty_like(qd)
+        api.cache_append(cache, k.cuda(), k.cuda(), pages, ends[1:], cu_new=ends, table=table.cuda(), q=q.cuda(), q_out=qo)
+        ko, vo = torch.empty_like(kd), torch.empty_like(kd)
+        api.cache_read(cache, pages, ends, ko, vo)
+        assert torch.equal(qo, qd) and torch.equal(ko, kd) and torch.equal(vo, k.cuda())
+
+
 def test_positions_of_a_zigzag_shard():
     cu = W.cu_seqlens_of([70, 5, 300, 129, 1, 200])
     t, hq, d = int(cu[-1]), 3, 128
