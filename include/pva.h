@@ -328,7 +328,8 @@ pva_status pva_attn_bwd(const void* q, const void* k, const void* v, const void*
  *   300 a position without a page: outside the table's columns, or an entry
  *       outside [0, num_pages)
  *   301 lengths that do not fit: more new tokens than kv_lens counts, or
- *       offsets that decrease or leave the tensor
+ *       offsets that decrease or leave the tensor (the rows of such a sequence
+ *       or document, and rows that such offsets place in none, are left out)
  *   303 a position outside the angle table (negative ones included)
  * What such a token would have read or written is left out; the rest is done. */
 

@@ -91,6 +91,24 @@ struct SeqView {
     int32_t num_seqs, num_tokens, max_pages, page_shift;
 };
 
+// Do the rows of sequence b, which find_seq has found, lie inside the tensor?  Those of a
+// sequence that says otherwise are left out: its count is not to be trusted, and positions
+// and slots follow from it.
+__device__ __forceinline__ bool rows_fit(const SeqView& s, int32_t b) {
+    return s.cu[b] >= 0 && s.cu[b + 1] <= s.num_tokens;
+}
+
+// Offsets that decrease or leave the tensor are told of, a sequence a thread (thread i of n).
+// Rows that such offsets place in no sequence meet no other check.
+__device__ __forceinline__ void tell_offsets(const SeqView& s, int64_t i, int64_t n) {
+    if (!s.cu || !s.status) return;
+#pragma unroll 1
+    for (; i < s.num_seqs; i += n) {
+        const int32_t first = s.cu[i], end = s.cu[i + 1];
+        if (first < 0 || end < first || end > s.num_tokens) raise_status(s.status, kErrLength);
+    }
+}
+
 // Page of key position `pos` of sequence b, or -1 where there is none.
 __device__ __forceinline__ int64_t page_of(const SeqView& s, int32_t b, int32_t pos) {
     const int32_t i = pos >> s.page_shift;

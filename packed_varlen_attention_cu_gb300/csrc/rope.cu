@@ -106,14 +106,15 @@ __device__ __forceinline__ uint32_t encode(const float* x, float low, float inv)
     return w;
 }
 
-// Sequence (or document) of row t0 + lane, for a warp's run of `rows` rows; -1: none.
+// Sequence (or document) of row t0 + lane, for a warp's run of `rows` rows; -1: none, or
+// one whose offsets leave the tensor.
 __device__ __forceinline__ int32_t seq_of_lane(const SeqView& s, int32_t t0, int32_t rows) {
     const int lane = threadIdx.x & 31;
     const int32_t t = t0 + lane;
     if (!s.cu) return lane < rows && t < s.num_seqs ? t : -1;
     const int32_t b0 = find_seq(s.cu, s.num_seqs, t0);
     if (lane >= rows) return -1;
-    if (b0 >= 0 && t < s.cu[b0 + 1]) return b0;
+    if (b0 >= 0 && t < s.cu[b0 + 1]) return rows_fit(s, b0) ? b0 : -1;
     // the run goes on into another sequence, or begins before the first
     int32_t lo = max(b0, 0), hi = s.num_seqs;
     while (hi - lo > 1) {
@@ -121,7 +122,7 @@ __device__ __forceinline__ int32_t seq_of_lane(const SeqView& s, int32_t t0, int
         if (s.cu[mid] <= t) lo = mid;
         else hi = mid;
     }
-    return s.num_seqs > 0 && s.cu[lo] <= t && t < s.cu[lo + 1] ? lo : -1;
+    return s.num_seqs > 0 && s.cu[lo] <= t && t < s.cu[lo + 1] && rows_fit(s, lo) ? lo : -1;
 }
 
 // One warp takes kUnroll passes of a token, whose loads go out before the token's place is
@@ -157,6 +158,7 @@ __global__ void __launch_bounds__(kThreads, 3) rotate_kernel(const RotArgs a) {
     }
     const int slot0 = blockIdx.y * kUnroll * kHpw + sub;
     const int64_t stride = (int64_t)gridDim.x * kWarps;
+    if (blockIdx.y == 0) tell_offsets(a.s, (int64_t)blockIdx.x * kThreads + threadIdx.x, (int64_t)gridDim.x * kThreads);
     for (int64_t tt = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5); tt < a.s.num_tokens;
          tt += stride) {
         const int32_t t = (int32_t)tt;
@@ -182,7 +184,7 @@ __global__ void __launch_bounds__(kThreads, 3) rotate_kernel(const RotArgs a) {
             int32_t b = t, first = t, n = 1;
             if (a.s.cu) {
                 b = find_seq(a.s.cu, a.s.num_seqs, t);
-                if (b < 0) continue;
+                if (b < 0 || !rows_fit(a.s, b)) continue;
                 first = a.s.cu[b];
                 n = a.s.cu[b + 1] - first;
             } else if (b >= a.s.num_seqs || a.s.kv_lens[b] == 0) {
@@ -195,7 +197,7 @@ __global__ void __launch_bounds__(kThreads, 3) rotate_kernel(const RotArgs a) {
             p = a.positions[t];
         } else if (a.s.cu) {
             const int32_t b = find_seq(a.s.cu, a.s.num_seqs, t);
-            if (b < 0) continue;
+            if (b < 0 || !rows_fit(a.s, b)) continue;
             p = t - a.s.cu[b];
         }
         if (p < 0 || (a.rot > 0 && p >= a.max_pos)) {
@@ -446,6 +448,7 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const ReadArgs a, int32_
             }
         }
     }
+    tell_offsets(a.s, (int64_t)blockIdx.x * kThreads + threadIdx.x, (int64_t)gridDim.x * kThreads);
 }
 
 // CTAs along the runs: up to 64 on an SM, then a stride.

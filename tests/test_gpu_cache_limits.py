@@ -1,0 +1,120 @@
+"""Ends of the rotation and cache calls' ranges on the GPU: offsets that do not fit."""
+import pytest
+import torch
+
+from cache_util import Problem, angles
+from packed_varlen_attention_cu_gb300 import api
+from test_gpu_cache import i32, on_gpu, word
+
+pytestmark = pytest.mark.gpu
+
+
+# ------------------------------------------------------------------ offsets that decrease or leave the tensor
+# Rows of a sequence whose offsets do so are left out and status 301 tells of it.
+
+def rows_that_fit(cu, t):
+    """(sequence, index in it) of every row that belongs to a sequence inside the tensor; None elsewhere."""
+    own = [None] * t
+    for b in range(len(cu) - 1):
+        if 0 <= cu[b] <= cu[b + 1] <= t:
+            for r in range(cu[b], cu[b + 1]):
+                own[r] = (b, r - cu[b])
+    return own
+
+
+OFFSETS = [[0, 2, 9], [0, 5, 3], [0, -3, 4], [0, 2, 1], [2, 5, 5], [-1, 2, 4], [0, 2 ** 31 - 1, -2 ** 31]]
+
+
+@pytest.mark.parametrize("int4", [False, True])
+@pytest.mark.parametrize("cu", OFFSETS)
+def test_append_leaves_out_sequences_whose_offsets_do_not_fit(cu, int4):
+    p = Problem([40, 40], [2, 2], 4, 2, 64, 16, int4, garbage=1.0)
+    cache, status, t = on_gpu(p), word(), 4
+    before = [x.clone() for x in (cache.k, cache.v)]
+    q, k, v = (x.contiguous().cuda() for x in (p.q, p.k_new, p.v_new))
+    qo, ko = torch.full_like(q, 7.0), torch.full_like(k, 7.0)
+    table = angles(64, 64).cuda()
+    args = (k, v, p.table.cuda(), i32([40, 40]))
+    api.cache_append(cache, *args, cu_new=i32(cu), table=table, q=q, q_out=qo, k_out=ko, status=status)
+    assert api.cache_status(status) == 301
+    slots = set()
+    for r, own in enumerate(rows_that_fit(cu, t)):
+        left_out = bool((qo[r] == 7).all()) and bool((ko[r] == 7).all())
+        assert left_out == (own is None)
+        if own is not None:
+            pos = 40 - (cu[own[0] + 1] - cu[own[0]]) + own[1]
+            slots.add((int(p.table[own[0], pos // 16]), pos % 16))
+    for x, old in zip((cache.k, cache.v), before):
+        changed = (x != old).any(-1).any(1).cpu()  # [page, slot]
+        assert {tuple(c) for c in changed.nonzero().tolist()} == slots
+    # without a status word the same rows are left out
+    again, qo2 = on_gpu(p), torch.full_like(q, 7.0)
+    api.cache_append(again, *args, cu_new=i32(cu), table=table, q=q, q_out=qo2)
+    assert torch.equal(again.k, cache.k) and torch.equal(again.v, cache.v) and torch.equal(qo2, qo)
+
+
+@pytest.mark.parametrize("int4", [False, True])
+@pytest.mark.parametrize("cu", OFFSETS)
+def test_read_leaves_out_sequences_whose_offsets_do_not_fit(cu, int4):
+    p = Problem([40, 40], [2, 2], 4, 2, 64, 16, int4)
+    ko, vo = (torch.full((4, 2, 64), 7.0, dtype=torch.bfloat16, device="cuda") for _ in "kv")
+    status = word()
+    api.cache_read(on_gpu(p), p.table.cuda(), i32(cu), ko, vo, starts=i32([3, 17]), status=status)
+    assert api.cache_status(status) == 301
+    for r, own in enumerate(rows_that_fit(cu, 4)):
+        for x, o in (("k", ko), ("v", vo)):
+            want = torch.full((2, 64), 7.0) if own is None else p.cached(x, own[0])[(3, 17)[own[0]] + own[1]].float()
+            assert torch.equal(o[r].cpu(), want.bfloat16())
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("cu", OFFSETS)
+def test_rotation_leaves_out_documents_whose_offsets_do_not_fit(cu, dtype):
+    x = torch.randn((4, 2, 64)).to(dtype).cuda()
+    table = angles(8, 64).cuda()
+    out, want, status = torch.full_like(x, 7.0), torch.full_like(x, 7.0), word()
+    api.rope(x, None, table, out, None, cu_seqlens=i32(cu), status=status)
+    assert api.cache_status(status) == 301
+    own = rows_that_fit(cu, 4)
+    pos = [-1 if o is None else o[1] for o in own]
+    api.rope(x, None, table, want, None, positions=i32(pos))  # (rows of no document: outside the table)
+    assert torch.equal(out, want)
+
+
+def test_one_bad_offset_among_thousands():
+    n = 5000
+    cu = torch.arange(n + 1, dtype=torch.int32)
+    cu[3333] = n + 7
+    x = torch.randn((n, 1, 64)).bfloat16().cuda()
+    out, status = torch.full_like(x, 7.0), word()
+    api.rope(x, None, angles(4, 64).cuda(), out, None, cu_seqlens=cu.cuda(), status=status)
+    assert api.cache_status(status) == 301
+    cache = api.KVCache.alloc(1, 1, 64, 16)
+    k = torch.empty((n, 1, 64), dtype=torch.bfloat16, device="cuda")
+    table, lens = torch.zeros((n, 1), dtype=torch.int32, device="cuda"), torch.ones(n, dtype=torch.int32, device="cuda")
+    status = word()
+    api.cache_read(cache, table, cu.cuda(), k, torch.empty_like(k), status=status)
+    assert api.cache_status(status) == 301
+    status = word()
+    api.cache_append(cache, x, x, table, lens, cu_new=cu.cuda(), status=status)
+    assert api.cache_status(status) == 301
+    status = word()  # offsets that fit, the first rows and the last ones of no sequence
+    api.rope(x, None, angles(4, 64).cuda(), out, None, cu_seqlens=torch.arange(5, n - 5, dtype=torch.int32).cuda(), status=status)
+    assert api.cache_status(status) == 0
+
+
+def test_a_long_pack_with_a_document_past_its_end():
+    """Runs of 32 rows a warp in the read-back; the last document says that it goes on behind the tensor."""
+    n, cu = 100000, [0, 40000, 80001, 100001]
+    x = torch.randn((n, 1, 64)).bfloat16().cuda()
+    pages = torch.arange(80001 // 64 + 1, dtype=torch.int32, device="cuda")[None].expand(3, -1).contiguous()
+    cache = api.KVCache.alloc(pages.shape[1], 1, 64, 64)
+    api.cache_append(cache, x[:80001], x[:80001], pages[:1], i32([80001]), cu_new=i32([0, 80001]))
+    ko, vo, status = torch.full_like(x, 7.0), torch.full_like(x, 7.0), word()
+    api.cache_read(cache, pages, i32(cu), ko, vo, status=status)
+    assert api.cache_status(status) == 301
+    assert torch.equal(ko[:40000], x[:40000]) and torch.equal(vo[40000:80001], x[:40001]) and bool((ko[80001:] == 7).all())
+    out, status = torch.full_like(x, 7.0), word()
+    api.rope(x, None, angles(50000, 64).cuda(), out, None, cu_seqlens=i32(cu), status=status)
+    assert api.cache_status(status) == 301
+    assert bool((out[80001:] == 7).all()) and bool((out[:80001] != 7).flatten(1).any(1).all())
