@@ -444,8 +444,10 @@ size_t pva_cache_attn_bytes(int32_t num_seqs, int32_t num_q_heads, int32_t num_k
  *              one call at a time
  * Keys without a page are left out (status 300); a row that sees no key gives
  * O = 0 and LSE = -inf.  What slots past kv_lens hold does not matter, nor what lies
- * before every new token's window.  A cached infinity or NaN that a token sees makes its
- * row NaN, and may reach the sequence's other new tokens.  fp32 sums; a bf16 cache's
+ * before every new token's window.  Of what a token sees, a score that is NaN or +inf makes
+ * its O and LSE NaN, one of -inf has the weight 0, and a value that is not finite leaves its
+ * dim of O (4 bits: its group of 64) not finite, whatever its weight; such a value may reach
+ * the sequence's other new tokens.  fp32 sums; a bf16 cache's
  * weights keep 16 bits in the products, a 4-bit cache's 8 (values up to 2^50).  The
  * result does not depend on timing.  softmax_scale <= 0 selects 1/sqrt(head_dim). */
 pva_status pva_cache_attn(const pva_cache_desc* cache, const pva_cache_batch* batch,

@@ -1072,11 +1072,15 @@ __global__ void __launch_bounds__(256) join_kernel(const AttnArgs a) {
         for (int e = 0; e < E; ++e) acc[e] *= old;
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-            const float f = k0 + u * WARPS >= n || ml[u].x == -INFINITY ? 0.f : ex2(ml[u].x - mn);
-            // (a weight of 0 must not meet a NaN of sums that are not this row's)
-            l += f == 0.f ? 0.f : f * ml[u].y;
+            // A piece of which the row sees no key has the sum 0 and no part in the result (its sums may
+            // hold a NaN of values that only other rows see).  Any other has, whatever its weight: scores
+            // that are NaN raise no maximum, so that -inf beside a sum of NaN is no empty piece, and a
+            // weight of 0 must meet a value that is not finite.
+            const bool none = k0 + u * WARPS >= n || ml[u].y == 0.f;
+            const float f = ex2(ml[u].x - mn);
+            l += none ? 0.f : f * ml[u].y;
 #pragma unroll
-            for (int e = 0; e < E; ++e) acc[e] += f == 0.f ? 0.f : f * v[u][e];
+            for (int e = 0; e < E; ++e) acc[e] += none ? 0.f : f * v[u][e];
         }
         mm = mn;
     }

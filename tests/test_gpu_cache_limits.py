@@ -1,10 +1,13 @@
-"""Ends of the rotation and cache calls' ranges on the GPU: offsets that do not fit."""
+"""Ends of the rotation and cache calls' ranges on the GPU: offsets that do not fit, values that are not
+finite."""
+import math
+
 import pytest
 import torch
 
-from cache_util import Problem, angles
+from cache_util import Problem, angles, check_attention
 from packed_varlen_attention_cu_gb300 import api
-from test_gpu_cache import i32, on_gpu, word
+from test_gpu_cache import attend, i32, on_gpu, word
 
 pytestmark = pytest.mark.gpu
 
@@ -118,3 +121,100 @@ def test_a_long_pack_with_a_document_past_its_end():
     api.rope(x, None, angles(50000, 64).cuda(), out, None, cu_seqlens=i32(cu), status=status)
     assert api.cache_status(status) == 301
     assert bool((out[80001:] == 7).all()) and bool((out[:80001] != 7).flatten(1).any(1).all())
+
+
+# ------------------------------------------------------------------ infinities and NaN that a token sees
+
+def poison(p, b, j, what, where, h, dim):
+    """A NaN or infinity in the key or the value (all dims of it with dim None) of token j, kv head h."""
+    page, slot = int(p.table[b, j // p.page]), j % p.page
+    if p.int4:
+        groups = slice(None) if dim is None else dim // 64
+        getattr(p, where + "_scales")[page, h, slot, groups] = what
+    else:
+        getattr(p, where)[page, h, slot, slice(None) if dim is None else dim] = what
+
+
+# one context that every piece of the line cuts, and a batch of whole ones
+SHAPES = [([4033], 32, 8, 128), ([4032], 32, 8, 128), ([700, 64, 65, 1] * 150, 4, 2, 64)]
+
+
+@pytest.mark.parametrize("int4", [False, True])
+@pytest.mark.parametrize("lens,hq,hkv,d", SHAPES)
+@pytest.mark.parametrize("at", ["last", "first", "middle", "page"])
+def test_a_nan_key_that_is_seen_reaches_its_rows(int4, lens, hq, hkv, d, at):
+    p = Problem(lens, [1] * len(lens), hq, hkv, d, 16, int4)
+    clean = attend(p, cu=False, fp32=True)
+    hit = torch.zeros((p.tokens, hq), dtype=torch.bool)
+    for b in range(0, len(lens), 3):
+        h = b % hkv if len(lens) > 1 else slice(None, None, 2)
+        n = lens[b]
+        j = {"last": [n - 1], "first": [0], "middle": [n // 2], "page": list(range(n // 2 // 16 * 16, min(n // 2 // 16 * 16 + 16, n)))}[at]
+        for x in j:
+            poison(p, b, x, math.nan, "k", h, None)
+        hit.view(p.tokens, hkv, -1)[b, h] = True
+    out, lse = attend(p, cu=False, fp32=True)
+    hit = hit.cuda()
+    assert bool(torch.isnan(out[hit]).all()) and bool(torch.isnan(lse.t()[hit]).all())
+    assert torch.equal(out[~hit], clean[0][~hit]) and torch.equal(lse.t()[~hit], clean[1].t()[~hit])
+
+
+@pytest.mark.parametrize("int4", [False, True])
+@pytest.mark.parametrize("lens,hq,hkv,d", SHAPES)
+@pytest.mark.parametrize("what", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("tiny", [False, True])
+def test_a_value_that_is_not_finite_reaches_its_dim(int4, lens, hq, hkv, d, what, tiny):
+    """Of a bf16 cache the dim, of a 4-bit cache the group of 64; LSE and the other dims stay.
+    tiny: the first key outweighs all others, whose weights underflow."""
+    p = Problem(lens, [1] * len(lens), hq, hkv, d, 16, int4)
+    if tiny:
+        if int4:
+            p.q.mul_(40)
+        else:
+            for b in range(len(lens)):
+                p.k[p.table[b, 0].long(), :, 0] *= 60
+    clean = attend(p, cu=False, fp32=True)
+    hit = torch.zeros((p.tokens, d), dtype=torch.bool)
+    for b in range(0, len(lens), 3):
+        poison(p, b, lens[b] - 1, what, "v", slice(None), d - 3)
+        hit[b, slice(d - 64, d) if int4 else d - 3] = True
+    out, lse = attend(p, cu=False, fp32=True)
+    hit = hit.cuda()[:, None].expand(out.shape)
+    assert not bool(torch.isfinite(out[hit]).any())
+    assert torch.equal(out[~hit], clean[0][~hit]) and torch.equal(lse, clean[1])
+
+
+@pytest.mark.parametrize("lens,hq,hkv,d", SHAPES)
+def test_infinite_keys(lens, hq, hkv, d):
+    """A score of -inf is a weight of 0; a score of +inf makes the row NaN, as the formula does."""
+    p = Problem(lens, [1] * len(lens), hq, hkv, d, 16)
+    p.q = p.q.contiguous()
+    p.q[..., 5] = p.q[..., 5].abs() + 0.5
+    without = {b: lens[b] // 2 for b in range(0, len(lens), 3) if lens[b] > 1}
+    for b, j in without.items():
+        poison(p, b, j, -math.inf, "k", slice(None), 5)
+    p.rows["k"] = p.k.double()
+    out, lse = attend(p, cu=False, fp32=True)
+    assert bool(torch.isfinite(out).all()) and bool(torch.isfinite(lse).all())
+    for b in list(without)[:2]:
+        k, v = p.cached("k", b), p.cached("v", b)
+        keep = torch.arange(lens[b]) != without[b]
+        s = torch.einsum("hgd,lhd->hgl", p.q[b].double().unflatten(0, (hkv, -1)), k[keep]) * d ** -0.5
+        o = torch.einsum("hgl,lhd->hgd", s.softmax(-1), v[keep]).flatten(0, 1)
+        # weights of 16 bits and scores good to 2e-5 (128 products of magnitude 10 in all, a last bit each)
+        assert float((out[b].double().cpu() - o).abs().max()) <= 4e-5 * float(v[keep].abs().max())
+        assert float((lse[:, b].double().cpu() - torch.logsumexp(s, -1).flatten()).abs().max()) <= 2e-5
+    for b, j in without.items():
+        poison(p, b, j, math.inf, "k", slice(None), 5)
+    out, lse = attend(p, cu=False, fp32=True)
+    hit = torch.zeros(p.tokens, dtype=torch.bool)
+    hit[list(without)] = True
+    assert bool(torch.isnan(out[hit.cuda()]).all()) and bool(torch.isfinite(out[~hit.cuda()]).all())
+    assert bool(torch.isnan(lse[:, hit.cuda()]).all()) and bool(torch.isfinite(lse[:, ~hit.cuda()]).all())
+
+
+@pytest.mark.parametrize("int4", [False, True])
+def test_rows_that_see_nothing_of_a_piece_stay_finite(int4):
+    """Drafts under a short window: pieces that hold no key of a row are not poisoned."""
+    p = Problem([4000], [16], 8, 2, 64, 16, int4)
+    check_attention(p, *attend(p, window=5), p.attend(5))
