@@ -24,6 +24,7 @@
 // the workspace, and a second, dependent kernel joins them in a fixed order.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
+#include <float.h>
 #include <stdint.h>
 
 #include "../../include/pva.h"
@@ -1189,6 +1190,11 @@ extern "C" pva_status pva_cache_attn(const pva_cache_desc* cache, const pva_cach
         (out_is_fp32 != 0 && out_is_fp32 != 1) || !(softmax_scale - softmax_scale == 0.f))
         return PVA_ERR_INVALID_ARG;
     AttnArgs a = {};
+    a.c = (softmax_scale > 0.f ? softmax_scale : 1.f / sqrtf((float)d)) * kLog2e;
+    if (cache->kind == PVA_CACHE_INT4) a.c *= kUp69;
+    if (!(a.c <= FLT_MAX)) return PVA_ERR_INVALID_ARG;
+    // (a slack past fp32's numbers would make -inf + slack a NaN: a first maximum has to rise from -inf)
+    a.slack = fminf(kSlack / a.c, FLT_MAX);
     a.q_stride = row_stride(q_stride, num_q_heads, d, 2);
     if (a.q_stride < 0) return PVA_ERR_INVALID_ARG;
     if (batch->num_tokens == 0 || batch->num_seqs == 0) return PVA_OK;
@@ -1213,12 +1219,6 @@ extern "C" pva_status pva_cache_attn(const pva_cache_desc* cache, const pva_cach
     a.group = num_q_heads / cache->num_kv_heads;
     a.window = window;
     a.out_fp32 = out_is_fp32;
-    a.c = (softmax_scale > 0.f ? softmax_scale : 1.f / sqrtf((float)d)) * kLog2e;
-    a.slack = kSlack / a.c;
-    if (cache->kind == PVA_CACHE_INT4) {
-        a.c *= kUp69;
-        a.slack *= 1.f / kUp69;
-    }
     const int64_t page_bytes =
         (int64_t)cache->num_kv_heads * cache->page_size * (cache->kind == PVA_CACHE_INT4 ? d / 2 : 2 * d);
     if (page_bytes > INT32_MAX) return PVA_ERR_UNSUPPORTED;

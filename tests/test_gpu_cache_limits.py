@@ -1,5 +1,5 @@
 """Ends of the rotation and cache calls' ranges on the GPU: offsets that do not fit, values that are not
-finite."""
+finite, scales and scores of any size."""
 import math
 
 import pytest
@@ -218,3 +218,21 @@ def test_rows_that_see_nothing_of_a_piece_stay_finite(int4):
     """Drafts under a short window: pieces that hold no key of a row are not poisoned."""
     p = Problem([4000], [16], 8, 2, 64, 16, int4)
     check_attention(p, *attend(p, window=5), p.attend(5))
+
+
+# ------------------------------------------------------------------ scales and scores of any size
+
+@pytest.mark.parametrize("int4", [False, True])
+@pytest.mark.parametrize("scale", [1e-45, 1e-40, 1e-38, 1e-30])
+def test_tiny_scales_weigh_equally(int4, scale):
+    """Scores that are 0 for fp32's weights: the result is the average, LSE the logarithm of the count."""
+    p = Problem([4033, 20, 1], [1, 2, 1], 8, 2, 128, 16, int4)
+    out, lse = attend(p, scale=scale, fp32=True)
+    for b, (n, m) in enumerate(zip(p.lens, p.news)):
+        v = p.cached("v", b)
+        for i in range(m):
+            c, r = n - m + i + 1, int(p.cu[b]) + i
+            mean = v[:c].mean(0).repeat_interleave(4, 0)
+            # equal weights of 1: sums of at most 4033 values below 6, each addition half a step of a sum below 2^15 / n
+            assert float((out[r].double().cpu() - mean).abs().max()) <= 1e-4
+            assert float((lse[:, r].double().cpu() - math.log(c)).abs().max()) <= 2e-6
