@@ -474,9 +474,10 @@ __global__ void __launch_bounds__(Shape<D, KIND, NT, H>::kThreads, Shape<D, KIND
     };
 
     // ---- state of the item in hand
-    // Scores stay as the products leave them; weights are 2^(c s + shift), shift = -c m
-    // (4 bits: + 64).
-    float o[NT][T][4], m_run[NT][2], shift[NT][2], l_run[NT][2];
+    // Scores stay as the products leave them; weights are 2^(c (s - m)) (4 bits: times 2^64),
+    // base being m, or 0 as long as m is -inf.  The difference is taken first: c m is rounded to
+    // its own last bit, which for scores past 2^30 is more than fp32's exponents hold.
+    float o[NT][T][4], m_run[NT][2], base[NT][2], l_run[NT][2];
     float zs[INT4 ? G : 1][NT][2];     // 4 bits: sums of weight * middle of the group
     float vs[INT4 ? G : 1][NT][4];     // 4 bits: sums of the rounded weight * scale
     uint32_t qs[HN][NT];                 // 4 bits: sums of the query's dims of a group
@@ -538,7 +539,7 @@ __global__ void __launch_bounds__(Shape<D, KIND, NT, H>::kThreads, Shape<D, KIND
 #pragma unroll
                     for (int e = 0; e < 4; ++e) o[nt][i][e] = 0.f;
                 m_run[nt][0] = m_run[nt][1] = -INFINITY;
-                shift[nt][0] = shift[nt][1] = 0.f;
+                base[nt][0] = base[nt][1] = 0.f;
                 l_run[nt][0] = l_run[nt][1] = 0.f;
                 const int32_t r = r0 + (H ? g & 3 : 8 * nt + g);
                 const int32_t tok = r / a.group;
@@ -746,7 +747,7 @@ __global__ void __launch_bounds__(Shape<D, KIND, NT, H>::kThreads, Shape<D, KIND
                         const float mn = fmaxf(m_run[nt][e], mx[nt][e]);
                         const float f = m_run[nt][e] == -INFINITY ? 0.f : ex2((m_run[nt][e] - mn) * a.c);
                         m_run[nt][e] = mn;
-                        shift[nt][e] = mn == -INFINITY ? 0.f : (INT4 ? 64.f : 0.f) - mn * a.c;
+                        base[nt][e] = mn == -INFINITY ? 0.f : mn;
                         l_run[nt][e] *= f;
 #pragma unroll
                         for (int i = 0; i < T; ++i) {
@@ -769,7 +770,7 @@ __global__ void __launch_bounds__(Shape<D, KIND, NT, H>::kThreads, Shape<D, KIND
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        s[z][nt][e] = ex2(fmaf(s[z][nt][e], a.c, shift[nt][e & 1]));
+                        s[z][nt][e] = ex2(fmaf(s[z][nt][e] - base[nt][e & 1], a.c, INT4 ? 64.f : 0.f));
                         l_run[nt][e & 1] += s[z][nt][e];
                     }
                 if (!INT4) {

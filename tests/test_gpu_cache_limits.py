@@ -236,3 +236,26 @@ def test_tiny_scales_weigh_equally(int4, scale):
             # equal weights of 1: sums of at most 4033 values below 6, each addition half a step of a sum below 2^15 / n
             assert float((out[r].double().cpu() - mean).abs().max()) <= 1e-4
             assert float((lse[:, r].double().cpu() - math.log(c)).abs().max()) <= 2e-6
+
+
+# scale, and what the queries are multiplied by: the scores' magnitude is the product of both
+@pytest.mark.parametrize("int4,scale,size", [(False, 1e38, 1e-38), (False, 1e30, 1.0), (False, 1.0, 1e12), (False, 1e-10, 1e30),
+                                             (True, 1e17, 1.0), (True, 1.0, 1e12), (True, 1e-10, 1e18), (True, 1e15, 1e-14)])
+def test_huge_scales_and_scores(int4, scale, size):
+    """Where the scores are further apart than fp32's weights reach, the largest key takes all the weight; else the formula."""
+    p = Problem([300, 4033], [1, 1], 4, 2, 64, 16, int4, seed=3)
+    p.q = (p.q.double() * size).bfloat16()
+    out, lse = attend(p, scale=scale, fp32=True, cu=False, q=p.q.contiguous().cuda())
+    for b in range(2):
+        k, v = p.cached("k", b), p.cached("v", b)
+        s = torch.einsum("hgd,lhd->hgl", p.q[b].double().unflatten(0, (2, 2)), k) * float(torch.tensor(scale, dtype=torch.float32))
+        want, ll = torch.einsum("hgl,lhd->hgd", s.softmax(-1), v).flatten(0, 1), torch.logsumexp(s, -1).flatten()
+        # small scores: 64 products of magnitude 40 in all, a last bit each (size 1e-38: of a subnormal number, 1.4e-45
+        # times 1e38): 64 * 40 * 2^-23 = 3e-4 of a weight, times values below 5; large ones: the best two are further
+        # apart than their rounding
+        top = s.topk(2, -1).values
+        clear = ((top[..., 0] - top[..., 1]) > 100) if scale * size > 1e3 else torch.ones(2, 2, dtype=torch.bool)
+        assert int(clear.sum()) >= 3
+        off = (out[b].double().cpu() - want).abs().amax(-1)
+        assert bool((off[clear.flatten()] <= 2e-3).all()), off
+        assert bool(((lse[:, b].double().cpu() - ll).abs() <= 1e-3 + 1e-4 * ll.abs()).all())
