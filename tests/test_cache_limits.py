@@ -1,6 +1,10 @@
-"""Ends of the rotation and cache calls' ranges that need no GPU: refusals, calls with nothing to do."""
+"""Ends of the rotation and cache calls' ranges that need no GPU: refusals, calls with nothing to do, and that
+the attention's error bounds notice what they are there for."""
 import pytest
+import torch
 
+import cache_bounds
+from cache_util import Problem
 from test_cache_abi import A, INVALID, L, attn, batch, cache  # noqa: F401
 
 
@@ -12,3 +16,24 @@ def test_scales_past_the_kernels_numbers_are_refused(L, kind, most, over):  # no
     assert attn(L, c=c, b=empty, scale=over) == INVALID
     for scale in (most, 1.0, 1e-30, 1e-38, 1e-45):
         assert attn(L, c=c, b=empty, scale=scale) == 0
+
+
+@pytest.mark.parametrize("int4", [False, True])
+@pytest.mark.parametrize("d", [64, 128])
+def test_bounds_notice_lost_keys_and_coarse_weights(int4, d):
+    p = Problem([5000, 300], [1, 2], 4, 2, d, 16, int4)
+    ref = cache_bounds.attend(p)
+    cache_bounds.check(ref[0].float(), ref[1].float(), ref)
+    with pytest.raises(AssertionError):
+        cache_bounds.check(torch.zeros_like(ref[0]), ref[1], ref)
+    for at in ((0, 0), (0, 2496), (0, 4984), (1, 160)):
+        lost = cache_bounds.attend(p, drop=at)
+        with pytest.raises(AssertionError, match="row"):
+            cache_bounds.check(lost[0], ref[1], ref)
+        with pytest.raises(AssertionError, match="lse"):
+            cache_bounds.check(ref[0], lost[1], ref)
+    with pytest.raises(AssertionError, match="row"):
+        cache_bounds.check(ref[0].bfloat16(), ref[1], ref)
+    if int4:
+        with pytest.raises(AssertionError, match="row"):
+            cache_bounds.check(cache_bounds.attend(p, eight=True)[0], ref[1], ref)

@@ -1,11 +1,12 @@
 """Ends of the rotation and cache calls' ranges on the GPU: offsets that do not fit, values that are not
-finite, scales and scores of any size."""
+finite, scales and scores of any size, long sums."""
 import math
 
 import pytest
 import torch
 
-from cache_util import Problem, angles, check_attention
+import cache_bounds
+from cache_util import Problem, angles, check_attention, unpack
 from packed_varlen_attention_cu_gb300 import api
 from test_gpu_cache import attend, i32, on_gpu, word
 
@@ -259,3 +260,82 @@ def test_huge_scales_and_scores(int4, scale, size):
         off = (out[b].double().cpu() - want).abs().amax(-1)
         assert bool((off[clear.flatten()] <= 2e-3).all()), off
         assert bool(((lse[:, b].double().cpu() - ll).abs() <= 1e-3 + 1e-4 * ll.abs()).all())
+
+
+# ------------------------------------------------------------------ long sums, precision of an fp32 result
+
+@pytest.mark.parametrize("int4", [False])
+@pytest.mark.parametrize("d,hq,hkv,lens,news,window", [
+    (128, 8, 2, [20000, 1, 777, 9000] + [50] * 30, [1] * 34, 0),
+    (64, 8, 2, [20000, 1, 777, 9000] + [50] * 30, [1] * 34, 0),
+    (128, 32, 8, [1000, 4033], [1, 1], 0),
+    (64, 14, 2, [300, 2500, 17], [4, 6, 1], 0),
+    (128, 6, 1, [300, 2500, 17], [16, 3, 1], 200),
+    (64, 4, 4, [64, 16, 5000], [1, 1, 2], 0)])
+def test_fp32_results(int4, d, hq, hkv, lens, news, window):
+    p = Problem(lens, news, hq, hkv, d, 16, int4, seed=len(lens))
+    out, lse = attend(p, window=window, fp32=True)
+    cache_bounds.check(out, lse, cache_bounds.attend(p, window))
+    # a bf16 result is the same sums, rounded once
+    short, same = attend(p, window=window)
+    assert torch.equal(short, out.bfloat16()) and torch.equal(same, lse)
+
+
+@pytest.mark.parametrize("int4", [False])
+def test_partials_of_disjoint_caches_merge_in_fp32(int4):
+    d, hq, hkv = 128, 8, 2
+    p = Problem([1600, 64], [1, 1], hq, hkv, d, 16, int4)
+    cache, q = on_gpu(p), p.q.contiguous().cuda()
+
+    def over(table, lens):
+        out, lse = torch.empty((2, hq, d), device="cuda"), torch.empty((hq, 2), device="cuda")
+        api.cache_attn(cache, q, table.contiguous().cuda(), i32(lens), out, lse, api.alloc_cache_workspace(2, hq, hkv, d))
+        return out, lse
+    a, la = over(p.table[:, :2], [32, 32])
+    b, lb = over(p.table[:, 2:], [1568, 32])
+    out, lse = torch.empty_like(a), torch.empty_like(la)
+    api.merge_partials(a, la, b, lb, out, lse)
+    cache_bounds.check(out, lse, cache_bounds.attend(p))
+
+
+@pytest.mark.parametrize("int4", [False])
+def test_long_sums_of_values_with_a_mean(int4):
+    """64 contexts of 131072 tokens, so that a warp sums tens of thousands of keys in one place, weights
+    near 1 and values of mean 1.  The weights' 16 bits and the scores' errors average out over so many
+    keys (below 1e-6); what is left is 2048 additions of fp32 a warp with errors of either sign, at most half
+    a step of a sum that grows to its end: 2^-24 * sqrt(2048 / 3) / sqrt(3) = 9e-7 expected, 2^-17 is eight times
+    that.  (A bias of half a last bit an addition would be 2048 / 2 * 2^-24 = 6e-5.)"""
+    d, hkv, page, ctx, batch = 128, 8, 64, 131072, 64
+    g = torch.Generator(device="cuda").manual_seed(2)
+    shape = (ctx // page, hkv, page)
+    if int4:
+        k, v = (torch.randint(0, 256, shape + (d // 2,), generator=g, dtype=torch.uint8, device="cuda") for _ in "kv")
+        ks, vs = (torch.empty(shape + (d // 64, 2), dtype=torch.bfloat16, device="cuda") for _ in "kv")
+        for s, mean in ((ks, 0.0), (vs, 1.0)):
+            s[..., 0] = torch.rand(shape + (2,), generator=g, device="cuda") * 0.05 + 0.1
+            s[..., 1] = mean - 7.5 * s[..., 0].float()
+        cache = api.KVCache(k, v, ks, vs)
+
+        def rows(h, x, s):
+            sc = s[:, h].double()
+            code = unpack(x[:, h].cpu()).cuda().double().unflatten(-1, (2, 64))
+            return (sc[..., 1:] + code * sc[..., :1]).flatten(-2).flatten(0, 1)
+    else:
+        k = torch.randn(shape + (d,), generator=g, device="cuda").bfloat16()
+        v = (torch.rand(shape + (d,), generator=g, device="cuda") * 1.5 + 0.25).bfloat16()
+        ks = vs = None
+        cache = api.KVCache(k, v)
+
+        def rows(h, x, s):
+            return x[:, h].flatten(0, 1).double()
+    table = torch.stack([torch.randperm(ctx // page, generator=g, device="cuda") for _ in range(batch)]).int()
+    q = (torch.randn((1, 4 * hkv, d), generator=g, device="cuda") * 0.3).bfloat16().expand(batch, -1, -1).contiguous()
+    out, lse = torch.empty((batch, 4 * hkv, d), device="cuda"), torch.empty((4 * hkv, batch), device="cuda")
+    api.cache_attn(cache, q, table, i32([ctx] * batch), out, lse, api.alloc_cache_workspace(batch, 4 * hkv, hkv, d))
+    for h in range(hkv):
+        kk, vv = rows(h, k, ks), rows(h, v, vs)
+        s = q[0, 4 * h:4 * h + 4].double() @ kk.t() * d ** -0.5
+        want = s.softmax(-1) @ vv
+        off = (out[:, 4 * h:4 * h + 4].double() - want) / want
+        assert float(off.abs().max()) <= 2 ** -17, (float(off.abs().max()), float(off.mean()))
+        assert float((lse[4 * h:4 * h + 4].double() - torch.logsumexp(s, -1)[:, None]).abs().max()) <= 1e-5
