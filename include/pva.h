@@ -447,10 +447,11 @@ size_t pva_cache_attn_bytes(int32_t num_seqs, int32_t num_q_heads, int32_t num_k
  * before every new token's window.  Of what a token sees, a score that is NaN or +inf makes
  * its O and LSE NaN, one of -inf has the weight 0, and a value that is not finite leaves its
  * dim of O (4 bits: its group of 64) not finite, whatever its weight; such a value may reach
- * the sequence's other new tokens.  fp32 sums; a bf16 cache's
- * weights keep 16 bits in the products, a 4-bit cache's 8 (values up to 2^50).  The
- * result does not depend on timing.  softmax_scale <= 0 selects 1/sqrt(head_dim);
- * it is finite, times log2(e) too, and with 4 bits at most 3.9e17. */
+ * the sequence's other new tokens.  fp32 sums; the
+ * weights keep 16 bits in the products.  With 4 bits queries are below 2^64 in magnitude and
+ * values at most 2^24; values below 2^-30 lose bits.  The result does not depend on timing.
+ * softmax_scale <= 0 selects 1/sqrt(head_dim); it is finite, times log2(e) too, and with
+ * 4 bits at most 3.9e17. */
 pva_status pva_cache_attn(const pva_cache_desc* cache, const pva_cache_batch* batch,
                           const void* q, int64_t q_stride, int32_t num_q_heads, int32_t max_new,
                           int32_t window, float softmax_scale, void* out, int32_t out_is_fp32,

@@ -742,7 +742,7 @@ __global__ void __launch_bounds__(Shape<D, KIND, NT, H>::kThreads, Shape<D, KIND
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
 #pragma unroll
-                        for (int d = 4; d < 32; d <<= 1)
+                        for (int d = H ? 2 : 4; d < 32; d <<= 1)  // (with H both halves of a row)
                             mx[nt][e] = fmaxf(mx[nt][e], __shfl_xor_sync(0xffffffffu, mx[nt][e], d));
                         const float mn = fmaxf(m_run[nt][e], mx[nt][e]);
                         const float f = m_run[nt][e] == -INFINITY ? 0.f : ex2((m_run[nt][e] - mn) * a.c);
@@ -806,11 +806,12 @@ __global__ void __launch_bounds__(Shape<D, KIND, NT, H>::kThreads, Shape<D, KIND
                     }
                 } else {
                     // v = middle + scale * (code - 7.5), middle = low + 7.5 scale.  weight * middle stays
-                    // in fp32; weight * scale meets the codes, rounded to bf16 once, and its own sum
-                    // takes the 7.5 off again at the item's end: so the rounding (2^-9) meets
-                    // scale * (code - 7.5), which is no larger than v, and not v - low (measured:
-                    // 0.0049 against 0.0022 of the result, whose own rounding is 0.0017).
-                    uint32_t sc[2][G], p[G][NT][2];
+                    // in fp32; weight * scale meets the codes as the sum of two bf16 numbers, 16 bits as
+                    // with a bf16 cache, and its own sum takes the 7.5 off again at the item's end: so the
+                    // rounding meets scale * (code - 7.5), which is no larger than v, and not v - low.
+                    // With H a tile's columns are half of the eight, so its low parts take the other half: both
+                    // halves of a row stand at one maximum and are added at the item's end.
+                    uint32_t sc[2][G], p[2][G][NT][2];
                     const int own_x = HN * z + mine;
                     scales(sc, buf + 2 * KS * ROWB + (KS + 16 * own_x + g) * Sh::kScaleBytes);
                     if (partial) no_token(sc, key0 + 16 * own_x + g, vlo, vhi, missing >> own_x & 1);
@@ -821,8 +822,11 @@ __global__ void __launch_bounds__(Shape<D, KIND, NT, H>::kThreads, Shape<D, KIND
 #pragma unroll
                             for (int y = 0; y < 2; ++y) {
                                 const float scl = lo_f(sc[y][gr]), mid = fmaf(7.5f, scl, hi_f(sc[y][gr]));
-                                p[gr][nt][y] = transpose8(
-                                    pack2(s[z][nt][2 * y] * scl, s[z][nt][2 * y + 1] * scl));
+                                const float p0 = s[z][nt][2 * y] * scl, p1 = s[z][nt][2 * y + 1] * scl;
+                                const uint32_t hi = pack2(p0, p1);
+                                p[0][gr][nt][y] = transpose8(hi);
+                                p[1][gr][nt][y] = transpose8(pack2(p0 - lo_f(hi), p1 - hi_f(hi)));
+                                if (H) p[1][gr][nt][y] = __shfl_xor_sync(0xffffffffu, p[1][gr][nt][y], 16);
                                 zs[gr][nt][0] = fmaf(s[z][nt][2 * y], mid, zs[gr][nt][0]);
                                 zs[gr][nt][1] = fmaf(s[z][nt][2 * y + 1], mid, zs[gr][nt][1]);
                             }
@@ -831,7 +835,8 @@ __global__ void __launch_bounds__(Shape<D, KIND, NT, H>::kThreads, Shape<D, KIND
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
                             const uint32_t ones[4] = {0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u};
-                            mma(vs[gr][nt], ones, p[gr][nt][0], p[gr][nt][1]);
+                            mma(vs[gr][nt], ones, p[0][gr][nt][0], p[0][gr][nt][1]);
+                            mma(vs[gr][nt], ones, p[1][gr][nt][0], p[1][gr][nt][1]);
                         }
 #pragma unroll
                     for (int hh = 0; hh < HN; ++hh) {
@@ -859,12 +864,12 @@ __global__ void __launch_bounds__(Shape<D, KIND, NT, H>::kThreads, Shape<D, KIND
                                                    __byte_perm(w[0][gr], w[1][gr], 0x7632),
                                                    __byte_perm(w[2][gr], w[3][gr], 0x5410),
                                                    __byte_perm(w[2][gr], w[3][gr], 0x7632)};
-                            uint32_t b[NT][2];  // with H: the columns of this tile
+                            uint32_t b[NT][2];
 #pragma unroll
                             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                                 for (int y = 0; y < 2; ++y)
-                                    b[nt][y] = !H || (g >> 2) == hh ? p[gr][nt][y] : 0u;
+                                    b[nt][y] = !H || (g >> 2) == hh ? p[0][gr][nt][y] : p[1][gr][nt][y];
 #pragma unroll
                             for (int h = 0; h < 2; ++h) {
                                 // tile 2h: the lower code of a byte; tile 2h + 1: the whole byte, from
@@ -879,6 +884,10 @@ __global__ void __launch_bounds__(Shape<D, KIND, NT, H>::kThreads, Shape<D, KIND
                                 for (int nt = 0; nt < NT; ++nt) {
                                     mma(o[nt][4 * gr + 2 * h], lo, b[nt][0], b[nt][1]);
                                     mma(o[nt][4 * gr + 2 * h + 1], f, b[nt][0], b[nt][1]);
+                                    if (!H) {
+                                        mma(o[nt][4 * gr + 2 * h], lo, p[1][gr][nt][0], p[1][gr][nt][1]);
+                                        mma(o[nt][4 * gr + 2 * h + 1], f, p[1][gr][nt][0], p[1][gr][nt][1]);
+                                    }
                                 }
                             }
                         }

@@ -264,7 +264,7 @@ def test_huge_scales_and_scores(int4, scale, size):
 
 # ------------------------------------------------------------------ long sums, precision of an fp32 result
 
-@pytest.mark.parametrize("int4", [False])
+@pytest.mark.parametrize("int4", [False, True])
 @pytest.mark.parametrize("d,hq,hkv,lens,news,window", [
     (128, 8, 2, [20000, 1, 777, 9000] + [50] * 30, [1] * 34, 0),
     (64, 8, 2, [20000, 1, 777, 9000] + [50] * 30, [1] * 34, 0),
@@ -281,7 +281,7 @@ def test_fp32_results(int4, d, hq, hkv, lens, news, window):
     assert torch.equal(short, out.bfloat16()) and torch.equal(same, lse)
 
 
-@pytest.mark.parametrize("int4", [False])
+@pytest.mark.parametrize("int4", [False, True])
 def test_partials_of_disjoint_caches_merge_in_fp32(int4):
     d, hq, hkv = 128, 8, 2
     p = Problem([1600, 64], [1, 1], hq, hkv, d, 16, int4)
@@ -298,7 +298,23 @@ def test_partials_of_disjoint_caches_merge_in_fp32(int4):
     cache_bounds.check(out, lse, cache_bounds.attend(p))
 
 
-@pytest.mark.parametrize("int4", [False])
+@pytest.mark.parametrize("size", [2.0 ** -30, 2.0 ** -15, 2.0 ** 22])
+def test_sizes_of_values_in_4_bits(size):
+    """The header's range of values (the largest of these are below 2^24), fp32 results."""
+    p = Problem([3000, 300, 17], [1, 2, 1], 8, 2, 128, 16, True, v_spread=size, garbage=0.0)
+    check = attend(p, fp32=True)
+    cache_bounds.check(*check, cache_bounds.attend(p))
+
+
+@pytest.mark.parametrize("window", [0, 40])
+@pytest.mark.parametrize("rows", [1, 2, 3, 4, 5, 8])
+def test_4_bits_by_rows_a_head(rows, window):
+    """Up to four rows share the columns of two key tiles, with one maximum for both; more do not."""
+    p = Problem([2100, 65, 16, 1], [1, 1, 1, 1], 2 * rows, 2, 128, 32, True, seed=rows)
+    cache_bounds.check(*attend(p, window=window, fp32=True), cache_bounds.attend(p, window))
+
+
+@pytest.mark.parametrize("int4", [False, True])
 def test_long_sums_of_values_with_a_mean(int4):
     """64 contexts of 131072 tokens, so that a warp sums tens of thousands of keys in one place, weights
     near 1 and values of mean 1.  The weights' 16 bits and the scores' errors average out over so many
