@@ -405,7 +405,8 @@ typedef struct {
  * positions kv_lens[b] - n_b + i.  fp32 arithmetic, rounded to bf16 as pva_rope
  * does; an INT4 row is made from the bf16 row: low = min of the group, scale =
  * bf16((max - min) / 15), code = round((x - low) / scale) to even, 0 to 15.  A
- * group with an infinity or NaN is read back as NaN.
+ * group with an infinity or NaN, or with finite values further apart than fp32's
+ * largest number, is read back as NaN.
  *   rope          or NULL: no rotation
  *   k, v          DEVICE bf16 [num_tokens, num_kv_heads, head_dim]
  *   q, q_out      DEVICE bf16 [num_tokens, num_q_heads, head_dim], both or neither

@@ -95,12 +95,13 @@ __device__ __forceinline__ void turn(float& a, float& b, float c, float s) {
     a = x;
 }
 
-// Codes of eight values of a group with (low, inv): one 32-bit word.
-__device__ __forceinline__ uint32_t encode(const float* x, float low, float inv) {
+// Codes of eight values of a group with (low, inv): one 32-bit word.  up is a power of two
+// that inv has been divided by.
+__device__ __forceinline__ uint32_t encode(const float* x, float low, float up, float inv) {
     uint32_t w = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const float c = fminf(fmaxf(rintf(__fmul_rn(__fsub_rn(x[i], low), inv)), 0.f), 15.f);
+        const float c = fminf(fmaxf(rintf(__fmul_rn(__fmul_rn(__fsub_rn(x[i], low), up), inv)), 0.f), 15.f);
         w |= (uint32_t)c << (4 * (i / 2) + 16 * (i % 2));
     }
     return w;
@@ -310,27 +311,29 @@ __global__ void __launch_bounds__(kThreads, 3) rotate_kernel(const RotArgs a) {
                         }
                     }
                     // The scale is kept in bf16 and the codes are taken against the kept one;
-                    // low is one of the bf16 values, so it is kept exactly.
-                    float inv[kG];
+                    // low is one of the bf16 values, so it is kept exactly.  Scales down to 2^-133
+                    // have a reciprocal in fp32 times 2^100 (a power of two changes no rounding).
+                    float inv[kG], up[kG];
                     uint32_t pair[kG];
 #pragma unroll
                     for (int g = 0; g < kG; ++g) {
                         const __nv_bfloat16 sc =
                             __float2bfloat16_rn(__fmul_rn(__fsub_rn(hi[g], lo[g]), 1.f / 15.f));
+                        constexpr float kUp100 = 1267650600228229401496703205376.f;  // 2^100
                         const float f = __bfloat162float(sc);
-                        inv[g] = f == 0.f ? 0.f : __frcp_rn(f);
+                        up[g] = f < 1.f / kUp100 ? kUp100 : 1.f;
+                        inv[g] = f == 0.f ? 0.f : __frcp_rn(f * up[g]);
                         pair[g] = (uint32_t)__bfloat16_as_ushort(sc) |
                                   (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(lo[g])) << 16;
                     }
                     if (put) {
                         uint32_t* o = (uint32_t*)(is_k ? a.k_pages : a.v_pages) + at * (D / 8);
                         uint32_t* so = (uint32_t*)(is_k ? a.k_scales : a.v_scales) + at * kG;
-                        o[word_of_octet<D>(oa)] =
-                            encode(x, kG == 2 && ga ? lo[kG - 1] : lo[0],
-                                   kG == 2 && ga ? inv[kG - 1] : inv[0]);
-                        o[word_of_octet<D>(ob)] =
-                            encode(x + 8, kG == 2 && gb ? lo[kG - 1] : lo[0],
-                                   kG == 2 && gb ? inv[kG - 1] : inv[0]);
+                        const bool ia = kG == 2 && ga > 0, ib = kG == 2 && gb > 0;  // of the second group
+                        o[word_of_octet<D>(oa)] = encode(x, ia ? lo[kG - 1] : lo[0], ia ? up[kG - 1] : up[0],
+                                                         ia ? inv[kG - 1] : inv[0]);
+                        o[word_of_octet<D>(ob)] = encode(x + 8, ib ? lo[kG - 1] : lo[0], ib ? up[kG - 1] : up[0],
+                                                         ib ? inv[kG - 1] : inv[0]);
                         if (j == 0) {
 #pragma unroll
                             for (int g = 0; g < kG; ++g) so[g] = pair[g];

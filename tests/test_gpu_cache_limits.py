@@ -1,12 +1,12 @@
 """Ends of the rotation and cache calls' ranges on the GPU: offsets that do not fit, values that are not
-finite, scales and scores of any size, long sums."""
+finite, scales and scores of any size, long sums, small rows."""
 import math
 
 import pytest
 import torch
 
 import cache_bounds
-from cache_util import Problem, angles, check_attention, unpack
+from cache_util import Problem, angles, check_attention, quantise, unpack, values
 from packed_varlen_attention_cu_gb300 import api
 from test_gpu_cache import attend, i32, on_gpu, word
 
@@ -355,3 +355,42 @@ def test_long_sums_of_values_with_a_mean(int4):
         off = (out[:, 4 * h:4 * h + 4].double() - want) / want
         assert float(off.abs().max()) <= 2 ** -17, (float(off.abs().max()), float(off.mean()))
         assert float((lse[4 * h:4 * h + 4].double() - torch.logsumexp(s, -1)[:, None]).abs().max()) <= 1e-5
+
+
+# ------------------------------------------------------------------ 4-bit rows of small magnitude
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("top", [2.0 ** -60, 2.0 ** -99, 2.0 ** -101, 2.0 ** -120, 2.0 ** -125, 2.0 ** -128, 2.0 ** -130])
+def test_codes_of_small_groups_are_the_nearest(d, top):
+    """Scales down to bf16's smallest subnormal number, 2^-133: every code is round((x - low) / scale)."""
+    g = torch.Generator().manual_seed(0)
+    rows = (torch.randn((40, 1, d), generator=g) * top).bfloat16()
+    rows[0, 0, :] = 0
+    rows[1, 0, ::2], rows[1, 0, 1::2] = 2.0 ** -133, 0
+    low, high = (f(rows.double().unflatten(-1, (-1, 64)), -1) for f in (torch.amin, torch.amax))
+    scale = ((high - low) / 15).float().bfloat16().double()
+    x = rows.double().unflatten(-1, (-1, 64))
+    ratio = (x - low[..., None]) / torch.where(scale > 0, scale, torch.ones_like(scale))[..., None]
+    code = torch.where(scale[..., None] > 0, ratio.round().clamp(0, 15), torch.zeros_like(x)).flatten(-2)
+    # (a quotient next to a border may go either way: reciprocal and product round, 2 * 2^-24 of at most 15)
+    clear = ((ratio - ratio.floor() - 0.5).abs() > 2.0 ** -18).flatten(-2)
+    cache = api.KVCache.alloc(3, 1, d, 16, api.CACHE_INT4)
+    dev, table, ends = rows.cuda(), i32([[2, 0, 1]]), i32([0, 40])
+    api.cache_append(cache, dev, dev, table, ends[1:], cu_new=ends)
+    j = torch.arange(40)
+    at = (torch.tensor([2, 0, 1])[j // 16], slice(None), j % 16)
+    for held, pair in ((cache.k, cache.k_scales), (cache.v, cache.v_scales)):
+        got = unpack(held.cpu()[at])
+        assert torch.equal(got[clear], code.long()[clear]) and bool(((got - code).abs() <= 1).all())
+        assert torch.equal(pair.cpu()[at].double(), torch.stack((scale, low), -1))
+    ko, vo = torch.empty_like(dev), torch.empty_like(dev)
+    api.cache_read(cache, table, ends, ko, vo)
+    want = values(got, scale.float(), low.float()).float().bfloat16()
+    assert torch.equal(ko.cpu(), want) and torch.equal(vo.cpu(), want)
+
+
+def test_codes_of_ordinary_groups_did_not_change():
+    rows = torch.randn((64, 2, 128), generator=torch.Generator().manual_seed(9)).bfloat16()
+    cache = api.KVCache.alloc(1, 2, 128, 64, api.CACHE_INT4)
+    api.cache_append(cache, rows.cuda(), rows.cuda(), i32([[0]]), i32([64]), cu_new=i32([0, 64]))
+    assert torch.equal(unpack(cache.k[0].transpose(0, 1).cpu()), quantise(rows)[0])
