@@ -586,8 +586,7 @@ extern "C" pva_status pva_cache_append(const pva_cache_desc* cache, const pva_ca
     if (st == PVA_OK) st = check_rope(rope, cache->head_dim);
     if (st != PVA_OK) return st;
     const int32_t d = cache->head_dim, hkv = cache->num_kv_heads;
-    if (num_q_heads < 0 || (num_q_heads > 0) != (q != nullptr) || (q == nullptr) != (q_out == nullptr))
-        return PVA_ERR_INVALID_ARG;
+    if (num_q_heads < 0) return PVA_ERR_INVALID_ARG;
     RotArgs a = {};
     a.q_stride = row_stride(q_stride, num_q_heads, d, 2);
     a.k_stride = row_stride(k_stride, hkv, d, 2);
@@ -597,7 +596,8 @@ extern "C" pva_status pva_cache_append(const pva_cache_desc* cache, const pva_ca
     if (a.q_stride < 0 || a.k_stride < 0 || a.v_stride < 0 || a.q_out_stride < 0 ||
         a.k_out_stride < 0)
         return PVA_ERR_INVALID_ARG;
-    if (batch->num_tokens == 0 || batch->num_seqs == 0) return PVA_OK;
+    if (batch->num_tokens == 0 || batch->num_seqs == 0) return PVA_OK;  // (empty tensors have no address)
+    if ((num_q_heads > 0) != (q != nullptr) || (q == nullptr) != (q_out == nullptr)) return PVA_ERR_INVALID_ARG;
     if (!k || !v || !aligned16(k) || !aligned16(v) || !aligned16(q) || !aligned16(q_out) ||
         !aligned16(k_out))
         return PVA_ERR_INVALID_ARG;

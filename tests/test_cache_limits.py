@@ -5,7 +5,7 @@ import torch
 
 import cache_bounds
 from cache_util import Problem
-from test_cache_abi import A, INVALID, L, attn, batch, cache  # noqa: F401
+from test_cache_abi import A, INVALID, L, append, attn, batch, cache  # noqa: F401
 
 
 @pytest.mark.parametrize("kind,most,over", [(0, 2e38, 3e38), (1, 3.9e17, 4.1e17)])
@@ -37,3 +37,12 @@ def test_bounds_notice_lost_keys_and_coarse_weights(int4, d):
     if int4:
         with pytest.raises(AssertionError, match="row"):
             cache_bounds.check(cache_bounds.attend(p, eight=True)[0], ref[1], ref)
+
+
+def test_an_empty_batch_needs_no_pointers(L):  # noqa: F811
+    """Empty tensors have no address: no new tokens, with or without queries, is nothing to do."""
+    for b in (batch(num_tokens=0, cu_new=A), batch(num_tokens=0), batch(num_seqs=0)):
+        assert append(L, b=b, k=None, v=None, q=None, hq=4, qo=None) == 0
+        assert append(L, b=b, k=None, v=None, q=None, hq=0, qo=None) == 0
+        assert append(L, b=b, hq=-1) == INVALID
+        assert attn(L, b=b, q=None, out=None, lse=None, ws=None) == 0

@@ -1,5 +1,5 @@
 """Ends of the rotation and cache calls' ranges on the GPU: offsets that do not fit, values that are not
-finite, scales and scores of any size, long sums, small rows."""
+finite, scales and scores of any size, long sums, small rows, empty batches."""
 import math
 
 import pytest
@@ -394,3 +394,22 @@ def test_codes_of_ordinary_groups_did_not_change():
     cache = api.KVCache.alloc(1, 2, 128, 64, api.CACHE_INT4)
     api.cache_append(cache, rows.cuda(), rows.cuda(), i32([[0]]), i32([64]), cu_new=i32([0, 64]))
     assert torch.equal(unpack(cache.k[0].transpose(0, 1).cpu()), quantise(rows)[0])
+
+
+# ------------------------------------------------------------------ nothing to do
+
+@pytest.mark.parametrize("sequences", [0, 3])
+def test_an_empty_batch(sequences):
+    """No new token in the whole batch: every call returns and writes nothing."""
+    cache = api.KVCache.alloc(2, 2, 64, 16)
+    kv, qs = (torch.empty((0, h, 64), dtype=torch.bfloat16, device="cuda") for h in (2, 4))
+    table, lens = torch.zeros((sequences, 2), dtype=torch.int32, device="cuda"), i32([5] * sequences)
+    cu, status = i32([0] * (sequences + 1)), word()
+    ang = angles(8, 64).cuda()
+    api.cache_append(cache, kv, kv, table, lens, cu_new=cu, table=ang, q=qs, q_out=qs, k_out=kv, status=status)
+    api.cache_append(cache, kv, kv, table, lens, cu_new=cu, status=status)
+    api.rope(qs, kv, ang, qs, kv, cu_seqlens=cu, status=status)
+    api.cache_read(cache, table, cu, kv, kv, status=status)
+    lse = torch.empty((4, 0), device="cuda")
+    api.cache_attn(cache, qs, table, lens, qs, lse, api.alloc_cache_workspace(sequences, 4, 2, 64), cu_new=cu, status=status)
+    assert api.cache_status(status) == 0 and not bool(cache.k.any()) and not bool(cache.v.any())
