@@ -501,6 +501,10 @@ pva_status launch_read(const ReadArgs& a, cudaStream_t st) {
                                                                                             : PVA_ERR_CUDA;
 }
 
+// Heads of one token past which no grid has blocks for them (65535 of at most 40), and far
+// below which sums of counts stay in 32 bits.
+constexpr int64_t kMaxSlots = 1 << 24;
+
 // The angle table: rot_dim 0 (or no descriptor) means no rotation.
 pva_status check_rope(const pva_rope_desc* r, int32_t head_dim) {
     if (!r) return PVA_OK;
@@ -538,6 +542,7 @@ extern "C" pva_status pva_rope(const void* q, int64_t q_stride, const void* k, i
     if (head_dim != 64 && head_dim != 128) return PVA_ERR_UNSUPPORTED;
     const pva_status rs = check_rope(rope, head_dim);
     if (rs != PVA_OK) return rs;
+    if ((int64_t)num_q_heads + num_kv_heads > kMaxSlots) return PVA_ERR_UNSUPPORTED;
     if (cu_seqlens_dev && positions_dev) return PVA_ERR_INVALID_ARG;
     if (!aligned4(cu_seqlens_dev) || !aligned4(positions_dev) || !aligned4(status_dev))
         return PVA_ERR_INVALID_ARG;
@@ -587,6 +592,7 @@ extern "C" pva_status pva_cache_append(const pva_cache_desc* cache, const pva_ca
     if (st != PVA_OK) return st;
     const int32_t d = cache->head_dim, hkv = cache->num_kv_heads;
     if (num_q_heads < 0) return PVA_ERR_INVALID_ARG;
+    if (num_q_heads + 2 * (int64_t)hkv > kMaxSlots) return PVA_ERR_UNSUPPORTED;
     RotArgs a = {};
     a.q_stride = row_stride(q_stride, num_q_heads, d, 2);
     a.k_stride = row_stride(k_stride, hkv, d, 2);

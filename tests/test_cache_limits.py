@@ -5,7 +5,7 @@ import torch
 
 import cache_bounds
 from cache_util import Problem
-from test_cache_abi import A, INVALID, L, append, attn, batch, cache  # noqa: F401
+from test_cache_abi import A, INVALID, UNSUPPORTED, L, append, attn, batch, cache, rope  # noqa: F401
 
 
 @pytest.mark.parametrize("kind,most,over", [(0, 2e38, 3e38), (1, 3.9e17, 4.1e17)])
@@ -46,3 +46,15 @@ def test_an_empty_batch_needs_no_pointers(L):  # noqa: F811
         assert append(L, b=b, k=None, v=None, q=None, hq=0, qo=None) == 0
         assert append(L, b=b, hq=-1) == INVALID
         assert attn(L, b=b, q=None, out=None, lse=None, ws=None) == 0
+
+
+def test_head_counts_past_the_grid_are_refused(L):  # noqa: F811
+    """Counts whose sum leaves 32 bits, or that fill more blocks than a grid has."""
+    top = 2 ** 31 - 1
+
+    def turn(hq, hkv):
+        return L.pva_rope(A, 0, A, 0, 5, hq, hkv, 64, 0, rope(), None, 0, None, 0, A, 0, A, 0, None, None)
+    assert turn(top, top) == turn(top, 1) == turn(2 ** 30, 2 ** 30) == turn(top, 0) == turn(0, top) == UNSUPPORTED
+    for hq, hkv in ((top, 2), (4, 2 ** 30), (top, 2 ** 30), (4, top), (2, 2 ** 30 - 1)):
+        assert append(L, c=cache(num_kv_heads=hkv), hq=hq) == UNSUPPORTED
+    assert append(L, c=cache(num_kv_heads=top), q=None, hq=0, qo=None) == UNSUPPORTED
