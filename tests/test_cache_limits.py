@@ -5,6 +5,7 @@ import torch
 
 import cache_bounds
 from cache_util import Problem
+from packed_varlen_attention_cu_gb300 import api
 from test_cache_abi import A, INVALID, UNSUPPORTED, L, append, attn, batch, cache, rope  # noqa: F401
 
 
@@ -58,3 +59,14 @@ def test_head_counts_past_the_grid_are_refused(L):  # noqa: F811
     for hq, hkv in ((top, 2), (4, 2 ** 30), (top, 2 ** 30), (4, top), (2, 2 ** 30 - 1)):
         assert append(L, c=cache(num_kv_heads=hkv), hq=hq) == UNSUPPORTED
     assert append(L, c=cache(num_kv_heads=top), q=None, hq=0, qo=None) == UNSUPPORTED
+
+
+def test_the_binding_needs_no_private_function_of_torch(monkeypatch):
+    """The stream's handle comes from a private function of torch where there is one, else from the Stream."""
+    class Stream:
+        cuda_stream = 0x1234
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: Stream)
+    monkeypatch.setattr(api, "_raw_stream", None)
+    assert api._queue(None, 0) == 0x1234 and api._queue(Stream, 0) == 0x1234 and api._queue(7, 0) == 7
+    monkeypatch.setattr(api, "_raw_stream", lambda dev: 0x5678 + dev)
+    assert api._queue(None, 1) == 0x5679 and api._queue(Stream, 1) == 0x1234 and api._queue(0, 1) == 0

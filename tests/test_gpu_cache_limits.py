@@ -413,3 +413,16 @@ def test_an_empty_batch(sequences):
     lse = torch.empty((4, 0), device="cuda")
     api.cache_attn(cache, qs, table, lens, qs, lse, api.alloc_cache_workspace(sequences, 4, 2, 64), cu_new=cu, status=status)
     assert api.cache_status(status) == 0 and not bool(cache.k.any()) and not bool(cache.v.any())
+
+
+def test_without_torchs_private_stream_function(monkeypatch):
+    """The calls go to the current stream also where torch has no function for its bare handle."""
+    p = Problem([50, 7], [1, 1], 4, 2, 64, 16)
+    want = attend(p)
+    monkeypatch.setattr(api, "_raw_stream", None)
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        assert api._queue(None, 0) == side.cuda_stream
+        got = attend(p)
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
