@@ -1,5 +1,5 @@
 """Ends of the rotation and cache calls' ranges on the GPU: offsets that do not fit, values that are not
-finite, scales and scores of any size, long sums, small rows, empty batches."""
+finite, scales and scores of any size, long sums, small rows, empty batches, the calls among other work."""
 import math
 
 import pytest
@@ -413,6 +413,52 @@ def test_an_empty_batch(sequences):
     lse = torch.empty((4, 0), device="cuda")
     api.cache_attn(cache, qs, table, lens, qs, lse, api.alloc_cache_workspace(sequences, 4, 2, 64), cu_new=cu, status=status)
     assert api.cache_status(status) == 0 and not bool(cache.k.any()) and not bool(cache.v.any())
+
+
+# ------------------------------------------------------------------ the calls among other work of a stream
+
+def test_captured_behind_a_copy_and_across_streams():
+    """The lengths and rows come by a copy right before the calls, the attention runs on another
+    stream behind an event: eagerly, captured, and replayed with other inputs."""
+    p = Problem([700, 33, 64], [1, 1, 1], 8, 2, 64, 16, garbage=0.0)
+    cache, table, ang = on_gpu(p), p.table.cuda(), angles(800, 64).cuda()
+    src = torch.randn((3, 12, 64), device="cuda").bfloat16()
+    wide, lens = torch.zeros_like(src), i32([0, 0, 0])
+    src_lens, qr = i32(p.lens), torch.empty((3, 8, 64), dtype=torch.bfloat16, device="cuda")
+    out, lse = torch.empty_like(qr), torch.empty((8, 3), device="cuda")
+    ws, side = api.alloc_cache_workspace(3, 8, 2, 64), torch.cuda.Stream()
+
+    def step():
+        wide.copy_(src)
+        lens.copy_(src_lens)
+        api.cache_append(cache, wide[:, 8:10], wide[:, 10:], table, lens, table=ang, q=wide[:, :8], q_out=qr)
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            api.cache_attn(cache, qr, table, lens, out, lse, ws)
+            lens.zero_()
+        torch.cuda.current_stream().wait_stream(side)
+        wide.zero_()
+    main = torch.cuda.Stream()
+    with torch.cuda.stream(main):
+        step()
+    torch.cuda.synchronize()
+    want = out.clone(), lse.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=main):
+        step()
+    out.zero_(), lse.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+    src.normal_()
+    src_lens.copy_(i32([650, 20, 1]))
+    torch.cuda.synchronize()
+    graph.replay()
+    torch.cuda.synchronize()
+    got = out.clone(), lse.clone()
+    step()
+    torch.cuda.synchronize()
+    assert torch.equal(out, got[0]) and torch.equal(lse, got[1]) and not torch.equal(got[0], want[0])
 
 
 def test_without_torchs_private_stream_function(monkeypatch):
