@@ -435,7 +435,7 @@ size_t pva_cache_attn_bytes(int32_t num_seqs, int32_t num_q_heads, int32_t num_k
 /* Attention of the new tokens over the cache: the token at position t sees the
  * cached keys j <= t of its sequence, and with window > 0 only t - j < window
  * (the masks of pva_attn_fwd).  Made for few new tokens a sequence (one, or some
- * drafts); any number is right, and from about 50 on pva_cache_read and
+ * drafts); any number is right, and from about 45 on pva_cache_read and
  * pva_attn_fwd (one CAUSAL slice a sequence) are faster.
  *   q          DEVICE bf16 [num_tokens, num_q_heads, head_dim], rotated as the keys are
  *   out        DEVICE [num_tokens, num_q_heads, head_dim], bf16 or fp32

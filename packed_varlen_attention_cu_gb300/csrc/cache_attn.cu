@@ -11,7 +11,7 @@
 // half of every product, of the softmax and of the registers on absent rows.  More
 // rows of a bf16 cache take two column tiles on the same K and V fragments, 16 rows an
 // item; four column tiles spilled and were slower than reading K and V again from L2
-// (32 rows of 128 dims, 64 contexts of 4000 .. 9001 keys: 567 us against 303 us).
+// (32 rows of 128 dims, 64 contexts of 4000 .. 9001 keys: 567 us against 305 us).
 // (tcgen05 tiles start at 64 rows of D and take their operands from shared memory,
 // where 4-bit rows would have to be written back expanded.)
 //
@@ -74,11 +74,12 @@ struct Shape {
     // Ring sizes: bf16 16 KB (128 dims) a step and warp in flight at 8 warps an SM keep HBM
     // busy (98% of the copy rate on a batch of 64 contexts).  4 bits are bounded by issue slots
     // and the integer pipe, not by HBM: 64 keys a step spread a step's fixed instructions (16
-    // keys: 143 us, 32: 91 us, 64: 84 us on 3 contexts of 131072), and twelve warps with two
-    // stages beat eight (84 -> 82 us).
+    // keys: 143 us, 32: 91 us, 64: 84 us on 3 contexts of 131072, with weights of 8 bits), and
+    // twelve warps with two stages beat eight (84 -> 82 us).  At 128 dims their 168 registers
+    // spill 28 (up to four rows) and 48 bytes.
     // An item's fixed cost (queries, join, results) in blocks of keys.  bf16: 256 contexts of
-    // 10 .. 1000 tokens 60.6 us at 1, 50.7 us at 3; 4 bits, whose block is four times as
-    // long: 2 is no better than 1, 0 is worse.
+    // 10 .. 1000 tokens 61.6 us at 1, 53.7 us at 3; 4 bits, whose block is four times as
+    // long: 96 contexts of 200 .. 16000 with their append 71.1 us at 0, 60.3 at 1, 61.4 at 2.
     static constexpr int kFixed = kInt4 ? 1 : 3;
     static constexpr int kBlock = kWarps * kKeys;  // keys of a unit
     static constexpr int kRowBytes = kInt4 ? D / 2 : 2 * D;
@@ -775,8 +776,8 @@ __global__ void __launch_bounds__(Shape<D, KIND, NT, H>::kThreads, Shape<D, KIND
                     }
                 if (!INT4) {
                     // the values are bf16, so the weights go in as the sum of two bf16 numbers: 16 of
-                    // their bits, and what the result loses is its own rounding.  (One bf16 number
-                    // alone adds as much again; the second product hides behind HBM.)
+                    // their bits (2^-17), and what a bf16 result loses is its own rounding (2^-8).  One
+                    // bf16 number alone adds as much again; the second product hides behind HBM.
                     uint32_t p[NT][2], q[NT][2];
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
@@ -809,6 +810,8 @@ __global__ void __launch_bounds__(Shape<D, KIND, NT, H>::kThreads, Shape<D, KIND
                     // in fp32; weight * scale meets the codes as the sum of two bf16 numbers, 16 bits as
                     // with a bf16 cache, and its own sum takes the 7.5 off again at the item's end: so the
                     // rounding meets scale * (code - 7.5), which is no larger than v, and not v - low.
+                    // (One number is off by 2^-8: an fp32 result over 32768 random values by 1.7e-3, with
+                    // two by 9e-5, most of it the sums' rounding; 82.7 against 86.7 us on 3 contexts of 131072.)
                     // With H a tile's columns are half of the eight, so its low parts take the other half: both
                     // halves of a row stand at one maximum and are added at the item's end.
                     uint32_t sc[2][G], p[2][G][NT][2];
@@ -1167,9 +1170,11 @@ pva_status launch(AttnArgs a, uint8_t* ws, cudaStream_t st) {
 }
 
 // Variants by rows a kv head: 4 bits up to 4 rows two key tiles in the columns, else items of 8
-// rows (two column tiles of 16 rows were slower: 12 contexts to 49635 tokens, 12 rows: 52 us
-// against 37 us; 32 contexts to 16000, 32 rows: 85 against 83); bf16 up to 8 rows one column
-// tile, else items of 16 rows (4 contexts of 8192, 4 rows 31 us, 16 rows 33 us).
+// rows (two column tiles of 16 rows were slower, with weights of 8 bits: 12 contexts to 49635
+// tokens, 12 rows: 52 us against 37 us; 32 contexts to 16000, 32 rows: 85 against 83; now 41 and
+// 99 us, append included); bf16 up to 8 rows one column tile, else items of 16 rows (4 contexts of
+// 8192: up to 16 rows 33.2 us, 32.6 with items of 8; up to 64 rows 35.5 and 42.5 us; 64 contexts
+// of 4000 .. 9001, up to 32 rows: 305 and 443 us).
 template <int D, int KIND>
 pva_status launch_rows(int64_t rows, const AttnArgs& a, uint8_t* ws, cudaStream_t st) {
     if constexpr (KIND == PVA_CACHE_INT4)

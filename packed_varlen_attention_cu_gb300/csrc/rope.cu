@@ -132,9 +132,9 @@ __device__ __forceinline__ int32_t seq_of_lane(const SeqView& s, int32_t t0, int
 // interleaved pairs, which lie inside a vector, one of each half of the head.  So a
 // rotation needs no shuffle, a warp's accesses are whole lines, and a lane's angles serve
 // all its heads.  The heads of q, k and v form one list of slots, whatever their counts.
-// Bounded by HBM; three CTAs an SM (85 registers) measured best: 131072 tokens of 40 heads
-// of 128, bf16: 472 us without the bound, 415 us with it (96% of the copy rate), 454 us
-// with four.
+// Bounded by HBM; three CTAs an SM (80 registers, of which five passes of bf16 spill 32 bytes)
+// measured best: 131072 tokens of 40 heads of 128, bf16: 419 us (95% of the copy rate), 488 us
+// with two, 547 us with four.
 template <int D, bool F32, int KIND, int kUnroll>
 __global__ void __launch_bounds__(kThreads, 3) rotate_kernel(const RotArgs a) {
     constexpr int kV = Vec<F32>::kDims;
@@ -473,9 +473,12 @@ pva_status launch_unrolled(const RotArgs& a, int sms, cudaStream_t st) {
 }
 
 // A few tokens take one pass a warp: what they cost is latency (96 tokens of 24 heads into
-// 4 bits: 5.7 us with three passes a warp, 3.6 us with one).  Many take no more passes a warp
-// than their heads fill (bf16, interleaved: 32768 tokens of 16 heads of 64, two passes: 34.9 us
-// with five, 31.4 us with two; 20383 of 8 heads, one pass: 18.0 and 13.8 us).
+// 4 bits: 5.7 us with three passes a warp, 3.6 us with one).  Of many, heads that fill one or two
+// passes take no more (bf16, interleaved: 32768 tokens of 16 heads of 64, two passes: 34.9 us
+// with five, 31.4 us with two; 20383 of 8 heads, one pass: 18.0 and 13.8 us).  All others run
+// Unroll's number a warp, and what the last warp has no heads for it loads in vain: of 131072
+// tokens with heads of 128 in bf16, 40 heads (ten passes) reach 95% of the copy rate, 32 (eight)
+// 89%, 16 (four) 86%, 24 (six) 80%.
 template <int D, bool F32, int KIND>
 pva_status launch_rotate(const RotArgs& a, cudaStream_t st) {
     const int sms = sm_count();
