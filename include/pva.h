@@ -64,11 +64,17 @@ typedef enum {
                                      (rows in pva_zigzag_shard order); same document and
                                      k position <= q position */
     PVA_MASK_SLICES = 4,          /* explicit slice list (AttnSlice, §4.4) */
-    PVA_MASK_ZIGZAG_STEP = 5      /* one ring step of all cp zigzag ranks at once: Q, K and V
+    PVA_MASK_ZIGZAG_STEP = 5,     /* one ring step of all cp zigzag ranks at once: Q, K and V
                                      in ring order (rank 0's shard rows, then rank 1's, ...;
                                      pva_zigzag_ring_map), the query rows of rank r see the
                                      key rows of rank (r - ring_step) mod cp under the
                                      ZIGZAG_PAIR rule; q_tokens = k_tokens = cu[num_docs] */
+    PVA_MASK_CROSS = 6            /* cross attention, pack to pack: cu_seqlens cuts Q into targets
+                                     and cu_keys cuts K and V into sources; every row of target
+                                     d sees every key of source d, and nothing else.  Targets of
+                                     one source that lie side by side count as one target.
+                                     q_tokens = cu[num_docs], k_tokens = cu_keys[num_docs];
+                                     either side of a pair may be empty */
 } pva_mask_kind;
 
 /* The four MaskTypes of "03 · 长文负载均衡" §4.4 (the pages name them without
@@ -111,6 +117,8 @@ typedef struct {
     int32_t q_tokens;        /* rows of Q / O (for ZIGZAG_PAIR: pva_zigzag_shard_len(q_rank)) */
     int32_t k_tokens;        /* rows of K / V */
     int32_t ring_step;       /* ZIGZAG_STEP (with cp): 0 <= ring_step < cp */
+    const int32_t* cu_keys;  /* CROSS (not read for other kinds): DEVICE int32 [num_docs + 1],
+                                0 = cu_keys[0] <= cu_keys[1] <= ... */
 } pva_mask_desc;
 
 /* Worklist parameters.  The attention kernel supports tile_m = tile_n = 128,
@@ -136,8 +144,10 @@ typedef struct {
                            SLIDING_WINDOW masks: consecutive documents shorter than tile_m are
                            grouped greedily, in order, into groups of at most tile_m rows; a
                            group of two or more non-empty documents is one query tile against
-                           one key tile, each row masked to its own document.  Other mask kinds
-                           ignore it.  0: every document has its own tiles. */
+                           one key tile, each row masked to its own document.  CROSS masks:
+                           consecutive pairs, both sides shorter than a tile and not empty, whose
+                           rows fit in one query tile and whose keys fit in one key tile.  Other
+                           mask kinds ignore it.  0: every document has its own tiles. */
 } pva_worklist_params;
 
 /* How the forward kernel hands units to its persistent CTAs.  Both follow the
@@ -457,6 +467,19 @@ pva_status pva_cache_attn(const pva_cache_desc* cache, const pva_cache_batch* ba
                           const void* q, int64_t q_stride, int32_t num_q_heads, int32_t max_new,
                           int32_t window, float softmax_scale, void* out, int32_t out_is_fp32,
                           float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Cross attention over the cache: every row of a sequence sees all of its kv_lens cached
+ * keys (a source's; rows are beams, or any tokens that answer about it), none of which is
+ * the row's own.  A row more than kv_lens counts is no failure, and kv_lens = 0 gives O = 0
+ * and LSE = -inf.  A source is read once for its rows and heads of a group, 16 rows at a time
+ * (8 with 4 bits), so rows of a source belong into one sequence of the batch.  Otherwise as
+ * pva_cache_attn, workspace (pva_cache_attn_bytes) and values too; a slot whose position has
+ * no page is left out for all rows. */
+pva_status pva_cache_cross_attn(const pva_cache_desc* cache, const pva_cache_batch* batch,
+                                const void* q, int64_t q_stride, int32_t num_q_heads,
+                                int32_t max_new, float softmax_scale, void* out,
+                                int32_t out_is_fp32, float* lse, void* workspace,
+                                size_t workspace_bytes, void* stream);
 
 /* Read a status word (HOST code_out).  Synchronizes `stream`. */
 pva_status pva_cache_status(const int32_t* status_dev, int32_t* code_out, void* stream);

@@ -28,7 +28,7 @@ EXPORTS = ("pva_worklist_bytes", "pva_build_worklist", "pva_attn_fwd", "pva_attn
            "pva_fit_tile_cost",
            "pva_bwd_plan_bytes", "pva_build_bwd_plan", "pva_attn_bwd",
            "pva_rope", "pva_cache_append", "pva_cache_read", "pva_cache_attn_bytes",
-           "pva_cache_attn", "pva_cache_status",
+           "pva_cache_attn", "pva_cache_cross_attn", "pva_cache_status",
            "pva_status_string", "pva_version")
 
 
@@ -44,7 +44,7 @@ class MaskDesc(ctypes.Structure):
                 ("q_rank", ctypes.c_int32), ("k_rank", ctypes.c_int32),
                 ("slices", ctypes.POINTER(Slice)), ("num_slices", ctypes.c_int32),
                 ("q_tokens", ctypes.c_int32), ("k_tokens", ctypes.c_int32),
-                ("ring_step", ctypes.c_int32)]
+                ("ring_step", ctypes.c_int32), ("cu_keys", ctypes.c_void_p)]
 
 
 class WorklistParams(ctypes.Structure):
@@ -160,6 +160,9 @@ def lib() -> ctypes.CDLL:
         L.pva_cache_attn.restype = ctypes.c_int
         L.pva_cache_attn.argtypes = [CP, BP, P, i64, i32, i32, i32, ctypes.c_float, P, i32, P, P,
                                      sz, P]
+        L.pva_cache_cross_attn.restype = ctypes.c_int
+        L.pva_cache_cross_attn.argtypes = [CP, BP, P, i64, i32, i32, ctypes.c_float, P, i32, P, P, sz,
+                                           P]
         L.pva_cache_status.restype = ctypes.c_int
         L.pva_cache_status.argtypes = [P, ctypes.POINTER(i32), P]
         L.pva_debug_withhold_kv_load.restype = None

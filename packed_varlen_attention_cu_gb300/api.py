@@ -14,7 +14,7 @@ import torch
 
 from . import _lib
 from ._lib import CacheBatch, MaskDesc, RopeDesc, Slice, WorklistParams, check, lib
-from .workloads import (MASK_CAUSAL, MASK_SHARED_QUESTION, MASK_SLICES, MASK_SLIDING_WINDOW,
+from .workloads import (MASK_CAUSAL, MASK_CROSS, MASK_SHARED_QUESTION, MASK_SLICES, MASK_SLIDING_WINDOW,
                         MASK_ZIGZAG_PAIR, MASK_ZIGZAG_STEP)
 
 SLICE_FULL, SLICE_CAUSAL, SLICE_INV_CAUSAL, SLICE_BI_CAUSAL = 0, 1, 2, 3
@@ -33,9 +33,11 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
 
 def make_mask(kind: int = MASK_CAUSAL, q_tokens: int = 0, k_tokens: int = 0, window: int = 0,
               num_prefix_docs: int = 0, cp: int = 0, q_rank: int = 0, k_rank: int = 0,
-              slices: Optional[np.ndarray] = None, ring_step: int = 0) -> MaskDesc:
+              slices: Optional[np.ndarray] = None, ring_step: int = 0,
+              cu_keys: Optional[torch.Tensor] = None) -> MaskDesc:
     """pva_mask_desc.  ``slices``: int32 [n, 8] rows (q_row0, q_len, q_pos0, k_row0, k_len,
-    k_pos0, type, window); the array is kept alive on the returned object."""
+    k_pos0, type, window); the array is kept alive on the returned object.  ``cu_keys``:
+    offsets of the sources (MASK_CROSS; int32 [docs + 1] on the device, kept alive too)."""
     m = MaskDesc()
     m.kind, m.window, m.num_prefix_docs = kind, window, num_prefix_docs
     m.cp, m.q_rank, m.k_rank = cp, q_rank, k_rank
@@ -46,6 +48,14 @@ def make_mask(kind: int = MASK_CAUSAL, q_tokens: int = 0, k_tokens: int = 0, win
         m._slices_keep = arr
         m.slices = arr.ctypes.data_as(ctypes.POINTER(Slice))
         m.num_slices = arr.shape[0]
+    if cu_keys is not None:
+        if kind != MASK_CROSS or cu_keys.dtype != torch.int32 or not cu_keys.is_cuda or \
+                cu_keys.dim() != 1 or not cu_keys.is_contiguous():
+            raise ValueError("cu_keys: a contiguous int32 CUDA tensor [docs + 1], for MASK_CROSS")
+        m._cu_keys_keep = cu_keys
+        m.cu_keys = cu_keys.data_ptr()
+    elif kind == MASK_CROSS:
+        raise ValueError("MASK_CROSS needs cu_keys")
     return m
 
 
@@ -98,6 +108,10 @@ def build_worklist(cu_seqlens: Optional[torch.Tensor], mask: MaskDesc, params: W
     nd = 0 if cu_seqlens is None else cu_seqlens.numel() - 1
     if cu_seqlens is not None:
         assert cu_seqlens.dtype == torch.int32 and cu_seqlens.is_cuda
+    if mask.kind == MASK_CROSS:
+        keys = mask._cu_keys_keep
+        if cu_seqlens is None or keys.numel() != nd + 1 or keys.device != cu_seqlens.device:
+            raise ValueError("build_worklist: cu_seqlens and cu_keys on one device, of docs + 1 entries each")
     check("pva_build_worklist", lib().pva_build_worklist(
         _ptr(cu_seqlens), nd, ctypes.byref(mask), ctypes.byref(params), _ptr(worklist),
         worklist.numel(), _stream(stream)))
@@ -529,21 +543,43 @@ def cache_attn(cache: KVCache, q: torch.Tensor, page_table: torch.Tensor, kv_len
     position kv_lens[b] - n + i and sees the keys up to it (window > 0: the last
     `window` of them).  out bf16 or fp32 like q, lse fp32 [heads, tokens]; max_new:
     an upper bound of n."""
+    dev, t, args = _attn_args("cache_attn", cache, q, out, lse, workspace)
+    rc = (_lib._lib or lib()).pva_cache_attn(
+        cache.desc, _cache_batch(cache, page_table, t, kv_lens, cu_new, status, dev), *args[:3],
+        max_new, window, softmax_scale, *args[3:], _queue(stream, dev))
+    if rc:
+        check("pva_cache_attn", rc)
+
+
+def _attn_args(name: str, cache: KVCache, q, out, lse, workspace):
+    """(device, tokens, the C call's q, q_stride, heads, out, out_is_fp32, lse, workspace, its bytes)."""
     dev = _device(q, "q")
     qs = _rows3(q, "q", dev)
     shape = q.shape
     t, h, d = shape
     if d != cache.head_dim:
-        raise ValueError("cache_attn: head_dim differs from the cache's")
+        raise ValueError(f"{name}: head_dim differs from the cache's")
     o, l = _whole(out, "out", dev, shape, _BF16, _F32), _whole(lse, "lse", dev, (h, t), _F32)
     if workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace: a contiguous tensor on cuda:{dev} is needed")
-    rc = (_lib._lib or lib()).pva_cache_attn(
-        cache.desc, _cache_batch(cache, page_table, t, kv_lens, cu_new, status, dev), q.data_ptr(),
-        qs, h, max_new, window, softmax_scale, o, 1 if out.dtype is _F32 else 0, l,
-        workspace.data_ptr(), workspace.nbytes, _queue(stream, dev))
+    return dev, t, (q.data_ptr(), qs, h, o, 1 if out.dtype is _F32 else 0, l, workspace.data_ptr(),
+                    workspace.nbytes)
+
+
+def cache_cross_attn(cache: KVCache, q: torch.Tensor, page_table: torch.Tensor, kv_lens: torch.Tensor,
+                     out: torch.Tensor, lse: torch.Tensor, workspace: torch.Tensor,
+                     cu_new: Optional[torch.Tensor] = None, max_new: int = 1,
+                     softmax_scale: float = 0.0, status: Optional[torch.Tensor] = None,
+                     stream=None) -> None:
+    """Attention of every row of a sequence (beams, or tokens that answer about a source)
+    over all kv_lens cached keys of that sequence.  Sequence b owns rows cu_new[b] ..
+    cu_new[b + 1] of q (None: row b), at most max_new; the rest as cache_attn."""
+    dev, t, args = _attn_args("cache_cross_attn", cache, q, out, lse, workspace)
+    rc = (_lib._lib or lib()).pva_cache_cross_attn(
+        cache.desc, _cache_batch(cache, page_table, t, kv_lens, cu_new, status, dev), *args[:3],
+        max_new, softmax_scale, *args[3:], _queue(stream, dev))
     if rc:
-        check("pva_cache_attn", rc)
+        check("pva_cache_cross_attn", rc)
 
 
 def cache_status(status: torch.Tensor, stream=None) -> int:

@@ -1175,9 +1175,12 @@ extern "C" pva_status pva_attn_bwd(const void* q, const void* k, const void* v, 
                                    const void* worklist_dev, void* plan_dev, void* dq, void* dk,
                                    void* dv, int32_t grads_are_fp32, float softmax_scale,
                                    void* stream) {
-    if (!mask || !params || !worklist_dev || !plan_dev || !q || !out || !lse || !dout || !dq ||
-        !dk || !dv)
+    if (!mask || !params || !worklist_dev || !plan_dev) return PVA_ERR_INVALID_ARG;
+    // a pack of targets without a row, or of sources without one, may have no tensor
+    const bool cross = mask->kind == PVA_MASK_CROSS;
+    if (!(cross && mask->q_tokens == 0) && (!q || !out || !lse || !dout || !dq))
         return PVA_ERR_INVALID_ARG;
+    if (!(cross && mask->k_tokens == 0) && (!dk || !dv)) return PVA_ERR_INVALID_ARG;
     if (mask->kind != PVA_MASK_SLICES && !cu_seqlens_dev) return PVA_ERR_INVALID_ARG;
     if (head_dim != 64 && head_dim != 128) return PVA_ERR_UNSUPPORTED;
     if (params->tile_m != 128 || params->tile_n != 128) return PVA_ERR_UNSUPPORTED;
@@ -1207,7 +1210,8 @@ extern "C" pva_status pva_attn_bwd(const void* q, const void* k, const void* v, 
             cudaSuccess)
         return PVA_ERR_CUDA;
     if ((mask->kind == PVA_MASK_SLICES || mask->kind == PVA_MASK_ZIGZAG_PAIR ||
-         mask->kind == PVA_MASK_ZIGZAG_STEP) &&
+         mask->kind == PVA_MASK_ZIGZAG_STEP ||
+         (cross && mask->q_tokens == 0 && mask->k_tokens > 0)) &&
         (cudaMemsetAsync(dk, 0, (size_t)mask->k_tokens * params->num_kv_heads * head_dim * es,
                          st) != cudaSuccess ||
          cudaMemsetAsync(dv, 0, (size_t)mask->k_tokens * params->num_kv_heads * head_dim * es,

@@ -152,8 +152,9 @@ __device__ __forceinline__ void write_empty_rows(const AttnParams& p, const SubT
 }
 
 // ACC: the fused ring step (pva_attn_fwd_accumulate), a separate instantiation
-// so that each kernel carries only the epilogue it runs.
-template <int D, bool ACC>
+// so that each kernel carries only the epilogue it runs.  CROSS: worklists of a
+// CROSS mask, which has slices of its own kind only.
+template <int D, bool ACC, bool CROSS>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_fwd_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
                     const __grid_constant__ CUtensorMap tmv, const __grid_constant__ CUtensorMap tmo,
@@ -175,7 +176,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     h->hq == p.hq && h->hkv == p.hkv && h->num_ctas == p.num_ctas &&
                     (int)gridDim.x == p.num_ctas && h->q_tokens == p.q_tokens &&
                     h->k_tokens == p.k_tokens &&
-                    (h->dispatch == PVA_DISPATCH_DYNAMIC) == (p.dynamic != 0);
+                    (h->dispatch == PVA_DISPATCH_DYNAMIC) == (p.dynamic != 0) &&
+                    (h->kind == PVA_MASK_CROSS) == CROSS;
     if (!ok) {
         if (tid == 0 && blockIdx.x == 0) atomicCAS(err_word, 0, kErrBadWorklist);
         return;
@@ -816,7 +818,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // allowed keys of this row, relative to the slice's first key:
                 // [lim_lo, lim_hi) (by the slice's MaskType; nothing for padding rows)
                 int64_t klo, khi;
-                slice_keys_of_query(s, q_pos, klo, khi, slice_mask(p.wl, h, s, run.slice));
+                if constexpr (CROSS) {  // whole slices and shared tiles only
+                    klo = 0;
+                    khi = s.k_len;
+                    if (s.type == kSlicePackedCross)
+                        packed_pair(slice_mask(p.wl, h, s, run.slice), r, klo, khi);
+                } else {
+                    slice_keys_of_query<false>(s, q_pos, klo, khi,
+                                               slice_mask<false>(p.wl, h, s, run.slice));
+                }
                 const int32_t lim_hi = valid ? (int32_t)khi : 0;
                 const int32_t lim_lo = (int32_t)klo;
                 for (int32_t jt = run.lo; jt < run.hi && live; ++jt) {
@@ -974,8 +984,9 @@ std::atomic<int32_t> g_withhold_kv{0};  // pva_debug_withhold_kv_load
 
 template <int D>
 pva_status launch(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
-                  const CUtensorMap& mo, const AttnParams& ap, cudaStream_t st) {
-    auto kern = ap.accumulate ? attn_fwd_kernel<D, true> : attn_fwd_kernel<D, false>;
+                  const CUtensorMap& mo, const AttnParams& ap, bool cross, cudaStream_t st) {
+    auto kern = cross ? (ap.accumulate ? attn_fwd_kernel<D, true, true> : attn_fwd_kernel<D, false, true>)
+                      : (ap.accumulate ? attn_fwd_kernel<D, true, false> : attn_fwd_kernel<D, false, false>);
     // setmaxnreg.inc draws from the registers the block was launched with: the
     // split must fit in (threads x registers per thread) or the increase would
     // never be granted.
@@ -1053,8 +1064,9 @@ pva_status attn_fwd_impl(const void* q, const void* k, const void* v,
     ap.withhold_kv = g_withhold_kv.load(std::memory_order_relaxed);
     ap.dynamic = params->dispatch == PVA_DISPATCH_STATIC ? 0 : 1;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    return head_dim == 128 ? launch<128>(mq, mk, mv, mo, ap, st)
-                           : launch<64>(mq, mk, mv, mo, ap, st);
+    const bool cross = mask->kind == PVA_MASK_CROSS;
+    return head_dim == 128 ? launch<128>(mq, mk, mv, mo, ap, cross, st)
+                           : launch<64>(mq, mk, mv, mo, ap, cross, st);
 }
 
 }  // namespace

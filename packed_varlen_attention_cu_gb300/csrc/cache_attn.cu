@@ -54,6 +54,7 @@ struct AttnArgs {
     int64_t q_stride;
     SeqView s;
     int32_t hq, hkv, group, window, out_fp32;
+    int32_t cross;  // every row sees all that its sequence has cached
     uint32_t num_pages, page_bytes;  // page_bytes: codes or values of a page, one of K and V
     float c;      // softmax scale * log2(e), times 2^69 with 4 bits (whose scores carry 2^-69)
     float slack;  // kSlack / c
@@ -190,11 +191,13 @@ __device__ __forceinline__ SeqInfo seq_info(const AttnArgs& a, int32_t b, bool t
     const int64_t room = (int64_t)a.s.max_pages << a.s.page_shift;
     if (tell) {
         // (without offsets a length of 0 is a row of no sequence: a padded batch)
-        if (bad || (kv < s.n && (a.s.cu || kv != 0))) raise_status(a.s.status, kErrLength);
+        if (bad || (a.cross ? kv < 0 : kv < s.n && (a.s.cu || kv != 0))) raise_status(a.s.status, kErrLength);
         if (s.n > 0 && kv > room) raise_status(a.s.status, kErrPage);
     }
     const int32_t kvp = max(kv, 0);
-    s.pos0 = kvp - s.n;
+    // Cross: each row stands at the last key or past it (by its number: no sum overflows), where
+    // the causal rule lets it see every key.
+    s.pos0 = a.cross ? min(kvp - 1, INT32_MAX - 1 - s.n) : kvp - s.n;
     s.khi = (int32_t)min((int64_t)kvp, min(room, (int64_t)INT32_MAX - 2 * BLOCK));
     s.klo = a.window > 0 ? (int32_t)max((int64_t)s.pos0 - a.window + 1, (int64_t)0) : 0;
     s.nrb = (int32_t)(((int64_t)s.n * a.group + R - 1) / R);
@@ -1198,11 +1201,12 @@ extern "C" size_t pva_cache_attn_bytes(int32_t num_seqs, int32_t num_q_heads, in
     return 256 + up256((size_t)num_seqs * 8) + (size_t)2 * kMaxCtas * r * (8 + 4 * (size_t)head_dim);
 }
 
-extern "C" pva_status pva_cache_attn(const pva_cache_desc* cache, const pva_cache_batch* batch,
-                                     const void* q, int64_t q_stride, int32_t num_q_heads,
-                                     int32_t max_new, int32_t window, float softmax_scale,
-                                     void* out, int32_t out_is_fp32, float* lse, void* workspace,
-                                     size_t workspace_bytes, void* stream) {
+namespace {
+
+pva_status cache_attn_impl(const pva_cache_desc* cache, const pva_cache_batch* batch, const void* q,
+                           int64_t q_stride, int32_t num_q_heads, int32_t max_new, int32_t window,
+                           bool cross, float softmax_scale, void* out, int32_t out_is_fp32, float* lse,
+                           void* workspace, size_t workspace_bytes, void* stream) {
     pva_status st = check_cache(cache);
     if (st == PVA_OK) st = check_batch(batch, true);
     if (st != PVA_OK) return st;
@@ -1239,6 +1243,7 @@ extern "C" pva_status pva_cache_attn(const pva_cache_desc* cache, const pva_cach
     a.hkv = cache->num_kv_heads;
     a.group = num_q_heads / cache->num_kv_heads;
     a.window = window;
+    a.cross = cross ? 1 : 0;
     a.out_fp32 = out_is_fp32;
     const int64_t page_bytes =
         (int64_t)cache->num_kv_heads * cache->page_size * (cache->kind == PVA_CACHE_INT4 ? d / 2 : 2 * d);
@@ -1254,4 +1259,24 @@ extern "C" pva_status pva_cache_attn(const pva_cache_desc* cache, const pva_cach
                         : launch_rows<64, PVA_CACHE_BF16>(rows, a, ws, s);
     return d == 128 ? launch_rows<128, PVA_CACHE_INT4>(rows, a, ws, s)
                     : launch_rows<64, PVA_CACHE_INT4>(rows, a, ws, s);
+}
+
+}  // namespace
+
+extern "C" pva_status pva_cache_attn(const pva_cache_desc* cache, const pva_cache_batch* batch,
+                                     const void* q, int64_t q_stride, int32_t num_q_heads,
+                                     int32_t max_new, int32_t window, float softmax_scale,
+                                     void* out, int32_t out_is_fp32, float* lse, void* workspace,
+                                     size_t workspace_bytes, void* stream) {
+    return cache_attn_impl(cache, batch, q, q_stride, num_q_heads, max_new, window, false, softmax_scale,
+                           out, out_is_fp32, lse, workspace, workspace_bytes, stream);
+}
+
+extern "C" pva_status pva_cache_cross_attn(const pva_cache_desc* cache, const pva_cache_batch* batch,
+                                           const void* q, int64_t q_stride, int32_t num_q_heads,
+                                           int32_t max_new, float softmax_scale, void* out,
+                                           int32_t out_is_fp32, float* lse, void* workspace,
+                                           size_t workspace_bytes, void* stream) {
+    return cache_attn_impl(cache, batch, q, q_stride, num_q_heads, max_new, 0, true, softmax_scale, out,
+                           out_is_fp32, lse, workspace, workspace_bytes, stream);
 }

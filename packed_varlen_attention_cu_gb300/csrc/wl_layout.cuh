@@ -17,6 +17,7 @@
 //   dorder     int32[cap_units]           uid of the r-th unit in dispatch order
 //   cls_work   uint64[64]                 summed cost per dispatch class
 //   smask      uint32[cap_slices][4]      per packed slice: rows that start a document
+//              (packed CROSS masks: uint16[cap_slices][256], intervals of rows and keys)
 // A worklist built for dynamic dispatch has no LPT bins: order, assign,
 // units and cta_off are left unwritten (units_enum and dorder describe it).
 #pragma once
@@ -80,6 +81,20 @@ __host__ __device__ inline int32_t packed_doc_end(const uint32_t* m, int32_t r, 
         }
     }
     return len;
+}
+
+// The same for a tile shared by several short (target, source) pairs of a CROSS mask,
+// consecutive pairs without an empty side: row r sees the keys of its own pair's source.
+// The slice's smask entry has the key interval of every row and the row interval of every
+// key of the group, lo + 256 * hi in 16 bits each: one load where the kernels need it
+// (finding the pair by its bits cost the forward kernel 32 bytes of spills at d = 64).
+constexpr int32_t kSlicePackedCross = 5;
+constexpr int32_t kCrossMaskWords = 128;  // 32-bit words of an entry: 128 rows, then 128 keys
+
+__host__ __device__ inline void packed_pair(const uint32_t* m, int32_t i, int64_t& lo, int64_t& hi) {
+    const uint32_t x = reinterpret_cast<const uint16_t*>(m)[i];
+    lo = x & 255u;
+    hi = x >> 8;
 }
 
 struct WlSeg {
@@ -176,6 +191,8 @@ static_assert(sizeof(BwdHeader) <= 256, "backward header fits in 256 bytes");
 // k >= q and k_end - k >= q_end - q.
 // Keys of slice s a query at position qp may see, as slice-local key indices
 // [lo, hi) (empty when hi <= lo).  pm: the slice's smask entry (packed slices).
+// kCross = false: the slices come from no CROSS mask.
+template <bool kCross = true>
 __host__ __device__ inline void slice_keys_of_query(const WlSlice& s, int64_t qp, int64_t& lo,
                                                     int64_t& hi, const uint32_t* pm = nullptr) {
     const int64_t d = qp - s.k_pos0;  // local index of the key at the query's position
@@ -195,6 +212,9 @@ __host__ __device__ inline void slice_keys_of_query(const WlSlice& s, int64_t qp
     } else if (s.type == 3) {  // BI_CAUSAL: local key j <= k_len - q_len + local row
         lo = d;
         hi = (int64_t)s.k_len - s.q_len + (qp - s.q_pos0) + 1;
+    } else if (kCross && s.type == kSlicePackedCross) {
+        const int32_t r = (int32_t)(qp - s.q_pos0) & 127;  // (a group is one tile)
+        if (pm) packed_pair(pm, r, lo, hi);
     }
     if (lo < 0) lo = 0;
     if (hi > s.k_len) hi = s.k_len;
@@ -212,6 +232,13 @@ __host__ __device__ inline void slice_queries_of_key(const WlSlice& s, int64_t k
         a = kp;
         b = (int64_t)s.q_pos0 + (pm ? packed_doc_end(pm, j, s.q_len) : j + 1);
         if (s.window > 0 && kp + s.window < b) b = kp + s.window;
+    } else if (s.type == kSlicePackedCross) {
+        const int32_t j = (int32_t)(kp - s.k_pos0);
+        if (pm) {
+            packed_pair(pm, 128 + (j & 127), a, b);
+            a += s.q_pos0;
+            b += s.q_pos0;
+        }
     } else if (s.type == 1) {  // CAUSAL
         a = kp;
         if (s.window > 0) b = kp + s.window;
@@ -243,11 +270,12 @@ __host__ __device__ inline void bwd_q_span(const WlSlice& sl, int32_t kt, int32_
 }
 
 // The smask entry of slice `si` if it is a packed slice, else nullptr.
+template <bool kCross = true>
 __host__ __device__ inline const uint32_t* slice_mask(const uint8_t* wl, const WlHeader* h,
                                                       const WlSlice& s, int32_t si) {
-    return s.type == kSlicePacked
-               ? reinterpret_cast<const uint32_t*>(wl + h->off.smask) + 4 * (int64_t)si
-               : nullptr;
+    const uint32_t* m = reinterpret_cast<const uint32_t*>(wl + h->off.smask);
+    if (kCross && s.type == kSlicePackedCross) return m + kCrossMaskWords * (int64_t)si;
+    return s.type == kSlicePacked ? m + 4 * (int64_t)si : nullptr;
 }
 
 // Device error codes (stored in WlHeader::error).

@@ -88,8 +88,9 @@ struct PlanArgs {
     WlHeader hinit;  // capacities and offsets computed on the host
     uint8_t* base;
     const int32_t* cu;
+    const int32_t* cu_keys;  // CROSS
     int32_t num_docs, kind, window, num_prefix, cp, q_rank, k_rank, num_slices;
-    int32_t tile_m, hq, hkv, q_tokens, k_tokens, ring_step, pack_docs;
+    int32_t tile_m, tile_n, hq, hkv, q_tokens, k_tokens, ring_step, pack_docs;
 };
 
 __device__ __forceinline__ void set_error(WlHeader* h, int32_t code) { atomicCAS(&h->error, 0, code); }
@@ -119,16 +120,19 @@ __global__ void __launch_bounds__(kPlanThreads) wl_plan_kernel(PlanArgs a) {
     __syncthreads();
 
     if (a.kind != PVA_MASK_SLICES) {
-        if (tid == 0 && a.cu[0] != 0) s_bad = 1;
+        const bool cross = a.kind == PVA_MASK_CROSS;
+        if (tid == 0 && (a.cu[0] != 0 || (cross && a.cu_keys[0] != 0))) s_bad = 1;
         for (int d = tid; d < nd; d += kPlanThreads) {
             const int32_t len = a.cu[d + 1] - a.cu[d];
-            if (len < 0) s_bad = 1;
+            if (len < 0 || a.cu[d + 1] < a.cu[d]) s_bad = 1;
+            if (cross && a.cu_keys[d + 1] < a.cu_keys[d]) s_bad = 1;
             if (a.kind == PVA_MASK_SHARED_QUESTION && d < a.num_prefix && len > 0)
                 atomicAdd(&s_npref, 1);
         }
         __syncthreads();
         const int32_t total = a.cu[nd];
-        if (a.kind != PVA_MASK_ZIGZAG_PAIR && (total != a.q_tokens || total != a.k_tokens))
+        const int32_t ktotal = cross ? a.cu_keys[nd] : total;
+        if (a.kind != PVA_MASK_ZIGZAG_PAIR && (total != a.q_tokens || ktotal != a.k_tokens))
             s_bad = 1;
         __syncthreads();
         if (s_bad) {
@@ -152,10 +156,17 @@ __global__ void __launch_bounds__(kPlanThreads) wl_plan_kernel(PlanArgs a) {
         // gend[head]: one past the group's last document.
         int32_t* grp = scan + 4 * (items + 1);
         int32_t* gend = scan + 5 * (items + 1);
-        const bool pack = a.pack_docs != 0 &&
-                          (a.kind == PVA_MASK_CAUSAL || a.kind == PVA_MASK_SLIDING_WINDOW);
+        // Under a CROSS mask a group's targets fit in one q tile and its sources in one
+        // key tile, and a pair with an empty side stays alone: the n-th target of a group
+        // is then the target of its n-th source.
+        const bool pack = a.pack_docs != 0 && (cross || a.kind == PVA_MASK_CAUSAL ||
+                                               a.kind == PVA_MASK_SLIDING_WINDOW);
+        auto key_len = [&](int32_t d) { return cross ? a.cu_keys[d + 1] - a.cu_keys[d] : 0; };
         if (pack) {
-            auto short_doc = [&](int32_t d) { return a.cu[d + 1] - a.cu[d] < a.tile_m; };
+            auto short_doc = [&](int32_t d) {
+                const int32_t l = a.cu[d + 1] - a.cu[d], kl = key_len(d);
+                return l < a.tile_m && (!cross || (l > 0 && kl > 0 && kl < a.tile_n));
+            };
             for (int d = tid; d < nd; d += kPlanThreads) {
                 if (!short_doc(d)) {
                     grp[d] = -1;
@@ -167,9 +178,12 @@ __global__ void __launch_bounds__(kPlanThreads) wl_plan_kernel(PlanArgs a) {
                 while (x < nd && short_doc(x)) {
                     const int32_t head = x;
                     int32_t rows = a.cu[x + 1] - a.cu[x], nonempty = rows > 0, y = x + 1;
-                    while (y < nd && short_doc(y) && rows + (a.cu[y + 1] - a.cu[y]) <= a.tile_m) {
+                    int32_t keys = key_len(x);
+                    while (y < nd && short_doc(y) && rows + (a.cu[y + 1] - a.cu[y]) <= a.tile_m &&
+                           keys + key_len(y) <= a.tile_n) {
                         const int32_t l = a.cu[y + 1] - a.cu[y];
                         rows += l;
+                        keys += key_len(y);
                         nonempty += l > 0;
                         ++y;
                     }
@@ -190,6 +204,15 @@ __global__ void __launch_bounds__(kPlanThreads) wl_plan_kernel(PlanArgs a) {
                 if (a.kind == PVA_MASK_CAUSAL || a.kind == PVA_MASK_SLIDING_WINDOW) {
                     if (pack && grp[d] >= 0) v[0] = v[1] = grp[d] == d;  // the group's head
                     else v[0] = v[1] = len > 0;
+                } else if (cross) {
+                    // a source without a target keeps its slice: the backward writes zeros
+                    // for its keys
+                    if (pack && grp[d] >= 0) {
+                        v[0] = v[1] = grp[d] == d;
+                    } else {
+                        v[0] = len > 0;
+                        v[1] = key_len(d) > 0;
+                    }
                 } else if (a.kind == PVA_MASK_SHARED_QUESTION) {
                     v[0] = len > 0;
                     v[1] = len > 0 ? (d >= a.num_prefix ? s_npref + 1 : 1) : 0;
@@ -262,6 +285,28 @@ __global__ void __launch_bounds__(kPlanThreads) wl_plan_kernel(PlanArgs a) {
                 if (len <= 0) continue;
                 slices[sl] = WlSlice{a.cu[d], len, 0, a.cu[d], len, 0, PVA_SLICE_CAUSAL, w};
                 segs[sg] = WlSeg{a.cu[d], len, 0, sl, 1, 0, 0, 0};
+            } else if (cross) {
+                const int32_t k0 = a.cu_keys[d], kl = key_len(d);
+                if (pack && grp[d] >= 0) {
+                    if (grp[d] != d) continue;
+                    const int32_t g0 = a.cu[d], e = gend[d];
+                    const int32_t rows = a.cu[e] - g0, keys = a.cu_keys[e] - k0;
+                    uint16_t* m = reinterpret_cast<uint16_t*>(smask + kCrossMaskWords * (int64_t)sl);
+                    for (int32_t z = d; z < e; ++z) {
+                        const int32_t r0 = a.cu[z] - g0, r1 = a.cu[z + 1] - g0;
+                        const int32_t j0 = a.cu_keys[z] - k0, j1 = a.cu_keys[z + 1] - k0;
+                        for (int32_t r = r0; r < r1; ++r) m[r] = (uint16_t)(j0 | j1 << 8);
+                        for (int32_t j = j0; j < j1; ++j) m[128 + j] = (uint16_t)(r0 | r1 << 8);
+                    }
+                    // (rows and keys past the group's are padding: nothing)
+                    for (int32_t r = rows; r < 128; ++r) m[r] = 0;
+                    for (int32_t j = keys; j < 128; ++j) m[128 + j] = 0;
+                    slices[sl] = WlSlice{g0, rows, 0, k0, keys, 0, kSlicePackedCross, 0};
+                    segs[sg] = WlSeg{g0, rows, 0, sl, 1, 0, 0, 0};
+                    continue;
+                }
+                if (kl > 0) slices[sl] = WlSlice{a.cu[d], len, 0, k0, kl, 0, PVA_SLICE_FULL, 0};
+                if (len > 0) segs[sg] = WlSeg{a.cu[d], len, 0, sl, kl > 0 ? 1 : 0, 0, 0, 0};
             } else if (a.kind == PVA_MASK_SHARED_QUESTION) {
                 if (len <= 0) continue;
                 const int32_t first = sl;
@@ -1086,12 +1131,16 @@ __global__ void __launch_bounds__(kMaxBins) wl_lpt_kernel(uint8_t* base, int32_t
 constexpr int kBwdPlanThreads = 1024;
 
 __global__ void __launch_bounds__(kBwdPlanThreads)
-    bwd_plan_kernel(const uint8_t* wl, uint8_t* plan) {
+    bwd_plan_kernel(const uint8_t* wl, uint8_t* plan, const BwdHeader init) {
     extern __shared__ unsigned long long bsm[];
     const WlHeader* h = reinterpret_cast<const WlHeader*>(wl);
     BwdHeader* bh = reinterpret_cast<BwdHeader*>(plan);
     __shared__ int32_t warp_tot[32];
     __shared__ int32_t carry;
+    // (the header comes with the launch: a copy from the caller's stack would be read again,
+    // long gone, whenever a captured build is replayed)
+    if (threadIdx.x == 0) *bh = init;
+    __syncthreads();
     if (h->error != 0) {
         if (threadIdx.x == 0) bh->error = h->error;
         return;
@@ -1239,6 +1288,11 @@ bool plan_layout(int32_t num_docs, const pva_mask_desc* m, const pva_worklist_pa
     case PVA_MASK_CAUSAL:
         cap_segs = cap_slices = num_docs;
         break;
+    case PVA_MASK_CROSS:
+        if (!m->cu_keys || (reinterpret_cast<uintptr_t>(m->cu_keys) & 3u)) return false;
+        if (p->pack_docs && p->tile_n > 128) return false;
+        cap_segs = cap_slices = num_docs;
+        break;
     case PVA_MASK_SLIDING_WINDOW:
         if (m->window < 1) return false;
         cap_segs = cap_slices = num_docs;
@@ -1328,7 +1382,10 @@ bool plan_layout(int32_t num_docs, const pva_mask_desc* m, const pva_worklist_pa
     h->refine_rounds = 0;
     h->dispatch = p->dispatch;
     h->pack_docs =
-        p->pack_docs && (m->kind == PVA_MASK_CAUSAL || m->kind == PVA_MASK_SLIDING_WINDOW) ? 1 : 0;
+        p->pack_docs && (m->kind == PVA_MASK_CAUSAL || m->kind == PVA_MASK_SLIDING_WINDOW ||
+                         m->kind == PVA_MASK_CROSS)
+            ? 1
+            : 0;
     int64_t o = 256;
     WlOffsets& f = h->off;
     f.slices = o; o = align256(o + (int64_t)h->cap_slices * sizeof(WlSlice));
@@ -1343,7 +1400,8 @@ bool plan_layout(int32_t num_docs, const pva_mask_desc* m, const pva_worklist_pa
     f.doc_scan = o; o = align256(o + 6 * (scan_items + 1) * 4);
     f.dorder = o; o = align256(o + cap_units * 4);
     f.cls_work = o; o = align256(o + 64 * 8);
-    f.smask = o; o = align256(o + (int64_t)h->cap_slices * 16);
+    f.smask = o; o = align256(o + (int64_t)h->cap_slices *
+                            (m->kind == PVA_MASK_CROSS && h->pack_docs ? 4 * kCrossMaskWords : 16));
     f.total = o;
     return true;
 }
@@ -1399,6 +1457,7 @@ extern "C" pva_status pva_build_worklist(const int32_t* cu_seqlens_dev, int32_t 
     pa.hinit = h;
     pa.base = base;
     pa.cu = cu_seqlens_dev;
+    pa.cu_keys = mask->kind == PVA_MASK_CROSS ? mask->cu_keys : nullptr;
     pa.num_docs = num_docs;
     pa.kind = mask->kind;
     pa.window = mask->window;
@@ -1408,6 +1467,7 @@ extern "C" pva_status pva_build_worklist(const int32_t* cu_seqlens_dev, int32_t 
     pa.k_rank = mask->k_rank;
     pa.num_slices = mask->num_slices;
     pa.tile_m = params->tile_m;
+    pa.tile_n = params->tile_n;
     pa.hq = params->num_q_heads;
     pa.hkv = params->num_kv_heads;
     pa.q_tokens = mask->q_tokens;
@@ -1654,15 +1714,13 @@ extern "C" pva_status pva_build_bwd_plan(const void* worklist_dev, int32_t num_d
     if (plan_bytes < (size_t)bh.total) return PVA_ERR_BUFFER_TOO_SMALL;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     uint8_t* base = reinterpret_cast<uint8_t*>(plan_dev);
-    if (cudaMemcpyAsync(base, &bh, sizeof bh, cudaMemcpyHostToDevice, st) != cudaSuccess)
-        return PVA_ERR_CUDA;
     // shared memory: sort keys, slice indices and group flags for every slice
     const size_t smem = (size_t)kBwdMaxSlices * 16;
     if (cudaFuncSetAttribute(bwd_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              (int)smem) != cudaSuccess)
         return PVA_ERR_CUDA;
     bwd_plan_kernel<<<1, kBwdPlanThreads, smem, st>>>(
-        reinterpret_cast<const uint8_t*>(worklist_dev), base);
+        reinterpret_cast<const uint8_t*>(worklist_dev), base, bh);
     SortArgs sa;
     sa.err = reinterpret_cast<const int32_t*>(base + offsetof(BwdHeader, error));
     sa.n = reinterpret_cast<const int32_t*>(base + offsetof(BwdHeader, nunits));

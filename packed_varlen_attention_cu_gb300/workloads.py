@@ -33,6 +33,7 @@ MASK_SHARED_QUESTION = 2
 MASK_ZIGZAG_PAIR = 3
 MASK_SLICES = 4
 MASK_ZIGZAG_STEP = 5
+MASK_CROSS = 6
 
 
 def lognormal_doc_lengths(total: int, mu: float, sigma: float, lo: int, hi: int,
