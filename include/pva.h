@@ -481,6 +481,76 @@ pva_status pva_cache_cross_attn(const pva_cache_desc* cache, const pva_cache_bat
                                 int32_t out_is_fp32, float* lse, void* workspace,
                                 size_t workspace_bytes, void* stream);
 
+/* ---- Beam search.  A group is the beams of one request, `beams` rows that lie side by
+ * side (row g * beams + b in the batch of the cache calls).  A step is pva_beam_select on
+ * the logits of all rows, pva_beam_reorder with the parents that it gives, and
+ * pva_cache_append of the chosen tokens' keys and values.  Further codes of the status word:
+ *   304 a row of logits with a NaN or +inf, a score that is NaN or +inf, or a norm that is
+ *       not positive and finite (such a row offers nothing)
+ *   305 a parent outside the group and not -1 (its row stays as it is) */
+
+/* The num_out best continuations of every group.  Row b offers every token t of a logit
+ * above -inf with the score scores[b] + x[t] - ln sum_t e^x[t]; a finished row offers itself
+ * alone (its end token, at its own score; its logits are not read), and a row whose score is
+ * -inf offers nothing.  Candidates are ranked by score * norm of their row, largest first; of
+ * equal ones the lower beam comes first, and inside a beam the larger logit, then the lower
+ * token.  Where fp32 rounds the score or its product with the norm to -inf there is none.
+ * fp32 exponentials, sums and ranks in 64 bits; the result does not depend on timing.
+ *   logits       DEVICE bf16 or fp32 [num_groups * beams, vocab], rows row_stride elements
+ *                apart (0: vocab), any alignment of the type
+ *   beams        1 to 64;  num_out 1 to 64
+ *   scores       DEVICE fp32 [num_groups, beams]: the beams' sums of logarithms so far
+ *   finished     DEVICE uint8 [num_groups, beams] or NULL: rows that have ended
+ *   norms        DEVICE fp32 [num_groups, beams] or NULL (1): such as a length's negative power
+ *   end_token    with finished or out_finished: 0 to vocab - 1; else not looked at
+ *   out_*        DEVICE [num_groups, num_out]: scores fp32 (not multiplied by the norm), parent
+ *                beams and tokens int32, and uint8 1 where the token is the end token or the
+ *                parent was finished (or NULL).  Places without a candidate: -inf, -1, -1, 0.
+ *                None of them may overlap an input
+ *   workspace    DEVICE, 256-byte aligned, pva_beam_select_bytes (HOST computation; 0 on
+ *                invalid arguments); its contents need not be kept between calls; one call
+ *                at a time */
+size_t pva_beam_select_bytes(int32_t num_groups, int32_t beams, int32_t vocab, int32_t num_out);
+pva_status pva_beam_select(const void* logits, int64_t row_stride, int32_t logits_are_fp32,
+                           int32_t num_groups, int32_t beams, int32_t vocab, int32_t num_out,
+                           const float* scores, const uint8_t* finished, const float* norms,
+                           int32_t end_token, float* out_scores, int32_t* out_beams,
+                           int32_t* out_tokens, uint8_t* out_finished, int32_t* status_dev,
+                           void* workspace, size_t workspace_bytes, void* stream);
+
+/* A tensor with one row for each beam (token histories, recurrent states, finished marks of
+ * 4 bytes): row i is row_bytes bytes at data + i * row_stride; all three multiples of 4 (of
+ * 16: wider accesses).  Rows do not overlap. */
+typedef struct {
+    void* data; /* DEVICE */
+    int64_t row_bytes, row_stride;
+} pva_state_desc;
+
+/* Every row becomes a copy of its parent, in place: row j of a group that of row
+ * parents[j] of the same group as it was before the call (-1: row j stays).  Any parents
+ * are right, exchanges and cycles too.
+ *   parents     DEVICE int32 [num_groups, beams], beams 1 to 64
+ *   caches      HOST array: caches of all layers that share the page table (one kind, size and
+ *               number of pages)
+ *   page_table  DEVICE int32 [num_groups * beams, max_pages], rows table_stride entries apart,
+ *               updated: with n = kv_lens[row] tokens cached, the first n / page_size entries
+ *               become the parent's.  Their pages are shared from then on and never written
+ *               again; the entry of the last, partly filled page stays, and the n % page_size
+ *               tokens of the parent's are copied into it.  So from that page on every row owns
+ *               the pages that its table names (prompts' full pages may be shared from the start)
+ *   kv_lens     DEVICE int32 [num_groups * beams]: cached tokens before the next append; one
+ *               number for all rows of a group.  Groups whose numbers differ, are negative or
+ *               pass the table are left as they were, states too (301; 300 past the table), and
+ *               a row whose last page, or its parent's, is outside [0, num_pages) keeps what
+ *               that page holds (300)
+ *   states      HOST array
+ * Launches once for up to 64 caches and 16 states. */
+pva_status pva_beam_reorder(const int32_t* parents, int32_t num_groups, int32_t beams,
+                            const pva_cache_desc* caches, int32_t num_caches, int32_t* page_table,
+                            int64_t table_stride, int32_t max_pages, const int32_t* kv_lens,
+                            const pva_state_desc* states, int32_t num_states, int32_t* status_dev,
+                            void* stream);
+
 /* Read a status word (HOST code_out).  Synchronizes `stream`. */
 pva_status pva_cache_status(const int32_t* status_dev, int32_t* code_out, void* stream);
 

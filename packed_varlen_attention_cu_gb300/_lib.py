@@ -29,6 +29,7 @@ EXPORTS = ("pva_worklist_bytes", "pva_build_worklist", "pva_attn_fwd", "pva_attn
            "pva_bwd_plan_bytes", "pva_build_bwd_plan", "pva_attn_bwd",
            "pva_rope", "pva_cache_append", "pva_cache_read", "pva_cache_attn_bytes",
            "pva_cache_attn", "pva_cache_cross_attn", "pva_cache_status",
+           "pva_beam_select_bytes", "pva_beam_select", "pva_beam_reorder",
            "pva_status_string", "pva_version")
 
 
@@ -73,6 +74,11 @@ class CacheBatch(ctypes.Structure):
                 ("max_pages", ctypes.c_int32), ("table_stride", ctypes.c_int64),
                 ("page_table", ctypes.c_void_p), ("kv_lens", ctypes.c_void_p),
                 ("cu_new", ctypes.c_void_p), ("status", ctypes.c_void_p)]
+
+
+class StateDesc(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("row_bytes", ctypes.c_int64),
+                ("row_stride", ctypes.c_int64)]
 
 
 class PvaError(RuntimeError):
@@ -163,6 +169,14 @@ def lib() -> ctypes.CDLL:
         L.pva_cache_cross_attn.restype = ctypes.c_int
         L.pva_cache_cross_attn.argtypes = [CP, BP, P, i64, i32, i32, ctypes.c_float, P, i32, P, P, sz,
                                            P]
+        L.pva_beam_select_bytes.restype = sz
+        L.pva_beam_select_bytes.argtypes = [i32, i32, i32, i32]
+        L.pva_beam_select.restype = ctypes.c_int
+        L.pva_beam_select.argtypes = [P, i64, i32, i32, i32, i32, i32, P, P, P, i32, P, P, P, P, P, P,
+                                      sz, P]
+        L.pva_beam_reorder.restype = ctypes.c_int
+        L.pva_beam_reorder.argtypes = [P, i32, i32, CP, i32, P, i64, i32, P, ctypes.POINTER(StateDesc),
+                                       i32, P, P]
         L.pva_cache_status.restype = ctypes.c_int
         L.pva_cache_status.argtypes = [P, ctypes.POINTER(i32), P]
         L.pva_debug_withhold_kv_load.restype = None

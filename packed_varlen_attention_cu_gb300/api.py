@@ -582,6 +582,114 @@ def cache_cross_attn(cache: KVCache, q: torch.Tensor, page_table: torch.Tensor, 
         check("pva_cache_cross_attn", rc)
 
 
+# ------------------------------------------------------ beam search
+_U8 = torch.uint8
+
+
+def beam_workspace_bytes(groups: int, beams: int, vocab: int, num_out: int) -> int:
+    n = lib().pva_beam_select_bytes(groups, beams, vocab, num_out)
+    if n == 0:
+        raise _lib.PvaError("pva_beam_select_bytes", 1)
+    return int(n)
+
+
+def alloc_beam_workspace(groups: int, beams: int, vocab: int, num_out: int, device="cuda") -> torch.Tensor:
+    """Workspace of beam_select for these sizes; one call at a time uses it."""
+    return torch.empty(beam_workspace_bytes(groups, beams, vocab, num_out), dtype=_U8, device=device)
+
+
+def beam_select(logits: torch.Tensor, scores: torch.Tensor, out_scores: torch.Tensor,
+                out_beams: torch.Tensor, out_tokens: torch.Tensor, workspace: torch.Tensor,
+                end_token: int = -1, finished: Optional[torch.Tensor] = None,
+                norms: Optional[torch.Tensor] = None, out_finished: Optional[torch.Tensor] = None,
+                status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """The best continuations of every group of beams: logits [groups * beams, vocab]
+    (bf16 or fp32, rows of any stride), scores fp32 [groups, beams], into out_scores
+    (fp32), out_beams (the parents) and out_tokens (int32), [groups, num_out], best
+    first.  finished (uint8 [groups, beams]): rows that offer only themselves, at
+    their own score with the end token; norms (fp32 [groups, beams]): scores are
+    ranked times these; out_finished (uint8 [groups, num_out])."""
+    dev = _device(logits, "logits")
+    kind = logits.dtype
+    if (kind is not _BF16 and kind is not _F32) or logits.dim() != 2 or scores.dim() != 2 or out_scores.dim() != 2:
+        raise ValueError("beam_select: logits bf16 or fp32 [groups * beams, vocab], scores [groups, beams], "
+                         "out_scores [groups, num_out]")
+    rows, vocab = logits.shape
+    shape, out = scores.shape, out_scores.shape
+    groups, beams = shape
+    if rows != groups * beams or out[0] != groups:
+        raise ValueError("beam_select: a row of logits for every beam, a row of results for every group")
+    stride, one = logits.stride()
+    if (one != 1 and vocab > 1) or (stride < vocab and rows > 1):
+        raise ValueError("logits: rows must be contiguous and must not overlap")
+    if workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace: a contiguous tensor on cuda:{dev} is needed")
+    s = _whole(scores, "scores", dev, shape, _F32)
+    o = _whole(out_scores, "out_scores", dev, out, _F32)
+    ob, ot = _whole(out_beams, "out_beams", dev, out, _I32), _whole(out_tokens, "out_tokens", dev, out, _I32)
+    f = None if finished is None else _whole(finished, "finished", dev, shape, _U8)
+    n = None if norms is None else _whole(norms, "norms", dev, shape, _F32)
+    of = None if out_finished is None else _whole(out_finished, "out_finished", dev, out, _U8)
+    rc = (_lib._lib or lib()).pva_beam_select(
+        logits.data_ptr(), stride if rows > 1 else 0, 1 if kind is _F32 else 0, groups, beams, vocab, out[1],
+        s, f, n, end_token, o, ob, ot, of, None if status is None else _ints(status, 1, "status", dev),
+        workspace.data_ptr(), workspace.nbytes, _queue(stream, dev))
+    if rc:
+        check("pva_beam_select", rc)
+
+
+def beam_reorder(parents: torch.Tensor, caches: Sequence[KVCache] = (),
+                 page_table: Optional[torch.Tensor] = None, kv_lens: Optional[torch.Tensor] = None,
+                 states: Sequence[torch.Tensor] = (), status: Optional[torch.Tensor] = None,
+                 stream=None) -> None:
+    """Every beam's row becomes a copy of its parent's, in place: parents int32
+    [groups, beams] (beam_select's out_beams where num_out = beams).  caches: those
+    of all layers, which share page_table (int32 [groups * beams, pages], updated:
+    full pages are shared, the last one is copied) and kv_lens (int32, the tokens
+    cached so far).  states: tensors [groups * beams, ...] of contiguous rows."""
+    dev = _device(parents, "parents")
+    if parents.dtype is not _I32 or parents.dim() != 2 or not parents.is_contiguous():
+        raise ValueError("parents: a contiguous int32 tensor [groups, beams]")
+    groups, beams = parents.shape
+    rows = groups * beams
+    n, table, stride, width, lens, descs = len(caches), None, 0, 0, None, None
+    if n:
+        if page_table is None or kv_lens is None:
+            raise ValueError("beam_reorder: caches go with page_table and kv_lens")
+        if page_table.dtype is not _I32 or page_table.get_device() != dev or page_table.dim() != 2 or \
+                page_table.shape[0] != rows:
+            raise ValueError(f"page_table: an int32 tensor [groups * beams, pages] on cuda:{dev} is needed")
+        width = page_table.shape[1]
+        stride = width
+        if not page_table.is_contiguous():
+            stride, one = page_table.stride()
+            _need(one == 1 or width <= 1, "page_table: rows must be contiguous")
+            stride = width if rows <= 1 else stride
+            _need(stride >= width, "page_table: rows overlap")
+        table, lens = page_table.data_ptr(), _ints(kv_lens, rows, "kv_lens", dev)
+        for c in caches:
+            if c.index != dev:
+                raise ValueError(f"a cache is on cuda:{c.index}, the call's tensors on cuda:{dev}")
+        descs = (_lib.CacheDesc * n)(*[c.desc for c in caches])
+    m, held = len(states), None
+    if m:
+        held = (_lib.StateDesc * m)()
+        for d, t in zip(held, states):
+            if t.get_device() != dev or t.dim() < 1 or t.shape[0] != rows or (rows and not t[0].is_contiguous()):
+                raise ValueError(f"states: tensors [groups * beams, ...] of contiguous rows on cuda:{dev} are needed")
+            size = t.element_size()
+            d.row_bytes = t.numel() // rows * size if rows else 0
+            d.row_stride = t.stride(0) * size if rows > 1 else d.row_bytes
+            if d.row_stride < d.row_bytes:
+                raise ValueError("states: rows overlap")
+            d.data = t.data_ptr()
+    rc = (_lib._lib or lib()).pva_beam_reorder(
+        parents.data_ptr(), groups, beams, descs, n, table, stride, width, lens, held, m,
+        None if status is None else _ints(status, 1, "status", dev), _queue(stream, dev))
+    if rc:
+        check("pva_beam_reorder", rc)
+
+
 def cache_status(status: torch.Tensor, stream=None) -> int:
     """The first failure met on the device by the calls that were given this status word
     (int32, 0 before them): 0, or a code of pva.h.  Synchronizes the stream."""
