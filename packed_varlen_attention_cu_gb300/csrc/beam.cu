@@ -29,18 +29,29 @@ constexpr int kMaxBeams = 64, kMaxOut = 64;
 constexpr int kScan = 256;           // threads of a scan CTA
 constexpr int kVecs = 4;             // 16-byte loads of a thread and tile
 constexpr int kTile = kScan * kVecs; // 16-byte vectors of a tile
-constexpr int kJoin = 1024;          // threads of a join CTA
+constexpr int kScanCtas = 4;         // scan CTAs on an SM
+constexpr int kRoom = 2048;          // candidates of a run that a scan CTA has room for
+constexpr int kHits = 1024;          // vectors that hold candidates of a run
+constexpr int kPlenty = 768;         // more than these are not ranked: a better bound is found first
+constexpr int kJoin = 1024;          // threads of a join CTA, at most
 constexpr int kJoinEach = 8;         // candidates of a thread
+constexpr int kFewCandidates = 128;  // up to which each candidate of a group counts the others
+constexpr int kPieceCost = 4;        // in tiles
 constexpr int kTargetCtas = 608;     // four CTAs on each of 152 SMs
 
 constexpr float kC = 1.4426950408889634f;  // log2(e)
 
 typedef unsigned long long u64;
 
+// x / y of whole numbers >= 0, by 32 bits where they fit.
+__device__ __forceinline__ int64_t quotient(int64_t x, int32_t y) {
+    return (x >> 32) == 0 ? (int64_t)((uint32_t)x / (uint32_t)y) : x / y;
+}
+
 struct PartHead {
-    double sum;   // sum of e^(x - ref)
-    float ref;    // about the largest logit; -inf where the part has none above -inf
-    int32_t count;
+    float hi, lo;   // hi + lo: sum of e^(x - ref)
+    float ref;      // about the largest logit; -inf where the part has none above -inf
+    int32_t pad;
 };
 
 struct SelectArgs {
@@ -54,8 +65,10 @@ struct SelectArgs {
     uint8_t* out_finished;
     int32_t* status;
     PartHead* heads;  // [rows][parts]
-    u64* lists;       // [rows][parts][k]: keys, largest first
-    int32_t groups, beams, vocab, k, parts, per, end_token;  // per: vectors of a part
+    u64* lists;       // [rows][parts][k]: keys, largest first; 0 where there is none
+    int32_t groups, beams, vocab, k, end_token;
+    int32_t tiles, per, parts;  // tiles of a row and of a CTA, room for a row's parts
+    int32_t whole;              // CTAs of a row, or 0: CTAs take pieces of the line of all rows
 };
 
 __device__ __forceinline__ float ex2_of(float x) {
@@ -96,44 +109,67 @@ __device__ __forceinline__ int row_state(const SelectArgs& a, int64_t row, bool&
     return a.finished && a.finished[row] ? kRowDone : kRowLive;
 }
 
-// One part of one row a CTA.  F32: fp32 logits, else bf16.
+// (a, b) becomes a sum of two floats that keeps what their addition rounds off.
+__device__ __forceinline__ void add_exact(float& hi, float& lo, float x, float y) {
+    const float s = hi + x, t = s - hi;
+    lo += (hi - (s - t)) + (x - t) + y;
+    hi = s;
+}
+
+// A CTA takes an equal piece of the line of all rows' tiles (16 KB each), so a row is cut into
+// parts where pieces end.  F32: fp32 logits, else bf16.
+//
+// What bounds it is HBM, so candidates must cost next to nothing.  Threads note the vectors in which
+// a logit passes a bound; warps stream without meeting.  After 1, 4, 16, ... tiles the noted vectors'
+// candidates go to a list, which is ranked and cut to its k best, and the bound is raised: each run
+// adds about 3 k.
+// (512 rows of 131071 bf16 logits, both kernels: a barrier and a count for each tile 78 us; warps
+// that look through their logits where they find one 55; vectors noted 42; without candidates 28.)
+// Should a run hold more than the lists, as ascending logits do, it is read again tile by tile
+// with a better bound.
+// The first bound is the smallest of the largest logits of 8, 16, 32 or 64 groups of threads: as
+// many logits as places reach it, and a few times as many in all.
 template <bool F32>
-__global__ void __launch_bounds__(kScan, 4) scan_kernel(const SelectArgs a) {
+__global__ void __launch_bounds__(kScan, kScanCtas) scan_kernel(const SelectArgs a) {
     constexpr int VE = F32 ? 4 : 8;  // logits of a vector
     constexpr int E = VE * kVecs;    // of a thread and tile
-    __shared__ u64 cand[kMaxOut + kMaxOut * E];  // the list, then what a tile adds to it
-    __shared__ u64 best[kMaxOut];
+    static_assert(kMaxOut * E <= kRoom, "what a tile may add after a bound by threads");
+    __shared__ uint4 hits[kHits];     // vectors that hold candidates of the run, and their numbers
+    __shared__ int32_t numbers[kHits];
+    __shared__ u64 cand[kRoom];       // the candidates in them
+    __shared__ u64 best[2][kMaxOut];  // the k best so far, largest first, and those before them
     __shared__ u64 tops[kScan];
     __shared__ u64 s_bound;
-    __shared__ int s_tops, s_new;
-    __shared__ double sm_sum[kScan / 32];
-    __shared__ float sm_ref[kScan / 32];
+    __shared__ int s_tops, s_n, s_hits;
+    __shared__ float sm_hi[kScan / 32], sm_lo[kScan / 32], sm_ref[kScan / 32];
     wait_previous();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int64_t row = blockIdx.x / (unsigned)a.parts;
-    const int part = blockIdx.x - (int)row * a.parts;
-    bool bad;
-    if (row_state(a, row, bad) != kRowLive) return;
     const int k = a.k;
+    int64_t u = (int64_t)blockIdx.x * a.per, u1 = min(u + a.per, (int64_t)a.groups * a.beams * a.tiles);
+    if (a.whole) {
+        const int64_t row = quotient(blockIdx.x, a.whole);
+        u = row * a.tiles + (blockIdx.x - row * a.whole) * a.per;
+        u1 = min(u + a.per, (row + 1) * a.tiles);
+    }
+    for (; u < u1;) {
+        const int64_t row = quotient(u, a.tiles);
+        const int32_t t0 = (int32_t)(u - row * a.tiles), t1 = (int32_t)min((int64_t)a.tiles, t0 + u1 - u);
+        const int part = a.whole ? t0 / a.per : (int)blockIdx.x - (int)quotient(row * a.tiles, a.per);
+        u += t1 - t0;
 
-    // Vectors start at 16-byte boundaries: vector v holds logits v * VE - shift on, the first
-    // and last ones fewer than VE of the row's.
-    const char* base = reinterpret_cast<const char*>(a.logits) + row * a.row_stride * (F32 ? 4 : 2);
-    const int shift = (int)(reinterpret_cast<uintptr_t>(base) & 15u) / (F32 ? 4 : 2);
-    const int32_t nv = (int32_t)(((int64_t)shift + a.vocab + VE - 1) / VE);
-    const int32_t v0 = min((int64_t)part * a.per, (int64_t)nv), v1 = min((int64_t)v0 + a.per, (int64_t)nv);
-    auto load = [&](uint4 (&v)[kVecs], int32_t tile) {
-#pragma unroll
-        for (int j = 0; j < kVecs; ++j) {
-            const int32_t x = tile + j * kScan + tid;
+        // Vectors start at 16-byte boundaries: vector v holds logits v * VE - shift on, the first
+        // and last ones fewer than VE of the row's.
+        const char* base = reinterpret_cast<const char*>(a.logits) + row * a.row_stride * (F32 ? 4 : 2);
+        const int shift = (int)(reinterpret_cast<uintptr_t>(base) & 15u) / (F32 ? 4 : 2);
+        const int32_t nv = (int32_t)(((int64_t)shift + a.vocab + VE - 1) / VE);
+        const int32_t whole0 = shift > 0 ? 1 : 0, whole1 = (int32_t)(((int64_t)shift + a.vocab) / VE);
+        // Vector x of the row; what is not the row's is -inf.
+        auto vector = [&](int32_t x) {
             const int64_t e0 = (int64_t)x * VE - shift;
+            if (x >= whole0 && x < whole1) return load16(base + e0 * (F32 ? 4 : 2));
             const uint32_t none = F32 ? 0xff800000u : 0xff80ff80u;
-            v[j] = make_uint4(none, none, none, none);
-            if (x >= v1) continue;
-            if (e0 >= 0 && e0 + VE <= a.vocab) {
-                v[j] = load16(base + e0 * (F32 ? 4 : 2));
-            } else {
-                uint32_t w[4] = {none, none, none, none};
+            uint32_t w[4] = {none, none, none, none};
+            if (x < nv) {
 #pragma unroll
                 for (int i = 0; i < VE; ++i) {
                     if (e0 + i < 0 || e0 + i >= a.vocab) continue;
@@ -144,268 +180,458 @@ __global__ void __launch_bounds__(kScan, 4) scan_kernel(const SelectArgs a) {
                         w[i >> 1] = i & 1 ? (w[i >> 1] & 0xffffu) | y << 16 : (w[i >> 1] & 0xffff0000u) | y;
                     }
                 }
-                v[j] = make_uint4(w[0], w[1], w[2], w[3]);
             }
-        }
-    };
-    auto word = [&](const uint4 (&v)[kVecs], int i) {
-        const uint4 q = v[i >> 2];
-        return (i & 3) == 0 ? q.x : (i & 3) == 1 ? q.y : (i & 3) == 2 ? q.z : q.w;
-    };
-    auto logit = [&](const uint4 (&v)[kVecs], int e) {
-        if (F32) return __uint_as_float(word(v, e));
-        const uint32_t w = word(v, e >> 1);
-        return __uint_as_float(e & 1 ? w & 0xffff0000u : w << 16);
-    };
+            return make_uint4(w[0], w[1], w[2], w[3]);
+        };
+        auto load = [&](uint4 (&v)[kVecs], int32_t t) {
+            const int32_t x = t * kTile + tid;
+            if (t * kTile >= whole0 && t * kTile + kTile <= whole1) {
+                const char* at = base + ((int64_t)x * VE - shift) * (F32 ? 4 : 2);
+#pragma unroll
+                for (int j = 0; j < kVecs; ++j) v[j] = load16(at + j * kScan * 16);
+            } else {
+#pragma unroll
+                for (int j = 0; j < kVecs; ++j) v[j] = vector(x + j * kScan);
+            }
+        };
+        uint4 v[kVecs];
+        load(v, t0);  // (beside the row's score, not after it)
+        bool bad;
+        if (row_state(a, row, bad) != kRowLive) continue;
+        if (tid == 0) s_n = s_hits = 0;
 
-    float ref = -INFINITY, sum = 0.f;
-    u64 bound = kNoKey;           // a candidate's key is larger
-    float bound_x = -INFINITY;    // its logit
-    int count = 0;                // entries of the list
-    uint4 v[kVecs], next[kVecs];
-    load(v, v0);
-    for (int32_t tile = v0; tile < v1; tile += kTile) {
-        load(next, tile + kTile);  // (past the part's end: nothing)
-        float top;
-        if (F32) {
-            top = logit(v, 0);
+        auto word = [&](int i) {
+            const uint4 q = v[i >> 2];
+            return (i & 3) == 0 ? q.x : (i & 3) == 1 ? q.y : (i & 3) == 2 ? q.z : q.w;
+        };
+        auto logit = [&](int e) {
+            if (F32) return __uint_as_float(word(e));
+            const uint32_t w = word(e >> 1);
+            return __uint_as_float(e & 1 ? w & 0xffff0000u : w << 16);
+        };
+        float ref = -INFINITY, sum = 0.f;
+        u64 bound = kNoKey;           // a candidate's key is larger
+        float bound_x = -INFINITY;    // its logit: a candidate's is larger (tokens ascend, so an equal one is no better)
+        float least_x = -INFINITY;    // a candidate's is at least this
+        int count = 0;                // entries of the list when it was cut
+        float tops4[kVecs], top;      // largest logits of a tile's vectors, and of all
+        auto find_top = [&]() {
 #pragma unroll
-            for (int e = 1; e < E; ++e) top = fmaxf(top, logit(v, e));
-        } else {
-            uint32_t w0 = word(v, 0);
-            __nv_bfloat162 m = *reinterpret_cast<const __nv_bfloat162*>(&w0);
+            for (int j = 0; j < kVecs; ++j) {
+                if (F32) {
+                    tops4[j] = fmaxf(fmaxf(logit(4 * j), logit(4 * j + 1)), fmaxf(logit(4 * j + 2), logit(4 * j + 3)));
+                } else {
+                    __nv_bfloat162 m[4];
 #pragma unroll
-            for (int i = 1; i < E / 2; ++i) {
-                const uint32_t w = word(v, i);
-                m = __hmax2(m, *reinterpret_cast<const __nv_bfloat162*>(&w));
-            }
-            top = fmaxf(__low2float(m), __high2float(m));
-        }
-        // Sum of e^(x - ref), the difference first: c x alone, rounded, is off by more than an
-        // exponent holds for logits past 2^30.  ref is a whole number, so it moves by 1 at least
-        // and the rounding of the sum's factors dies away.
-        const float want = rintf(top);
-        if (want > ref) {
-            sum *= ex2_of((ref - want) * kC);
-            ref = want;
-        }
-        const float neg = ref == -INFINITY ? 0.f : -ref;
-        {
-            float2 part2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-            const float2 c2 = make_float2(kC, kC), n2 = make_float2(neg, neg);
-#pragma unroll
-            for (int e = 0; e < E; e += 2) {
-                const float2 y = __fmul2_rn(__fadd2_rn(make_float2(logit(v, e), logit(v, e + 1)), n2), c2);
-                part2[(e >> 1) & 1] = __fadd2_rn(part2[(e >> 1) & 1], make_float2(ex2_of(y.x), ex2_of(y.y)));
-            }
-            sum += (part2[0].x + part2[1].x) + (part2[0].y + part2[1].y);
-        }
-        // ---- candidates: logits above the list's last.  (Tokens ascend, so an equal one is no better.)
-        const int above = __syncthreads_count(top > bound_x);
-        if (above > 0) {
-            u64 least = bound + 1;  // the smallest key that is taken
-            if (above > k) {
-                // More threads than places hold one.  The k-th largest of the threads' largest keys is
-                // a bound: k keys reach it, and at most k threads hold any that do.
-                u64 mine = 0;
-                if (top > bound_x) {
-                    int32_t at = 0;
-#pragma unroll
-                    for (int e = E - 1; e >= 0; --e) at = logit(v, e) == top ? e : at;
-                    mine = key_of(top, (tile + (at / VE) * kScan + tid) * VE - shift + at % VE);
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t w = word(4 * j + i);
+                        m[i] = *reinterpret_cast<const __nv_bfloat162*>(&w);
+                    }
+                    m[0] = __hmax2(__hmax2(m[0], m[1]), __hmax2(m[2], m[3]));
+                    tops4[j] = fmaxf(__low2float(m[0]), __high2float(m[0]));
                 }
-                int ahead = 0;
-#pragma unroll
-                for (int o = 1; o < 32; ++o) ahead += __shfl_xor_sync(0xffffffffu, mine, o) > mine;
-                if (tid == 0) s_tops = 0;
-                __syncthreads();
-                if (mine != 0 && ahead < k) tops[atomicAdd(&s_tops, 1)] = mine;
-                __syncthreads();
-                const int n = s_tops;
-                if (tid < n) {
-                    const u64 x = tops[tid];
-                    int r = 0;
-                    for (int i = 0; i < n; ++i) r += tops[i] > x;
-                    if (r == k - 1) s_bound = x;
-                }
-                __syncthreads();
-                least = s_bound;
             }
-            if (tid == 0) s_new = 0;
+            top = fmaxf(fmaxf(tops4[0], tops4[1]), fmaxf(tops4[2], tops4[3]));
+        };
+        // Notes this thread's vectors that hold a candidate.  (Looking for it here would have a warp run
+        // through its logits for the sake of one lane.)
+        auto note = [&](int32_t t) {
+            if (!(top > bound_x && top >= least_x)) return;
+#pragma unroll
+            for (int j = 0; j < kVecs; ++j)
+                if (tops4[j] > bound_x && tops4[j] >= least_x) {
+                    const int at = atomicAdd(&s_hits, 1);
+                    if (at < kHits) {
+                        hits[at] = v[j];
+                        numbers[at] = t * kTile + j * kScan + tid;
+                    }
+                }
+        };
+        // Takes the candidates out of the noted vectors, ranks them with the k best so far and keeps the
+        // k best of all.  False, and nothing done, where there are more than `most`.
+        int now = 0;  // which of best[] holds the list
+        auto cut = [&](int most) {
             __syncthreads();
-            if (top > bound_x && ordered(top) >= (uint32_t)(least >> 32)) {
+            const int noted = s_hits;
+            if (noted > kHits) return false;
+            for (int i = tid; i < noted; i += kScan) {
+                const uint4 q = hits[i];
+                const int32_t first = numbers[i] * VE - shift;
 #pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    const float x = logit(v, e);
-                    if (x > bound_x) {
-                        const u64 key = key_of(x, (tile + (e / VE) * kScan + tid) * VE - shift + e % VE);
-                        if (key >= least) cand[count + atomicAdd(&s_new, 1)] = key;
+                for (int e = 0; e < VE; ++e) {
+                    const uint32_t w = (F32 ? e : e >> 1) == 0 ? q.x : (F32 ? e : e >> 1) == 1 ? q.y
+                                       : (F32 ? e : e >> 1) == 2 ? q.z : q.w;
+                    const float y = __uint_as_float(F32 ? w : e & 1 ? w & 0xffff0000u : w << 16);
+                    if (y > bound_x && y >= least_x) {
+                        const int at = atomicAdd(&s_n, 1);
+                        if (at < kRoom) cand[at] = key_of(y, first + e);
                     }
                 }
             }
             __syncthreads();
-            const int n = count + s_new;
-            for (int i = tid; i < n; i += kScan) {
-                const u64 x = cand[i];
+            const int fresh = s_n, n = count + fresh;
+            if (fresh > most) return false;
+            if (tid == 0) s_hits = 0;
+            const u64* list = best[now];
+            // (a short list's entries are compared by two or four lanes each)
+            const int lanes = n <= kScan / 4 ? 4 : n <= kScan / 2 ? 2 : 1;
+            for (int i = tid / lanes; i < ((n + 31) & ~31); i += kScan) {
+                const u64 x = i < count ? list[i] : cand[min(i - count, kRoom - 1)];
                 int r = 0;
-                for (int j = 0; j < n; ++j) r += cand[j] > x;
-                if (r < k) best[r] = x;
+                for (int j = tid & (lanes - 1); j < count; j += lanes) r += list[j] > x;
+#pragma unroll 4
+                for (int j = tid & (lanes - 1); j < fresh; j += lanes) r += cand[j] > x;
+                if (lanes > 1) r += __shfl_xor_sync(0xffffffffu, r, 1);
+                if (lanes > 2) r += __shfl_xor_sync(0xffffffffu, r, 2);
+                if (i < n && r < k) best[now ^ 1][r] = x;
             }
             __syncthreads();
+            if (tid == 0) s_n = 0;  // (appended to after the next call's first barrier only)
+            now ^= 1;
             count = min(n, k);
-            if (tid < count) cand[tid] = best[tid];
             if (count == k) {
-                bound = best[k - 1];
+                bound = best[now][k - 1];
                 bound_x = unordered((uint32_t)(bound >> 32));
             }
-            // (the next tile's barrier comes before anything is added to the list or put into `best`)
+            least_x = -INFINITY;
+            return true;
+        };
+        // Tiles ta .. tb once more, from the list of the last cut.  Where more threads than places
+        // hold a logit above the bound, the k-th largest of the threads' largest keys is a better one:
+        // k keys reach it, and at most k threads hold any that do.
+        auto again = [&](int32_t ta, int32_t tb) {
+#pragma unroll 1
+            for (int32_t t = ta; t < tb; ++t) {
+                load(v, t);
+                find_top();
+                __syncthreads();
+                if (tid == 0) s_n = s_tops = s_hits = 0;
+                const int above = __syncthreads_count(top > bound_x);
+                u64 least = bound + 1;
+                if (above > k) {
+                    u64 mine = 0;
+                    if (top > bound_x) {
+                        int32_t at = 0;
+#pragma unroll
+                        for (int e = E - 1; e >= 0; --e) at = logit(e) == top ? e : at;
+                        mine = key_of(top, (t * kTile + (at / VE) * kScan + tid) * VE - shift + at % VE);
+                    }
+                    int ahead = 0;
+#pragma unroll 1
+                    for (int o = 1; o < 32; ++o) ahead += __shfl_xor_sync(0xffffffffu, mine, o) > mine;
+                    if (mine != 0 && ahead < k) tops[atomicAdd(&s_tops, 1)] = mine;
+                    __syncthreads();
+                    const int n = s_tops;
+                    if (tid < n) {
+                        const u64 x = tops[tid];
+                        int r = 0;
+                        for (int i = 0; i < n; ++i) r += tops[i] > x;
+                        if (r == k - 1) s_bound = x;
+                    }
+                    __syncthreads();
+                    least = s_bound;
+                }
+                if (top > bound_x && ordered(top) >= (uint32_t)(least >> 32)) {
+#pragma unroll
+                    for (int e = 0; e < E; ++e) {
+                        const u64 key = key_of(logit(e), (t * kTile + (e / VE) * kScan + tid) * VE - shift + e % VE);
+                        if (logit(e) > bound_x && key >= least) cand[atomicAdd(&s_n, 1)] = key;
+                    }
+                }
+                cut(kRoom);
+            }
+        };
+        int32_t from = t0, goal = t0 + 1;  // first tile of the run, and where it ends
+        for (int32_t t = t0; t < t1; ++t) {
+            find_top();
+            // Sum of e^(x - ref), the difference first: c x alone, rounded, is off by more than an
+            // exponent holds for logits past 2^30.  ref is a whole number, so it moves by 1 at least
+            // and the rounding of the sum's factors dies away.
+            const float want = rintf(top);
+            if (want > ref) {
+                sum *= ex2_of((ref - want) * kC);
+                ref = want;
+            }
+            const float neg = ref == -INFINITY ? 0.f : -ref;
+            {
+                float2 part2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                const float2 c2 = make_float2(kC, kC), n2 = make_float2(neg, neg);
+#pragma unroll
+                for (int e = 0; e < E; e += 2) {
+                    const float2 y = __fmul2_rn(__fadd2_rn(make_float2(logit(e), logit(e + 1)), n2), c2);
+                    part2[(e >> 1) & 1] = __fadd2_rn(part2[(e >> 1) & 1], make_float2(ex2_of(y.x), ex2_of(y.y)));
+                }
+                sum += (part2[0].x + part2[1].x) + (part2[0].y + part2[1].y);
+            }
+            if (t == t0) {
+                const int group = k <= 8 ? 32 : k <= 16 ? 16 : k <= 32 ? 8 : 4;  // threads
+                float x = top == top ? top : -INFINITY;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {  // the largest of a group, then the smallest of the groups
+                    const float y = __shfl_xor_sync(0xffffffffu, x, o);
+                    x = o < group ? fmaxf(x, y) : fminf(x, y);
+                }
+                if (lane == 0) sm_ref[warp] = x;
+                __syncthreads();
+#pragma unroll
+                for (int w = 0; w < kScan / 32; ++w) x = fminf(x, sm_ref[w]);
+                least_x = x;
+            }
+            note(t);
+            // (Warps are at different tiles, so others compute while one waits; a second tile in registers
+            // was slower, 71 against 65 us.)
+            if (t + 1 < t1) load(v, t + 1);
+            if (t + 1 == goal || t + 1 == t1) {
+                if (!cut(kPlenty)) {
+                    again(from, t + 1);
+                    if (t + 1 < t1) load(v, t + 1);
+                }
+                from = t + 1;
+                goal = t0 + 4 * (goal - t0);
+            }
         }
+        // ---- the part's sum, two floats wide over the threads, and its list
+        float r = ref;
 #pragma unroll
-        for (int j = 0; j < kVecs; ++j) v[j] = next[j];
-    }
-    // ---- the part's sum, in 64 bits over the threads, and its list
-    float r = ref;
+        for (int o = 16; o > 0; o >>= 1) r = fmaxf(r, __shfl_xor_sync(0xffffffffu, r, o));
+        float hi = ref == -INFINITY ? sum : sum * ex2_of((ref - r) * kC), lo = 0.f;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) r = fmaxf(r, __shfl_xor_sync(0xffffffffu, r, o));
-    double d = ref == -INFINITY ? (double)sum : (double)(sum * ex2_of((ref - r) * kC));
+        for (int o = 16; o > 0; o >>= 1)
+            add_exact(hi, lo, __shfl_xor_sync(0xffffffffu, hi, o), __shfl_xor_sync(0xffffffffu, lo, o));
+        if (lane == 0) {
+            sm_ref[warp] = r;
+            sm_hi[warp] = hi;
+            sm_lo[warp] = lo;
+        }
+        __syncthreads();
+        const int64_t at = row * a.parts + part;
+        if (tid == 0) {
+            float rr = sm_ref[0];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
-    if (lane == 0) {
-        sm_ref[warp] = r;
-        sm_sum[warp] = d;
+            for (int w = 1; w < kScan / 32; ++w) rr = fmaxf(rr, sm_ref[w]);
+            float h = 0.f, l = 0.f;
+#pragma unroll
+            for (int w = 0; w < kScan / 32; ++w) {
+                const float f = sm_ref[w] == -INFINITY ? 1.f : ex2_of((sm_ref[w] - rr) * kC);
+                add_exact(h, l, f * sm_hi[w], f * sm_lo[w]);
+            }
+            a.heads[at] = PartHead{h, l, rr, 0};
+        }
+        if (tid < k) a.lists[at * k + tid] = tid < count ? best[now][tid] : 0;
+        __syncthreads();  // the next row's piece may write what this one reads
     }
-    __syncthreads();
-    const int64_t at = row * a.parts + part;
-    if (tid == 0) {
-        float rr = sm_ref[0];
-        for (int w = 1; w < kScan / 32; ++w) rr = fmaxf(rr, sm_ref[w]);
-        double dd = 0;
-        for (int w = 0; w < kScan / 32; ++w)
-            dd += sm_ref[w] == -INFINITY ? sm_sum[w] : sm_sum[w] * (double)ex2_of((sm_ref[w] - rr) * kC);
-        a.heads[at] = PartHead{dd, rr, count};
-    }
-    if (tid < count) a.lists[at * k + tid] = cand[tid];
 }
 
 // One group a CTA: every row's logarithm from its parts, then the best candidates of all lists.
-// The k-th largest score is bracketed by halving over the scores' order as whole numbers (rounded
-// to fp32, which keeps the order) until few candidates are left, and those are ranked in 64 bits.
+// 64-bit arithmetic is slow here (two operations a clock and SM), so candidates are first judged by
+// an interval around their rank in fp32: what k others are surely above is dropped (few candidates:
+// each counts the others; many: the k-th largest lower end is bracketed by halving), and the rest is
+// ranked in 64 bits.
+// EACH: candidates of a thread.  (One where they suffice: this code runs once, and waits for its
+// instructions more than for anything else.)
+template <int EACH>
 __global__ void __launch_bounds__(kJoin) join_kernel(const SelectArgs a) {
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ double add[kMaxBeams];  // what a row adds to its logits
     __shared__ double norm[kMaxBeams];
-    __shared__ int state[kMaxBeams];
+    __shared__ float add_f[kMaxBeams], norm_f[kMaxBeams], refs[kMaxBeams];
+    __shared__ float sums[kMaxBeams], rests[kMaxBeams];
+    __shared__ int state[kMaxBeams], cuts[kMaxBeams];
     __shared__ int s_count[3], s_kept;
+    __shared__ uint32_t s_max;
     wait_previous();
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = blockDim.x;
     const int64_t row0 = (int64_t)blockIdx.x * a.beams;
     const int k = a.k, parts = a.parts, total = a.beams * parts * k;
-    double* rank = reinterpret_cast<double*>(smem);        // [total]
-    u64* keys = reinterpret_cast<u64*>(rank + total);      // [total]
+    u64* rank = reinterpret_cast<u64*>(smem);              // [total]: in the order of the ranks
+    u64* keys = rank + total;                              // [total]
     int* from = reinterpret_cast<int*>(keys + total);      // [total]
-    for (int b = warp; b < a.beams; b += kJoin / 32) {
-        bool bad;
-        int st = row_state(a, row0 + b, bad);
-        double lse = 0;
-        if (st == kRowLive) {
-            const PartHead* h = a.heads + (row0 + b) * parts;
-            float r = -INFINITY;
-            for (int p = lane; p < parts; p += 32) r = fmaxf(r, h[p].ref);
+    float* low = reinterpret_cast<float*>(smem);           // [total], before the ranks
+    bool bad = false;
+    int st = kRowNone;
+    float score = 0.f, weight = 1.f;
+    if (tid < a.beams) {
+        st = row_state(a, row0 + tid, bad);
+        score = a.scores[row0 + tid];
+        if (a.norms) weight = a.norms[row0 + tid];
+    }
+    // this thread's candidates: entry i % k of list i / k
+    u64 mine[EACH];
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) r = fmaxf(r, __shfl_xor_sync(0xffffffffu, r, o));
-            double s = 0;
-            for (int p = lane; p < parts; p += 32)
-                s += h[p].ref == -INFINITY ? h[p].sum : h[p].sum * (double)ex2_of((h[p].ref - r) * kC);
+    for (int e = 0; e < EACH; ++e) {
+        const int i = e * threads + tid;
+        mine[e] = i < total ? a.lists[row0 * parts * k + i] : 0;
+    }
+    // parts that row b was cut into
+    auto parts_here = [&](int b) {
+        if (a.whole) return a.whole;
+        const int64_t first = (row0 + b) * a.tiles;
+        return (int)(quotient(first + a.tiles - 1, a.per) - quotient(first, a.per)) + 1;
+    };
+    for (int b = warp; b < a.beams; b += threads / 32) {
+        const PartHead* h = a.heads + (row0 + b) * parts;
+        const int cut = parts_here(b);
+        float r = -INFINITY;
+        for (int p = lane; p < cut; p += 32) r = fmaxf(r, h[p].ref);
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-            if (!(s - s == 0)) {  // a NaN or +inf among the logits
-                bad = true;
-                st = kRowNone;
-            } else if (s == 0) {  // nothing above -inf
-                st = kRowNone;
-            } else {
-                lse = (double)r + log(s);
-            }
+        for (int o = 16; o > 0; o >>= 1) r = fmaxf(r, __shfl_xor_sync(0xffffffffu, r, o));
+        float hi = 0.f, lo = 0.f;
+        for (int p = lane; p < cut; p += 32) {
+            const float f = h[p].ref == -INFINITY ? 1.f : ex2_of((h[p].ref - r) * kC);
+            add_exact(hi, lo, f * h[p].hi, f * h[p].lo);
         }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+            add_exact(hi, lo, __shfl_xor_sync(0xffffffffu, hi, o), __shfl_xor_sync(0xffffffffu, lo, o));
         if (lane == 0) {
-            if (bad) raise_status(a.status, kErrLogits);
-            state[b] = st;
-            add[b] = (double)a.scores[row0 + b] - lse;
-            norm[b] = a.norms ? (double)a.norms[row0 + b] : 1.0;
+            cuts[b] = cut;
+            refs[b] = r;
+            sums[b] = hi;
+            rests[b] = lo;
         }
     }
     if (tid < 3) s_count[tid] = 0;
-    if (tid == 0) s_kept = 0;
+    if (tid == 0) s_kept = s_max = 0;
     __syncthreads();
-    // candidate i of the group: entry i % k of list i / k
+    if (tid < a.beams) {
+        double lse = 0;
+        if (st == kRowLive) {
+            float s = sums[tid];
+            if (!(s - s == 0.f)) {  // a NaN or +inf among the logits
+                bad = true;
+                st = kRowNone;
+            } else if (s == 0.f) {  // nothing above -inf
+                st = kRowNone;
+            } else {
+                // ln(s + rest), s = m 2^e: a float's logarithm of m near 1 is off by 3e-8 at most, which the
+                // logarithm of s itself would not be
+                int e;
+                const float rest = rests[tid] / s;
+                s = frexpf(s, &e);
+                if (s < 0.70710678f) {
+                    s *= 2.f;
+                    --e;
+                }
+                lse = (double)refs[tid] + (double)e * 0.6931471805599453 + (double)(logf(s) + rest);
+            }
+        }
+        if (bad) raise_status(a.status, kErrLogits);
+        state[tid] = st;
+        add[tid] = (double)score - lse;
+        add_f[tid] = (float)add[tid];
+        norm_f[tid] = weight;
+        norm[tid] = (double)weight;
+    }
+    __syncthreads();
     auto score_of = [&](int b, u64 key) {
         return state[b] == kRowDone ? add[b] : add[b] + (double)unordered((uint32_t)(key >> 32));
     };
-    uint32_t coarse[kJoinEach];
-    u64 mine[kJoinEach];
+    // the interval of a candidate's rank: four roundings of fp32 on either side
+    float up[EACH];
+    uint32_t lows[EACH];
 #pragma unroll
-    for (int e = 0; e < kJoinEach; ++e) {
-        const int i = e * kJoin + tid;
-        coarse[e] = 0;
-        mine[e] = 0;
-        if (i >= total) continue;
-        const int list = i / k, b = list / parts, at = i - list * k;
-        const int64_t l = row0 * parts + list;
-        if (state[b] == kRowDone ? at == 0 && list == b * parts : state[b] == kRowLive && at < a.heads[l].count) {
-            mine[e] = state[b] == kRowDone ? 0 : a.lists[l * k + at];
-            // (a score that fp32 rounds to -inf, or that its norm takes there, is no candidate's)
-            const double x = score_of(b, mine[e]);
-            const float f = (float)(x * norm[b]);
-            coarse[e] = f == -INFINITY || (float)x == -INFINITY ? 0 : ordered(f);
+    for (int e = 0; e < EACH; ++e) {
+        const int i = e * threads + tid;
+        up[e] = -INFINITY;
+        lows[e] = 0;
+        if (i < total) {
+            const int list = i / k, b = list / parts;
+            const bool done = state[b] == kRowDone && i == b * parts * k;
+            if (done || (state[b] == kRowLive && list - b * parts < cuts[b] && mine[e] != 0)) {
+                const float x = done ? 0.f : unordered((uint32_t)(mine[e] >> 32));
+                const float y = (add_f[b] + x) * norm_f[b];
+                const float err = (fabsf(add_f[b]) + fabsf(x)) * norm_f[b] * 2.4e-7f + 1e-37f;
+                // (a score that fp32 rounds to -inf, or that its norm takes there, is no candidate's)
+                if (y > -3.4e38f || ((float)score_of(b, mine[e]) != -INFINITY &&
+                                     (float)(score_of(b, mine[e]) * norm[b]) != -INFINITY)) {
+                    up[e] = fmaxf(y + err, -3.4028234e38f);
+                    lows[e] = ordered(fmaxf(y - err, -3.4028234e38f));
+                }
+            }
+            if (total <= kFewCandidates) low[i] = lows[e] ? unordered(lows[e]) : -INFINITY;
         }
     }
-    int round = 0;
-    auto reaching = [&](uint32_t x) {  // candidates whose order is at least x
-        int n = 0;
-#pragma unroll
-        for (int e = 0; e < kJoinEach; ++e) n += coarse[e] >= x;
-        n = __reduce_add_sync(0xffffffffu, n);
-        const int now = round % 3;
-        if (lane == 0 && n) atomicAdd(&s_count[now], n);
-        if (tid == 0) s_count[(now + 1) % 3] = 0;
+    uint32_t keep = 1;  // order of the upper end that a kept candidate has at least
+    bool kept[EACH];
+    int n = 0;
+    if (total <= kFewCandidates) {
         __syncthreads();
-        ++round;
-        return s_count[now];
-    };
-    const int few = k + 32;
-    uint32_t lo = 1, hi = 0xffffffffu;  // at least min(k, all) candidates reach lo, fewer than k reach hi
-    int n = reaching(1);
-    if (n > few) {
-        while (hi - lo > 1) {
+#pragma unroll
+        for (int e = 0; e < EACH; ++e) {
+            kept[e] = lows[e] != 0;
+            if (!kept[e]) continue;
+            int surely = 0;
+#pragma unroll 8
+            for (int j = 0; j < total; ++j) surely += low[j] > up[e];
+            kept[e] = surely < k;
+        }
+        __syncthreads();
+    } else {
+        uint32_t top = 0;
+#pragma unroll
+        for (int e = 0; e < EACH; ++e) top = max(top, lows[e]);
+        top = __reduce_max_sync(0xffffffffu, top);
+        if (lane == 0) atomicMax(&s_max, top);
+        __syncthreads();
+        top = s_max;
+        int round = 0;
+        auto reaching = [&](uint32_t x) {  // candidates whose lower end is x in order at least
+            int m = 0;
+#pragma unroll
+            for (int e = 0; e < EACH; ++e) m += lows[e] >= x;
+            m = __reduce_add_sync(0xffffffffu, m);
+            const int now = round % 3;
+            if (lane == 0 && m) atomicAdd(&s_count[now], m);
+            if (tid == 0) s_count[(now + 1) % 3] = 0;
+            __syncthreads();
+            ++round;
+            return s_count[now];
+        };
+        // k candidates or all there are reach lo, fewer than k reach hi: from the largest down in
+        // growing steps, then by halves, until not many more than k are left
+        uint32_t lo = top, hi = top + 1, step = 1u << 20;
+        int m = reaching(lo);
+        while (m < k && lo > 1) {
+            hi = lo;
+            lo = lo > step ? lo - step : 1;
+            step *= 2;
+            m = reaching(lo);
+        }
+        while (m > k + 32 && hi - lo > 1) {
             const uint32_t mid = lo + (hi - lo) / 2;
-            const int m = reaching(mid);
-            if (m >= k) {
+            const int c = reaching(mid);
+            if (c >= k) {
                 lo = mid;
-                n = m;
-                if (n <= few) break;
+                m = c;
             } else {
                 hi = mid;
             }
         }
+        keep = lo;
+#pragma unroll
+        for (int e = 0; e < EACH; ++e) kept[e] = lows[e] != 0 && ordered(up[e]) >= keep;
     }
 #pragma unroll
-    for (int e = 0; e < kJoinEach; ++e) {
-        if (coarse[e] < lo) continue;
-        const int b = (e * kJoin + tid) / k / parts, at = atomicAdd(&s_kept, 1);
-        rank[at] = score_of(b, mine[e]) * norm[b];
-        keys[at] = mine[e];
+    for (int e = 0; e < EACH; ++e) {
+        if (!kept[e]) continue;
+        const int b = (e * threads + tid) / k / parts, at = atomicAdd(&s_kept, 1);
+        const u64 key = state[b] == kRowDone ? 0 : mine[e];
+        // (64-bit floats in the order of whole numbers, whose comparison is cheap; -0 is 0)
+        const u64 bits = (u64)__double_as_longlong(score_of(b, key) * norm[b] + 0.0);
+        rank[at] = bits >> 63 ? ~bits : bits | (u64)1 << 63;
+        keys[at] = key;
         from[at] = b;
     }
     __syncthreads();
+    n = s_kept;
     // larger score first, then the lower beam, then the larger logit, then the lower token
     const int64_t out = (int64_t)blockIdx.x * k;
-    for (int i = tid; i < n; i += kJoin) {
-        const double x = rank[i];
-        const u64 key = keys[i];
+    for (int i = tid; i < n; i += threads) {
+        const u64 x = rank[i], key = keys[i];
         const int b = from[i];
         int r = 0;
         for (int j = 0; j < n; ++j) {
-            const double y = rank[j];
+            const u64 y = rank[j];
             r += y > x || (y == x && (from[j] < b || (from[j] == b && keys[j] > key)));
         }
         if (r >= k) continue;
@@ -416,23 +642,39 @@ __global__ void __launch_bounds__(kJoin) join_kernel(const SelectArgs a) {
         a.out_tokens[out + r] = token;
         if (a.out_finished) a.out_finished[out + r] = done || token == a.end_token;
     }
-    for (int i = n + tid; i < k; i += kJoin) {  // fewer candidates than places
+    for (int i = n + tid; i < k; i += threads) {  // fewer candidates than places
         a.out_scores[out + i] = -INFINITY;
         a.out_beams[out + i] = a.out_tokens[out + i] = -1;
         if (a.out_finished) a.out_finished[out + i] = 0;
     }
 }
 
-// Parts that a row is cut into: whole tiles, enough CTAs for the machine where rows are few, and
-// no more candidates than the join's threads hold.
-int parts_of(int64_t rows, int32_t beams, int32_t k, int64_t vectors) {
-    const int64_t tiles = (vectors + kTile - 1) / kTile;
-    int64_t parts = (kTargetCtas + rows - 1) / rows;
-    const int64_t most = (int64_t)kJoin * kJoinEach / (beams * k);
+// How the rows' tiles are cut: tiles of a CTA, room for a row's parts, CTAs of a row or 0.
+struct Cut {
+    int64_t tiles, per, parts, whole;
+};
+// A piece of a row costs about four tiles more than it has, so rows are cut into equal parts of
+// their own unless that leaves the last round of CTAs too empty (512 rows of 16 tiles: 42 us a CTA
+// a row, 48 in 581 pieces of the line, 1.9 rows each; 120 rows of 13: 15.5 and 19.9 us).
+Cut cut_of(int64_t rows, int32_t beams, int32_t k, int64_t vectors) {
+    Cut c;
+    c.tiles = (vectors + kTile - 1) / kTile;
+    // no more candidates of a group than the join's threads hold
+    const int64_t most = (int64_t)kJoin * kJoinEach / ((int64_t)beams * k);
+    int64_t parts = rows < kTargetCtas ? kTargetCtas / rows : 1;
     parts = parts < most ? parts : most;
-    parts = parts < tiles ? parts : tiles;
-    const int64_t each = (tiles + parts - 1) / parts;
-    return (int)((tiles + each - 1) / each);
+    parts = parts < c.tiles ? parts : c.tiles;
+    c.per = (c.tiles + parts - 1) / parts;
+    c.parts = c.whole = (c.tiles + c.per - 1) / c.per;
+    const int64_t rounds = (rows * c.whole + kTargetCtas - 1) / kTargetCtas;
+    const int64_t line = (rows * c.tiles + kTargetCtas - 1) / kTargetCtas;
+    if (rounds * (c.per + kPieceCost) <= line + kPieceCost * (line / c.tiles + 2)) return c;
+    // (a row may touch one piece more than it fills)
+    c.whole = 0;
+    for (c.per = line;; ++c.per) {
+        c.parts = (c.tiles + c.per - 2) / c.per + 1;
+        if (c.parts <= most) return c;
+    }
 }
 
 int64_t vectors_of(int32_t vocab, bool f32) {  // of a row that starts anywhere
@@ -619,9 +861,8 @@ extern "C" size_t pva_beam_select_bytes(int32_t num_groups, int32_t beams, int32
     const int64_t rows = (int64_t)num_groups * beams;
     if (rows > INT32_MAX / kTargetCtas) return 0;
     if (rows == 0) return 256;
-    // (fp32 rows have more vectors, so at least as many parts)
-    const int a = parts_of(rows, beams, num_out, vectors_of(vocab, true));
-    const int b = parts_of(rows, beams, num_out, vectors_of(vocab, false));
+    const int64_t a = cut_of(rows, beams, num_out, vectors_of(vocab, true)).parts;
+    const int64_t b = cut_of(rows, beams, num_out, vectors_of(vocab, false)).parts;
     return 256 + (size_t)rows * (a > b ? a : b) * (sizeof(PartHead) + 8 * (size_t)num_out);
 }
 
@@ -667,19 +908,30 @@ extern "C" pva_status pva_beam_select(const void* logits, int64_t row_stride, in
     a.vocab = vocab;
     a.k = num_out;
     a.end_token = finished || out_finished ? end_token : -1;
-    a.parts = parts_of(rows, beams, num_out, vectors);
-    a.per = (int32_t)((vectors + a.parts - 1) / a.parts);
+    const Cut c = cut_of(rows, beams, num_out, vectors);
+    a.tiles = (int32_t)c.tiles;
+    a.per = (int32_t)c.per;
+    a.parts = (int32_t)c.parts;
     a.heads = reinterpret_cast<PartHead*>(workspace);
     a.lists = reinterpret_cast<u64*>(a.heads + rows * a.parts);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     const size_t smem = (size_t)beams * a.parts * num_out * 20;
-    if (cudaFuncSetAttribute(join_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             kJoin * kJoinEach * 20) != cudaSuccess)
-        return PVA_ERR_CUDA;
-    const dim3 grid((unsigned)(rows * a.parts));
+    a.whole = (int32_t)c.whole;
+    const dim3 grid((unsigned)(c.whole ? rows * c.whole : (rows * c.tiles + c.per - 1) / c.per));
     cudaError_t e = f32 ? launch_after(scan_kernel<true>, grid, kScan, 0, st, a)
                         : launch_after(scan_kernel<false>, grid, kScan, 0, st, a);
-    if (e == cudaSuccess) e = launch_after(join_kernel, dim3((unsigned)num_groups), kJoin, smem, st, a);
+    if (e == cudaSuccess) {
+        const int total = (int)(beams * c.parts * num_out);
+        const dim3 groups((unsigned)num_groups);
+        if (total <= kJoin) {
+            const int threads = total <= 64 ? 64 : (total + 31) / 32 * 32;  // (a thread for every beam)
+            e = launch_after(join_kernel<1>, groups, threads, smem, st, a);
+        } else {
+            e = cudaFuncSetAttribute(join_kernel<kJoinEach>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     kJoin * kJoinEach * 20);
+            if (e == cudaSuccess) e = launch_after(join_kernel<kJoinEach>, groups, kJoin, smem, st, a);
+        }
+    }
     return e == cudaSuccess ? PVA_OK : PVA_ERR_CUDA;
 }
 
