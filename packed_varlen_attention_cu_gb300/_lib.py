@@ -175,8 +175,8 @@ def lib() -> ctypes.CDLL:
         L.pva_beam_select.argtypes = [P, i64, i32, i32, i32, i32, i32, P, P, P, i32, P, P, P, P, P, P,
                                       sz, P]
         L.pva_beam_reorder.restype = ctypes.c_int
-        L.pva_beam_reorder.argtypes = [P, i32, i32, CP, i32, P, i64, i32, P, ctypes.POINTER(StateDesc),
-                                       i32, P, P]
+        # (arrays of structs, or their bytes one after the other)
+        L.pva_beam_reorder.argtypes = [P, i32, i32, P, i32, P, i64, i32, P, P, i32, P, P]
         L.pva_cache_status.restype = ctypes.c_int
         L.pva_cache_status.argtypes = [P, ctypes.POINTER(i32), P]
         L.pva_debug_withhold_kv_load.restype = None

@@ -7,6 +7,7 @@ kernels.  PyTorch supplies device memory and streams.
 from __future__ import annotations
 
 import ctypes
+import struct
 from typing import Optional, Sequence
 
 import numpy as np
@@ -431,6 +432,7 @@ class KVCache:
         self.device, self.index = k.device, k.get_device()
         self.desc = _lib.CacheDesc(self.kind, heads, self.head_dim, page, pages, _ptr(k), _ptr(v),
                                    _ptr(k_scales), _ptr(v_scales))
+        self.raw = bytes(self.desc)  # for calls that take the caches of several layers
 
     @classmethod
     def alloc(cls, num_pages: int, num_kv_heads: int, head_dim: int, page_size: int = 64,
@@ -659,8 +661,7 @@ def beam_reorder(parents: torch.Tensor, caches: Sequence[KVCache] = (),
         if page_table.dtype is not _I32 or page_table.get_device() != dev or page_table.dim() != 2 or \
                 page_table.shape[0] != rows:
             raise ValueError(f"page_table: an int32 tensor [groups * beams, pages] on cuda:{dev} is needed")
-        width = page_table.shape[1]
-        stride = width
+        width = stride = page_table.shape[1]
         if not page_table.is_contiguous():
             stride, one = page_table.stride()
             _need(one == 1 or width <= 1, "page_table: rows must be contiguous")
@@ -670,24 +671,34 @@ def beam_reorder(parents: torch.Tensor, caches: Sequence[KVCache] = (),
         for c in caches:
             if c.index != dev:
                 raise ValueError(f"a cache is on cuda:{c.index}, the call's tensors on cuda:{dev}")
-        descs = (_lib.CacheDesc * n)(*[c.desc for c in caches])
-    m, held = len(states), None
-    if m:
-        held = (_lib.StateDesc * m)()
-        for d, t in zip(held, states):
-            if t.get_device() != dev or t.dim() < 1 or t.shape[0] != rows or (rows and not t[0].is_contiguous()):
-                raise ValueError(f"states: tensors [groups * beams, ...] of contiguous rows on cuda:{dev} are needed")
-            size = t.element_size()
-            d.row_bytes = t.numel() // rows * size if rows else 0
-            d.row_stride = t.stride(0) * size if rows > 1 else d.row_bytes
-            if d.row_stride < d.row_bytes:
-                raise ValueError("states: rows overlap")
-            d.data = t.data_ptr()
+        descs = b"".join([c.raw for c in caches])
     rc = (_lib._lib or lib()).pva_beam_reorder(
-        parents.data_ptr(), groups, beams, descs, n, table, stride, width, lens, held, m,
+        parents.data_ptr(), groups, beams, descs, n, table, stride, width, lens,
+        b"".join([_state(t, rows, dev) for t in states]) if states else None, len(states),
         None if status is None else _ints(status, 1, "status", dev), _queue(stream, dev))
     if rc:
         check("pva_beam_reorder", rc)
+
+
+_STATE = struct.Struct("Pqq")  # pva_state_desc
+
+
+def _state(t: torch.Tensor, rows: int, dev: int) -> bytes:
+    """The bytes of the pva_state_desc of a tensor [rows, ...] of contiguous rows."""
+    if t.get_device() != dev or t.dim() < 1 or t.shape[0] != rows:
+        raise ValueError(f"states: tensors [groups * beams, ...] of contiguous rows on cuda:{dev} are needed")
+    if rows == 0:
+        return _STATE.pack(t.data_ptr(), 0, 0)
+    if t.is_contiguous():
+        size = t.numel() // rows * t.element_size()
+        return _STATE.pack(t.data_ptr(), size, size)
+    if not t[0].is_contiguous():
+        raise ValueError("states: rows must be contiguous")
+    size = t[0].numel() * t.element_size()
+    stride = t.stride(0) * t.element_size() if rows > 1 else size
+    if stride < size:
+        raise ValueError("states: rows overlap")
+    return _STATE.pack(t.data_ptr(), size, stride)
 
 
 def cache_status(status: torch.Tensor, stream=None) -> int:

@@ -685,9 +685,9 @@ int64_t vectors_of(int32_t vocab, bool f32) {  // of a row that starts anywhere
 // ---------------------------------------------------------------- reordering
 
 constexpr int kMove = 256;            // threads of a CTA
-constexpr int kStage = 6144;          // bytes of a warp's staging buffer
+constexpr int kStage = 8192;          // bytes of a warp's staging buffer
 constexpr int kLaunchCaches = 64, kLaunchStates = 16;
-constexpr int kPiece = 16384;         // bytes of a row that a warp takes at a time, at most
+constexpr int kPiece = 8192;          // bytes of a row that a warp takes at a time, at most
 
 struct MoveState {
     uint8_t* data;
@@ -798,10 +798,19 @@ __global__ void __launch_bounds__(kMove) move_kernel(const __grid_constant__ Mov
                 if (!to || !at(p)) continue;
                 to += (u0 << shift);
                 const uint8_t* got = stage + ((__popcll(source & ((1ull << p) - 1)) * run) << shift);
-                if (wide)
-                    for (int i = lane; i < m; i += 32)
-                        reinterpret_cast<uint4*>(to)[i] = reinterpret_cast<const uint4*>(got)[i];
-                else
+                if (wide) {
+                    uint4* out = reinterpret_cast<uint4*>(to);
+                    const uint4* in = reinterpret_cast<const uint4*>(got);
+                    int i = lane;
+                    for (; i + 96 < m; i += 128) {  // (four at a time: one by one they wait for shared memory)
+                        const uint4 a0 = in[i], a1 = in[i + 32], a2 = in[i + 64], a3 = in[i + 96];
+                        out[i] = a0;
+                        out[i + 32] = a1;
+                        out[i + 64] = a2;
+                        out[i + 96] = a3;
+                    }
+                    for (; i < m; i += 32) out[i] = in[i];
+                } else
                     for (int i = lane; i < m; i += 32)
                         reinterpret_cast<uint32_t*>(to)[i] = reinterpret_cast<const uint32_t*>(got)[i];
             }
