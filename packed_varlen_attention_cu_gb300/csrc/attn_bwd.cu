@@ -34,6 +34,7 @@
 
 #include "../../include/pva.h"
 #include "common.h"
+#include "launch.cuh"
 #include "ptx.cuh"
 #include "tma_map.h"
 #include "unit_feed.cuh"
@@ -101,6 +102,7 @@ struct BShared {
 // ------------------------------------------------------------ D = rowsum(dO O)
 // 8 threads per (row, head), 16 bytes each per step.
 __global__ void __launch_bounds__(256) bwd_pre_kernel(const BwdParams p) {
+    let_next_start();
     const int64_t rows = (int64_t)p.q_tokens * p.hq;
     const int sub = threadIdx.x & 7;
     for (int64_t r = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 3;
@@ -228,6 +230,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const WlHeader* h = reinterpret_cast<const WlHeader*>(p.wl);
     int32_t* err_word = const_cast<int32_t*>(&h->error);
+    // This kernel may start while the one that makes D still runs.  Once it has ended, the kernel of
+    // dK and dV may start wherever this one leaves a multiprocessor free: it reads nothing that this
+    // one writes, and ends after it (see there).
+    wait_previous();
+    let_next_start();
     if (h->error != 0) return;
     // the worklist's dispatch: static per-CTA lists of `units`, or (dynamic)
     // ranks of `dorder` claimed at run time from the worklist's counter
@@ -680,6 +687,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     const WlHeader* h = reinterpret_cast<const WlHeader*>(p.wl);
     const BwdHeader* bh = reinterpret_cast<const BwdHeader*>(p.plan);
     int32_t* err_word = const_cast<int32_t*>(&h->error);
+    // This kernel may run beside that of dQ, which began only when all before it had ended.  No block
+    // leaves before dQ is done, so that the end of this kernel is the end of both.
+    struct EndAfterPrevious {
+        __device__ ~EndAfterPrevious() { wait_previous(); }
+    } end_after;
     if (h->error != 0) return;
     if (bh->magic != kBwdMagic || bh->hq != p.hq || bh->hkv != p.hkv ||
         bh->q_tokens != p.q_tokens || bh->k_tokens != p.k_tokens || bh->error != 0) {
@@ -1155,9 +1167,13 @@ pva_status launch_bwd(const CUtensorMap& mq, const CUtensorMap& mk, const CUtens
         cudaFuncSetAttribute(kk, cudaFuncAttributeMaxDynamicSharedMemorySize, BCfg<D>::kSmemKv) !=
             cudaSuccess)
         return PVA_ERR_CUDA;
-    kq<<<bp.num_ctas, kThreads, BCfg<D>::kSmemDq, st>>>(mq, mk64, mv64, mdo, bp);
-    kk<<<dkdv_ctas, kThreads, BCfg<D>::kSmemKv, st>>>(mq64, mk, mv, mdo64, bp);
-    return cudaGetLastError() == cudaSuccess ? PVA_OK : PVA_ERR_CUDA;
+    if (cudaGetLastError() != cudaSuccess ||
+        launch_after(kq, dim3(bp.num_ctas), kThreads, BCfg<D>::kSmemDq, st, mq, mk64, mv64, mdo, bp) !=
+            cudaSuccess ||
+        launch_after(kk, dim3(dkdv_ctas), kThreads, BCfg<D>::kSmemKv, st, mq64, mk, mv, mdo64, bp) !=
+            cudaSuccess)
+        return PVA_ERR_CUDA;
+    return PVA_OK;
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
