@@ -8,7 +8,7 @@ import numpy as np
 import pytest
 import torch
 
-from cache_util import U16, U32, Problem, check_attention
+from cache_util import U16, U32, Problem, check_attention, pack, quantise, values
 from gpu_util import compare, to_np
 from packed_varlen_attention_cu_gb300 import api
 from test_gpu_bwd import REL_L2, _check
@@ -365,6 +365,85 @@ def test_rows_see_the_whole_source(int4, hq, hkv, d, page, fp32):
     check_attention(p, out, lse, p.attend(), f"{int4} {page}")
     t = int(p.cu[-1])
     assert bool(torch.isnan(out[t:]).all()) and bool(torch.isnan(lse[:, t:]).all())
+
+
+@pytest.mark.parametrize("int4", [False, True])
+@pytest.mark.parametrize("hq,hkv,d,most", [(4, 2, 128, 8), (8, 2, 128, 4), (8, 2, 64, 7), (8, 2, 128, 12), (14, 2, 64, 11), (4, 4, 64, 60),
+                                           (16, 1, 128, 9)])
+@pytest.mark.parametrize("page", [16, 32, 256])
+def test_many_rows(int4, hq, hkv, d, most, page):
+    """9 to 144 rows a kv head: every variant that divides rows over warps, sources around tiles of 64 keys, cut over
+    CTAs and whole, without keys, without rows."""
+    lens = [64, 1, 0, 65, 3000, 129, 15, 16, 17, 192, 10000, 63]
+    news = [most, 1, most, 2, most, 0, most, 3, 1, most, most, most]
+    p = Source(lens, news, hq, hkv, d, page, int4, seed=d + page + most, spare_rows=1, strided=page == 32)
+    status = word()
+    out, lse = over_cache(p, status=status, fp32=page == 256, strided=page == 32)
+    assert api.cache_status(status) == 0
+    check_attention(p, out, lse, p.attend(), f"{int4} {hq}/{hkv} {most}")
+    assert bool(torch.isnan(out[-1]).all()) and bool(torch.isnan(lse[:, -1]).all())
+    again = over_cache(p, fp32=page == 256, strided=page == 32)
+    assert torch.equal(out[:-1], again[0][:-1]) and torch.equal(lse[:, :-1], again[1][:, :-1])
+
+
+@pytest.mark.parametrize("int4", [False, True])
+@pytest.mark.parametrize("most", [5, 12])
+def test_many_rows_with_missing_pages(int4, most):
+    p = Source([200, 100, 640], [most, 3, most], 8, 2, 128, 16, int4, seed=8)
+    p.table[0, 2] = p.table[2, 4] = p.table[2, 5] = -1
+    p.table[1, :] = 10 ** 6
+    status = word()
+    out, lse = over_cache(p, status=status)
+    assert api.cache_status(status) == 300
+    p.table[1, :] = -1
+    check_attention(p, out, lse, p.attend())
+
+
+@pytest.mark.parametrize("int4", [False, True])
+def test_long_sources_of_many_rows_have_no_bias(int4):
+    """Equal weights over values of mean 1: sums of 40000 products that all go one way."""
+    p = Source([40000], [6], 8, 2, 64, 64, int4, seed=9)
+    for x in "v":
+        rows = p.rows[x] * 0.05 + 1
+        if int4:
+            code, scale, low = quantise(rows.float().bfloat16())
+            p.v, p.v_scales = pack(code), torch.stack((scale, low), -1).bfloat16()
+            p.rows[x] = values(code, scale, low)
+        else:
+            p.v = rows.bfloat16()
+            p.rows[x] = p.v.double()
+    p.v_scales = p.v_scales.nan_to_num() if int4 else None
+    p.wide = None
+    p.q = torch.zeros_like(p.q)
+    out, lse = over_cache(p, fp32=True)
+    o, l, _, _ = p.attend()
+    # weights are 1 (exact in bf16; with 4 bits times the scale: 2^-9 of 8 scales, averaged over 40000 random codes), a
+    # tile's sum of up to eight products rounded towards 0 (2^-21) and about 300 additions of fp32 a piece, joined
+    tol = 2.0 ** -20 + (8 * 2.0 ** -9 * 0.05 * 8 / 15 / 40000 ** 0.5 * 4 if int4 else 0) + 64 * U32
+    off = (out.double().cpu() - o).abs().mean()
+    assert off <= tol, (off, tol)
+
+
+@pytest.mark.parametrize("int4", [False, True])
+def test_scores_and_values_that_are_not_finite(int4):
+    """A NaN among the keys that rows see makes their results NaN, in other sequences nothing changes; weights of 0 meet
+    values that are not finite."""
+    p = Source([100, 90, 80], [5, 5, 5], 8, 2, 128, 16, int4, seed=10)
+    o, l, e, le = p.attend()
+    cache = on_gpu(p)
+    at = int(p.table[1, 2])
+    if int4:
+        cache.k_scales[at, 0, 3, 0, 1] = math.nan
+    else:
+        cache.k[at, 0, 3, 7] = math.nan
+    out, lse = over_cache(p, cache=cache)
+    bad = torch.zeros_like(l, dtype=torch.bool)
+    bad[:4, 5:10] = True  # the heads of kv head 0, sequence 1
+    assert bool(torch.isnan(lse.cpu()[bad]).all()) and bool(torch.isnan(out.cpu()[bad.t()]).all())
+    l2, o2 = l.clone(), o.clone()
+    fin = ~bad
+    assert bool(((lse.cpu().double() - l).abs()[fin] <= le[fin]).all())
+    assert bool(((out.cpu().double() - o).abs()[fin.t()] <= e[fin.t()]).all())
 
 
 @pytest.mark.parametrize("int4", [False, True])
