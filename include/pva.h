@@ -471,10 +471,11 @@ pva_status pva_cache_attn(const pva_cache_desc* cache, const pva_cache_batch* ba
 /* Cross attention over the cache: every row of a sequence sees all of its kv_lens cached
  * keys (a source's; rows are beams, or any tokens that answer about it), none of which is
  * the row's own.  A row more than kv_lens counts is no failure, and kv_lens = 0 gives O = 0
- * and LSE = -inf.  A source is read once for its rows and heads of a group, 16 rows at a time
- * (8 with 4 bits), so rows of a source belong into one sequence of the batch.  Otherwise as
+ * and LSE = -inf.  A source is read once for its rows and heads of a group, up to 64 of
+ * them, so rows of a source belong into one sequence of the batch.  Otherwise as
  * pva_cache_attn, workspace (pva_cache_attn_bytes) and values too; a slot whose position has
- * no page is left out for all rows. */
+ * no page is left out for all rows.  With more than 32 rows of a kv head, or more than 16
+ * with 4 bits, weights have 8 bits in the products. */
 pva_status pva_cache_cross_attn(const pva_cache_desc* cache, const pva_cache_batch* batch,
                                 const void* q, int64_t q_stride, int32_t num_q_heads,
                                 int32_t max_new, float softmax_scale, void* out,

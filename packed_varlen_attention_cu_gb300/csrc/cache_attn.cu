@@ -929,7 +929,7 @@ pva_status cache_attn_impl(const pva_cache_desc* cache, const pva_cache_batch* b
     const int64_t rows = (int64_t)a.group * (batch->cu_new ? max_new : 1);
     uint8_t* ws = reinterpret_cast<uint8_t*>(workspace);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (cross && rows > (cache->kind == PVA_CACHE_BF16 ? kRowsMinBf16 : kRowsMinInt4))
+    if (cross && rows > kRowsMin)
         return launch_many_rows(cache->kind, d, rows, a, ws, s);
     if (cache->kind == PVA_CACHE_BF16)
         return d == 128 ? launch_rows<128, PVA_CACHE_BF16>(rows, a, ws, s)

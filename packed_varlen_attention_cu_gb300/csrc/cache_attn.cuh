@@ -354,10 +354,10 @@ inline cudaError_t launch_join(const AttnArgs& a, cudaStream_t st) {
 
 }  // namespace
 
-// cache_rows.cu: cross attention of `rows` > kRowsMin rows of a kv head.
+// cache_rows.cu: cross attention of more than kRowsMin rows of a kv head.
 pva_status launch_many_rows(int32_t kind, int32_t head_dim, int64_t rows, const AttnArgs& a, uint8_t* ws,
                             cudaStream_t st);
-constexpr int kRowsMinBf16 = 16, kRowsMinInt4 = 8;
+constexpr int kRowsMin = 16;
 // Rows of an item in the workspace.
 inline int workspace_rows(int64_t rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
 

@@ -3,13 +3,15 @@
 //
 // The formulas and the transposed products are those of cache_attn.cu.  There every warp streams keys
 // of its own for all rows of an item, 16 of them at most (8 with 4 bits), and an item more reads K and V
-// again: 32 rows of a bf16 cache took twice its bytes' time, 48 rows three times.  Here the four warps
+// again: 32 rows of a bf16 cache took twice its bytes' time, 48 rows three times (and so still goes up to 16
+// rows: with 4 bits 16 rows took 137 us here against 133).  Here the four warps
 // of a CTA share each tile of 64 keys and divide the rows, up to 64, between them, so K and V are read
 // once.  4-bit tiles are expanded in shared memory once for all rows: masks alone make the codes of K
 // numbers (subnormal bf16, see there), those of V are taken around their middle, code - 8, so that
 // sums over a long context have no bias; scales stay apart, on the scores and on the weights.
 //
-// With up to 16 or 32 rows of a 4-bit cache two warps have rows, and the pairs divide the keys of a
+// With 4 bits and up to 32 rows two warps have all rows, 16 each (a warp's K and V fragments then serve
+// twice the products: 191 against 202 us with four warps of 8 rows), and the pairs divide the keys of a
 // tile; their sums meet at the item's end.
 #include "cache_attn.cuh"
 
@@ -60,7 +62,8 @@ __global__ void __launch_bounds__(128, Sh::kCtas) rows_kernel(const AttnArgs a) 
     constexpr int G = Sh::G, T = D / 16, KEYS = Sh::kKeys, ROWB = Sh::kRowBytes, JP = Sh::kPitch;
     constexpr bool INT4 = Sh::kInt4;
     constexpr int GA = INT4 ? G : 1;   // groups with products of their own
-    constexpr int PP = INT4 ? G : 2;   // operands made of a weight: one a group, or two bf16 numbers
+    constexpr bool TWO = !INT4 && NT == 1;  // weights as two bf16 numbers
+    constexpr int PP = INT4 ? G : TWO ? 2 : 1;  // operands made of a weight
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ float join_m[WK][R], join_l[WK][R];
     wait_previous();
@@ -323,7 +326,10 @@ __global__ void __launch_bounds__(128, Sh::kCtas) rows_kernel(const AttnArgs a) 
                                 }
                             }
                     }
-                    // ---- weights as operands.  bf16: the sum of two bf16 numbers, 16 of a weight's bits.
+                    // ---- weights as operands.  bf16, up to 32 rows: the sum of two bf16 numbers, 16 of a
+                    // weight's bits, whose products hide behind HBM.  With more rows the tensor cores are
+                    // half busy, and one number (2^-9 of each weight, about what the bf16 result loses
+                    // again) takes 48 rows of 128 dims from 253 to 197 us, 56 of 64 dims from 128 to 102.
                     // 4 bits: weight * scale as one number (2^-9 of scale * |code - 8|, which is no larger
                     // than the values); weight * (low + 8 scale) stays in fp32.
                     uint32_t pf[Z][PP][NT][2];
@@ -354,7 +360,7 @@ __global__ void __launch_bounds__(128, Sh::kCtas) rows_kernel(const AttnArgs a) 
                                 } else {
                                     const uint32_t hi = pack2(p[0], p[1]);
                                     pf[z][0][nt][y] = transpose8(hi);
-                                    pf[z][PP - 1][nt][y] = transpose8(pack2(p[0] - lo_f(hi), p[1] - hi_f(hi)));
+                                    if (TWO) pf[z][PP - 1][nt][y] = transpose8(pack2(p[0] - lo_f(hi), p[1] - hi_f(hi)));
                                 }
                             }
                     }
@@ -373,7 +379,7 @@ __global__ void __launch_bounds__(128, Sh::kCtas) rows_kernel(const AttnArgs a) 
                             for (int nt = 0; nt < NT; ++nt) {
                                 if (z == 0) mma0(y[nt], f, pf[z][gr][nt][0], pf[z][gr][nt][1]);
                                 else mma(y[nt], f, pf[z][gr][nt][0], pf[z][gr][nt][1]);
-                                if (!INT4) mma(y[nt], f, pf[z][PP - 1][nt][0], pf[z][PP - 1][nt][1]);
+                                if (TWO) mma(y[nt], f, pf[z][PP - 1][nt][0], pf[z][PP - 1][nt][1]);
                             }
                         }
 #pragma unroll
@@ -490,9 +496,7 @@ pva_status launch_kind(int32_t kind, int64_t rows, const AttnArgs& a, uint8_t* w
     constexpr int B = PVA_CACHE_BF16, I = PVA_CACHE_INT4;
     if (kind == B)
         return rows <= 32 ? launch<Rows<D, B, 1, 4>, B>(a, ws, st) : launch<Rows<D, B, 2, 4>, B>(a, ws, st);
-    return rows <= 16   ? launch<Rows<D, I, 1, 2>, I>(a, ws, st)
-           : rows <= 32 ? launch<Rows<D, I, 2, 2>, I>(a, ws, st)
-                        : launch<Rows<D, I, 2, 4>, I>(a, ws, st);
+    return rows <= 32 ? launch<Rows<D, I, 2, 2>, I>(a, ws, st) : launch<Rows<D, I, 2, 4>, I>(a, ws, st);
 }
 
 }  // namespace
