@@ -106,6 +106,16 @@ struct Unit {
     SubTile st[2];
 };
 
+// A slot of the unit ring: the unit as the producer found it, with its first run and that run's
+// slice.  Units of one key tile are bounded by the softmax role's chain, in which four dependent reads
+// of the worklist for every unit were 2 of 5.7 us (209 groups of short pairs, 16 heads).
+struct UnitSlot {
+    int32_t idx;  // -1: no more work
+    int32_t slice, lo, hi;
+    Unit u;
+    WlSlice s;
+};
+
 __device__ __forceinline__ Unit decode_unit(const WlUnit& u, const WlSeg* segs) {
     const WlSeg g = segs[u.seg];
     Unit r;
@@ -132,7 +142,7 @@ struct Shared {
     // C::kSplitP only: S read by the softmax (4 warp arrivals), PV complete (commit)
     uint64_t s_free[2], pv_done[2];
     uint64_t kv_full[8], kv_empty[8];
-    UnitRing<kURing> ur;  // the producer hands each unit's index to the other roles
+    UnitRing<kURing, UnitSlot> ur;  // the producer hands each unit to the other roles
     uint32_t tmem_base;
     int32_t abort_flag;
 };
@@ -293,11 +303,32 @@ __global__ void __launch_bounds__(kThreads, 1)
                 } else {
                     idx = ub + (int32_t)nu < ue ? ub + (int32_t)nu : -1;
                 }
-                uring_put(sh.ur, nu, idx);
-                if (idx < 0) break;
+                UnitSlot& slot = sh.ur.slot[nu % kURing];
+                slot.idx = idx;
+                if (idx < 0) {
+                    mbar_arrive(&sh.ur.full[nu % kURing]);
+                    break;
+                }
                 const WlUnit wu = ubase[idx];
+                WlRun first_run{0, 0, 0, 0};
+                if (wu.run_count > 0) first_run = runs[wu.run_begin];
                 const Unit u = decode_unit(wu, segs);
-                if (u.ntiles == 0) continue;
+                WlSlice first_slice{0, 0, 0, 0, 0, 0, 0, 0};
+                if (wu.run_count > 0) first_slice = slices[first_run.slice];
+                // Q goes out before the slice is here, and the slot after it: release, it is seen by
+                // the readers
+                auto publish = [&]() {
+                    slot.u = u;
+                    slot.slice = first_run.slice;
+                    slot.lo = first_run.lo;
+                    slot.hi = first_run.hi;
+                    slot.s = first_slice;
+                    mbar_arrive(&sh.ur.full[nu % kURing]);
+                };
+                if (u.ntiles == 0) {
+                    publish();
+                    continue;
+                }
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     if (i >= u.nsub || !live) break;
@@ -310,6 +341,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                                     u.st[i].q_row);
                     ++q_it[i];
                 }
+                publish();
+                if (!live) break;
                 // the next ring stage: the K tile of key row krow_k and/or the V tile of
                 // krow_v (-1: none)
                 auto load_stage = [&](int32_t krow_k, int32_t krow_v) {
@@ -339,10 +372,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // (K_0), (K_1, V_0), (K_2, V_1), ..., (V_{n-1})
                 int32_t pend_v = -1;
                 for (int32_t r = 0; r < u.run_count && live; ++r) {
-                    const WlRun run = runs[u.run_begin + r];
-                    const WlSlice s = slices[run.slice];
+                    const WlRun run = r == 0 ? first_run : runs[u.run_begin + r];
+                    const int32_t k_row0 = r == 0 ? first_slice.k_row0 : slices[run.slice].k_row0;
                     for (int32_t jt = run.lo; jt < run.hi && live; ++jt) {
-                        const int32_t krow = s.k_row0 + jt * 128;
+                        const int32_t krow = k_row0 + jt * 128;
                         if (C::kSplitP) {
                             load_stage(krow, pend_v);
                             pend_v = krow;
@@ -434,15 +467,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ++s_used;
             };
             for (uint32_t nu = 0; live; ++nu) {
-                int32_t idx;
-                live = uring_get_warp(sh.ur, nu, idx, abort_flag, err_word, kErrTimeoutBase + 14,
-                                      kWaitNs);
-                if (!live || idx < 0) break;
-                const WlUnit wu = ubase[idx];
-                const Unit u = decode_unit(wu, segs);
-                const int32_t n = u.ntiles;
+                live = uring_wait_warp(sh.ur, nu, abort_flag, err_word, kErrTimeoutBase + 14, kWaitNs);
+                if (!live) break;
+                const volatile UnitSlot& slot = sh.ur.slot[nu % kURing];
+                const int32_t idx = slot.idx, n = slot.u.ntiles, nsub = slot.u.nsub;
+                uring_release_warp(sh.ur, nu);
+                if (idx < 0) break;
                 if (n == 0) continue;
-                const bool mine = i < u.nsub;
+                const bool mine = i < nsub;
                 if (mine) {
                     live = mbar_wait_warp(&sh.q_full[i], q_it & 1, abort_flag, err_word,
                                           kErrTimeoutBase + 3, kWaitNs);
@@ -510,16 +542,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             } else {
             for (uint32_t nu = 0; live; ++nu) {
-                int32_t idx;
-                live = uring_get_warp(sh.ur, nu, idx, abort_flag, err_word, kErrTimeoutBase + 14,
-                                      kWaitNs);
-                if (!live || idx < 0) break;
-                const WlUnit wu = ubase[idx];
-                const Unit u = decode_unit(wu, segs);
-                const int32_t n = u.ntiles;
+                live = uring_wait_warp(sh.ur, nu, abort_flag, err_word, kErrTimeoutBase + 14, kWaitNs);
+                if (!live) break;
+                const volatile UnitSlot& slot = sh.ur.slot[nu % kURing];
+                const int32_t idx = slot.idx, n = slot.u.ntiles, nsub = slot.u.nsub;
+                uring_release_warp(sh.ur, nu);
+                if (idx < 0) break;
                 if (n == 0) continue;
-                const bool mine = i < u.nsub;
-                const bool pair = u.nsub == 2;
+                const bool mine = i < nsub;
+                const bool pair = nsub == 2;
                 if (mine) {
                     live = mbar_wait_warp(&sh.q_full[i], q_it & 1, abort_flag, err_word,
                                      kErrTimeoutBase + 3, kWaitNs);
@@ -631,15 +662,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t tO = tmem + lane_base + 256 + i * 128;
         uint32_t s_cnt = 0, o_cnt = 0;
         bool live = true;
-        // The roles take unit n from the producer's ring; the softmax takes the
-        // next one before its epilogue (the producer published it once it had
-        // issued this unit's loads), so that the unit's description is read from
-        // global memory while the epilogue runs.
+        // The roles take unit n from the producer's ring.  The softmax keeps its slot until it has
+        // done with the unit's tiles.  pair_keys: under a CROSS mask, the key interval of this
+        // row in a shared tile, asked for as soon as the unit is known.
         int32_t idx = -1;
-        WlUnit wu;
+        uint32_t pair_keys = 0;
         auto take_unit = [&](uint32_t n) {
-            live = uring_get(sh.ur, n, idx, abort_flag, err_word, kErrTimeoutBase + 14, kWaitNs);
-            if (live && idx >= 0) wu = ubase[idx];
+            live = uring_wait(sh.ur, n, abort_flag, err_word, kErrTimeoutBase + 14, kWaitNs);
+            if (!live) return;
+            const UnitSlot& slot = sh.ur.slot[n % kURing];
+            idx = slot.idx;
+            if (CROSS && idx >= 0 && slot.u.run_count > 0 && slot.s.type == kSlicePackedCross)
+                pair_keys = reinterpret_cast<const uint16_t*>(slice_mask(p.wl, h, slot.s, slot.slice))[r];
         };
         // The epilogue of a unit (O / l and the LSE out) runs after the softmax of
         // the next unit's first kv tile has handed its P over, so that the tensor
@@ -788,7 +822,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         take_unit(0);
         for (uint32_t nu = 0; live && idx >= 0; ++nu) {
-            const Unit u = decode_unit(wu, segs);
+            const UnitSlot& slot = sh.ur.slot[nu % kURing];
+            const Unit& u = slot.u;
             if (i >= u.nsub || u.ntiles == 0) {
                 // this sub-tile has no tiles here: the pending epilogue runs now
                 if (!ACC && pend) epilogue();
@@ -796,6 +831,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // no key for these rows: O = 0, LSE = -inf, which a running
                 // (O, LSE) absorbs unchanged
                 if (i < u.nsub && !ACC) write_empty_rows(p, u.st[i], r, D);
+                uring_release(sh.ur, nu);
                 take_unit(nu + 1);
                 continue;
             }
@@ -813,16 +849,22 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             float m_used = -INFINITY, l_sum = 0.f;
             for (int32_t rr = 0; rr < u.run_count && live; ++rr) {
-                const WlRun run = runs[u.run_begin + rr];
-                const WlSlice s = slices[run.slice];
+                WlRun run{slot.slice, slot.lo, slot.hi, 0};
+                WlSlice s = slot.s;
+                if (rr > 0) {
+                    run = runs[u.run_begin + rr];
+                    s = slices[run.slice];
+                }
                 // allowed keys of this row, relative to the slice's first key:
                 // [lim_lo, lim_hi) (by the slice's MaskType; nothing for padding rows)
                 int64_t klo, khi;
                 if constexpr (CROSS) {  // whole slices and shared tiles only
                     klo = 0;
                     khi = s.k_len;
-                    if (s.type == kSlicePackedCross)
-                        packed_pair(slice_mask(p.wl, h, s, run.slice), r, klo, khi);
+                    if (s.type == kSlicePackedCross) {  // (a unit's only slice)
+                        klo = pair_keys & 255u;
+                        khi = pair_keys >> 8;
+                    }
                 } else {
                     slice_keys_of_query<false>(s, q_pos, klo, khi,
                                                slice_mask<false>(p.wl, h, s, run.slice));
@@ -835,6 +877,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int32_t kt0 = jt * 128;
                     const int32_t c_hi = min(128, lim_hi - kt0), c_lo = max(0, lim_lo - kt0);
                     const bool need_mask = __any_sync(0xffffffffu, c_lo > 0 || c_hi < 128);
+                    // CROSS: the 32-column chunks that some row of this warp may see.  In a tile that
+                    // short pairs share these are two or so of the four, and the others cost nothing.
+                    uint32_t seen = 15u;
+                    if (CROSS && need_mask) {
+                        const bool some = c_hi > c_lo;
+                        const int w_lo = __reduce_min_sync(0xffffffffu, some ? c_lo : 128);
+                        const int w_hi = __reduce_max_sync(0xffffffffu, some ? c_hi : 0);
+                        seen = w_hi > w_lo ? (15u >> (3 - ((w_hi - 1) >> 5))) & (15u << (w_lo >> 5)) : 0u;
+                    }
                     live = mbar_wait(&sh.s_full[i], s_cnt & 1, abort_flag, err_word,
                                      kErrTimeoutBase + 9, kWaitNs);
                     if (!live) break;
@@ -851,7 +902,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                         __syncwarp();
                         if (lane == 0) mbar_arrive(&sh.s_free[i]);
                     }
-                    if (need_mask) {
+                    if (CROSS && need_mask) {
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            // bit e: column 32 c + e is allowed
+                            const int lo = c_lo - 32 * c, hi = c_hi - 32 * c;
+                            const uint32_t allowed = (hi >= 32 ? ~0u : hi <= 0 ? 0u : (1u << hi) - 1u) &
+                                                     (lo <= 0 ? ~0u : lo >= 32 ? 0u : ~0u << lo);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                sr[c][e] = allowed >> e & 1 ? sr[c][e] : __float_as_uint(-INFINITY);
+                        }
+                    }
+                    if (!CROSS && need_mask) {
 #pragma unroll
                         for (int c = 0; c < 4; ++c)
 #pragma unroll
@@ -921,15 +984,20 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
                         part[c] = make_float2(0.f, 0.f);
+                        if (!CROSS || (seen >> c & 1)) {
 #pragma unroll
-                        for (int e = 0; e < 32; e += 2) {
-                            const float2 x = __ffma2_rn(
-                                make_float2(__uint_as_float(sr[c][e]), __uint_as_float(sr[c][e + 1])),
-                                sl2, nm2);
-                            const float p0 = ex2_approx(x.x);
-                            const float p1 = ex2_approx(x.y);
-                            part[c] = __fadd2_rn(part[c], make_float2(p0, p1));
-                            sr[c][e >> 1] = pack_bf16x2(p0, p1);
+                            for (int e = 0; e < 32; e += 2) {
+                                const float2 x = __ffma2_rn(
+                                    make_float2(__uint_as_float(sr[c][e]), __uint_as_float(sr[c][e + 1])),
+                                    sl2, nm2);
+                                const float p0 = ex2_approx(x.x);
+                                const float p1 = ex2_approx(x.y);
+                                part[c] = __fadd2_rn(part[c], make_float2(p0, p1));
+                                sr[c][e >> 1] = pack_bf16x2(p0, p1);
+                            }
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) sr[c][e] = 0u;
                         }
                         // the first half is announced after chunk 2's exponentials, so
                         // that the wait for its stores overlaps them
@@ -956,6 +1024,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             if (!live) break;
+            uring_release(sh.ur, nu);
             take_unit(nu + 1);
             if (!live) break;
             pend = true;

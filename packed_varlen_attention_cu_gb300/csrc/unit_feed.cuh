@@ -21,15 +21,16 @@
 
 namespace pva {
 
-template <int R>
+// T: what a slot holds: a unit's index, or all that the other roles need of it.
+template <int R, class T = int32_t>
 struct UnitRing {
     uint64_t full[R], empty[R];
-    int32_t slot[R];
+    T slot[R];
 };
 
 // `readers` arrivals free a slot.
-template <int R>
-__device__ __forceinline__ void uring_init(UnitRing<R>& r, uint32_t readers) {
+template <int R, class T>
+__device__ __forceinline__ void uring_init(UnitRing<R, T>& r, uint32_t readers) {
     for (int s = 0; s < R; ++s) {
         mbar_init(&r.full[s], 1);
         mbar_init(&r.empty[s], readers);
@@ -38,8 +39,8 @@ __device__ __forceinline__ void uring_init(UnitRing<R>& r, uint32_t readers) {
 
 // Producer: slot n (the n-th unit of this CTA) is free once every reader has
 // taken unit n - R.
-template <int R>
-__device__ __forceinline__ bool uring_wait_free(UnitRing<R>& r, uint32_t n,
+template <int R, class T>
+__device__ __forceinline__ bool uring_wait_free(UnitRing<R, T>& r, uint32_t n,
                                                 volatile int* abort_flag, int* err_word, int site,
                                                 uint64_t timeout_ns) {
     return mbar_wait(&r.empty[n % R], ((n / R) & 1) ^ 1, abort_flag, err_word, site, timeout_ns);
@@ -50,6 +51,28 @@ template <int R>
 __device__ __forceinline__ void uring_put(UnitRing<R>& r, uint32_t n, int32_t idx) {
     r.slot[n % R] = idx;
     mbar_arrive(&r.full[n % R]);  // release: the slot write is seen by the readers
+}
+
+// The n-th unit's slot, once it is published: for a whole converged warp, and for one thread.  It
+// stays as it is until released, once by each reader (warp or thread).
+template <int R, class T>
+__device__ __forceinline__ bool uring_wait_warp(UnitRing<R, T>& r, uint32_t n, volatile int* abort_flag,
+                                                int* err_word, int site, uint64_t timeout_ns) {
+    return mbar_wait_warp(&r.full[n % R], (n / R) & 1, abort_flag, err_word, site, timeout_ns);
+}
+template <int R, class T>
+__device__ __forceinline__ void uring_release_warp(UnitRing<R, T>& r, uint32_t n) {
+    __syncwarp();
+    mbar_arrive_elect(&r.empty[n % R]);
+}
+template <int R, class T>
+__device__ __forceinline__ bool uring_wait(UnitRing<R, T>& r, uint32_t n, volatile int* abort_flag,
+                                           int* err_word, int site, uint64_t timeout_ns) {
+    return mbar_wait(&r.full[n % R], (n / R) & 1, abort_flag, err_word, site, timeout_ns);
+}
+template <int R, class T>
+__device__ __forceinline__ void uring_release(UnitRing<R, T>& r, uint32_t n) {
+    mbar_arrive(&r.empty[n % R]);
 }
 
 // A whole converged warp takes the n-th unit (one arrival for the warp).
