@@ -545,7 +545,9 @@ typedef struct {
  *               a row whose last page, or its parent's, is outside [0, num_pages) keeps what
  *               that page holds (300)
  *   states      HOST array
- * Launches once for up to 64 caches and 16 states. */
+ * What moves is moved in place, so no state and no cache's pages may overlap another's, the
+ * parents, the table or kv_lens (an address that is listed twice is refused).  Launches once
+ * for up to 64 caches and 16 states. */
 pva_status pva_beam_reorder(const int32_t* parents, int32_t num_groups, int32_t beams,
                             const pva_cache_desc* caches, int32_t num_caches, int32_t* page_table,
                             int64_t table_stride, int32_t max_pages, const int32_t* kv_lens,

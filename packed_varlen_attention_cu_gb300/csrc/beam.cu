@@ -974,6 +974,18 @@ extern "C" pva_status pva_beam_reorder(const int32_t* parents, int32_t num_group
     }
     if (num_groups == 0 || (num_caches == 0 && num_states == 0)) return PVA_OK;
     if (!parents || (num_caches > 0 && (!kv_lens || (max_pages > 0 && !page_table)))) return PVA_ERR_INVALID_ARG;
+    // what is listed twice would be moved twice, by warps that do not meet
+    for (int32_t i = 0; i < num_caches && c0->num_pages > 0; ++i) {
+        const void *k = caches[i].k_pages, *v = caches[i].v_pages;
+        if (k == v) return PVA_ERR_INVALID_ARG;
+        for (int32_t j = 0; j < i; ++j)
+            if (k == caches[j].k_pages || k == caches[j].v_pages || v == caches[j].k_pages || v == caches[j].v_pages)
+                return PVA_ERR_INVALID_ARG;
+    }
+    for (int32_t i = 0; i < num_states; ++i)
+        for (int32_t j = 0; j < i; ++j)
+            if (states[i].data == states[j].data && states[i].row_bytes > 0 && states[j].row_bytes > 0)
+                return PVA_ERR_INVALID_ARG;
     MoveArgs a = {};
     a.parents = parents;
     a.status = status_dev;

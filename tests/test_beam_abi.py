@@ -70,6 +70,19 @@ def test_reorder_refuses_bad_caches(L, kw, code):
     assert reorder(L, caches=[cache(), cache(**kw)]) == code
 
 
+B = A + (1 << 20)
+
+
+@pytest.mark.parametrize("caches,states", [
+    ([cache(v_pages=A)], ()),                                               # one array for K and V
+    ([cache(v_pages=B), cache(v_pages=B + 4096)], ()),                      # two layers with the same K
+    ([cache(v_pages=B), cache(k_pages=B + 4096, v_pages=B)], ()),           # ... the same V
+    ([cache(v_pages=B), cache(k_pages=B + 4096, v_pages=A)], ()),           # ... K of one as V of the other
+    ([], [(A, 8, 8), (B, 8, 8), (A, 4, 8)]), ([], [(A, 16, 16), (A, 16, 16)])])
+def test_reorder_refuses_what_would_move_twice(L, caches, states):
+    assert reorder(L, caches=caches, states=states) == INVALID
+
+
 def test_nothing_to_reorder(L):
     assert reorder(L, groups=0, parents=None, table=None, lens=None) == 0
     assert reorder(L, caches=[], parents=None, table=None, lens=None) == 0
