@@ -84,14 +84,25 @@ struct BwdParams {
     float scale, scale_log2;
 };
 
+constexpr int kURing = 8;  // units the producer may run ahead
 constexpr int kLdSlots = 8;
 constexpr int kMaxStages = 12;
 
+// A slot of the unit ring of dK and dV: the unit as the producer found it, with its first slice and
+// the q tiles of that slice.
+struct KvSlot {
+    int32_t idx;  // -1: no more work
+    int32_t slice, qlo, qhi;
+    BwdUnit u;
+    WlSlice s;
+};
+
+template <class Slot>
 struct BShared {
     uint64_t a_full, a_empty, o_full, o_empty, done, done2;
     uint64_t s2_full[3], p2_full[3];  // per half-item tensor-memory buffer
     uint64_t r_full[kMaxStages], r_empty[kMaxStages];
-    UnitRing<8> ur;  // the producer hands each unit's index to the other roles
+    UnitRing<kURing, Slot> ur;  // the producer hands each unit to the other roles
     // bwd_dkdv: (LSE log2, D) of each half-item's 64 queries, staged ahead by a
     // loader warp (ld_full: 32 lane arrivals; ld_empty: one per element-wise warp)
     uint64_t ld_full[kLdSlots], ld_empty[kLdSlots];
@@ -177,7 +188,8 @@ __device__ __forceinline__ void store_zero_row(void* base, int64_t row_elem, boo
 // per use and reads every unit.  acc_issuers: the warps that commit o_full (the
 // ones whose MMAs write the accumulators).  item_warps: the element-wise warps
 // that work on each half-item (p2_full and ld_empty count one arrival each)
-__device__ __forceinline__ void init_barriers(BShared& sh, int stages, int elem_threads,
+template <class Slot>
+__device__ __forceinline__ void init_barriers(BShared<Slot>& sh, int stages, int elem_threads,
                                               int extra_readers, int issuers, int acc_issuers,
                                               int item_warps) {
     mbar_init(&sh.a_full, 1);
@@ -226,7 +238,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t* sQ = smem;
     uint8_t* sDO = smem + C::kTileBytes;
     uint8_t* sKV = smem + 2 * C::kTileBytes;
-    __shared__ BShared sh;
+    __shared__ BShared<UnitSlot> sh;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const WlHeader* h = reinterpret_cast<const WlHeader*>(p.wl);
     int32_t* err_word = const_cast<int32_t*>(&h->error);
@@ -267,17 +279,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem = sh.tmem_base;
     volatile int32_t* abort_flag = &sh.abort_flag;
 
-    // the two query sub-tiles of a unit, one after the other
-    auto sub_of = [&](const WlUnit& u, int i, int32_t& q_row, int32_t& nrows, int32_t& q_pos,
-                      int32_t& head) {
-        const WlSeg g = segs[u.seg];
-        const int32_t t = i == 0 ? u.t0 : u.t1;
-        q_row = g.q_row0 + t * 128;
-        nrows = min(128, g.q_len - t * 128);
-        q_pos = g.q_pos0 + t * 128;
-        head = i == 0 ? u.h0 : u.h1;
-    };
-
     if (warp == 0) {
         // ------------------------------------------------------- TMA producer
         if (lane == 0) {
@@ -298,26 +299,44 @@ __global__ void __launch_bounds__(kThreads, 1)
                 } else {
                     idx = ub + (int32_t)nu < ue ? ub + (int32_t)nu : -1;
                 }
-                uring_put(sh.ur, nu, idx);
-                if (idx < 0) break;
-                const WlUnit u = ubase[idx];
+                UnitSlot& slot = sh.ur.slot[nu % kURing];
+                slot.idx = idx;
+                if (idx < 0) {
+                    mbar_arrive(&sh.ur.full[nu % kURing]);
+                    break;
+                }
+                const WlUnit wu = ubase[idx];
+                WlRun first_run{0, 0, 0, 0};
+                if (wu.run_count > 0) first_run = runs[wu.run_begin];
+                const Unit u = decode_unit(wu, segs);
+                WlSlice first_slice{0, 0, 0, 0, 0, 0, 0, 0};
+                if (wu.run_count > 0) first_slice = slices[first_run.slice];
+                slot.u = u;
+                slot.slice = first_run.slice;
+                slot.lo = first_run.lo;
+                slot.hi = first_run.hi;
+                slot.s = first_slice;
+                mbar_arrive(&sh.ur.full[nu % kURing]);  // release: the readers see the slot
                 if (u.ntiles == 0) continue;
-                const int nsub = u.h1 >= 0 ? 2 : 1;
-                for (int i = 0; i < nsub && live; ++i) {
-                    int32_t q_row, nrows, q_pos, head;
-                    sub_of(u, i, q_row, nrows, q_pos, head);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {  // the two query sub-tiles, one after the other
+                    if (i >= u.nsub || !live) break;
                     live = mbar_wait(&sh.a_empty, (a_it & 1) ^ 1, abort_flag, err_word,
                                      kErrTimeoutBase + 21, kWaitNs);
                     if (!live) break;
                     mbar_arrive_expect_tx(&sh.a_full, 2 * C::kTileBytes);
                     for (int b = 0; b < D / 64; ++b) {
-                        tma_load_3d(sQ + b * 16384, &tmq, &sh.a_full, b * 64, head, q_row);
-                        tma_load_3d(sDO + b * 16384, &tmdo, &sh.a_full, b * 64, head, q_row);
+                        tma_load_3d(sQ + b * 16384, &tmq, &sh.a_full, b * 64, u.st[i].head, u.st[i].q_row);
+                        tma_load_3d(sDO + b * 16384, &tmdo, &sh.a_full, b * 64, u.st[i].head, u.st[i].q_row);
                     }
                     ++a_it;
                     for (int32_t rr = 0; rr < u.run_count && live; ++rr) {
-                        const WlRun run = runs[u.run_begin + rr];
-                        const WlSlice s = slices[run.slice];
+                        WlRun run = first_run;
+                        WlSlice s = first_slice;
+                        if (rr > 0) {
+                            run = runs[u.run_begin + rr];
+                            s = slices[run.slice];
+                        }
                         for (int32_t jt = run.lo; jt < run.hi && live; ++jt) {
                             const int32_t halves = min(128, s.k_len - jt * 128) > 64 ? 2 : 1;
                             for (int32_t hf = 0; hf < halves && live; ++hf) {
@@ -389,13 +408,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             return true;
         };
         for (uint32_t nu = 0; live; ++nu) {
-            int32_t idx;
-            live = uring_get_warp(sh.ur, nu, idx, abort_flag, err_word, kErrTimeoutBase + 30,
-                                  kWaitNs);
-            if (!live || idx < 0) break;
-            const WlUnit u = ubase[idx];
-            if (u.ntiles == 0) continue;
-            const int nsub = u.h1 >= 0 ? 2 : 1;
+            live = uring_wait_warp(sh.ur, nu, abort_flag, err_word, kErrTimeoutBase + 30, kWaitNs);
+            if (!live) break;
+            const volatile UnitSlot& slot = sh.ur.slot[nu % kURing];
+            const int32_t idx = slot.idx, ntiles = slot.u.ntiles, nsub = slot.u.nsub;
+            const int32_t run_begin = slot.u.run_begin, run_count = slot.u.run_count;
+            const WlRun first_run{slot.slice, slot.lo, slot.hi, 0};
+            const int32_t first_len = slot.s.k_len;
+            uring_release_warp(sh.ur, nu);
+            if (idx < 0) break;
+            if (ntiles == 0) continue;
             for (int i = 0; i < nsub && live; ++i) {
                 live = mbar_wait_warp(&sh.a_full, a_it & 1, abort_flag, err_word,
                                       kErrTimeoutBase + 23, kWaitNs);
@@ -408,11 +430,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 mma_commit_elect(&sh.a_empty);  // Q copied (warp 3 copies dO)
                 first = true;
-                for (int32_t rr = 0; rr < u.run_count && live; ++rr) {
-                    const WlRun run = runs[u.run_begin + rr];
-                    const WlSlice s = slices[run.slice];
+                for (int32_t rr = 0; rr < run_count && live; ++rr) {
+                    const WlRun run = rr > 0 ? runs[run_begin + rr] : first_run;
+                    const int32_t k_len = rr > 0 ? slices[run.slice].k_len : first_len;
                     for (int32_t jt = run.lo; jt < run.hi && live; ++jt) {
-                        const int32_t halves = min(128, s.k_len - jt * 128) > 64 ? 2 : 1;
+                        const int32_t halves = min(128, k_len - jt * 128) > 64 ? 2 : 1;
                         for (int32_t hf = 0; hf < halves && live; ++hf) {
                             const uint32_t st = it % C::kStagesDq;
                             live = mbar_wait_warp(&sh.r_full[st], (it / C::kStagesDq) & 1,
@@ -466,13 +488,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         constexpr uint32_t kIdescHalf = idesc_bf16_f32(128, 64, false);
         const uint32_t tDOA = tmem + 256 + D + D / 2;
         for (uint32_t nu = 0; live; ++nu) {
-            int32_t idx;
-            live = uring_get_warp(sh.ur, nu, idx, abort_flag, err_word, kErrTimeoutBase + 46,
-                                  kWaitNs);
-            if (!live || idx < 0) break;
-            const WlUnit u = ubase[idx];
-            if (u.ntiles == 0) continue;
-            const int nsub = u.h1 >= 0 ? 2 : 1;
+            live = uring_wait_warp(sh.ur, nu, abort_flag, err_word, kErrTimeoutBase + 46, kWaitNs);
+            if (!live) break;
+            const volatile UnitSlot& slot = sh.ur.slot[nu % kURing];
+            const int32_t idx = slot.idx, ntiles = slot.u.ntiles, nsub = slot.u.nsub;
+            const int32_t run_begin = slot.u.run_begin, run_count = slot.u.run_count;
+            const WlRun first_run{slot.slice, slot.lo, slot.hi, 0};
+            const int32_t first_len = slot.s.k_len;
+            uring_release_warp(sh.ur, nu);
+            if (idx < 0) break;
+            if (ntiles == 0) continue;
             for (int i = 0; i < nsub && live; ++i) {
                 live = mbar_wait_warp(&sh.a_full, a_it & 1, abort_flag, err_word,
                                       kErrTimeoutBase + 47, kWaitNs);
@@ -484,11 +509,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int k = 0; k < D / 16; ++k)
                     tmem_cp_elect(tDOA + k * 8, dDO + (k >> 2) * 1024 + (k & 3) * 2);
                 mma_commit_elect(&sh.a_empty);
-                for (int32_t rr = 0; rr < u.run_count && live; ++rr) {
-                    const WlRun run = runs[u.run_begin + rr];
-                    const WlSlice s = slices[run.slice];
+                for (int32_t rr = 0; rr < run_count && live; ++rr) {
+                    const WlRun run = rr > 0 ? runs[run_begin + rr] : first_run;
+                    const int32_t k_len = rr > 0 ? slices[run.slice].k_len : first_len;
                     for (int32_t jt = run.lo; jt < run.hi && live; ++jt) {
-                        const int32_t halves = min(128, s.k_len - jt * 128) > 64 ? 2 : 1;
+                        const int32_t halves = min(128, k_len - jt * 128) > 64 ? 2 : 1;
                         for (int32_t hf = 0; hf < halves && live; ++hf) {
                             const uint32_t st = it % C::kStagesDq;
                             const uint32_t b = gu & 1;
@@ -535,34 +560,70 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t tS = tmem + lane_base, tQ = tmem + lane_base + 256;
         uint32_t gu = 0, o_cnt = 0;
         bool live = true;
-        for (uint32_t nu = 0; live; ++nu) {
-            int32_t idx;
-            live = uring_get(sh.ur, nu, idx, abort_flag, err_word, kErrTimeoutBase + 30, kWaitNs);
-            if (!live || idx < 0) break;
-            const WlUnit u = ubase[idx];
-            const int nsub = u.h1 >= 0 ? 2 : 1;
+        // Unit n from the producer's ring, kept until this thread has done with its tiles: the (LSE, D)
+        // of its rows and, in a tile shared by pairs, the key interval of the row are asked for as soon
+        // as it is known, before the epilogue of the unit before it.
+        int32_t idx = -1;
+        uint32_t pair_keys = 0;
+        float lse_of[2], d_of[2];
+        auto take_unit = [&](uint32_t n) {
+            live = uring_wait(sh.ur, n, abort_flag, err_word, kErrTimeoutBase + 30, kWaitNs);
+            if (!live) return;
+            const UnitSlot& slot = sh.ur.slot[n % kURing];
+            idx = slot.idx;
+            if (idx < 0 || slot.u.ntiles == 0) return;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                lse_of[i] = -INFINITY;
+                d_of[i] = 0.f;
+                if (i < slot.u.nsub && r < slot.u.st[i].nrows) {
+                    const int64_t li = (int64_t)slot.u.st[i].head * p.q_tokens + slot.u.st[i].q_row + r;
+                    lse_of[i] = p.lse[li];
+                    d_of[i] = p.dvec[li];
+                }
+            }
+            if (slot.s.type == kSlicePackedCross)
+                pair_keys = reinterpret_cast<const uint16_t*>(slice_mask(p.wl, h, slot.s, slot.slice))[r];
+        };
+        take_unit(0);
+        for (uint32_t nu = 0; live && idx >= 0; ++nu) {
+            const UnitSlot& slot = sh.ur.slot[nu % kURing];
+            const int nsub = slot.u.nsub;
+            if (slot.u.ntiles == 0) {  // rows without keys: zero gradient
+                for (int i = 0; i < nsub; ++i) {
+                    const SubTile& st = slot.u.st[i];
+                    if (r < st.nrows)
+                        store_zero_row(p.dq, ((int64_t)(st.q_row + r) * p.hq + st.head) * D + wg * (D / 2),
+                                       p.grads_fp32, D / 2);
+                }
+                uring_release(sh.ur, nu);
+                take_unit(nu + 1);
+                continue;
+            }
+#pragma unroll 1
             for (int i = 0; i < nsub && live; ++i) {
-                int32_t q_row, nrows, q_pos0, head;
-                sub_of(u, i, q_row, nrows, q_pos0, head);
-                const bool valid = r < nrows;
-                const int64_t grow = ((int64_t)(q_row + r) * p.hq + head) * D;
-                if (u.ntiles == 0) {  // rows without keys: zero gradient
-                    if (valid) store_zero_row(p.dq, grow + wg * (D / 2), p.grads_fp32, D / 2);
-                    continue;
-                }
-                const int32_t q_pos = q_pos0 + r;
-                const int64_t li = (int64_t)head * p.q_tokens + q_row + r;
-                float lse2 = INFINITY, dd = 0.f;  // no key: every P is 0
-                if (valid) {
-                    const float l = p.lse[li];
-                    if (l != -INFINITY) lse2 = l * 1.4426950408889634f;
-                    dd = p.dvec[li];
-                }
-                for (int32_t rr = 0; rr < u.run_count && live; ++rr) {
-                    const WlRun run = runs[u.run_begin + rr];
-                    const WlSlice s = slices[run.slice];
+                const SubTile& st = slot.u.st[i];
+                const bool valid = r < st.nrows;
+                const int64_t grow = ((int64_t)(st.q_row + r) * p.hq + st.head) * D;
+                const int32_t q_pos = st.q_pos + r;
+                const float l = i == 0 ? lse_of[0] : lse_of[1];
+                const float lse2 = l == -INFINITY ? INFINITY : l * 1.4426950408889634f;  // no key: every P is 0
+                const float dd = i == 0 ? d_of[0] : d_of[1];
+                const int32_t run_count = slot.u.run_count;
+                for (int32_t rr = 0; rr < run_count && live; ++rr) {
+                    WlRun run{slot.slice, slot.lo, slot.hi, 0};
+                    WlSlice s = slot.s;
+                    if (rr > 0) {
+                        run = runs[slot.u.run_begin + rr];
+                        s = slices[run.slice];
+                    }
                     int64_t klo, khi;  // allowed keys of this row (slice-local)
-                    slice_keys_of_query(s, q_pos, klo, khi, slice_mask(p.wl, h, s, run.slice));
+                    if (s.type == kSlicePackedCross) {  // (a unit's only slice)
+                        klo = pair_keys & 255u;
+                        khi = pair_keys >> 8;
+                    } else {
+                        slice_keys_of_query<false>(s, q_pos, klo, khi, slice_mask<false>(p.wl, h, s, run.slice));
+                    }
                     const int32_t lim_hi = valid ? (int32_t)khi : 0;
                     const int32_t lim_lo = (int32_t)klo;
                     for (int32_t jt = run.lo; jt < run.hi && live; ++jt) {
@@ -621,6 +682,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 if (!live) break;
+                if (i + 1 == nsub) {
+                    uring_release(sh.ur, nu);
+                    take_unit(nu + 1);
+                    if (!live) break;
+                }
                 live = mbar_wait(&sh.o_full, o_cnt & 1, abort_flag, err_word,
                                  kErrTimeoutBase + 28, kWaitNs);
                 if (!live) break;
@@ -682,7 +748,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t* sK = smem;
     uint8_t* sV = smem + C::kTileBytes;
     uint8_t* sR = smem + 2 * C::kTileBytes;  // half-item stage x at x * 2 * kHalfBytes
-    __shared__ BShared sh;
+    __shared__ BShared<KvSlot> sh;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const WlHeader* h = reinterpret_cast<const WlHeader*>(p.wl);
     const BwdHeader* bh = reinterpret_cast<const BwdHeader*>(p.plan);
@@ -755,11 +821,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                     atomicCAS(err_word, 0, kErrBadWorklist);
                     idx = -1;
                 }
-                uring_put(sh.ur, rd, idx);
-                if (idx < 0) break;
+                KvSlot& slot = sh.ur.slot[rd % kURing];
+                slot.idx = idx;
+                if (idx < 0) {
+                    mbar_arrive(&sh.ur.full[rd % kURing]);
+                    break;
+                }
                 const BwdUnit u = bunits[idx];
+                const int32_t si = gsl[u.gbegin];
+                const WlSlice s = slices[si];
+                int32_t qlo0 = 0, qhi0 = 0;
+                if (u.cost > 1) bwd_q_span(s, u.kt, qlo0, qhi0, slice_mask(p.wl, h, s, si));
+                slot.u = u;
+                slot.slice = si;
+                slot.qlo = qlo0;
+                slot.qhi = qhi0;
+                slot.s = s;
+                mbar_arrive(&sh.ur.full[rd % kURing]);  // release: the readers see the slot
                 if (u.cost <= 1) continue;  // no query sees these keys
-                const WlSlice s = slices[gsl[u.gbegin]];
                 live = mbar_wait(&sh.a_empty, (a_it & 1) ^ 1, abort_flag, err_word,
                                  kErrTimeoutBase + 31, kWaitNs);
                 if (!live) break;
@@ -770,9 +849,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 ++a_it;
                 for (int32_t m = 0; m < u.gcount && live; ++m) {
-                    const WlSlice sm = slices[gsl[u.gbegin + m]];
-                    int32_t qlo, qhi;
-                    bwd_q_span(sm, u.kt, qlo, qhi, slice_mask(p.wl, h, sm, gsl[u.gbegin + m]));
+                    WlSlice sm = s;
+                    int32_t qlo = qlo0, qhi = qhi0;
+                    if (m > 0) {
+                        sm = slices[gsl[u.gbegin + m]];
+                        bwd_q_span(sm, u.kt, qlo, qhi, slice_mask(p.wl, h, sm, gsl[u.gbegin + m]));
+                    }
                     for (int32_t t = qlo; t < qhi && live; ++t) {
                         const int32_t nq = min(128, sm.q_len - t * 128);
                         const int32_t halves = nq > 64 ? 2 : 1;
@@ -864,22 +946,28 @@ __global__ void __launch_bounds__(kThreads, 1)
             return true;
         };
         for (uint32_t rd = 0; live; ++rd) {
-            int32_t idx;
-            live = uring_get_warp(sh.ur, rd, idx, abort_flag, err_word,
-                                  kErrTimeoutBase + (sdv ? 40 : 54), kWaitNs);
-            if (!live || idx < 0) break;
-            const BwdUnit u = bunits[idx];
-            if (u.cost <= 1) continue;
+            live = uring_wait_warp(sh.ur, rd, abort_flag, err_word, kErrTimeoutBase + (sdv ? 40 : 54), kWaitNs);
+            if (!live) break;
+            const volatile KvSlot& slot = sh.ur.slot[rd % kURing];
+            const int32_t idx = slot.idx, kt = slot.u.kt, gbegin = slot.u.gbegin, gcount = slot.u.gcount;
+            const bool none = slot.u.cost <= 1;
+            const int32_t qlo0 = slot.qlo, qhi0 = slot.qhi, q_len0 = slot.s.q_len;
+            uring_release_warp(sh.ur, rd);
+            if (idx < 0) break;
+            if (none) continue;
             live = mbar_wait_warp(&sh.a_full, a_it & 1, abort_flag, err_word,
                                   kErrTimeoutBase + 33 + site, kWaitNs);
             if (!live) break;
             first = true;
-            for (int32_t m = 0; m < u.gcount && live; ++m) {
-                const WlSlice sm = slices[gsl[u.gbegin + m]];
-                int32_t qlo, qhi;
-                bwd_q_span(sm, u.kt, qlo, qhi, slice_mask(p.wl, h, sm, gsl[u.gbegin + m]));
+            for (int32_t m = 0; m < gcount && live; ++m) {
+                int32_t qlo = qlo0, qhi = qhi0, q_len = q_len0;
+                if (m > 0) {
+                    const WlSlice sm = slices[gsl[gbegin + m]];
+                    bwd_q_span(sm, kt, qlo, qhi, slice_mask(p.wl, h, sm, gsl[gbegin + m]));
+                    q_len = sm.q_len;
+                }
                 for (int32_t t = qlo; t < qhi && live; ++t) {
-                    const int32_t nq = min(128, sm.q_len - t * 128);
+                    const int32_t nq = min(128, q_len - t * 128);
                     const uint32_t halves = nq > 64 ? 2 : 1;
                     for (int32_t hh = 0; hh < G && live; ++hh) {
                         for (uint32_t hf = 0; hf < halves && live; ++hf) {
@@ -940,22 +1028,30 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t li = 0;
         bool live = true;
         for (uint32_t rd = 0; live; ++rd) {
-            int32_t idx;
-            live = uring_get_warp(sh.ur, rd, idx, abort_flag, err_word, kErrTimeoutBase + 41,
-                                  kWaitNs);
-            if (!live || idx < 0) break;
-            const BwdUnit u = bunits[idx];
-            if (u.cost <= 1) continue;
-            for (int32_t m = 0; m < u.gcount && live; ++m) {
-                const WlSlice s = slices[gsl[u.gbegin + m]];
-                int32_t qlo, qhi;
-                bwd_q_span(s, u.kt, qlo, qhi, slice_mask(p.wl, h, s, gsl[u.gbegin + m]));
+            live = uring_wait_warp(sh.ur, rd, abort_flag, err_word, kErrTimeoutBase + 41, kWaitNs);
+            if (!live) break;
+            const volatile KvSlot& slot = sh.ur.slot[rd % kURing];
+            const int32_t idx = slot.idx, kt = slot.u.kt, gbegin = slot.u.gbegin, gcount = slot.u.gcount;
+            const int32_t kvh = slot.u.kvh;
+            const bool none = slot.u.cost <= 1;
+            const int32_t qlo0 = slot.qlo, qhi0 = slot.qhi, q_len0 = slot.s.q_len, q_row00 = slot.s.q_row0;
+            uring_release_warp(sh.ur, rd);
+            if (idx < 0) break;
+            if (none) continue;
+            for (int32_t m = 0; m < gcount && live; ++m) {
+                int32_t qlo = qlo0, qhi = qhi0, q_len = q_len0, q_row0 = q_row00;
+                if (m > 0) {
+                    const WlSlice s = slices[gsl[gbegin + m]];
+                    bwd_q_span(s, kt, qlo, qhi, slice_mask(p.wl, h, s, gsl[gbegin + m]));
+                    q_len = s.q_len;
+                    q_row0 = s.q_row0;
+                }
                 for (int32_t t = qlo; t < qhi && live; ++t) {
-                    const int32_t qrow0 = s.q_row0 + t * 128;
-                    const int32_t nq = min(128, s.q_len - t * 128);
+                    const int32_t qrow0 = q_row0 + t * 128;
+                    const int32_t nq = min(128, q_len - t * 128);
                     const uint32_t halves = nq > 64 ? 2 : 1;
                     for (int32_t hh = 0; hh < G && live; ++hh) {
-                        const int32_t head = u.kvh * G + hh;
+                        const int32_t head = kvh * G + hh;
                         for (uint32_t hf = 0; hf < halves && live; ++hf, ++li) {
                             const uint32_t slot = li % kLdSlots;
                             live = mbar_wait_warp(&sh.ld_empty[slot], ((li / kLdSlots) & 1) ^ 1,
@@ -995,29 +1091,51 @@ __global__ void __launch_bounds__(kThreads, 1)
                        tK = tmem + lane_base + 128 * NB + D;
         uint32_t gu = 0, o_cnt = 0, li = 0;
         bool live = true;
-        for (uint32_t rd = 0; live; ++rd) {
-            int32_t idx;
-            live = uring_get(sh.ur, rd, idx, abort_flag, err_word, kErrTimeoutBase + 40, kWaitNs);
-            if (!live || idx < 0) break;
-            const BwdUnit u = bunits[idx];
-            const WlSlice s0 = slices[gsl[u.gbegin]];  // the group's key range
-            const int32_t krows = min(128, s0.k_len - u.kt * 128);
+        // Unit n from the producer's ring, kept until this thread has done with its tiles.  In a tile
+        // shared by pairs the row interval of the key is asked for as soon as it is known, before the
+        // epilogue of the unit before it.
+        int32_t idx = -1;
+        uint32_t pair_rows = 0;
+        auto take_unit = [&](uint32_t x) {
+            live = uring_wait(sh.ur, x, abort_flag, err_word, kErrTimeoutBase + 40, kWaitNs);
+            if (!live) return;
+            const KvSlot& slot = sh.ur.slot[x % kURing];
+            idx = slot.idx;
+            if (idx >= 0 && slot.s.type == kSlicePackedCross)
+                pair_rows = reinterpret_cast<const uint16_t*>(slice_mask(p.wl, h, slot.s, slot.slice))[128 + kr];
+        };
+        take_unit(0);
+        for (uint32_t rd = 0; live && idx >= 0; ++rd) {
+            const KvSlot& slot = sh.ur.slot[rd % kURing];
+            const int32_t kt = slot.u.kt, kvh = slot.u.kvh;
+            const int32_t krows = min(128, slot.s.k_len - kt * 128);  // of the group's key range
             const bool kvalid = kr < krows;
-            const int64_t grow = ((int64_t)(s0.k_row0 + u.kt * 128 + kr) * p.hkv + u.kvh) * D;
-            if (u.cost <= 1) {  // keys no query sees: zero gradient
+            const int64_t grow = ((int64_t)(slot.s.k_row0 + kt * 128 + kr) * p.hkv + kvh) * D;
+            if (slot.u.cost <= 1) {  // keys no query sees: zero gradient
                 if (kvalid) {
                     store_zero_row(wg == 0 ? p.dv : p.dk, grow, p.grads_fp32, D);
                 }
+                uring_release(sh.ur, rd);
+                take_unit(rd + 1);
                 continue;
             }
-            for (int32_t m = 0; m < u.gcount && live; ++m) {
-                const WlSlice s = slices[gsl[u.gbegin + m]];
-                const uint32_t* pm = slice_mask(p.wl, h, s, gsl[u.gbegin + m]);
-                const int32_t k_pos = s.k_pos0 + u.kt * 128 + kr;
+            const int32_t gcount = slot.u.gcount;
+            for (int32_t m = 0; m < gcount && live; ++m) {
+                WlSlice s = slot.s;
+                int32_t qlo = slot.qlo, qhi = slot.qhi;
                 int64_t qa, qb;  // query positions that may see this key
-                slice_queries_of_key(s, k_pos, qa, qb, pm);
-                int32_t qlo, qhi;
-                bwd_q_span(s, u.kt, qlo, qhi, pm);
+                if (m > 0) {
+                    const int32_t si = gsl[slot.u.gbegin + m];
+                    s = slices[si];
+                    const uint32_t* pm = slice_mask(p.wl, h, s, si);
+                    slice_queries_of_key(s, s.k_pos0 + kt * 128 + kr, qa, qb, pm);
+                    bwd_q_span(s, kt, qlo, qhi, pm);
+                } else if (s.type == kSlicePackedCross) {  // (a unit's only slice; positions are rows)
+                    qa = pair_rows & 255u;
+                    qb = pair_rows >> 8;
+                } else {
+                    slice_queries_of_key(s, s.k_pos0 + kt * 128 + kr, qa, qb, slice_mask(p.wl, h, s, slot.slice));
+                }
                 for (int32_t t = qlo; t < qhi && live; ++t) {
                     // this q tile's rows: query c has position q_pos0 + t*128 + c
                     const int32_t nq = min(128, s.q_len - t * 128);
@@ -1115,6 +1233,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             }
+            if (!live) break;
+            uring_release(sh.ur, rd);
+            take_unit(rd + 1);
             if (!live) break;
             live = mbar_wait(&sh.o_full, o_cnt & 1, abort_flag, err_word, kErrTimeoutBase + 38,
                              kWaitNs);

@@ -18,6 +18,7 @@
 #include <stdint.h>
 
 #include "ptx.cuh"
+#include "wl_layout.cuh"
 
 namespace pva {
 
@@ -51,6 +52,46 @@ template <int R>
 __device__ __forceinline__ void uring_put(UnitRing<R>& r, uint32_t n, int32_t idx) {
     r.slot[n % R] = idx;
     mbar_arrive(&r.full[n % R]);  // release: the slot write is seen by the readers
+}
+
+struct SubTile {
+    int32_t q_row, nrows, q_pos, head;
+};
+
+struct Unit {
+    int32_t nsub, kvh, run_begin, run_count, ntiles;
+    SubTile st[2];
+};
+
+// A slot of the unit ring: the unit as the producer found it, with its first run and that run's
+// slice.  Units of one key tile are bounded by the chain of the role that computes on their scores, in
+// which four dependent reads of the worklist for every unit were 2 of 5.7 us (forward, 209 groups of
+// short pairs, 16 heads).
+struct UnitSlot {
+    int32_t idx;  // -1: no more work
+    int32_t slice, lo, hi;
+    Unit u;
+    WlSlice s;
+};
+
+__device__ __forceinline__ Unit decode_unit(const WlUnit& u, const WlSeg* segs) {
+    const WlSeg g = segs[u.seg];
+    Unit r;
+    r.nsub = u.h1 >= 0 ? 2 : 1;
+    r.kvh = u.kvh;
+    r.run_begin = u.run_begin;
+    r.run_count = u.run_count;
+    r.ntiles = u.ntiles;
+    const int32_t ts[2] = {u.t0, u.t1};
+    const int32_t hs[2] = {u.h0, u.h1};
+    for (int i = 0; i < 2; ++i) {
+        const int32_t t = ts[i] >= 0 ? ts[i] : 0;
+        r.st[i].q_row = g.q_row0 + t * 128;
+        r.st[i].nrows = min(128, g.q_len - t * 128);
+        r.st[i].q_pos = g.q_pos0 + t * 128;
+        r.st[i].head = hs[i];
+    }
+    return r;
 }
 
 // The n-th unit's slot, once it is published: for a whole converged warp, and for one thread.  It
