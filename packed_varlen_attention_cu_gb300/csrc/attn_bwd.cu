@@ -111,22 +111,37 @@ struct BShared {
 };
 
 // ------------------------------------------------------------ D = rowsum(dO O)
-// 8 threads per (row, head), 16 bytes each per step.
+// 8 threads per (row, head), 16 bytes each per step, the loads of kRows of them first.  (237 K rows of 128
+// dims, the whole backward: 156.5 us; 157.5 with one row, 164 with four, 162.5 with a loop of unknown
+// length, a 64-bit division and half the blocks.)
+template <int D>
 __global__ void __launch_bounds__(256) bwd_pre_kernel(const BwdParams p) {
+    constexpr int kRows = 2, S = D / 64;
     let_next_start();
-    const int64_t rows = (int64_t)p.q_tokens * p.hq;
+    const int64_t rows = (int64_t)p.q_tokens * p.hq, stride = ((int64_t)gridDim.x * blockDim.x) >> 3;
     const int sub = threadIdx.x & 7;
-    for (int64_t r = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 3;
-         r - (threadIdx.x & 31) / 8 < rows; r += ((int64_t)gridDim.x * blockDim.x) >> 3) {
-        float acc = 0.f;
-        if (r < rows) {
-            const uint4* o = reinterpret_cast<const uint4*>(
-                reinterpret_cast<const __nv_bfloat16*>(p.out) + r * p.d);
-            const uint4* g = reinterpret_cast<const uint4*>(
-                reinterpret_cast<const __nv_bfloat16*>(p.dout) + r * p.d);
-            for (int c = sub; c < p.d / 8; c += 8) {
-                const uint4 a = o[c], b = g[c];
-                const uint32_t av[4] = {a.x, a.y, a.z, a.w}, bv[4] = {b.x, b.y, b.z, b.w};
+    for (int64_t r0 = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 3;
+         r0 - (threadIdx.x & 31) / 8 < rows; r0 += kRows * stride) {
+        uint4 a[kRows][S], b[kRows][S];
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+            const int64_t r = r0 + i * stride;
+            const uint4* o = reinterpret_cast<const uint4*>(p.out) + r * (D / 8) + sub;
+            const uint4* g = reinterpret_cast<const uint4*>(p.dout) + r * (D / 8) + sub;
+#pragma unroll
+            for (int c = 0; c < S; ++c) {
+                a[i][c] = r < rows ? o[8 * c] : make_uint4(0, 0, 0, 0);
+                b[i][c] = r < rows ? g[8 * c] : make_uint4(0, 0, 0, 0);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+            const int64_t r = r0 + i * stride;
+            float acc = 0.f;
+#pragma unroll
+            for (int c = 0; c < S; ++c) {
+                const uint32_t av[4] = {a[i][c].x, a[i][c].y, a[i][c].z, a[i][c].w};
+                const uint32_t bv[4] = {b[i][c].x, b[i][c].y, b[i][c].z, b[i][c].w};
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const float2 fa = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&av[e]));
@@ -134,14 +149,14 @@ __global__ void __launch_bounds__(256) bwd_pre_kernel(const BwdParams p) {
                     acc += fa.x * fb.x + fa.y * fb.y;
                 }
             }
-        }
-        acc += __shfl_xor_sync(0xffffffffu, acc, 1);
-        acc += __shfl_xor_sync(0xffffffffu, acc, 2);
-        acc += __shfl_xor_sync(0xffffffffu, acc, 4);
-        if (r < rows && sub == 0) {
-            const int64_t t = r / p.hq;
-            const int32_t h = (int32_t)(r - t * p.hq);
-            p.dvec[(int64_t)h * p.q_tokens + t] = acc;
+            acc += __shfl_xor_sync(0xffffffffu, acc, 1);
+            acc += __shfl_xor_sync(0xffffffffu, acc, 2);
+            acc += __shfl_xor_sync(0xffffffffu, acc, 4);
+            if (r < rows && sub == 0) {
+                const int64_t t = rows >> 31 ? r / p.hq : (int64_t)((uint32_t)r / (uint32_t)p.hq);
+                const int32_t h = (int32_t)(r - t * p.hq);
+                p.dvec[(int64_t)h * p.q_tokens + t] = acc;
+            }
         }
     }
 }
@@ -682,6 +697,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 if (!live) break;
+                // (Storing dQ after dS of the next sub-tile's first half-item, as the forward does with O,
+                // was slower: its products wait for the stores.  Short pairs 160 against 156.5 us, long
+                // documents by 3%.)
                 if (i + 1 == nsub) {
                     uring_release(sh.ur, nu);
                     take_unit(nu + 1);
@@ -1272,8 +1290,8 @@ pva_status launch_bwd(const CUtensorMap& mq, const CUtensorMap& mk, const CUtens
                       const CUtensorMap& mdo, const CUtensorMap& mq64, const CUtensorMap& mdo64,
                       const CUtensorMap& mk64, const CUtensorMap& mv64, const BwdParams& bp,
                       int32_t dkdv_ctas, cudaStream_t st) {
-    const int grid_pre = 4 * bp.num_ctas;
-    bwd_pre_kernel<<<grid_pre, 256, 0, st>>>(bp);
+    const int grid_pre = 8 * bp.num_ctas;
+    bwd_pre_kernel<D><<<grid_pre, 256, 0, st>>>(bp);
     auto kq = bwd_dq_kernel<D>;
     auto kk = bwd_dkdv_kernel<D>;
     // setmaxnreg.inc draws from the registers the block was launched with: the
