@@ -1,11 +1,11 @@
 // unit_feed.cuh -- how a persistent CTA's roles learn which work unit comes next.
 //
-// One producer thread decides the CTA's next unit and publishes its index in
-// a small shared-memory ring (UnitRing); every other role reads the slots in
-// the same order and releases each after reading it.  The index is -1 once
-// the CTA has no more work.  The producer decides either from a fixed list
-// (static dispatch) or by claiming the next rank of a dispatch order from a
-// global counter (dynamic dispatch: "数据并行负载均衡" §4.4's LPT rule with the
+// One producer thread decides the CTA's next unit and publishes it in a small
+// shared-memory ring (UnitRing): its index, -1 once the CTA has no more work, and
+// what the other roles need of the worklist.  These read the slots in the same
+// order and release each when they have done with it.  The producer decides
+// either from a fixed list (static dispatch) or by claiming the next rank of a
+// dispatch order from a global counter (dynamic dispatch: "数据并行负载均衡" §4.4's LPT rule with the
 // least loaded worker being whichever CTA frees up first).
 //
 // A dispatch counter is a pair (next, done) in device memory that starts at
@@ -22,8 +22,8 @@
 
 namespace pva {
 
-// T: what a slot holds: a unit's index, or all that the other roles need of it.
-template <int R, class T = int32_t>
+// R slots of T.
+template <int R, class T>
 struct UnitRing {
     uint64_t full[R], empty[R];
     T slot[R];
@@ -45,13 +45,6 @@ __device__ __forceinline__ bool uring_wait_free(UnitRing<R, T>& r, uint32_t n,
                                                 volatile int* abort_flag, int* err_word, int site,
                                                 uint64_t timeout_ns) {
     return mbar_wait(&r.empty[n % R], ((n / R) & 1) ^ 1, abort_flag, err_word, site, timeout_ns);
-}
-
-// Producer: publish unit index `idx` (-1: no more work) as the n-th unit.
-template <int R>
-__device__ __forceinline__ void uring_put(UnitRing<R>& r, uint32_t n, int32_t idx) {
-    r.slot[n % R] = idx;
-    mbar_arrive(&r.full[n % R]);  // release: the slot write is seen by the readers
 }
 
 struct SubTile {
@@ -114,31 +107,6 @@ __device__ __forceinline__ bool uring_wait(UnitRing<R, T>& r, uint32_t n, volati
 template <int R, class T>
 __device__ __forceinline__ void uring_release(UnitRing<R, T>& r, uint32_t n) {
     mbar_arrive(&r.empty[n % R]);
-}
-
-// A whole converged warp takes the n-th unit (one arrival for the warp).
-template <int R>
-__device__ __forceinline__ bool uring_get_warp(UnitRing<R>& r, uint32_t n, int32_t& idx,
-                                               volatile int* abort_flag, int* err_word, int site,
-                                               uint64_t timeout_ns) {
-    if (!mbar_wait_warp(&r.full[n % R], (n / R) & 1, abort_flag, err_word, site, timeout_ns))
-        return false;
-    idx = *reinterpret_cast<volatile int32_t*>(&r.slot[n % R]);
-    __syncwarp();
-    mbar_arrive_elect(&r.empty[n % R]);
-    return true;
-}
-
-// One thread takes the n-th unit (one arrival per thread).
-template <int R>
-__device__ __forceinline__ bool uring_get(UnitRing<R>& r, uint32_t n, int32_t& idx,
-                                          volatile int* abort_flag, int* err_word, int site,
-                                          uint64_t timeout_ns) {
-    if (!mbar_wait(&r.full[n % R], (n / R) & 1, abort_flag, err_word, site, timeout_ns))
-        return false;
-    idx = *reinterpret_cast<volatile int32_t*>(&r.slot[n % R]);
-    mbar_arrive(&r.empty[n % R]);
-    return true;
 }
 
 // Dynamic dispatch: the next rank for this CTA.
