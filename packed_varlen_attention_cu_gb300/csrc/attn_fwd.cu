@@ -19,6 +19,8 @@
 //               memory), completion via tcgen05.commit
 //   warps 4-7   softmax + epilogue of sub-tile 0 (one query row per thread)
 //   warps 8-11  softmax + epilogue of sub-tile 1
+// (CROSS: a unit of one sub-tile and several key tiles is split, its even key tiles
+// are sub-tile 0's, the odd ones sub-tile 1's, with the same queries.)
 // A warp reaches tensor-memory lanes 32*(warp % 4).
 // Tensor memory (512 columns): S0 [0,128), S1 [128,256), O0 [256,..),
 // O1 [384,..).  At d = 128 P (bf16) overwrites the first half of S in place,
@@ -60,7 +62,9 @@ struct Regs {
 constexpr uint64_t kWaitNs = 2000000000ull;   // 2 s per wait
 constexpr uint64_t kDrainNs = 200000000ull;   // 0.2 s per drain wait
 constexpr float kRescaleThreshold = 8.0f;     // log2 domain
-constexpr int kURing = 8;                     // units the producer may run ahead
+// units the producer may run ahead (fewer where split units need the shared memory)
+template <bool CROSS>
+constexpr int kRing = CROSS ? 4 : 8;
 // readers of a unit slot: the two MMA warps (one arrival each) and every
 // softmax thread
 constexpr uint32_t kUReaders = 2 + 256;
@@ -97,13 +101,17 @@ struct AttnParams {
     int32_t dynamic;      // 1: claim units in LPT order from the worklist's counter
 };
 
+template <bool CROSS>
 struct Shared {
     uint64_t q_full[2], q_empty[2], s_full[2], p_half[2], p_full[2], o_full[2], o_empty[2], done[2],
         turn[2];
     // C::kSplitP only: S read by the softmax (4 warp arrivals), PV complete (commit)
     uint64_t s_free[2], pv_done[2];
     uint64_t kv_full[8], kv_empty[8];
-    UnitRing<kURing, UnitSlot> ur;  // the producer hands each unit to the other roles
+    UnitRing<kRing<CROSS>, UnitSlot> ur;  // the producer hands each unit to the other roles
+    // split units: (m, l) of sub-tile 1's rows for sub-tile 0's epilogue
+    uint64_t half_full, half_empty;
+    float2 half_ml[CROSS ? 128 : 1];
     uint32_t tmem_base;
     int32_t abort_flag;
 };
@@ -137,7 +145,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t* sQ[2] = {smem, smem + C::kTileBytes};
     uint8_t* sKV = smem + 2 * C::kTileBytes;
     uint8_t* sStage = sKV + C::kStages * C::kTileBytes;  // 4 KB per softmax warp, 1 KB aligned
-    __shared__ Shared sh;
+    __shared__ Shared<CROSS> sh;
+    constexpr int kURing = kRing<CROSS>;
+    static_assert(C::kSmem + sizeof(sh) <= 227 * 1024, "shared memory of a block");
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const WlHeader* h = reinterpret_cast<const WlHeader*>(p.wl);
@@ -201,6 +211,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&sh.kv_empty[s], 2);
         }
         uring_init(sh.ur, kUReaders);
+        mbar_init(&sh.half_full, 128);
+        mbar_init(&sh.half_empty, 128);
         sh.abort_flag = 0;
         fence_barrier_init();
     }
@@ -273,13 +285,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const WlUnit wu = ubase[idx];
                 WlRun first_run{0, 0, 0, 0};
                 if (wu.run_count > 0) first_run = runs[wu.run_begin];
-                const Unit u = decode_unit(wu, segs);
+                Unit u = decode_unit(wu, segs);
+                // CROSS: a unit of one sub-tile (one head over its own keys, up to 128 rows) would leave
+                // half of the CTA idle, so its key tiles are dealt to both halves, which meet in the
+                // epilogue.  (77 rows over 1500 keys, 8 heads of 128: 24.9 -> 20.3 us; 64 targets of 100 rows
+                // over 1500 keys each, 16 heads of 64: 126 -> 109 us, of 128: 153 -> 145, near HBM's rate.)
+                const bool split = CROSS && u.nsub == 1 && u.ntiles >= 2;
+                if (split) {
+                    u.nsub = 2;
+                    u.st[1] = u.st[0];
+                }
                 WlSlice first_slice{0, 0, 0, 0, 0, 0, 0, 0};
                 if (wu.run_count > 0) first_slice = slices[first_run.slice];
                 // Q goes out before the slice is here, and the slot after it: release, it is seen by
                 // the readers
                 auto publish = [&]() {
                     slot.u = u;
+                    slot.split = split;
                     slot.slice = first_run.slice;
                     slot.lo = first_run.lo;
                     slot.hi = first_run.hi;
@@ -432,6 +454,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!live) break;
                 const volatile UnitSlot& slot = sh.ur.slot[nu % kURing];
                 const int32_t idx = slot.idx, n = slot.u.ntiles, nsub = slot.u.nsub;
+                const bool split = CROSS && slot.split != 0;
                 uring_release_warp(sh.ur, nu);
                 if (idx < 0) break;
                 if (n == 0) continue;
@@ -440,6 +463,45 @@ __global__ void __launch_bounds__(kThreads, 1)
                     live = mbar_wait_warp(&sh.q_full[i], q_it & 1, abort_flag, err_word,
                                           kErrTimeoutBase + 3, kWaitNs);
                     if (!live) break;
+                }
+                if (split) {
+                    // stage x: K_x for issuer x % 2, V_{x-1} for the other
+                    for (int32_t x = 0; x <= n && live; ++x) {
+                        const uint32_t st = kv_it % C::kRingStages;
+                        live = mbar_wait_warp(&sh.kv_full[st], (kv_it / C::kRingStages) & 1,
+                                              abort_flag, err_word, kErrTimeoutBase + 4, kWaitNs);
+                        if (!live) break;
+                        const bool qk = x < n && (x & 1) == i, pv = x > 0 && (x & 1) != i;
+                        if (qk) {
+                            issue_qk(st);
+                            if (!live) break;
+                            if (x + 2 >= n) mma_commit_elect(&sh.q_empty[i]);
+                        }
+                        if (pv) {
+                            if (x - 1 == i)
+                                live = mbar_wait_warp(&sh.o_empty[i], (o_cnt & 1) ^ 1, abort_flag,
+                                                      err_word, kErrTimeoutBase + 7, kWaitNs);
+                            if (!live) break;
+                            live = mbar_wait_warp(&sh.p_full[i], p_cnt & 1, abort_flag, err_word,
+                                                  kErrTimeoutBase + 12, kWaitNs);
+                            if (!live) break;
+                            ++p_cnt;
+                            tc_fence_after();
+                            const uint64_t dV = dV0 + ((st * C::kStageBytes + C::kTileBytes) >> 4);
+#pragma unroll
+                            for (int k = 0; k < 8; ++k)
+                                mma_ts_elect(tO, tP + k * 8, dV + k * 128, C::kIdescPV,
+                                             (x - 1 > i || k > 0) ? 1u : 0u);
+                            mma_commit_elect(&sh.pv_done[i]);
+                        }
+                        release(qk || pv, st);
+                        ++kv_it;
+                    }
+                    if (!live) break;
+                    mma_commit_elect(&sh.o_full[i]);
+                    ++o_cnt;
+                    ++q_it;
+                    continue;
                 }
                 {  // stage (K_0)
                     const uint32_t st = kv_it % C::kRingStages;
@@ -507,6 +569,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!live) break;
                 const volatile UnitSlot& slot = sh.ur.slot[nu % kURing];
                 const int32_t idx = slot.idx, n = slot.u.ntiles, nsub = slot.u.nsub;
+                const bool split = CROSS && slot.split != 0;
                 uring_release_warp(sh.ur, nu);
                 if (idx < 0) break;
                 if (n == 0) continue;
@@ -516,6 +579,71 @@ __global__ void __launch_bounds__(kThreads, 1)
                     live = mbar_wait_warp(&sh.q_full[i], q_it & 1, abort_flag, err_word,
                                      kErrTimeoutBase + 3, kWaitNs);
                     if (!live) break;
+                }
+                if (split) {
+                    for (int32_t j = 0; j < n && live; ++j, kv_it += 2) {
+                        const uint32_t stk = kv_it % C::kStages, stv = (kv_it + 1) % C::kStages;
+                        auto landed = [&](uint32_t x) {
+                            return mbar_wait_warp(&sh.kv_full[x % C::kStages], (x / C::kStages) & 1,
+                                                  abort_flag, err_word, kErrTimeoutBase + 5, kWaitNs);
+                        };
+                        if ((j & 1) != i) {  // the other issuer's; its K is freed ahead of this one's PV
+                            if (j == 0) {
+                                live = landed(kv_it);
+                                if (!live) break;
+                                release(false, stk);
+                            }
+                            live = landed(kv_it + 1);
+                            if (!live) break;
+                            release(false, stv);
+                            continue;
+                        }
+                        live = landed(kv_it);
+                        if (!live) break;
+                        tc_fence_after();
+                        const uint64_t dK = dK0 + ((stk * C::kTileBytes) >> 4);
+                        const uint64_t dV = dV0 + ((stv * C::kTileBytes) >> 4);
+#pragma unroll
+                        for (int k = 0; k < D / 16; ++k) {
+                            const uint32_t off16 = (k >> 2) * 1024 + (k & 3) * 2;
+                            mma_ss_elect(tS, dQ + off16, dK + off16, C::kIdescQK, k > 0);
+                        }
+                        mma_commit_elect(&sh.s_full[i]);
+                        if (j + 2 >= n) mma_commit_elect(&sh.q_empty[i]);
+                        release(true, stk);
+                        if (j + 1 < n) {
+                            live = landed(kv_it + 2);
+                            if (!live) break;
+                            release(false, (kv_it + 2) % C::kStages);
+                        }
+                        live = landed(kv_it + 1);
+                        if (live && j == i)
+                            live = mbar_wait_warp(&sh.o_empty[i], (o_cnt & 1) ^ 1, abort_flag,
+                                                  err_word, kErrTimeoutBase + 7, kWaitNs);
+                        if (!live) break;
+                        live = mbar_wait_warp(&sh.p_half[i], p_cnt & 1, abort_flag, err_word,
+                                              kErrTimeoutBase + 6, kWaitNs);
+                        if (!live) break;
+                        tc_fence_after();
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            mma_ts_elect(tO, tS + k * 8, dV + k * 128, C::kIdescPV,
+                                         (j > i || k > 0) ? 1u : 0u);
+                        live = mbar_wait_warp(&sh.p_full[i], p_cnt & 1, abort_flag, err_word,
+                                              kErrTimeoutBase + 12, kWaitNs);
+                        if (!live) break;
+                        ++p_cnt;
+                        tc_fence_after();
+#pragma unroll
+                        for (int k = 4; k < 8; ++k)
+                            mma_ts_elect(tO, tS + k * 8, dV + k * 128, C::kIdescPV, 1u);
+                        release(true, stv);
+                    }
+                    if (!live) break;
+                    mma_commit_elect(&sh.o_full[i]);
+                    ++o_cnt;
+                    ++q_it;
+                    continue;
                 }
                 // prologue: S_i = Q_i K_0^T
                 {
@@ -644,15 +772,54 @@ __global__ void __launch_bounds__(kThreads, 1)
         // pl: the pending unit's sub-tile and its running max and sum.  The fused
         // ring step (ACC: read-modify-write of the running fp32 O and LSE) runs its
         // epilogue at once: deferred, it measured slower.
-        bool pend = false;
+        // psplit: the pending unit is a split one; o1_cnt: units with a sub-tile 1 so far, as
+        // sub-tile 0 counts them.
+        bool pend = false, psplit = false;
         SubTile pst{0, 0, 0, 0};
         float pm = 0.f, pl = 0.f;
+        uint32_t o1_cnt = 0, half_cnt = 0, po1 = 0;
+        // Sub-tile 0 takes the other half's maximum, sum and O into its own, in tensor memory, so that the
+        // epilogue is the same for all units (with its own form of it short pairs took 2 us more, of 57).
+        auto meet_halves = [&]() {
+            live = mbar_wait(&sh.half_full, half_cnt & 1, abort_flag, err_word, kErrTimeoutBase + 10, kWaitNs) &&
+                   mbar_wait(&sh.o_full[1], po1 & 1, abort_flag, err_word, kErrTimeoutBase + 10, kWaitNs);
+            if (!live) return;
+            ++half_cnt;
+            const float2 x = sh.half_ml[CROSS ? r : 0];
+            mbar_arrive(&sh.half_empty);
+            tc_fence_after();
+            const float mm = fmaxf(pm, x.x);
+            const float f0 = pm == -INFINITY ? 0.f : ex2_approx(pm - mm);
+            const float f1 = x.x == -INFINITY ? 0.f : ex2_approx(x.x - mm);
+            pm = mm;
+            pl = pl * f0 + x.y * f1;
+            __syncwarp();
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+                uint32_t a[32], b[32];
+                tmem_ld32(tO + c * 32, a);
+                tmem_ld32(tO + 128 + c * 32, b);
+                tmem_ld_wait(a);
+                tmem_ld_wait(b);
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                    a[e] = __float_as_uint(__uint_as_float(a[e]) * f0 + __uint_as_float(b[e]) * f1);
+                tmem_st32(tO + c * 32, a);
+            }
+            tmem_st_wait();
+            tc_fence_before();
+            mbar_arrive(&sh.o_empty[1]);
+        };
         auto epilogue = [&]() {
             pend = false;
             live = mbar_wait(&sh.o_full[i], o_cnt & 1, abort_flag, err_word, kErrTimeoutBase + 10,
                              kWaitNs);
             if (!live) return;
             ++o_cnt;
+            if (CROSS && psplit) {
+                meet_halves();
+                if (!live) return;
+            }
             const SubTile& st = pst;
             const bool valid = r < st.nrows;
             const float m_used = pm, l_sum = pl;
@@ -809,6 +976,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 prefetch_l2(p.lse + (int64_t)st.head * p.q_tokens + st.q_row + r);
             }
             float m_used = -INFINITY, l_sum = 0.f;
+            const bool split = CROSS && slot.split != 0;
+            const int32_t step = split ? 2 : 1;  // (a CROSS unit has one run)
             for (int32_t rr = 0; rr < u.run_count && live; ++rr) {
                 WlRun run{slot.slice, slot.lo, slot.hi, 0};
                 WlSlice s = slot.s;
@@ -832,7 +1001,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 const int32_t lim_hi = valid ? (int32_t)khi : 0;
                 const int32_t lim_lo = (int32_t)klo;
-                for (int32_t jt = run.lo; jt < run.hi && live; ++jt) {
+                for (int32_t jt = run.lo + (split ? i : 0); jt < run.hi && live; jt += step) {
                     // allowed columns [c_lo, c_hi) in this kv tile, settled while S
                     // is still being computed
                     const int32_t kt0 = jt * 128;
@@ -985,9 +1154,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             if (!live) break;
+            if (CROSS) {
+                psplit = split;
+                po1 = o1_cnt;
+                if (u.nsub == 2) ++o1_cnt;
+            }
             uring_release(sh.ur, nu);
             take_unit(nu + 1);
             if (!live) break;
+            if (CROSS && split && i == 1) {  // sub-tile 0 stores for both, and frees O
+                live = mbar_wait(&sh.half_empty, (half_cnt & 1) ^ 1, abort_flag, err_word,
+                                 kErrTimeoutBase + 10, kWaitNs);
+                if (!live) break;
+                ++half_cnt;
+                sh.half_ml[r] = make_float2(m_used, l_sum);
+                mbar_arrive(&sh.half_full);
+                ++o_cnt;
+                continue;
+            }
             pend = true;
             pst = st;
             pm = m_used;

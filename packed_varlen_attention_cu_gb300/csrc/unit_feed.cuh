@@ -63,6 +63,7 @@ struct Unit {
 struct UnitSlot {
     int32_t idx;  // -1: no more work
     int32_t slice, lo, hi;
+    int32_t split;  // forward: both sub-tiles are the unit's one, with alternate key tiles each
     Unit u;
     WlSlice s;
 };

@@ -248,6 +248,40 @@ def test_sources_cut_in_two_are_joined_by_accumulation():
     compare(to_np(o_run), to_np(l_run), o.numpy(), l.numpy(), "two parts")
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("hq", [1, 5])
+@pytest.mark.parametrize("dispatch", [api.DISPATCH_DYNAMIC, api.DISPATCH_STATIC])
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_targets_of_one_tile_over_sources_of_many(d, hq, dispatch, accumulate):
+    """Targets of up to 128 rows with a kv head of their own, over sources of 2 to 12 tiles, between pairs of one key tile,
+    without keys, and of two row tiles; several units a CTA.  Some sources have their largest scores in their last tile."""
+    sizes = [(77, 1500), (1, 129), (128, 256), (33, 257), (9, 100), (200, 300), (5, 0), (64, 640), (127, 385), (300, 130), (2, 1024)]
+    p = Pack([sizes[(3 * i) % len(sizes)] for i in range(60 if hq == 5 else 22)], hq, hq, d, seed=d + hq, spread=1.5)
+    for i, (c, f) in enumerate(zip(p.ck[:-1].tolist(), p.ck[1:].tolist())):
+        if i % 3 == 0 and f - c > 128:
+            p.k[f - 20:f] *= 4
+    r = Run(p, 0, dispatch, fp32=accumulate).build()
+    if accumulate:
+        r.lse.fill_(-math.inf)
+        api.attn_fwd_accumulate(r.q, r.k, r.v, r.cu, r.mask, r.params, r.wl, r.out, r.lse)
+    else:
+        r.forward()
+    torch.cuda.synchronize()
+    assert api.worklist_error(r.wl) == 0
+    o, l = p.forward()
+    seen = torch.isfinite(l[0])  # (accumulated, rows without keys keep what was there)
+    assert accumulate or (not r.out.cpu()[~seen].any() and torch.isneginf(r.lse.cpu()[:, ~seen]).all())
+    # Scores are sums of d exact products in fp32: off by e <= d 2^-23 sum |q k| scale, and so is the LSE, beside its own
+    # logarithm's rounding.  Weights are off by a factor e^+-2e and, as bf16 operands, by 2^-8 of each, the output by 2^-8 of itself.
+    e = d * 2.0 ** -23 * p.scale * p.q.abs().double().sum(-1).max() * p.k.abs().max().double()
+    assert e < 0.05
+    top = p.v.abs().max().double()
+    err = (r.out.double().cpu() - o)[seen].abs()
+    assert (err <= 2.0 ** -8 * (o[seen].abs() + top) + 3 * e * top).all()
+    assert (err.norm() / o[seen].norm()) <= 3e-3  # two roundings to 8 bits, each 2^-8 / sqrt(3) at most in the mean
+    assert ((r.lse.double().cpu() - l)[:, seen].abs() <= e + 2.0 ** -21 * (1 + l[:, seen].abs())).all()
+
+
 def test_captured_with_other_lengths():
     """Worklist, forward, plan and backward in one graph, replayed for other lengths of the same totals."""
     pairs = [[(40, 300), (200, 20), (16, 64)], [(100, 50), (100, 50), (56, 284)], [(0, 384), (255, 0), (1, 0)]]
