@@ -153,7 +153,8 @@ __global__ void __launch_bounds__(kScan, kScanCtas) scan_kernel(const SelectArgs
     }
     for (; u < u1;) {
         const int64_t row = quotient(u, a.tiles);
-        const int32_t t0 = (int32_t)(u - row * a.tiles), t1 = (int32_t)min((int64_t)a.tiles, t0 + u1 - u);
+        const int32_t t0 = (int32_t)(u - row * a.tiles);
+        int32_t t1 = (int32_t)min((int64_t)a.tiles, t0 + u1 - u);
         const int part = a.whole ? t0 / a.per : (int)blockIdx.x - (int)quotient(row * a.tiles, a.per);
         u += t1 - t0;
 
@@ -162,6 +163,9 @@ __global__ void __launch_bounds__(kScan, kScanCtas) scan_kernel(const SelectArgs
         const char* base = reinterpret_cast<const char*>(a.logits) + row * a.row_stride * (F32 ? 4 : 2);
         const int shift = (int)(reinterpret_cast<uintptr_t>(base) & 15u) / (F32 ? 4 : 2);
         const int32_t nv = (int32_t)(((int64_t)shift + a.vocab + VE - 1) / VE);
+        // (rows have tiles for any start; the last one may be empty: 512 rows of 131071, 42.2 -> 40.2 us;
+        // tiles on their way to L2 by prefetches, 1, 2, 4, 8 or 16 ahead, 40.8 to 45.4)
+        t1 = min(t1, (nv + kTile - 1) / kTile);
         const int32_t whole0 = shift > 0 ? 1 : 0, whole1 = (int32_t)(((int64_t)shift + a.vocab) / VE);
         // Vector x of the row; what is not the row's is -inf.
         auto vector = [&](int32_t x) {
