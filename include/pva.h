@@ -74,7 +74,10 @@ typedef enum {
                                      d sees every key of source d, and nothing else.  Targets of
                                      one source that lie side by side count as one target.
                                      q_tokens = cu[num_docs], k_tokens = cu_keys[num_docs];
-                                     either side of a pair may be empty */
+                                     either side of a pair may be empty.  As under the other
+                                     masks tensors hold finite values: one that is not may reach
+                                     the results of other documents in the same tile of 128 rows
+                                     or keys (a weight of 0 meets it there) */
 } pva_mask_kind;
 
 /* The four MaskTypes of "03 · 长文负载均衡" §4.4 (the pages name them without
