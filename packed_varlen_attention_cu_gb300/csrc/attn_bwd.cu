@@ -398,7 +398,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         // S = Q K^T and dP = dO V^T (TS MMAs read only the K / V halves from shared
         // memory, so N = 64 runs at the full rate)
         const uint32_t tQA = tmem + 256 + D;
-        bool pend = false, first = true;
+        // pend: a half-item whose dQ MMAs are still to be issued, after S of the next one, which may be
+        // the next sub-tile's.  last: it ends its sub-tile.
+        bool pend = false, first = true, last = false;
         uint32_t pend_u = 0, pend_st = 0;
         auto finish_pending = [&]() -> bool {
             const uint32_t b = pend_u & 1;
@@ -420,6 +422,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             first = false;
             mma_commit_elect(&sh.r_empty[pend_st]);
             pend = false;
+            if (last) {
+                mma_commit_elect(&sh.o_full);
+                ++o_cnt;
+                first = true;
+                last = false;
+            }
             return true;
         };
         for (uint32_t nu = 0; live; ++nu) {
@@ -432,7 +440,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int32_t first_len = slot.s.k_len;
             uring_release_warp(sh.ur, nu);
             if (idx < 0) break;
-            if (ntiles == 0) continue;
+            if (ntiles == 0) {
+                // (the element-wise warps store what is pending before they leave this unit)
+                if (pend && !finish_pending()) break;
+                continue;
+            }
             for (int i = 0; i < nsub && live; ++i) {
                 live = mbar_wait_warp(&sh.a_full, a_it & 1, abort_flag, err_word,
                                       kErrTimeoutBase + 23, kWaitNs);
@@ -444,7 +456,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tmem_cp_elect(tQA + k * 8, dQd + off16);
                 }
                 mma_commit_elect(&sh.a_empty);  // Q copied (warp 3 copies dO)
-                first = true;
                 for (int32_t rr = 0; rr < run_count && live; ++rr) {
                     const WlRun run = rr > 0 ? runs[run_begin + rr] : first_run;
                     const int32_t k_len = rr > 0 ? slices[run.slice].k_len : first_len;
@@ -480,12 +491,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 if (!live) break;
-                if (pend && !finish_pending()) break;
-                mma_commit_elect(&sh.o_full);
-                ++o_cnt;
+                last = true;
                 ++a_it;
             }
         }
+        if (live && pend) finish_pending();
         mma_commit_elect(&sh.done);
         mbar_wait_drain(&sh.done, 0, kDrainNs);
         __syncwarp();
@@ -600,11 +610,42 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (slot.s.type == kSlicePackedCross)
                 pair_keys = reinterpret_cast<const uint16_t*>(slice_mask(p.wl, h, slot.s, slot.slice))[r];
         };
+        // dQ of a sub-tile goes out after dS of the next one's first key tile, whose scores are there by then:
+        // the MMA warps go on to it before the last dQ MMAs.  (Short pairs, the whole backward: 156.0 -> 154.3 us,
+        // 167.6 -> 161.2 with dynamic dispatch.  After the first half-item 151.5 and 158.3, but with the check in
+        // the innermost loop long documents lose 1 to 3%.)  pend_valid, pend_row: this thread's row of the
+        // sub-tile whose dQ is still to be stored.
+        bool pend = false, pend_valid = false;
+        int64_t pend_row = 0;
+        auto epilogue = [&]() {
+            pend = false;
+            live = mbar_wait(&sh.o_full, o_cnt & 1, abort_flag, err_word, kErrTimeoutBase + 28, kWaitNs);
+            if (!live) return;
+            ++o_cnt;
+            tc_fence_after();
+            // this warpgroup's half of the dQ columns
+            constexpr int kHalfChunks = D / 64;
+            uint32_t o[kHalfChunks][32];
+#pragma unroll
+            for (int c = 0; c < kHalfChunks; ++c) tmem_ld32(tQ + (wg * kHalfChunks + c) * 32, o[c]);
+#pragma unroll
+            for (int c = 0; c < kHalfChunks; ++c) tmem_ld_wait(o[c]);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.o_empty);
+            if (pend_valid) {
+#pragma unroll
+                for (int c = 0; c < kHalfChunks; ++c)
+                    store_row32(p.dq, pend_row + (wg * kHalfChunks + c) * 32, p.grads_fp32, o[c], p.scale);
+            }
+        };
         take_unit(0);
         for (uint32_t nu = 0; live && idx >= 0; ++nu) {
             const UnitSlot& slot = sh.ur.slot[nu % kURing];
             const int nsub = slot.u.nsub;
             if (slot.u.ntiles == 0) {  // rows without keys: zero gradient
+                if (pend) epilogue();
+                if (!live) break;
                 for (int i = 0; i < nsub; ++i) {
                     const SubTile& st = slot.u.st[i];
                     if (r < st.nrows)
@@ -694,41 +735,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                             __syncwarp();
                             if (lane == 0) mbar_arrive(&sh.p2_full[b]);
                         }
+                        if (live && pend) epilogue();
                     }
                 }
                 if (!live) break;
-                // (Storing dQ after dS of the next sub-tile's first half-item, as the forward does with O,
-                // was slower: its products wait for the stores.  Short pairs 160 against 156.5 us, long
-                // documents by 3%.)
                 if (i + 1 == nsub) {
                     uring_release(sh.ur, nu);
                     take_unit(nu + 1);
                     if (!live) break;
                 }
-                live = mbar_wait(&sh.o_full, o_cnt & 1, abort_flag, err_word,
-                                 kErrTimeoutBase + 28, kWaitNs);
-                if (!live) break;
-                ++o_cnt;
-                tc_fence_after();
-                // this warpgroup's half of the dQ columns
-                constexpr int kHalfChunks = D / 64;
-                uint32_t o[kHalfChunks][32];
-#pragma unroll
-                for (int c = 0; c < kHalfChunks; ++c)
-                    tmem_ld32(tQ + (wg * kHalfChunks + c) * 32, o[c]);
-#pragma unroll
-                for (int c = 0; c < kHalfChunks; ++c) tmem_ld_wait(o[c]);
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sh.o_empty);
-                if (valid) {
-#pragma unroll
-                    for (int c = 0; c < kHalfChunks; ++c)
-                        store_row32(p.dq, grow + (wg * kHalfChunks + c) * 32, p.grads_fp32, o[c],
-                                    p.scale);
-                }
+                pend = true;
+                pend_valid = valid;
+                pend_row = grow;
             }
         }
+        if (live && pend) epilogue();
     }
     tc_fence_before();
     __syncthreads();
