@@ -134,6 +134,29 @@ def test_backward(d, hq, hkv, pack):
             assert not got[0][a:a + m].any() and not got[1][c:c + n].any() and not got[2][c:c + n].any()
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("pack", [0, 1])
+def test_sources_of_one_key_move_no_scores(d, pack):
+    """With one key P is 1 and dS = P (dP - D) is 0, whatever dO and V are.  P is off by its LSE's and exponent's
+    rounding, 2^-24 of numbers below 2^6 in base 2 and 2^-22, so by less than 2^-17, and as far is dS from 0, of |dP|;
+    D from an O in bf16 would leave 2^-8 of it."""
+    p = Pack([(1 + i % 50, 1) for i in range(40)], 4, 2, d, seed=d)
+    got = Run(p, pack).build().forward().backward(fp32=True)
+    dp = (p.dout.double().norm(dim=-1).max() * p.v.double().norm(dim=-1).max())
+    assert (p.q.double().norm(dim=-1).max() * p.k.double().norm(dim=-1).max()) * p.scale * math.log2(math.e) < 2 ** 6
+    one = p.scale * dp * 2.0 ** -17
+    assert got[0].abs().max() <= one * p.k.abs().max().double()
+    assert got[1].abs().max() <= one * p.q.abs().max().double() * 50 * 2  # a key's rows, and its two heads
+
+
+def test_gradients_of_short_sources():
+    """dS goes into the products as bf16 and the results leave as bf16: each rounding is 2^-8 of a number at most, evenly
+    spread, so below 2^-8 / sqrt(3) in the mean, both together below 0.0032."""
+    p = Pack([(1 + i % 30, 2 + i % 7) for i in range(200)], 4, 2, 128, seed=2)
+    for g, r in zip(Run(p).build().forward().backward(), p.gradients()):
+        assert (g.double().cpu() - r).norm() <= 0.0032 * r.norm()
+
+
 def test_gradients_against_differences():
     """Along random directions, (f(x + h u) - f(x - h u)) / 2h of the 64-bit forward, f = sum(out * dout): h = 1e-5
     leaves h^2 of the third derivative and 1e-16 / h of rounding, both below 1e-9; the gradients' own error is REL_L2."""
