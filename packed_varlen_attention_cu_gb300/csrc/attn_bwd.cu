@@ -6,7 +6,8 @@
 //   dP = dO V^T,  D = rowsum(dO * O),  dS = P (dP - D),
 //   dQ = scale dS K,  dK = scale dS^T Q,  dV = P^T dO.
 // Three kernels, no atomics (each output row has one writer):
-//   bwd_pre   D per (row, head), HBM-bound;
+//   bwd_pre   D per (row, head), HBM-bound (under a CROSS mask for sources past 128
+//             keys; bwd_dq makes the others');
 //   bwd_dq    q-major over the forward worklist's units, dispatched as the
 //             worklist says (static per-CTA LPT lists, or claimed at run time):
 //             per query sub-tile (Q and dO copied into tensor memory), every
@@ -330,6 +331,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     wait_previous();
     let_next_start();
     if (h->error != 0) return;
+    if ((h->kind == PVA_MASK_CROSS) != CROSS) {  // a worklist of another mask
+        if (tid == 0 && blockIdx.x == 0) atomicCAS(err_word, 0, kErrBadWorklist);
+        return;
+    }
     // the worklist's dispatch: static per-CTA lists of `units`, or (dynamic)
     // ranks of `dorder` claimed at run time from the worklist's counter
     const bool dyn = h->dispatch == PVA_DISPATCH_DYNAMIC;

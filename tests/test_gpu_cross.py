@@ -244,6 +244,22 @@ def test_a_worklist_of_another_kind_is_refused():
     r.build().forward().check()
 
 
+def test_a_worklist_of_another_kind_is_refused_by_the_backward():
+    p = Pack([(40, 40), (30, 30)], 4, 2, 64)
+    r = Run(p).build().forward()
+    causal = api.make_mask(api.MASK_CAUSAL, p.tq, p.tk)
+    for built, called in ((causal, r.mask), (r.mask, causal)):
+        api.build_worklist(r.cu, built, r.params, r.wl)
+        plan = api.alloc_bwd_plan(2, r.mask, r.params)
+        api.build_bwd_plan(r.wl, 2, built, r.params, plan)
+        dq, dk, dv = (torch.full(x.shape, math.nan, dtype=torch.bfloat16, device="cuda") for x in (r.q, r.k, r.v))
+        api.attn_bwd(r.q, r.k, r.v, r.out, r.lse, r.dout, r.cu, 2, called, r.params, r.wl, plan, dq, dk, dv)
+        torch.cuda.synchronize()
+        assert api.worklist_error(r.wl) == 102 and bool(torch.isnan(dq).all())
+    got = r.build().backward()
+    _check([to_np(x) for x in got], [x.numpy() for x in p.gradients()], "after a refusal")
+
+
 def test_refused_by_the_binding():
     p = Pack([(40, 50), (30, 60)], 4, 2, 64)
     r = Run(p)
