@@ -1200,7 +1200,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // query past the tile gets LSE = +inf: every P of it is 0.
         uint32_t li = 0;
         bool live = true;
-        if (h->kind == PVA_MASK_CROSS) wait_previous();
+        bool waits = h->kind == PVA_MASK_CROSS;  // until dQ is done, before the first D that its kernel makes
         for (uint32_t rd = 0; live; ++rd) {
             live = uring_wait_warp(sh.ur, rd, abort_flag, err_word, kErrTimeoutBase + 41, kWaitNs);
             if (!live) break;
@@ -1209,9 +1209,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int32_t kvh = slot.u.kvh;
             const bool none = slot.u.cost <= 1;
             const int32_t qlo0 = slot.qlo, qhi0 = slot.qhi, q_len0 = slot.s.q_len, q_row00 = slot.s.q_row0;
+            const bool one_tile = slot.s.k_len <= 128;
             uring_release_warp(sh.ur, rd);
             if (idx < 0) break;
             if (none) continue;
+            if (waits && one_tile) {
+                wait_previous();
+                waits = false;
+            }
             for (int32_t m = 0; m < gcount && live; ++m) {
                 int32_t qlo = qlo0, qhi = qhi0, q_len = q_len0, q_row0 = q_row00;
                 if (m > 0) {
