@@ -309,13 +309,16 @@ pva_status pva_build_bwd_plan(const void* worklist_dev, int32_t num_docs,
 
 /* Attention backward over the forward worklist and the backward plan.
  *   q, k, v        DEVICE bf16, as for pva_attn_fwd
- *   out, lse       DEVICE: the forward's bf16 output and fp32 LSE [Hq, q_tokens]
+ *   out, lse       DEVICE: the forward's bf16 output and fp32 LSE [Hq, q_tokens].  Where the
+ *                  keys are attended in parts (pva_attn_fwd_accumulate, pva_merge_partials)
+ *                  every part's call takes the joined ones: its dk and dv are then those of
+ *                  its keys, and the parts' dq add up
  *   dout           DEVICE bf16 [q_tokens, Hq, head_dim]
  *   dq             DEVICE [q_tokens, Hq, head_dim], dk/dv DEVICE [k_tokens, Hkv,
  *                  head_dim]; bf16 (grads_are_fp32 = 0) or fp32 (= 1); written
  *                  (rows no slice reaches get 0)
  *   softmax_scale  <= 0 selects 1/sqrt(head_dim)
- * Four kernels on `stream` (D, dQ, dK/dV); device failures go to the forward
+ * Three kernels on `stream` (D, dQ, dK/dV); device failures go to the forward
  * worklist's error word. */
 pva_status pva_attn_bwd(const void* q, const void* k, const void* v, const void* out,
                         const float* lse, const void* dout, const int32_t* cu_seqlens_dev,

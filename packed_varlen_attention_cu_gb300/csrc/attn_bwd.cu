@@ -6,8 +6,9 @@
 //   dP = dO V^T,  D = rowsum(dO * O),  dS = P (dP - D),
 //   dQ = scale dS K,  dK = scale dS^T Q,  dV = P^T dO.
 // Three kernels, no atomics (each output row has one writer):
-//   bwd_pre   D per (row, head), HBM-bound (under a CROSS mask for sources past 128
-//             keys; bwd_dq makes the others');
+//   bwd_pre   D per (row, head), HBM-bound.  Never from this call's own P and dP: the
+//             caller's O and LSE may be joined from more keys than the call has (sources
+//             attended in parts), and then sum P dP over these is not D;
 //   bwd_dq    q-major over the forward worklist's units, dispatched as the
 //             worklist says (static per-CTA LPT lists, or claimed at run time):
 //             per query sub-tile (Q and dO copied into tensor memory), every
@@ -34,7 +35,6 @@
 #include <string.h>
 
 #include "../../include/pva.h"
-#include "cache.cuh"
 #include "common.h"
 #include "launch.cuh"
 #include "ptx.cuh"
@@ -84,8 +84,10 @@ struct BwdParams {
     void* dv;            // [Tk, Hkv, d]
     int32_t q_tokens, k_tokens, hq, hkv, grads_fp32, num_ctas, d;
     float scale, scale_log2;
+    int32_t cross;       // 1: a CROSS mask
 };
 
+constexpr int kURing = 8;  // units the producer may run ahead
 constexpr int kLdSlots = 8;
 constexpr int kMaxStages = 12;
 
@@ -98,12 +100,12 @@ struct KvSlot {
     WlSlice s;
 };
 
-template <class Slot, int R>
+template <class Slot>
 struct BShared {
     uint64_t a_full, a_empty, o_full, o_empty, done, done2;
     uint64_t s2_full[3], p2_full[3];  // per half-item tensor-memory buffer
     uint64_t r_full[kMaxStages], r_empty[kMaxStages];
-    UnitRing<R, Slot> ur;  // the producer hands each unit to the other roles
+    UnitRing<kURing, Slot> ur;  // the producer hands each unit to the other roles
     // bwd_dkdv: (LSE log2, D) of each half-item's 64 queries, staged ahead by a
     // loader warp (ld_full: 32 lane arrivals; ld_empty: one per element-wise warp)
     uint64_t ld_full[kLdSlots], ld_empty[kLdSlots];
@@ -162,68 +164,6 @@ __global__ void __launch_bounds__(256) bwd_pre_kernel(const BwdParams p) {
     }
 }
 
-struct PreCross {
-    const int32_t *cu, *cu_keys;  // null: another mask
-    int32_t num_docs, chunk;      // chunk: tokens of a block
-};
-
-// The same under a CROSS mask, for the rows of sources past 128 keys; of the others bwd_dq makes D itself.  A
-// block takes a chunk of tokens, document by document.
-template <int D>
-__global__ void __launch_bounds__(256) bwd_pre_cross_kernel(const BwdParams p, const PreCross x) {
-    constexpr int S = D / 64;
-    let_next_start();
-    const int32_t t0 = blockIdx.x * x.chunk, t1 = min(t0 + x.chunk, p.q_tokens);
-    const int32_t group = threadIdx.x >> 3, sub = threadIdx.x & 7;
-    int32_t doc = find_seq(x.cu, x.num_docs, t0);
-    // (offsets that do not fit were refused when the worklist was built; here they only must not lead outside)
-    for (int32_t lo = t0; lo < t1;) {
-        int32_t hi = t1;
-        if (doc >= 0 && doc < x.num_docs) {
-            hi = min(t1, x.cu[doc + 1]);
-            const int32_t n = x.cu_keys[doc + 1] - x.cu_keys[doc];
-            ++doc;
-            if (hi <= lo) continue;
-            if (n <= 128) {
-                lo = hi;
-                continue;
-            }
-        }
-        const int64_t r0 = (int64_t)lo * p.hq;
-        const int32_t items = (hi - lo) * p.hq;
-        for (int32_t i0 = 0; i0 < items; i0 += 32) {
-            const bool live = i0 + group < items;
-            const int32_t i = live ? i0 + group : 0;
-            const int32_t t = lo + (int32_t)((uint32_t)i / (uint32_t)p.hq), h = i - (t - lo) * p.hq;
-            const uint4* o = reinterpret_cast<const uint4*>(p.out) + (r0 + i) * (D / 8) + sub;
-            const uint4* g = reinterpret_cast<const uint4*>(p.dout) + (r0 + i) * (D / 8) + sub;
-            uint4 a[S], b[S];
-#pragma unroll
-            for (int c = 0; c < S; ++c) {
-                a[c] = o[8 * c];
-                b[c] = g[8 * c];
-            }
-            float acc = 0.f;
-#pragma unroll
-            for (int c = 0; c < S; ++c) {
-                const uint32_t av[4] = {a[c].x, a[c].y, a[c].z, a[c].w};
-                const uint32_t bv[4] = {b[c].x, b[c].y, b[c].z, b[c].w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float2 fa = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&av[e]));
-                    const float2 fb = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&bv[e]));
-                    acc += fa.x * fb.x + fa.y * fb.y;
-                }
-            }
-            acc += __shfl_xor_sync(0xffffffffu, acc, 1);
-            acc += __shfl_xor_sync(0xffffffffu, acc, 2);
-            acc += __shfl_xor_sync(0xffffffffu, acc, 4);
-            if (live && sub == 0) p.dvec[(int64_t)h * p.q_tokens + t] = acc;
-        }
-        lo = hi;
-    }
-}
-
 // Writes 32 fp32 accumulator columns of one row, scaled, as fp32 or bf16.
 __device__ __forceinline__ void store_row32(void* base, int64_t row_elem, bool fp32,
                                             const uint32_t (&v)[32], float scale) {
@@ -266,8 +206,8 @@ __device__ __forceinline__ void store_zero_row(void* base, int64_t row_elem, boo
 // per use and reads every unit.  acc_issuers: the warps that commit o_full (the
 // ones whose MMAs write the accumulators).  item_warps: the element-wise warps
 // that work on each half-item (p2_full and ld_empty count one arrival each)
-template <class Slot, int R>
-__device__ __forceinline__ void init_barriers(BShared<Slot, R>& sh, int stages, int elem_threads,
+template <class Slot>
+__device__ __forceinline__ void init_barriers(BShared<Slot>& sh, int stages, int elem_threads,
                                               int extra_readers, int issuers, int acc_issuers,
                                               int item_warps) {
     mbar_init(&sh.a_full, 1);
@@ -302,7 +242,7 @@ __device__ __forceinline__ void init_barriers(BShared<Slot, R>& sh, int stages, 
 // of two 64-column buffers (s2_full/p2_full) and are issued before dQ += dS K
 // of half-item u - 1, so dS of u - 1 is computed while the pipe works on u.
 // o_full/o_empty: dQ accumulated / read out.
-template <int D, bool CROSS>
+template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     bwd_dq_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
                   const __grid_constant__ CUtensorMap tmv, const __grid_constant__ CUtensorMap tmdo,
@@ -316,22 +256,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t* sQ = smem;
     uint8_t* sDO = smem + C::kTileBytes;
     uint8_t* sKV = smem + 2 * C::kTileBytes;
-    constexpr int kURing = 4;  // units the producer may run ahead
-    __shared__ BShared<UnitSlot, kURing> sh;
-    // CROSS: sums of P dP over the two warpgroups' columns
-    __shared__ uint64_t sum_full, sum_empty;
-    __shared__ float sums[2][CROSS ? 128 : 1];
-    static_assert(C::kSmemDq + sizeof(sh) + sizeof(sums) + 16 <= 227 * 1024, "shared memory of a block");
+    __shared__ BShared<UnitSlot> sh;
+    static_assert(C::kSmemDq + sizeof(sh) <= 227 * 1024, "shared memory of a block");
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const WlHeader* h = reinterpret_cast<const WlHeader*>(p.wl);
     int32_t* err_word = const_cast<int32_t*>(&h->error);
     // This kernel may start while the one that makes D still runs.  Once it has ended, the kernel of
     // dK and dV may start wherever this one leaves a multiprocessor free: it reads nothing that this
-    // one writes, but under a CROSS mask parts of D, and ends after it (see there).
+    // one writes, and ends after it (see there).
     wait_previous();
     let_next_start();
     if (h->error != 0) return;
-    if ((h->kind == PVA_MASK_CROSS) != CROSS) {  // a worklist of another mask
+    if ((h->kind == PVA_MASK_CROSS) != (p.cross != 0)) {  // a worklist of another mask
         if (tid == 0 && blockIdx.x == 0) atomicCAS(err_word, 0, kErrBadWorklist);
         return;
     }
@@ -349,11 +285,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int32_t* cta_off = reinterpret_cast<const int32_t*>(p.wl + h->off.cta_off);
     const int32_t ub = dyn ? 0 : cta_off[blockIdx.x], ue = dyn ? 0 : cta_off[blockIdx.x + 1];
     if (!dyn && ub >= ue) return;
-    if (tid == 0) {
-        mbar_init(&sum_full, 8);
-        mbar_init(&sum_empty, 8);
-        init_barriers(sh, C::kStagesDq, 256, 0, 2, 1, 8);
-    }
+    if (tid == 0) init_barriers(sh, C::kStagesDq, 256, 0, 2, 1, 8);
     if (warp == 1) {
         tmem_alloc(&sh.tmem_base, 512);
         tmem_relinquish();
@@ -659,7 +591,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int r = (warp & 3) * 32 + lane;  // query row = tensor-memory lane
         const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t tS = tmem + lane_base, tQ = tmem + lane_base + 256;
-        uint32_t gu = 0, o_cnt = 0, sum_cnt = 0;
+        uint32_t gu = 0, o_cnt = 0;
         bool live = true;
         // Unit n from the producer's ring, kept until this thread has done with its tiles: the (LSE, D)
         // of its rows and, in a tile shared by pairs, the key interval of the row are asked for as soon
@@ -680,7 +612,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (i < slot.u.nsub && r < slot.u.st[i].nrows) {
                     const int64_t li = (int64_t)slot.u.st[i].head * p.q_tokens + slot.u.st[i].q_row + r;
                     lse_of[i] = p.lse[li];
-                    if (!CROSS || slot.u.ntiles > 1) d_of[i] = p.dvec[li];
+                    d_of[i] = p.dvec[li];
                 }
             }
             if (slot.s.type == kSlicePackedCross)
@@ -740,63 +672,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int32_t q_pos = st.q_pos + r;
                 const float l = i == 0 ? lse_of[0] : lse_of[1];
                 const float lse2 = l == -INFINITY ? INFINITY : l * 1.4426950408889634f;  // no key: every P is 0
-                float dd = i == 0 ? d_of[0] : d_of[1];
-                if (CROSS && slot.u.ntiles == 1) {
-                    // All keys of the row in one tile: D = sum_j P_j dP_j is at hand before any dS, and exact,
-                    // where the rowsum of dO and the O that the forward has rounded is not: with few keys dP - D
-                    // is small beside D.  (Sources of 1 to 8 keys: dQ and dK off by 0.0030, now 0.0024; of 5 to
-                    // 120: 0.0025, now 0.0023, which is the bf16 dS and result.  The whole backward of 209 groups of
-                    // short pairs 154 -> 162 us, though O is not read again.  P is computed twice: kept in
-                    // registers it took 160, but spilled, and long sources lost 4%.)
-                    int32_t lo = 0, hi = valid ? slot.s.k_len : 0;
-                    if (slot.s.type == kSlicePackedCross) {
-                        lo = pair_keys & 255u;
-                        hi = valid ? pair_keys >> 8 : 0u;
-                    }
-                    const int32_t halves = slot.s.k_len > 64 ? 2 : 1;
-                    const float2 sc = make_float2(p.scale_log2, p.scale_log2);
-                    const float2 nl = make_float2(-lse2, -lse2);
-                    float part = 0.f;
-#pragma unroll 1
-                    for (int hf = 0; hf < halves; ++hf) {
-                        const uint32_t b = (gu + hf) & 1;
-                        live = mbar_wait(&sh.s2_full[b], ((gu + hf) >> 1) & 1, abort_flag, err_word,
-                                         kErrTimeoutBase + 27, kWaitNs);
-                        if (!live) break;
-                        tc_fence_after();
-                        uint32_t sv[32], pv[32];
-                        tmem_ld32(tS + 64 * b + wg * 32, sv);
-                        tmem_ld32(tS + 128 + 64 * b + wg * 32, pv);
-                        tmem_ld_wait(sv);
-                        tmem_ld_wait(pv);
-                        float2 acc = make_float2(0.f, 0.f);
-#pragma unroll
-                        for (int e = 0; e < 32; e += 2) {
-                            const int col = hf * 64 + wg * 32 + e;
-                            const float2 x = __ffma2_rn(
-                                make_float2(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1])), sc, nl);
-                            float p0 = ex2_approx(x.x), p1 = ex2_approx(x.y);
-                            if (col < lo || col >= hi) p0 = 0.f;
-                            if (col + 1 < lo || col + 1 >= hi) p1 = 0.f;
-                            acc = __ffma2_rn(make_float2(p0, p1),
-                                             make_float2(__uint_as_float(pv[e]), __uint_as_float(pv[e + 1])), acc);
-                        }
-                        part += acc.x + acc.y;
-                    }
-                    live = live && mbar_wait(&sum_empty, (sum_cnt & 1) ^ 1, abort_flag, err_word,
-                                             kErrTimeoutBase + 27, kWaitNs);
-                    if (!live) break;
-                    sums[wg][CROSS ? r : 0] = part;
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&sum_full);
-                    live = mbar_wait(&sum_full, sum_cnt & 1, abort_flag, err_word, kErrTimeoutBase + 27, kWaitNs);
-                    if (!live) break;
-                    ++sum_cnt;
-                    dd = part + sums[wg ^ 1][CROSS ? r : 0];  // (the same in both orders)
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&sum_empty);
-                    if (wg == 0 && valid) p.dvec[(int64_t)st.head * p.q_tokens + st.q_row + r] = dd;
-                }
+                const float dd = i == 0 ? d_of[0] : d_of[1];
                 const int32_t run_count = slot.u.run_count;
                 for (int32_t rr = 0; rr < run_count && live; ++rr) {
                     WlRun run{slot.slice, slot.lo, slot.hi, 0};
@@ -919,15 +795,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t* sK = smem;
     uint8_t* sV = smem + C::kTileBytes;
     uint8_t* sR = smem + 2 * C::kTileBytes;  // half-item stage x at x * 2 * kHalfBytes
-    constexpr int kURing = 8;  // units the producer may run ahead
-    __shared__ BShared<KvSlot, kURing> sh;
+    __shared__ BShared<KvSlot> sh;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const WlHeader* h = reinterpret_cast<const WlHeader*>(p.wl);
     const BwdHeader* bh = reinterpret_cast<const BwdHeader*>(p.plan);
     int32_t* err_word = const_cast<int32_t*>(&h->error);
     // This kernel may run beside that of dQ, which began only when all before it had ended.  No block
     // leaves before dQ is done, so that the end of this kernel is the end of both.
-    // (CROSS: dQ's kernel makes part of D, and the warp that reads D waits first.)
     struct EndAfterPrevious {
         __device__ ~EndAfterPrevious() { wait_previous(); }
     } end_after;
@@ -1200,7 +1074,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         // query past the tile gets LSE = +inf: every P of it is 0.
         uint32_t li = 0;
         bool live = true;
-        bool waits = h->kind == PVA_MASK_CROSS;  // until dQ is done, before the first D that its kernel makes
         for (uint32_t rd = 0; live; ++rd) {
             live = uring_wait_warp(sh.ur, rd, abort_flag, err_word, kErrTimeoutBase + 41, kWaitNs);
             if (!live) break;
@@ -1209,14 +1082,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int32_t kvh = slot.u.kvh;
             const bool none = slot.u.cost <= 1;
             const int32_t qlo0 = slot.qlo, qhi0 = slot.qhi, q_len0 = slot.s.q_len, q_row00 = slot.s.q_row0;
-            const bool one_tile = slot.s.k_len <= 128;
             uring_release_warp(sh.ur, rd);
             if (idx < 0) break;
             if (none) continue;
-            if (waits && one_tile) {
-                wait_previous();
-                waits = false;
-            }
             for (int32_t m = 0; m < gcount && live; ++m) {
                 int32_t qlo = qlo0, qhi = qhi0, q_len = q_len0, q_row0 = q_row00;
                 if (m > 0) {
@@ -1450,12 +1318,10 @@ template <int D>
 pva_status launch_bwd(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
                       const CUtensorMap& mdo, const CUtensorMap& mq64, const CUtensorMap& mdo64,
                       const CUtensorMap& mk64, const CUtensorMap& mv64, const BwdParams& bp,
-                      const PreCross& px, int32_t dkdv_ctas, cudaStream_t st) {
+                      int32_t dkdv_ctas, cudaStream_t st) {
     const int grid_pre = 8 * bp.num_ctas;
-    const bool cross = px.cu_keys != nullptr;
-    if (cross) bwd_pre_cross_kernel<D><<<(bp.q_tokens + px.chunk - 1) / px.chunk, 256, 0, st>>>(bp, px);
-    else bwd_pre_kernel<D><<<grid_pre, 256, 0, st>>>(bp);
-    auto kq = cross ? bwd_dq_kernel<D, true> : bwd_dq_kernel<D, false>;
+    bwd_pre_kernel<D><<<grid_pre, 256, 0, st>>>(bp);
+    auto kq = bwd_dq_kernel<D>;
     auto kk = bwd_dkdv_kernel<D>;
     // setmaxnreg.inc draws from the registers the block was launched with: the
     // dK/dV split must fit in (threads x registers per thread)
@@ -1471,14 +1337,14 @@ pva_status launch_bwd(const CUtensorMap& mq, const CUtensorMap& mk, const CUtens
         return PVA_ERR_CUDA;
     if (cudaGetLastError() != cudaSuccess ||
         launch_after(kq, dim3(bp.num_ctas), kThreads, BCfg<D>::kSmemDq, st, mq, mk64, mv64, mdo, bp) !=
+            cudaSuccess ||
+        launch_after(kk, dim3(dkdv_ctas), kThreads, BCfg<D>::kSmemKv, st, mq64, mk, mv, mdo64, bp) !=
             cudaSuccess)
         return PVA_ERR_CUDA;
-    return launch_after(kk, dim3(dkdv_ctas), kThreads, BCfg<D>::kSmemKv, st, mq64, mk, mv, mdo64, bp) ==
-                   cudaSuccess
-               ? PVA_OK
-               : PVA_ERR_CUDA;
+    return PVA_OK;
 }
 
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 }  // namespace
 }  // namespace pva
@@ -1571,8 +1437,7 @@ extern "C" pva_status pva_attn_bwd(const void* q, const void* k, const void* v, 
     bp.d = head_dim;
     bp.scale = softmax_scale > 0.f ? softmax_scale : 1.0f / sqrtf((float)head_dim);
     bp.scale_log2 = bp.scale * 1.4426950408889634f;
-    const PreCross px{cu_seqlens_dev, cross ? mask->cu_keys : nullptr, num_docs,
-                      bp.hq >= 64 ? 4 : 256 / bp.hq};  // eight passes of 32 rows
-    return head_dim == 128 ? launch_bwd<128>(mq, mk, mv, mdo, mq64, mdo64, mk64, mv64, bp, px, nc, st)
-                           : launch_bwd<64>(mq, mk, mv, mdo, mq64, mdo64, mk64, mv64, bp, px, nc, st);
+    bp.cross = cross ? 1 : 0;
+    return head_dim == 128 ? launch_bwd<128>(mq, mk, mv, mdo, mq64, mdo64, mk64, mv64, bp, nc, st)
+                           : launch_bwd<64>(mq, mk, mv, mdo, mq64, mdo64, mk64, mv64, bp, nc, st);
 }

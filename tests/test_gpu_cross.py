@@ -288,6 +288,64 @@ def test_sources_cut_in_two_are_joined_by_accumulation():
 
 
 @pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("pack", [0, 1])
+def test_gradients_of_sources_cut_in_two(d, pack):
+    """Each part's call gets the joined O and LSE, so its P sums to less than 1 and D = rowsum(dO O) is of all keys: dK and dV
+    of a part are those of its keys, dQ adds up.  Parts of 1 to 128 keys and of more, in shared tiles and in their own."""
+    p = Pack([(40, 120), (100, 300), (7, 20), (150, 129), (3, 2), (60, 256), (33, 500), (2, 12), (20, 30)], 4, 2, d, seed=11 + d)
+    cuts = [60, 100, 10, 64, 1, 128, 1, 5, 29]
+    o_run = torch.full(p.q.shape, math.nan, device="cuda")
+    l_run = torch.full((4, p.tq), -math.inf, device="cuda")
+    parts = []
+    for first in (True, False):
+        rows = [i for c, (_, n), cut in zip(p.ck.tolist(), p.pairs, cuts) for i in range(c, c + n) if (i - c < cut) == first]
+        part = Pack([(m, cut if first else n - cut) for (m, n), cut in zip(p.pairs, cuts)], 4, 2, d)
+        part.q, part.dout, part.k, part.v = p.q, p.dout, p.k[rows], p.v[rows]
+        r = Run(part, pack).build()
+        api.attn_fwd_accumulate(r.q, r.k, r.v, r.cu, r.mask, r.params, r.wl, o_run, l_run)
+        parts.append((rows, part, r))
+    whole, joined = p.gradients(), p.forward()
+    total, norms = torch.zeros_like(whole[0]), 0
+    for rows, part, r in parts:
+        part.forward = lambda: joined  # (the formulas read O and LSE from here)
+        r.out, r.lse = o_run.bfloat16(), l_run
+        got = r.backward(fp32=True)
+        want = part.gradients()
+        _check([to_np(x) for x in got], [x.numpy() for x in want], f"part of {len(rows)} keys")
+        assert (want[1] - whole[1][rows]).norm() < 1e-9 * whole[1].norm() and (want[2] - whole[2][rows]).norm() < 1e-9 * whole[2].norm()
+        total += got[0].double().cpu()
+        norms += want[0].norm()
+    assert (total - whole[0]).norm() <= REL_L2 * norms
+
+
+def test_short_sources_beside_long_ones_on_one_cta():
+    """dQ of one CTA takes more than two seconds, as long as a wait may take, while dK and dV begin with the short source:
+    nothing of theirs may wait for the end of dQ under that limit.  All results are those of every CTA, bit for bit."""
+    g = torch.Generator(device="cuda").manual_seed(1)
+    hq, hkv, d, rows, keys = 32, 8, 128, [45056, 90112], [45056, 100]
+    q, dout = (torch.randn((sum(rows), hq, d), generator=g, device="cuda").bfloat16() for _ in range(2))
+    k, v = (torch.randn((sum(keys), hkv, d), generator=g, device="cuda").bfloat16() for _ in range(2))
+    cu, ck = i32([0, rows[0], sum(rows)]), i32([0, keys[0], sum(keys)])
+    mask = api.make_mask(api.MASK_CROSS, sum(rows), sum(keys), cu_keys=ck)
+    got = []
+    for ctas in (0, 1):
+        params = api.make_params(hq, hkv, c_tile=api.default_c_tile(d), num_ctas=ctas)
+        wl, plan = api.alloc_worklist(2, mask, params), api.alloc_bwd_plan(2, mask, params)
+        api.build_worklist(cu, mask, params, wl)
+        api.build_bwd_plan(wl, 2, mask, params, plan)
+        if ctas == 0:
+            out, lse = torch.empty_like(q), torch.empty((hq, sum(rows)), device="cuda")
+            api.attn_fwd(q, k, v, cu, mask, params, wl, out, lse)
+        grads = [torch.full_like(x, math.nan) for x in (q, k, v)]
+        api.attn_bwd(q, k, v, out, lse, dout, cu, 2, mask, params, wl, plan, *grads)
+        torch.cuda.synchronize()
+        assert api.worklist_error(wl) == 0
+        got.append(grads)
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("hq", [1, 5])
 @pytest.mark.parametrize("dispatch", [api.DISPATCH_DYNAMIC, api.DISPATCH_STATIC])
 @pytest.mark.parametrize("accumulate", [False, True])
