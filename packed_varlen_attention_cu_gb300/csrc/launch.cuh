@@ -30,8 +30,8 @@ inline cudaError_t launch_after(void (*kernel)(P...), dim3 grid, int threads, si
     return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
 }
 
-// The backward lets its next kernel start early: once every block has come here (or has ended),
-// blocks of the kernel launched after this one take the multiprocessors that become free.
+// The kernel of the backward that makes D lets the next one start early: once every block has come here (or
+// has ended), blocks of the kernel launched after this one take the multiprocessors that are free, and wait.
 __device__ __forceinline__ void let_next_start() {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
