@@ -480,8 +480,9 @@ pva_status pva_cache_attn(const pva_cache_desc* cache, const pva_cache_batch* ba
  * and LSE = -inf.  A source is read once for its rows and heads of a group, up to 64 of
  * them, so rows of a source belong into one sequence of the batch.  Otherwise as
  * pva_cache_attn, workspace (pva_cache_attn_bytes) and values too; a slot whose position has
- * no page is left out for all rows.  With more than 32 rows of a kv head, or more than 16
- * with 4 bits, weights have 8 bits in the products. */
+ * no page is left out for all rows.  Weights
+ * have 16 bits in the products where out is fp32; where it is bf16 and max_new tokens make
+ * more than 32 rows of a kv head, or more than 16 with 4 bits, they have 8. */
 pva_status pva_cache_cross_attn(const pva_cache_desc* cache, const pva_cache_batch* batch,
                                 const void* q, int64_t q_stride, int32_t num_q_heads,
                                 int32_t max_new, float softmax_scale, void* out,

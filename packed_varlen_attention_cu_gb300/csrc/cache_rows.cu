@@ -62,14 +62,13 @@ __device__ __forceinline__ uint4 spread_centred(uint32_t w) {
                       centred(low_codes(w >> 12)));
 }
 
-template <class Sh, int KIND>
+// TWO: weights are operands as the sum of two bf16 numbers, 16 of their bits, else as one.
+template <class Sh, bool TWO>
 __global__ void __launch_bounds__(128, Sh::kCtas) rows_kernel(const AttnArgs a) {
     constexpr int D = Sh::D, NT = Sh::NT, WR = Sh::WR, WK = Sh::WK, Z = Sh::Z, R = Sh::R, S = Sh::kStages;
     constexpr int G = Sh::G, T = D / 16, KEYS = Sh::kKeys, ROWB = Sh::kRowBytes, JP = Sh::kPitch;
     constexpr bool INT4 = Sh::kInt4;
     constexpr int GA = INT4 ? G : 1;   // groups with products of their own
-    constexpr bool TWO = !INT4 && NT == 1;  // weights as two bf16 numbers
-    constexpr int PP = INT4 ? G : TWO ? 2 : 1;  // operands made of a weight
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ float join_m[WK][R], join_l[WK][R];
     wait_previous();
@@ -332,66 +331,72 @@ __global__ void __launch_bounds__(128, Sh::kCtas) rows_kernel(const AttnArgs a) 
                                 }
                             }
                     }
-                    // ---- weights as operands.  bf16, up to 32 rows: the sum of two bf16 numbers, 16 of a
-                    // weight's bits, whose products hide behind HBM.  With more rows the tensor cores are
-                    // half busy, and one number (2^-9 of each weight, about what the bf16 result loses
-                    // again) takes 48 rows of 128 dims from 253 to 197 us, 56 of 64 dims from 128 to 102.
-                    // 4 bits: weight * scale as one number (2^-9 of scale * |code - 8|, which is no larger
-                    // than the values); weight * (low + 8 scale) stays in fp32.
-                    uint32_t pf[Z][PP][NT][2];
+                    // ---- weights, in place of the scores
 #pragma unroll
-                    for (int z = 0; z < Z; ++z) {
-                        uint32_t sc[2][G];
-                        if (INT4) scales(sc, true, 16 * (wk * Z + z) + g);
+                    for (int z = 0; z < Z; ++z)
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                            for (int y = 0; y < 2; ++y) {
-                                float p[2];
-#pragma unroll
-                                for (int e = 0; e < 2; ++e) {
-                                    const float base = m_run[nt][e] == -INFINITY ? 0.f : m_run[nt][e];
-                                    p[e] = ex2((s[z][nt][2 * y + e] - base) * a.c);
-                                    l_run[nt][e] += p[e];
-                                }
-                                if (INT4) {
-#pragma unroll
-                                    for (int gr = 0; gr < G; ++gr) {
-                                        const float scl = lo_f(sc[y][gr]), mid = fmaf(8.f, scl, hi_f(sc[y][gr]));
-                                        pf[z][gr % PP][nt][y] = transpose8(pack2(p[0] * scl, p[1] * scl));
-#pragma unroll
-                                        for (int e = 0; e < 2; ++e)
-                                            zs[INT4 ? gr : 0][nt][e] = fmaf(p[e], mid, zs[INT4 ? gr : 0][nt][e]);
-                                    }
-                                } else {
-                                    const uint32_t hi = pack2(p[0], p[1]);
-                                    pf[z][0][nt][y] = transpose8(hi);
-                                    if (TWO) pf[z][PP - 1][nt][y] = transpose8(pack2(p[0] - lo_f(hi), p[1] - hi_f(hi)));
-                                }
+                            for (int e = 0; e < 4; ++e) {
+                                const float base = m_run[nt][e & 1] == -INFINITY ? 0.f : m_run[nt][e & 1];
+                                s[z][nt][e] = ex2((s[z][nt][e] - base) * a.c);
+                                l_run[nt][e & 1] += s[z][nt][e];
                             }
-                    }
-                    // ---- O^T.  The products round their sums towards 0: those of a tile start from 0 and go
-                    // onto the sums by additions, which round to nearest.
+                    // ---- O^T, group by group of dims.  Operands are the weights, with 4 bits weight * scale, as the sum
+                    // of two bf16 numbers where that hides behind HBM (a bf16 cache, up to 32 rows) or the result
+                    // is fp32, which keeps the difference.  A bf16 result takes one number otherwise, as the packs do:
+                    // 2^-9 of each weight, about what it loses again itself (off by 0.0024, not 0.0017), for 105 us
+                    // instead of 121 (24 sources to 30000 keys in 4 bits, 32 rows of 128 dims), 241 instead of 301 (64
+                    // sources to 8192, 48 rows), 431 instead of 575 (64 sources of 8192, bf16, 48 rows).  4 bits: what
+                    // the weights meet, scale * (code - 8), is no larger than the values; weight * (low + 8 scale)
+                    // stays in fp32.
 #pragma unroll
-                    for (int i = 0; i < T; ++i) {
-                        float y[NT][4];
-                        const int gr = INT4 ? i / 4 : 0;
+                    for (int gr = 0; gr < GA; ++gr) {
+                        uint32_t pf[Z][TWO ? 2 : 1][NT][2];
 #pragma unroll
                         for (int z = 0; z < Z; ++z) {
-                            uint32_t f[4];
-                            const int r = (lane & 7) + ((lane >> 4) << 3), ch = 2 * i + ((lane >> 3) & 1);
-                            ldsm_t(f, vb + (16 * (wk * Z + z) + r) * 2 * D + ((ch ^ (r & 7)) << 4));
+                            uint32_t sc[2][G];
+                            if (INT4) scales(sc, true, 16 * (wk * Z + z) + g);
 #pragma unroll
-                            for (int nt = 0; nt < NT; ++nt) {
-                                if (z == 0) mma0(y[nt], f, pf[z][gr][nt][0], pf[z][gr][nt][1]);
-                                else mma(y[nt], f, pf[z][gr][nt][0], pf[z][gr][nt][1]);
-                                if (TWO) mma(y[nt], f, pf[z][PP - 1][nt][0], pf[z][PP - 1][nt][1]);
-                            }
+                            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                                for (int y = 0; y < 2; ++y) {
+                                    float p0 = s[z][nt][2 * y], p1 = s[z][nt][2 * y + 1];
+                                    if (INT4) {
+                                        const float scl = lo_f(sc[y][gr]), mid = fmaf(8.f, scl, hi_f(sc[y][gr]));
+                                        zs[gr][nt][0] = fmaf(p0, mid, zs[gr][nt][0]);
+                                        zs[gr][nt][1] = fmaf(p1, mid, zs[gr][nt][1]);
+                                        p0 *= scl;
+                                        p1 *= scl;
+                                    }
+                                    const uint32_t hi = pack2(p0, p1);
+                                    pf[z][0][nt][y] = transpose8(hi);
+                                    if (TWO) pf[z][TWO ? 1 : 0][nt][y] = transpose8(pack2(p0 - lo_f(hi), p1 - hi_f(hi)));
+                                }
                         }
+                        // The products round their sums towards 0: those of a tile start from 0 and go onto the sums
+                        // by additions, which round to nearest.
+                        constexpr int IG = T / GA;  // tiles of 16 dims of a group
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
+                        for (int i = gr * IG; i < (gr + 1) * IG; ++i) {
+                            float y[NT][4];
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) o[nt][i][e] += y[nt][e];
+                            for (int z = 0; z < Z; ++z) {
+                                uint32_t f[4];
+                                const int r = (lane & 7) + ((lane >> 4) << 3), ch = 2 * i + ((lane >> 3) & 1);
+                                ldsm_t(f, vb + (16 * (wk * Z + z) + r) * 2 * D + ((ch ^ (r & 7)) << 4));
+#pragma unroll
+                                for (int nt = 0; nt < NT; ++nt) {
+                                    if (z == 0) mma0(y[nt], f, pf[z][0][nt][0], pf[z][0][nt][1]);
+                                    else mma(y[nt], f, pf[z][0][nt][0], pf[z][0][nt][1]);
+                                    if (TWO) mma(y[nt], f, pf[z][TWO ? 1 : 0][nt][0], pf[z][TWO ? 1 : 0][nt][1]);
+                                }
+                            }
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) o[nt][i][e] += y[nt][e];
+                        }
                     }
                     stage = stage + 1 == S ? 0 : stage + 1;
                 }
@@ -483,16 +488,16 @@ __global__ void __launch_bounds__(128, Sh::kCtas) rows_kernel(const AttnArgs a) 
     }
 }
 
-template <class Sh, int KIND>
+template <class Sh, bool TWO>
 pva_status launch(AttnArgs a, uint8_t* ws, cudaStream_t st) {
     static_assert((Sh::kSmem + 4096) * Sh::kCtas <= 228 * 1024, "the CTAs share an SM");
     place_workspace<Sh>(a, ws);
     const int sms = sm_count();
     if (sms <= 0) return PVA_ERR_CUDA;
     const int ctas = sms * Sh::kCtas < kMaxCtas ? sms * Sh::kCtas : kMaxCtas;
-    if (cudaFuncSetAttribute(rows_kernel<Sh, KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kSmem) !=
+    if (cudaFuncSetAttribute(rows_kernel<Sh, TWO>, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kSmem) !=
             cudaSuccess ||
-        launch_after(rows_kernel<Sh, KIND>, dim3(ctas), Sh::kThreads, Sh::kSmem, st, a) != cudaSuccess)
+        launch_after(rows_kernel<Sh, TWO>, dim3(ctas), Sh::kThreads, Sh::kSmem, st, a) != cudaSuccess)
         return PVA_ERR_CUDA;
     return launch_join<Sh::D, Sh>(a, st) == cudaSuccess ? PVA_OK : PVA_ERR_CUDA;
 }
@@ -500,9 +505,13 @@ pva_status launch(AttnArgs a, uint8_t* ws, cudaStream_t st) {
 template <int D>
 pva_status launch_kind(int32_t kind, int64_t rows, const AttnArgs& a, uint8_t* ws, cudaStream_t st) {
     constexpr int B = PVA_CACHE_BF16, I = PVA_CACHE_INT4;
-    if (kind == B)
-        return rows <= 32 ? launch<Rows<D, B, 1, 4>, B>(a, ws, st) : launch<Rows<D, B, 2, 4>, B>(a, ws, st);
-    return rows <= 32 ? launch<Rows<D, I, 2, 2>, I>(a, ws, st) : launch<Rows<D, I, 2, 4>, I>(a, ws, st);
+    const bool f32 = a.out_fp32 != 0;
+    if (kind == B) {
+        if (rows <= 32) return launch<Rows<D, B, 1, 4>, true>(a, ws, st);
+        return f32 ? launch<Rows<D, B, 2, 4>, true>(a, ws, st) : launch<Rows<D, B, 2, 4>, false>(a, ws, st);
+    }
+    if (rows <= 32) return f32 ? launch<Rows<D, I, 2, 2>, true>(a, ws, st) : launch<Rows<D, I, 2, 2>, false>(a, ws, st);
+    return f32 ? launch<Rows<D, I, 2, 4>, true>(a, ws, st) : launch<Rows<D, I, 2, 4>, false>(a, ws, st);
 }
 
 }  // namespace

@@ -8,7 +8,7 @@ import numpy as np
 import pytest
 import torch
 
-from cache_util import U16, U32, Problem, check_attention, pack, quantise, values
+from cache_util import U16, U32, Problem, check_attention, pack, quantise, unpack, values
 from gpu_util import compare, to_np
 from packed_varlen_attention_cu_gb300 import api
 from test_gpu_bwd import REL_L2, _check
@@ -515,6 +515,41 @@ def test_many_rows(int4, hq, hkv, d, most, page):
     assert bool(torch.isnan(out[-1]).all()) and bool(torch.isnan(lse[:, -1]).all())
     again = over_cache(p, fp32=page == 256, strided=page == 32)
     assert torch.equal(out[:-1], again[0][:-1]) and torch.equal(lse[:, :-1], again[1][:, :-1])
+
+
+@pytest.mark.parametrize("int4", [False, True])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("most", [1, 4, 5, 8, 9, 16, 17])
+def test_weights_have_16_bits_for_any_number_of_rows(int4, d, most):
+    """4 to 68 rows a kv head, fp32 results.  Queries are whole numbers and so are cached keys (4 bits: codes - 8), so scores
+    and their products with the scale 2^-4 are exact.  Weights: 2^-16 of each as the sum of two bf16 numbers, 2^-19 for the
+    exponent's argument and the exponential.  4 bits: they meet scale * (code - 8), no larger than 8 scale, and
+    middle = low + 8 scale, rounded to fp32.  Sums in fp32: 50 tiles of 64 keys and their joins, each 2^-23 of a sum of
+    magnitudes: 2^-17.  In all less than 2^-15 of the weighted magnitudes; one bf16 number a weight is off by up to 2^-8."""
+    p = Source([3000, 40, 7, 1, 130], [most, most, 1, most, most], 8, 2, d, 64, int4, seed=most + d)
+    g = torch.Generator().manual_seed(most)
+    p.q = torch.randint(-2, 3, p.q.shape, generator=g).bfloat16()
+    garbage = torch.isnan(p.k_scales if int4 else p.k)
+    if int4:
+        code = unpack(p.k)
+        pair = torch.tensor([1.0, -8.0]).expand(p.k_scales.shape)
+        p.rows["k"] = values(code, pair[..., 0], pair[..., 1])
+        p.k_scales = torch.where(garbage, torch.nan, pair).bfloat16()
+        scale, low = p.v_scales.double().nan_to_num().unbind(-1)
+        size = (8 * scale + (low + 8 * scale).abs())[..., None].expand(code.shape[:-1] + (d // 64, 64)).flatten(-2)
+    else:
+        k = torch.randint(-3, 4, p.k.shape, generator=g).double()
+        p.rows["k"] = k
+        p.k = torch.where(garbage, torch.nan, k).bfloat16()
+        size = p.rows["v"].abs().nan_to_num()
+    out, lse = over_cache(p, scale=2.0 ** -4, fp32=True)
+    o, l, _, _ = p.attend(scale=2.0 ** -4)
+    p.rows["v"] = size
+    bound = 2.0 ** -15 * p.attend(scale=2.0 ** -4)[0]
+    off = (out.double().cpu() - o).abs()
+    assert bool((off <= bound).all()), f"{(off / bound).max():.3g} of the bound"
+    # a sum of weights, its logarithm, the maximum in base 2 (below 2^6) and back
+    assert bool(((lse.double().cpu() - l).abs() <= 2.0 ** -17).all())
 
 
 @pytest.mark.parametrize("int4", [False, True])
