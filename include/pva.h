@@ -516,8 +516,8 @@ pva_status pva_cache_cross_attn(const pva_cache_desc* cache, const pva_cache_bat
  *                parent was finished (or NULL).  Places without a candidate: -inf, -1, -1, 0.
  *                None of them may overlap an input
  *   workspace    DEVICE, 256-byte aligned, pva_beam_select_bytes (HOST computation; 0 on
- *                invalid arguments); its contents need not be kept between calls; one call
- *                at a time */
+ *                invalid arguments), which is enough for fewer groups and a smaller vocab too;
+ *                its contents need not be kept between calls; one call at a time */
 size_t pva_beam_select_bytes(int32_t num_groups, int32_t beams, int32_t vocab, int32_t num_out);
 pva_status pva_beam_select(const void* logits, int64_t row_stride, int32_t logits_are_fp32,
                            int32_t num_groups, int32_t beams, int32_t vocab, int32_t num_out,

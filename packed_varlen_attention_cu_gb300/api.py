@@ -597,7 +597,7 @@ def beam_workspace_bytes(groups: int, beams: int, vocab: int, num_out: int) -> i
 
 
 def alloc_beam_workspace(groups: int, beams: int, vocab: int, num_out: int, device="cuda") -> torch.Tensor:
-    """Workspace of beam_select for these sizes; one call at a time uses it."""
+    """Workspace of beam_select for these sizes, and for fewer groups; one call at a time uses it."""
     return torch.empty(beam_workspace_bytes(groups, beams, vocab, num_out), dtype=_U8, device=device)
 
 

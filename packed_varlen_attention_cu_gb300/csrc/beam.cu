@@ -653,6 +653,9 @@ __global__ void __launch_bounds__(kJoin) join_kernel(const SelectArgs a) {
     }
 }
 
+// No more candidates of a group than the join's threads hold.
+int64_t parts_most(int32_t beams, int32_t k) { return (int64_t)kJoin * kJoinEach / ((int64_t)beams * k); }
+
 // How the rows' tiles are cut: tiles of a CTA, room for a row's parts, CTAs of a row or 0.
 struct Cut {
     int64_t tiles, per, parts, whole;
@@ -663,8 +666,7 @@ struct Cut {
 Cut cut_of(int64_t rows, int32_t beams, int32_t k, int64_t vectors) {
     Cut c;
     c.tiles = (vectors + kTile - 1) / kTile;
-    // no more candidates of a group than the join's threads hold
-    const int64_t most = (int64_t)kJoin * kJoinEach / ((int64_t)beams * k);
+    const int64_t most = parts_most(beams, k);
     int64_t parts = rows < kTargetCtas ? kTargetCtas / rows : 1;
     parts = parts < most ? parts : most;
     parts = parts < c.tiles ? parts : c.tiles;
@@ -684,6 +686,13 @@ Cut cut_of(int64_t rows, int32_t beams, int32_t k, int64_t vectors) {
 int64_t vectors_of(int32_t vocab, bool f32) {  // of a row that starts anywhere
     const int ve = f32 ? 4 : 8;
     return ((int64_t)vocab + ve - 1 + ve - 1) / ve;
+}
+
+// Parts of a row that the workspace has room for: the most that any number of rows is cut into (one for each
+// tile at most), so that a workspace serves every smaller number of groups, whose rows have more parts each.
+int64_t parts_room(int32_t beams, int32_t k, int32_t vocab) {
+    const int64_t most = parts_most(beams, k), tiles = (vectors_of(vocab, true) + kTile - 1) / kTile;
+    return most < tiles ? most : tiles;
 }
 
 // ---------------------------------------------------------------- reordering
@@ -874,9 +883,7 @@ extern "C" size_t pva_beam_select_bytes(int32_t num_groups, int32_t beams, int32
     const int64_t rows = (int64_t)num_groups * beams;
     if (rows > INT32_MAX / kTargetCtas) return 0;
     if (rows == 0) return 256;
-    const int64_t a = cut_of(rows, beams, num_out, vectors_of(vocab, true)).parts;
-    const int64_t b = cut_of(rows, beams, num_out, vectors_of(vocab, false)).parts;
-    return 256 + (size_t)rows * (a > b ? a : b) * (sizeof(PartHead) + 8 * (size_t)num_out);
+    return 256 + (size_t)rows * parts_room(beams, num_out, vocab) * (sizeof(PartHead) + 8 * (size_t)num_out);
 }
 
 extern "C" pva_status pva_beam_select(const void* logits, int64_t row_stride, int32_t logits_are_fp32,

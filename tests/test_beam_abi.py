@@ -42,6 +42,20 @@ def test_workspace_sizes(L):
         assert per_row % (16 + 8 * k) == 0 and per_row // (16 + 8 * k) * beams * k <= 8192
 
 
+@pytest.mark.parametrize("beams,k", [(1, 1), (4, 4), (4, 8), (8, 16), (5, 5), (64, 64), (3, 6), (7, 1)])
+@pytest.mark.parametrize("vocab", [100, 32000, 50021, 131071, 2 ** 20, 2 ** 31 - 100])
+def test_a_workspace_serves_fewer_groups_and_smaller_vocabularies(L, beams, k, vocab):
+    """A batch shrinks as requests finish, and fewer rows are cut into more parts each."""
+    size = L.pva_beam_select_bytes
+    most = 0
+    for groups in list(range(0, 700)) + [1000, 5000]:
+        n = size(groups, beams, vocab, k)
+        assert n >= most > -1
+        most = n
+    for groups in (1, 16, 600):
+        assert size(groups, beams, vocab, k) >= max(size(groups, beams, v, k) for v in (1, vocab // 3 + 1, vocab // 2 + 1, vocab - 1))
+
+
 def reorder(L, parents=A, groups=2, beams=3, caches=None, n=None, table=A, stride=4, width=4, lens=A, states=(), status=None):
     caches = [cache()] if caches is None else caches
     c = (_lib.CacheDesc * len(caches))(*caches) if caches else None

@@ -251,6 +251,17 @@ def test_two_streams_with_their_own_workspaces():
         r.check(ranking(x, scores, 8))
 
 
+@pytest.mark.parametrize("kind", [torch.bfloat16, torch.float32])
+def test_one_workspace_for_a_batch_that_shrinks(kind):
+    beams, vocab, k = 8, 40001, 16
+    ws = api.alloc_beam_workspace(40, beams, vocab, k)
+    for groups in (40, 39, 17, 16, 9, 8, 3, 1):
+        view, x = rows_of(kind, groups, beams, vocab, groups)
+        s = scores_of(groups, beams, groups)
+        ws.fill_(255)
+        Select(view, s, k, ws=ws).check(ranking(x, s, k))
+
+
 def test_select_refusals_of_the_binding():
     view, _ = rows_of(torch.float32, 2, 3, 50, 1)
     s, i = torch.zeros((2, 3), device="cuda"), torch.zeros((2, 3), dtype=torch.int32, device="cuda")
