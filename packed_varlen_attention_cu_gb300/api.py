@@ -124,12 +124,29 @@ def build_worklist(cu_seqlens: Optional[torch.Tensor], mask: MaskDesc, params: W
         worklist.numel(), _stream(stream)))
 
 
+def _cross_sizes(mask: MaskDesc, params: WorklistParams, cu_seqlens, rows: dict, keys: dict, lse) -> None:
+    """Under a CROSS mask targets and sources have lengths of their own: the tensors of either side are
+    compared with the mask's (the library sees addresses only)."""
+    if mask.kind != MASK_CROSS:
+        return
+    d = rows["q"].shape[-1]
+    for names, shape in ((rows, (mask.q_tokens, params.num_q_heads, d)), (keys, (mask.k_tokens, params.num_kv_heads, d)),
+                         (lse, (params.num_q_heads, mask.q_tokens))):
+        for name, t in names.items():
+            if t.shape != shape:
+                raise ValueError(f"{name}: {tuple(t.shape)}, the mask and the head counts ask for {shape}")
+    offsets = getattr(mask, "_cu_keys_keep", None)
+    if cu_seqlens is None or (offsets is not None and offsets.numel() != cu_seqlens.numel()):
+        raise ValueError("cu_seqlens: one entry for each of the mask's cu_keys")
+
+
 def attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
              cu_seqlens: Optional[torch.Tensor], mask: MaskDesc, params: WorklistParams,
              worklist: torch.Tensor, out: torch.Tensor, lse: torch.Tensor,
              softmax_scale: float = 0.0, cta_busy: Optional[torch.Tensor] = None,
              stream=None) -> None:
     """out [Tq, Hq, d] bf16 or fp32, lse [Hq, Tq] fp32 (written by the kernel)."""
+    _cross_sizes(mask, params, cu_seqlens, {"q": q, "out": out}, {"k": k, "v": v}, {"lse": lse})
     for t in (q, k, v, out, lse):
         assert t.is_cuda and t.is_contiguous()
     assert q.dtype == k.dtype == v.dtype == torch.bfloat16
@@ -148,6 +165,11 @@ def attn_fwd_host(q_host: torch.Tensor, k_host: torch.Tensor, v_host: torch.Tens
     stream.  Host tensors (pinned for asynchronous copies) hold the inputs and
     receive O and LSE; dev_bufs holds the device buffers "q", "k", "v", "cu",
     "worklist", "out", "lse" (see alloc_host_path_buffers)."""
+    _cross_sizes(mask, params, cu_host, {"q": q_host, "out": out_host}, {"k": k_host, "v": v_host}, {"lse": lse_host})
+    if mask.kind == MASK_CROSS:
+        for name, t in (("q", q_host), ("k", k_host), ("v", v_host), ("out", out_host), ("lse", lse_host), ("cu", cu_host)):
+            if dev_bufs[name].numel() < t.numel():
+                raise ValueError(f"dev_bufs: {name} has less room than the mask's tensor")
     for t in (q_host, k_host, v_host, out_host, lse_host):
         assert not t.is_cuda and t.is_contiguous()
     wl = dev_bufs["worklist"]
@@ -180,6 +202,7 @@ def attn_fwd_accumulate(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
                         cta_busy: Optional[torch.Tensor] = None, stream=None) -> None:
     """Fused ring step: merge this call's attention into the running fp32
     o_run [Tq, Hq, d] and lse_run [Hq, Tq] in place (start with lse_run = -inf)."""
+    _cross_sizes(mask, params, cu_seqlens, {"q": q, "o_run": o_run}, {"k": k, "v": v}, {"lse_run": lse_run})
     for t in (q, k, v, o_run, lse_run):
         assert t.is_cuda and t.is_contiguous()
     assert q.dtype == k.dtype == v.dtype == torch.bfloat16
@@ -288,6 +311,8 @@ def attn_bwd(q, k, v, out, lse, dout, cu_seqlens: Optional[torch.Tensor], num_do
              dq: torch.Tensor, dk: torch.Tensor, dv: torch.Tensor, softmax_scale: float = 0.0,
              stream=None) -> None:
     """Gradients into dq [Tq, Hq, d], dk/dv [Tk, Hkv, d] (all bf16 or all fp32)."""
+    _cross_sizes(mask, params, cu_seqlens, {"q": q, "out": out, "dout": dout, "dq": dq},
+                 {"k": k, "v": v, "dk": dk, "dv": dv}, {"lse": lse})
     for t in (q, k, v, out, lse, dout, dq, dk, dv):
         assert t.is_cuda and t.is_contiguous()
     assert dq.dtype == dk.dtype == dv.dtype and dq.dtype in (torch.bfloat16, torch.float32)

@@ -65,6 +65,64 @@ def test_make_mask_wants_the_offsets_on_the_device():
         api.make_mask(api.MASK_CROSS, 10, 10, cu_keys=torch.tensor([0, 10], dtype=torch.int32))
 
 
+ROWS, KEYS, LSE = (30, 4, 64), (70, 2, 64), (4, 30)
+
+
+def tensors(**other):
+    """Everything that the attention calls take for 30 rows of 4 heads over 70 keys of 2, on the CPU."""
+    t = {n: torch.zeros(ROWS, dtype=torch.bfloat16) for n in ("q", "out", "dout", "dq")}
+    t |= {n: torch.zeros(KEYS, dtype=torch.bfloat16) for n in ("k", "v", "dk", "dv")}
+    t |= dict(lse=torch.zeros(LSE), o_run=torch.zeros(ROWS), cu=torch.zeros(4, dtype=torch.int32), ws=torch.zeros(256, dtype=torch.uint8))
+    t |= {n: torch.zeros(shape, dtype=t[n].dtype) for n, shape in other.items()}
+    return t
+
+
+def calls(t, kind=api.MASK_CROSS):
+    m = mask(kind, 30, 70)
+    m._cu_keys_keep = torch.zeros(4, dtype=torch.int32)
+    p = api.make_params(4, 2, num_ctas=152)
+    bufs = dict(q=t["q"], k=t["k"], v=t["v"], out=t["out"], lse=t["lse"], cu=t["cu"], worklist=t["ws"])
+    return dict(
+        fwd=lambda: api.attn_fwd(t["q"], t["k"], t["v"], t["cu"], m, p, t["ws"], t["out"], t["lse"], stream=0),
+        acc=lambda: api.attn_fwd_accumulate(t["q"], t["k"], t["v"], t["cu"], m, p, t["ws"], t["o_run"], t["lse"], stream=0),
+        bwd=lambda: api.attn_bwd(t["q"], t["k"], t["v"], t["out"], t["lse"], t["dout"], t["cu"], 3, m, p, t["ws"], t["ws"], t["dq"],
+                                 t["dk"], t["dv"], stream=0),
+        host=lambda: api.attn_fwd_host(t["q"], t["k"], t["v"], t["cu"], 3, m, p, t["out"], t["lse"], bufs, stream=0))
+
+
+@pytest.mark.parametrize("call,name,shape", [
+    (call, name, shape) for call, names in (("fwd", "q k v out lse cu"), ("acc", "q k v o_run lse cu"), ("host", "q k v out lse cu"),
+                                            ("bwd", "q k v out lse dout dq dk dv cu"))
+    for name in names.split()
+    for shape in ([(5,), (1,)] if name == "cu" else [(4, 70), (30, 4), (2, 30)] if name == "lse" else
+                  [ROWS[::-1], (70, 4, 64), (29, 4, 64)] if name in ("q", "out", "o_run", "dout", "dq") else
+                  [(30, 2, 64), (70, 4, 64), (69, 2, 64), (70, 2, 128)])])
+def test_tensors_that_are_not_the_masks(call, name, shape):
+    """A pack of the other side, or of another batch, would be read or written past its end."""
+    with pytest.raises(ValueError, match="cu_seqlens" if name == "cu" else "mask"):
+        calls(tensors(**{name: shape}))[call]()
+    with pytest.raises(ValueError):  # swapped
+        calls(tensors(q=KEYS, k=ROWS))[call]()
+
+
+@pytest.mark.parametrize("name", ["q", "k", "v", "out", "lse", "cu"])
+def test_device_buffers_without_room(name):
+    t = tensors()
+    m, p = mask(q=30, k=70), api.make_params(4, 2, num_ctas=152)
+    bufs = dict({n: t[n] for n in ("q", "k", "v", "out", "lse", "cu")}, worklist=t["ws"])
+    bufs[name] = bufs[name].flatten()[1:]
+    with pytest.raises(ValueError, match="room"):
+        api.attn_fwd_host(t["q"], t["k"], t["v"], t["cu"], 3, m, p, t["out"], t["lse"], bufs, stream=0)
+
+
+@pytest.mark.parametrize("call", ["fwd", "acc", "bwd"])
+def test_tensors_that_are_the_masks(call):
+    with pytest.raises(AssertionError):  # the next check: they are not on a GPU
+        calls(tensors())[call]()
+    with pytest.raises(AssertionError):  # other masks keep their rules
+        calls(tensors(k=(30, 2, 64)), kind=api.MASK_CAUSAL)[call]()
+
+
 def cross(L, c=None, b=None, q=A, qs=0, hq=4, new=1, scale=0.0, out=A, f32=0, lse=A, ws=A, n=1 << 40):
     return L.pva_cache_cross_attn(c or cache(), b or batch(), q, qs, hq, new, scale, out, f32, lse, ws, n, None)
 
