@@ -758,8 +758,7 @@ __global__ void __launch_bounds__(kMove) move_kernel(const __grid_constant__ Mov
         s_parent[tid] = p;
         int32_t page = -1;
         if (a.lens) {
-            if (a.lens[row0 + tid] != len || len < 0) s_bad = kErrLength;
-            else if (full > a.max_pages) s_bad = kErrPage;
+            if (a.lens[row0 + tid] != len || len < 0) s_bad = 1;
             if (part > 0 && full < a.max_pages) {
                 page = a.table[(row0 + tid) * a.table_stride + full];
                 if (page < 0 || page >= a.num_pages) page = -1;
@@ -772,9 +771,10 @@ __global__ void __launch_bounds__(kMove) move_kernel(const __grid_constant__ Mov
         }
     }
     __syncthreads();
-    // A group whose lengths differ, or lie past its table, is left as it was.
-    if (s_bad) {
-        if (tid == 0 && a.tell && blockIdx.y == 0) raise_status(a.status, s_bad);
+    // A group whose lengths differ, or need a page past its table, is left as it was.
+    const int bad = s_bad ? kErrLength : a.lens && full + (part > 0) > a.max_pages ? kErrPage : 0;
+    if (bad) {
+        if (tid == 0 && a.tell && blockIdx.y == 0) raise_status(a.status, bad);
         return;
     }
     const u64 moved = s_moved, source = s_source;

@@ -439,6 +439,36 @@ def test_groups_and_pages_that_do_not_fit(int4):
         assert api.cache_status(status) == code
 
 
+@pytest.mark.parametrize("int4", [False, True])
+def test_a_length_whose_last_page_is_past_the_table(int4):
+    """One token past the table's last column is past the table: nothing of the group moves, its table and states neither."""
+    b = Beams([47, 31, 47], 4, int4=int4, seed=12, states=STATES)  # tables of three pages
+    assert b.width == 3
+    for at, n in ((0, 49), (8, 63)):
+        b.g_lens[at:at + 4] = n
+    parents = random_parents(3, 4, 13)
+    parents[0], parents[2] = torch.tensor([1, 0, 0, 2]), torch.tensor([3, 3, 0, 0])
+    status = word()
+    b.run(parents, status)
+    b.expect(parents, skip=(0, 2))
+    b.check()
+    assert api.cache_status(status) == 300
+
+
+@pytest.mark.parametrize("first", [True, False])
+def test_lengths_that_differ_and_pass_the_table(first):
+    """Numbers of a group that differ are told of as that, whatever else is wrong with them."""
+    b = Beams([47, 47], 4, seed=14, states=STATES)
+    b.g_lens[0 if first else 1] = 1000
+    b.g_lens[2] = 999
+    parents = torch.tensor([[1, 0, 0, 2], [1, 0, 0, 2]])
+    status = word()
+    b.run(parents.int(), status)
+    b.expect(parents, skip=(0,))
+    b.check()
+    assert api.cache_status(status) == 301
+
+
 def test_a_table_with_a_stride_and_a_full_one():
     b = Beams([48, 31], 4, seed=9)  # 48 tokens: three full pages, and the table's last column is the next one
     wide = torch.full((8, b.width + 5), -7, dtype=torch.int32, device="cuda")
