@@ -985,18 +985,46 @@ extern "C" pva_status pva_beam_reorder(const int32_t* parents, int32_t num_group
     }
     if (num_groups == 0 || (num_caches == 0 && num_states == 0)) return PVA_OK;
     if (!parents || (num_caches > 0 && (!kv_lens || (max_pages > 0 && !page_table)))) return PVA_ERR_INVALID_ARG;
-    // what is listed twice would be moved twice, by warps that do not meet
-    for (int32_t i = 0; i < num_caches && c0->num_pages > 0; ++i) {
-        const void *k = caches[i].k_pages, *v = caches[i].v_pages;
-        if (k == v) return PVA_ERR_INVALID_ARG;
-        for (int32_t j = 0; j < i; ++j)
-            if (k == caches[j].k_pages || k == caches[j].v_pages || v == caches[j].k_pages || v == caches[j].v_pages)
-                return PVA_ERR_INVALID_ARG;
+    // What is listed twice would be moved twice, by warps that do not meet; what the call reads must not move.
+    const bool scales = num_caches > 0 && c0->kind == PVA_CACHE_INT4, pages = num_caches > 0 && c0->num_pages > 0;
+    const int arrays = pages ? (scales ? 4 : 2) : 0;
+    struct Arrays {
+        const void* at[4];
+    };
+    auto arrays_of = [&](int32_t i) {
+        const pva_cache_desc& c = caches[i];
+        return Arrays{{c.k_pages, c.v_pages, c.k_scales, c.v_scales}};
+    };
+    const void* const given[3] = {parents, num_caches > 0 ? kv_lens : nullptr, num_caches > 0 ? page_table : nullptr};
+    auto is_given = [&](const void* x) { return x == given[0] || x == given[1] || x == given[2]; };
+    if (given[2] && (given[2] == given[0] || given[2] == given[1])) return PVA_ERR_INVALID_ARG;
+    for (int32_t i = 0; i < num_caches && arrays > 0; ++i) {
+        const Arrays x = arrays_of(i);
+        for (int k = 0; k < arrays; ++k) {
+            if (is_given(x.at[k])) return PVA_ERR_INVALID_ARG;
+            for (int m = 0; m < k; ++m)
+                if (x.at[k] == x.at[m]) return PVA_ERR_INVALID_ARG;
+        }
+        for (int32_t j = 0; j < i; ++j) {
+            const Arrays y = arrays_of(j);
+            bool same = false;
+            for (int k = 0; k < arrays; ++k)
+                for (int m = 0; m < arrays; ++m) same |= x.at[k] == y.at[m];
+            if (same) return PVA_ERR_INVALID_ARG;
+        }
     }
-    for (int32_t i = 0; i < num_states; ++i)
+    for (int32_t i = 0; i < num_states; ++i) {
+        const void* x = states[i].data;
+        if (states[i].row_bytes == 0) continue;
+        if (is_given(x)) return PVA_ERR_INVALID_ARG;
         for (int32_t j = 0; j < i; ++j)
-            if (states[i].data == states[j].data && states[i].row_bytes > 0 && states[j].row_bytes > 0)
-                return PVA_ERR_INVALID_ARG;
+            if (x == states[j].data && states[j].row_bytes > 0) return PVA_ERR_INVALID_ARG;
+        for (int32_t j = 0; j < num_caches; ++j) {
+            const Arrays y = arrays_of(j);
+            for (int k = 0; k < arrays; ++k)
+                if (x == y.at[k]) return PVA_ERR_INVALID_ARG;
+        }
+    }
     MoveArgs a = {};
     a.parents = parents;
     a.status = status_dev;

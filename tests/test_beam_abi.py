@@ -97,6 +97,26 @@ def test_reorder_refuses_what_would_move_twice(L, caches, states):
     assert reorder(L, caches=caches, states=states) == INVALID
 
 
+C, D, E, F = (A + (n << 21) for n in range(1, 5))
+
+
+def four(k=C, v=D, ks=E, vs=F):
+    return cache(kind=1, k_pages=k, v_pages=v, k_scales=ks, v_scales=vs)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(caches=[four(ks=C)]), dict(caches=[four(vs=E)]), dict(caches=[four(ks=D)]),                # inside one cache
+    dict(caches=[four(), four(B, B + 4096, E, B + 8192)]), dict(caches=[four(), four(B, B + 4096, B + 8192, E)]),  # scales of another
+    dict(caches=[four(), four(F, B + 4096, B + 8192, B + 12288)]),                                  # pages that are scales of another
+    dict(caches=[four()], states=[(C, 8, 8)]), dict(caches=[four()], states=[(F, 8, 8)]),           # a state that is a cache's
+    dict(caches=[four()], states=[(A, 8, 8)]), dict(caches=[four()], states=[(B, 8, 8)]),           # ... the parents, the lengths
+    dict(caches=[four()], states=[(B + 4096, 8, 8)]), dict(caches=[], states=[(A, 8, 8)]),          # ... the table
+    dict(caches=[four()], table=A), dict(caches=[four()], table=B), dict(caches=[four(k=A)]), dict(caches=[four(vs=B + 4096)])])
+def test_reorder_refuses_addresses_that_are_listed_twice(L, kw):
+    """Whatever they are listed as: pages, scales, states, and what the call reads (parents at A, lengths at B, table at B + 4096)."""
+    assert reorder(L, **{**dict(lens=B, table=B + 4096), **kw}) == INVALID
+
+
 def test_nothing_to_reorder(L):
     assert reorder(L, groups=0, parents=None, table=None, lens=None) == 0
     assert reorder(L, caches=[], parents=None, table=None, lens=None) == 0
