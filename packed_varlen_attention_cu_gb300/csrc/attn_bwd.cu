@@ -6,9 +6,8 @@
 //   dP = dO V^T,  D = rowsum(dO * O),  dS = P (dP - D),
 //   dQ = scale dS K,  dK = scale dS^T Q,  dV = P^T dO.
 // Three kernels, no atomics (each output row has one writer):
-//   bwd_pre   D per (row, head), HBM-bound.  Never from this call's own P and dP: the
-//             caller's O and LSE may be joined from more keys than the call has (sources
-//             attended in parts), and then sum P dP over these is not D;
+//   bwd_pre   D per (row, head), HBM-bound (under a CROSS mask for sources past 128
+//             keys; bwd_dq makes the others');
 //   bwd_dq    q-major over the forward worklist's units, dispatched as the
 //             worklist says (static per-CTA LPT lists, or claimed at run time):
 //             per query sub-tile (Q and dO copied into tensor memory), every
@@ -35,6 +34,7 @@
 #include <string.h>
 
 #include "../../include/pva.h"
+#include "cache.cuh"
 #include "common.h"
 #include "launch.cuh"
 #include "ptx.cuh"
@@ -84,10 +84,8 @@ struct BwdParams {
     void* dv;            // [Tk, Hkv, d]
     int32_t q_tokens, k_tokens, hq, hkv, grads_fp32, num_ctas, d;
     float scale, scale_log2;
-    int32_t cross;       // 1: a CROSS mask
 };
 
-constexpr int kURing = 8;  // units the producer may run ahead
 constexpr int kLdSlots = 8;
 constexpr int kMaxStages = 12;
 
@@ -100,12 +98,12 @@ struct KvSlot {
     WlSlice s;
 };
 
-template <class Slot>
+template <class Slot, int R>
 struct BShared {
     uint64_t a_full, a_empty, o_full, o_empty, done, done2;
     uint64_t s2_full[3], p2_full[3];  // per half-item tensor-memory buffer
     uint64_t r_full[kMaxStages], r_empty[kMaxStages];
-    UnitRing<kURing, Slot> ur;  // the producer hands each unit to the other roles
+    UnitRing<R, Slot> ur;  // the producer hands each unit to the other roles
     // bwd_dkdv: (LSE log2, D) of each half-item's 64 queries, staged ahead by a
     // loader warp (ld_full: 32 lane arrivals; ld_empty: one per element-wise warp)
     uint64_t ld_full[kLdSlots], ld_empty[kLdSlots];
@@ -114,6 +112,36 @@ struct BShared {
 };
 
 // ------------------------------------------------------------ D = rowsum(dO O)
+// acc + the products of eight bf16 numbers each.
+__device__ __forceinline__ float dot8(const uint4& a, const uint4& b, float acc) {
+    const uint32_t av[4] = {a.x, a.y, a.z, a.w}, bv[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const float2 fa = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&av[e]));
+        const float2 fb = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&bv[e]));
+        acc += fa.x * fb.x + fa.y * fb.y;
+    }
+    return acc;
+}
+// The sum over the 8 threads of a row.
+__device__ __forceinline__ float sum8(float x) {
+    x += __shfl_xor_sync(0xffffffffu, x, 1);
+    x += __shfl_xor_sync(0xffffffffu, x, 2);
+    x += __shfl_xor_sync(0xffffffffu, x, 4);
+    return x;
+}
+
+// The same by one thread, of the row that starts at element `at`.
+template <int D>
+__device__ __noinline__ float row_dot(const BwdParams& p, int64_t at) {
+    const uint4* o = reinterpret_cast<const uint4*>(p.out) + at / 8;
+    const uint4* g = reinterpret_cast<const uint4*>(p.dout) + at / 8;
+    float acc = 0.f;
+#pragma unroll 4
+    for (int c = 0; c < D / 8; ++c) acc = dot8(o[c], g[c], acc);
+    return acc;
+}
+
 // 8 threads per (row, head), 16 bytes each per step, the loads of kRows of them first.  (237 K rows of 128
 // dims, the whole backward: 156.5 us; 157.5 with one row, 164 with four, 162.5 with a loop of unknown
 // length, a 64-bit division and half the blocks.)
@@ -142,25 +170,65 @@ __global__ void __launch_bounds__(256) bwd_pre_kernel(const BwdParams p) {
             const int64_t r = r0 + i * stride;
             float acc = 0.f;
 #pragma unroll
-            for (int c = 0; c < S; ++c) {
-                const uint32_t av[4] = {a[i][c].x, a[i][c].y, a[i][c].z, a[i][c].w};
-                const uint32_t bv[4] = {b[i][c].x, b[i][c].y, b[i][c].z, b[i][c].w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float2 fa = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&av[e]));
-                    const float2 fb = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&bv[e]));
-                    acc += fa.x * fb.x + fa.y * fb.y;
-                }
-            }
-            acc += __shfl_xor_sync(0xffffffffu, acc, 1);
-            acc += __shfl_xor_sync(0xffffffffu, acc, 2);
-            acc += __shfl_xor_sync(0xffffffffu, acc, 4);
+            for (int c = 0; c < S; ++c) acc = dot8(a[i][c], b[i][c], acc);
+            acc = sum8(acc);
             if (r < rows && sub == 0) {
                 const int64_t t = rows >> 31 ? r / p.hq : (int64_t)((uint32_t)r / (uint32_t)p.hq);
                 const int32_t h = (int32_t)(r - t * p.hq);
                 p.dvec[(int64_t)h * p.q_tokens + t] = acc;
             }
         }
+    }
+}
+
+struct PreCross {
+    const int32_t *cu, *cu_keys;  // null: another mask
+    int32_t num_docs, chunk;      // chunk: tokens of a block
+};
+
+// The same under a CROSS mask, for the rows of sources past 128 keys; of the others bwd_dq makes D itself.  A
+// block takes a chunk of tokens, document by document.
+template <int D>
+__global__ void __launch_bounds__(256) bwd_pre_cross_kernel(const BwdParams p, const PreCross x) {
+    constexpr int S = D / 64;
+    let_next_start();
+    const int32_t t0 = blockIdx.x * x.chunk, t1 = min(t0 + x.chunk, p.q_tokens);
+    const int32_t group = threadIdx.x >> 3, sub = threadIdx.x & 7;
+    int32_t doc = find_seq(x.cu, x.num_docs, t0);
+    // (offsets that do not fit were refused when the worklist was built; here they only must not lead outside)
+    for (int32_t lo = t0; lo < t1;) {
+        int32_t hi = t1;
+        if (doc >= 0 && doc < x.num_docs) {
+            hi = min(t1, x.cu[doc + 1]);
+            const int32_t n = x.cu_keys[doc + 1] - x.cu_keys[doc];
+            ++doc;
+            if (hi <= lo) continue;
+            if (n <= 128) {
+                lo = hi;
+                continue;
+            }
+        }
+        const int64_t r0 = (int64_t)lo * p.hq;
+        const int32_t items = (hi - lo) * p.hq;
+        for (int32_t i0 = 0; i0 < items; i0 += 32) {
+            const bool live = i0 + group < items;
+            const int32_t i = live ? i0 + group : 0;
+            const int32_t t = lo + (int32_t)((uint32_t)i / (uint32_t)p.hq), h = i - (t - lo) * p.hq;
+            const uint4* o = reinterpret_cast<const uint4*>(p.out) + (r0 + i) * (D / 8) + sub;
+            const uint4* g = reinterpret_cast<const uint4*>(p.dout) + (r0 + i) * (D / 8) + sub;
+            uint4 a[S], b[S];
+#pragma unroll
+            for (int c = 0; c < S; ++c) {
+                a[c] = o[8 * c];
+                b[c] = g[8 * c];
+            }
+            float acc = 0.f;
+#pragma unroll
+            for (int c = 0; c < S; ++c) acc = dot8(a[c], b[c], acc);
+            acc = sum8(acc);
+            if (live && sub == 0) p.dvec[(int64_t)h * p.q_tokens + t] = acc;
+        }
+        lo = hi;
     }
 }
 
@@ -206,8 +274,8 @@ __device__ __forceinline__ void store_zero_row(void* base, int64_t row_elem, boo
 // per use and reads every unit.  acc_issuers: the warps that commit o_full (the
 // ones whose MMAs write the accumulators).  item_warps: the element-wise warps
 // that work on each half-item (p2_full and ld_empty count one arrival each)
-template <class Slot>
-__device__ __forceinline__ void init_barriers(BShared<Slot>& sh, int stages, int elem_threads,
+template <class Slot, int R>
+__device__ __forceinline__ void init_barriers(BShared<Slot, R>& sh, int stages, int elem_threads,
                                               int extra_readers, int issuers, int acc_issuers,
                                               int item_warps) {
     mbar_init(&sh.a_full, 1);
@@ -242,7 +310,7 @@ __device__ __forceinline__ void init_barriers(BShared<Slot>& sh, int stages, int
 // of two 64-column buffers (s2_full/p2_full) and are issued before dQ += dS K
 // of half-item u - 1, so dS of u - 1 is computed while the pipe works on u.
 // o_full/o_empty: dQ accumulated / read out.
-template <int D>
+template <int D, bool CROSS>
 __global__ void __launch_bounds__(kThreads, 1)
     bwd_dq_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
                   const __grid_constant__ CUtensorMap tmv, const __grid_constant__ CUtensorMap tmdo,
@@ -256,15 +324,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t* sQ = smem;
     uint8_t* sDO = smem + C::kTileBytes;
     uint8_t* sKV = smem + 2 * C::kTileBytes;
-    __shared__ BShared<UnitSlot> sh;
-    static_assert(C::kSmemDq + sizeof(sh) <= 227 * 1024, "shared memory of a block");
+    constexpr int kURing = CROSS ? 4 : 8;  // units the producer may run ahead
+    __shared__ BShared<UnitSlot, kURing> sh;
+    // CROSS: warpgroup 1's sums of P and P dP over its columns go to warpgroup 0, and D comes back in their place
+    __shared__ float2 sums[CROSS ? 128 : 1];
+    __shared__ uint64_t sums_full[4], d_full[4];  // of 32 rows each: one warp to one
+    static_assert(C::kSmemDq + sizeof(sh) + sizeof(sums) + sizeof(sums_full) + sizeof(d_full) <= 227 * 1024,
+                  "shared memory of a block");
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const WlHeader* h = reinterpret_cast<const WlHeader*>(p.wl);
     int32_t* err_word = const_cast<int32_t*>(&h->error);
     // This kernel may start while the one that makes D still runs.
     wait_previous();
     if (h->error != 0) return;
-    if ((h->kind == PVA_MASK_CROSS) != (p.cross != 0)) {  // a worklist of another mask
+    if ((h->kind == PVA_MASK_CROSS) != CROSS) {  // a worklist of another mask
         if (tid == 0 && blockIdx.x == 0) atomicCAS(err_word, 0, kErrBadWorklist);
         return;
     }
@@ -282,7 +355,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int32_t* cta_off = reinterpret_cast<const int32_t*>(p.wl + h->off.cta_off);
     const int32_t ub = dyn ? 0 : cta_off[blockIdx.x], ue = dyn ? 0 : cta_off[blockIdx.x + 1];
     if (!dyn && ub >= ue) return;
-    if (tid == 0) init_barriers(sh, C::kStagesDq, 256, 0, 2, 1, 8);
+    if (tid == 0) {
+        for (int w = 0; w < 4; ++w) {
+            mbar_init(&sums_full[w], 1);
+            mbar_init(&d_full[w], 1);
+        }
+        init_barriers(sh, C::kStagesDq, 256, 0, 2, 1, 8);
+    }
     if (warp == 1) {
         tmem_alloc(&sh.tmem_base, 512);
         tmem_relinquish();
@@ -588,7 +667,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int r = (warp & 3) * 32 + lane;  // query row = tensor-memory lane
         const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t tS = tmem + lane_base, tQ = tmem + lane_base + 256;
-        uint32_t gu = 0, o_cnt = 0;
+        uint32_t gu = 0, o_cnt = 0, d_cnt = 0;
         bool live = true;
         // Unit n from the producer's ring, kept until this thread has done with its tiles: the (LSE, D)
         // of its rows and, in a tile shared by pairs, the key interval of the row are asked for as soon
@@ -609,7 +688,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (i < slot.u.nsub && r < slot.u.st[i].nrows) {
                     const int64_t li = (int64_t)slot.u.st[i].head * p.q_tokens + slot.u.st[i].q_row + r;
                     lse_of[i] = p.lse[li];
-                    d_of[i] = p.dvec[li];
+                    if (!CROSS || slot.u.ntiles > 1) d_of[i] = p.dvec[li];
                 }
             }
             if (slot.s.type == kSlicePackedCross)
@@ -669,7 +748,80 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int32_t q_pos = st.q_pos + r;
                 const float l = i == 0 ? lse_of[0] : lse_of[1];
                 const float lse2 = l == -INFINITY ? INFINITY : l * 1.4426950408889634f;  // no key: every P is 0
-                const float dd = i == 0 ? d_of[0] : d_of[1];
+                float dd = i == 0 ? d_of[0] : d_of[1];
+                if (CROSS && slot.u.ntiles == 1) {
+                    // All keys of the row that this call has lie in one tile, so sum_j P_j and sum_j P_j dP_j are at hand
+                    // before any dS.  Where the former is 1 but for rounding, the caller's O and LSE are of these
+                    // keys, and D is the latter: the rowsum of dO and O is off by O's rounding, and with few keys dP - D
+                    // is small beside D.  (Sources of 1 to 8 keys: dQ and dK off by 0.0030, so 0.0024; 512 pairs of up to
+                    // 120 keys 0.0026, so 0.0024, which is the bf16 dS and result; their backward takes 167 us instead
+                    // of 160.)  Elsewhere O and LSE are of more keys (a source attended in parts), and D is the rowsum.
+                    // Rounding: the LSE and its product with log2 e, 2^-24 of |lse2| each, here, in the forward and in
+                    // a few joins; exponentials and the logarithm, 2^-21; two sums of 128 terms.  So only keys outside
+                    // the call whose weights sum to less than that bound go uncounted.
+                    int32_t lo = 0, hi = valid ? slot.s.k_len : 0;
+                    if (slot.s.type == kSlicePackedCross) {
+                        lo = pair_keys & 255u;
+                        hi = valid ? pair_keys >> 8 : 0u;
+                    }
+                    const int32_t k_len = slot.s.k_len;
+                    const float2 sc = make_float2(p.scale_log2, p.scale_log2);
+                    const float2 nl = make_float2(-lse2, -lse2);
+                    float sum_p = 0.f;
+                    dd = 0.f;
+#pragma unroll 1
+                    for (int col0 = wg * 32; col0 < k_len; col0 += 64) {
+                        if (!__any_sync(0xffffffffu, lo < col0 + 32 && hi > col0)) continue;
+                        const uint32_t x = gu + (col0 >> 6), b = x & 1;
+                        live = mbar_wait_warp(&sh.s2_full[b], (x >> 1) & 1, abort_flag, err_word,
+                                              kErrTimeoutBase + 27, kWaitNs);
+                        if (!live) break;
+                        tc_fence_after();
+                        uint32_t sv[32], pv[32];
+                        tmem_ld32(tS + 64 * b + wg * 32, sv);
+                        tmem_ld32(tS + 128 + 64 * b + wg * 32, pv);
+                        tmem_ld_wait(sv);
+                        tmem_ld_wait(pv);
+                        float2 acc = make_float2(0.f, 0.f), accp = make_float2(0.f, 0.f);
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2) {
+                            const int col = col0 + e;
+                            const float2 y = __ffma2_rn(
+                                make_float2(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1])), sc, nl);
+                            float p0 = ex2_approx(y.x), p1 = ex2_approx(y.y);
+                            if (col < lo || col >= hi) p0 = 0.f;
+                            if (col + 1 < lo || col + 1 >= hi) p1 = 0.f;
+                            accp = __fadd2_rn(accp, make_float2(p0, p1));
+                            acc = __ffma2_rn(make_float2(p0, p1),
+                                             make_float2(__uint_as_float(pv[e]), __uint_as_float(pv[e + 1])), acc);
+                        }
+                        sum_p += accp.x + accp.y;
+                        dd += acc.x + acc.y;
+                    }
+                    if (!live) break;
+                    if (wg == 1) {
+                        sums[CROSS ? r : 0] = make_float2(sum_p, dd);
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&sums_full[warp & 3]);
+                        live = mbar_wait_warp(&d_full[warp & 3], d_cnt & 1, abort_flag, err_word,
+                                              kErrTimeoutBase + 27, kWaitNs);
+                        if (!live) break;
+                        dd = sums[CROSS ? r : 0].x;
+                    } else {
+                        live = mbar_wait_warp(&sums_full[warp & 3], d_cnt & 1, abort_flag, err_word,
+                                              kErrTimeoutBase + 27, kWaitNs);
+                        if (!live) break;
+                        const float2 other = sums[CROSS ? r : 0];
+                        sum_p += other.x;
+                        dd += other.y;
+                        if (valid && !(fabsf(sum_p - 1.f) <= 0x1p-17f + 0x1p-21f * fabsf(lse2))) dd = row_dot<D>(p, grow);
+                        sums[CROSS ? r : 0].x = dd;
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&d_full[warp & 3]);
+                        if (valid) p.dvec[(int64_t)st.head * p.q_tokens + st.q_row + r] = dd;
+                    }
+                    ++d_cnt;
+                }
                 const int32_t run_count = slot.u.run_count;
                 for (int32_t rr = 0; rr < run_count && live; ++rr) {
                     WlRun run{slot.slice, slot.lo, slot.hi, 0};
@@ -792,13 +944,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t* sK = smem;
     uint8_t* sV = smem + C::kTileBytes;
     uint8_t* sR = smem + 2 * C::kTileBytes;  // half-item stage x at x * 2 * kHalfBytes
-    __shared__ BShared<KvSlot> sh;
+    constexpr int kURing = 8;  // units the producer may run ahead
+    __shared__ BShared<KvSlot, kURing> sh;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const WlHeader* h = reinterpret_cast<const WlHeader*>(p.wl);
     const BwdHeader* bh = reinterpret_cast<const BwdHeader*>(p.plan);
     int32_t* err_word = const_cast<int32_t*>(&h->error);
-    // The wait comes before the first read.  This kernel reads nothing that the kernel of dQ writes, but D and
-    // LSE come from kernels before that one, and only a grid that has waited is given sight of what they wrote.
+    // The wait comes before the first read: under a CROSS mask the kernel of dQ makes part of D, and what else this
+    // one reads was written before that, which only a grid that has waited is given sight of.
     // (Beside the tail of dQ, without the wait, 3 short pairs, forward and gradients, took 38 us instead of 45, 209
     // groups of them 222 instead of 225, long packs the same.)
     wait_previous();
@@ -1315,10 +1468,12 @@ template <int D>
 pva_status launch_bwd(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
                       const CUtensorMap& mdo, const CUtensorMap& mq64, const CUtensorMap& mdo64,
                       const CUtensorMap& mk64, const CUtensorMap& mv64, const BwdParams& bp,
-                      int32_t dkdv_ctas, cudaStream_t st) {
+                      const PreCross& px, int32_t dkdv_ctas, cudaStream_t st) {
     const int grid_pre = 8 * bp.num_ctas;
-    bwd_pre_kernel<D><<<grid_pre, 256, 0, st>>>(bp);
-    auto kq = bwd_dq_kernel<D>;
+    const bool cross = px.cu_keys != nullptr;
+    if (cross) bwd_pre_cross_kernel<D><<<(bp.q_tokens + px.chunk - 1) / px.chunk, 256, 0, st>>>(bp, px);
+    else bwd_pre_kernel<D><<<grid_pre, 256, 0, st>>>(bp);
+    auto kq = cross ? bwd_dq_kernel<D, true> : bwd_dq_kernel<D, false>;
     auto kk = bwd_dkdv_kernel<D>;
     // setmaxnreg.inc draws from the registers the block was launched with: the
     // dK/dV split must fit in (threads x registers per thread)
@@ -1340,8 +1495,6 @@ pva_status launch_bwd(const CUtensorMap& mq, const CUtensorMap& mk, const CUtens
         return PVA_ERR_CUDA;
     return PVA_OK;
 }
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 }  // namespace
 }  // namespace pva
@@ -1434,7 +1587,8 @@ extern "C" pva_status pva_attn_bwd(const void* q, const void* k, const void* v, 
     bp.d = head_dim;
     bp.scale = softmax_scale > 0.f ? softmax_scale : 1.0f / sqrtf((float)head_dim);
     bp.scale_log2 = bp.scale * 1.4426950408889634f;
-    bp.cross = cross ? 1 : 0;
-    return head_dim == 128 ? launch_bwd<128>(mq, mk, mv, mdo, mq64, mdo64, mk64, mv64, bp, nc, st)
-                           : launch_bwd<64>(mq, mk, mv, mdo, mq64, mdo64, mk64, mv64, bp, nc, st);
+    const PreCross px{cu_seqlens_dev, cross ? mask->cu_keys : nullptr, num_docs,
+                      bp.hq >= 64 ? 4 : 256 / bp.hq};  // eight passes of 32 rows
+    return head_dim == 128 ? launch_bwd<128>(mq, mk, mv, mdo, mq64, mdo64, mk64, mv64, bp, px, nc, st)
+                           : launch_bwd<64>(mq, mk, mv, mdo, mq64, mdo64, mk64, mv64, bp, px, nc, st);
 }

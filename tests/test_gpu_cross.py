@@ -318,6 +318,30 @@ def test_gradients_of_sources_cut_in_two(d, pack):
     assert (total - whole[0]).norm() <= REL_L2 * norms
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("shift", [6.0, 8.0, 10.0])
+def test_keys_outside_the_call_count_where_they_weigh_little(d, shift):
+    """A source's second part has scores lower by `shift` (weights of e^-6 to e^-10 beside the first part's) and values 1024
+    times as large, so D of the first part's call is still moved by it."""
+    p = Pack([(40, 60), (7, 20), (100, 128), (3, 2), (64, 100)], 4, 2, d, seed=21 + d)
+    cuts = [30, 10, 64, 1, 50]
+    second = torch.cat([torch.arange(n) >= cut for (_, n), cut in zip(p.pairs, cuts)])
+    p.q[..., 0] = 4.0
+    p.k[..., 0] = 0.0
+    p.k[second, :, 0] = -shift * d ** 0.5 / 4
+    p.v[second] *= 1024
+    joined = p.forward()
+    for first in (True, False):
+        rows = torch.nonzero(second != first).flatten().tolist()
+        part = Pack([(m, cut if first else n - cut) for (m, n), cut in zip(p.pairs, cuts)], 4, 2, d)
+        part.q, part.dout, part.k, part.v = p.q, p.dout, p.k[rows], p.v[rows]
+        r = Run(part).build()
+        r.out, r.lse = joined[0].bfloat16().cuda(), joined[1].float().cuda()
+        # D = rowsum(dO O) of the O that is passed: its rounding is the caller's
+        part.forward = lambda: (joined[0].bfloat16().double(), joined[1])
+        _check([to_np(x) for x in r.backward(fp32=True)], [x.numpy() for x in part.gradients()], f"first: {first}, {shift}")
+
+
 def test_short_sources_beside_long_ones_on_one_cta():
     """dQ of one CTA takes more than two seconds, as long as a wait may take, while dK and dV begin with the short source:
     nothing of theirs may wait for the end of dQ under that limit.  All results are those of every CTA, bit for bit."""
