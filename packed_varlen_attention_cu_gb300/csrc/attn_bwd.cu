@@ -142,41 +142,33 @@ __device__ __noinline__ float row_dot(const BwdParams& p, int64_t at) {
     return acc;
 }
 
-// 8 threads per (row, head), 16 bytes each per step, the loads of kRows of them first.  (237 K rows of 128
-// dims, the whole backward: 156.5 us; 157.5 with one row, 164 with four, 162.5 with a loop of unknown
-// length, a 64-bit division and half the blocks.)
+// 8 threads per (row, head), 16 bytes each per step.  (1581 short documents, 131072 tokens of 32/8 heads of 128, the
+// whole backward: 2359 us; with two rows in flight 2417, four 2575, two with half the blocks 2466.  Long packs: the
+// same.)
 template <int D>
 __global__ void __launch_bounds__(256) bwd_pre_kernel(const BwdParams p) {
-    constexpr int kRows = 2, S = D / 64;
+    constexpr int S = D / 64;
     let_next_start();
     const int64_t rows = (int64_t)p.q_tokens * p.hq, stride = ((int64_t)gridDim.x * blockDim.x) >> 3;
     const int sub = threadIdx.x & 7;
-    for (int64_t r0 = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 3;
-         r0 - (threadIdx.x & 31) / 8 < rows; r0 += kRows * stride) {
-        uint4 a[kRows][S], b[kRows][S];
+    for (int64_t r = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 3;
+         r - (threadIdx.x & 31) / 8 < rows; r += stride) {  // (whole warps)
+        const uint4* o = reinterpret_cast<const uint4*>(p.out) + r * (D / 8) + sub;
+        const uint4* g = reinterpret_cast<const uint4*>(p.dout) + r * (D / 8) + sub;
+        uint4 a[S], b[S];
 #pragma unroll
-        for (int i = 0; i < kRows; ++i) {
-            const int64_t r = r0 + i * stride;
-            const uint4* o = reinterpret_cast<const uint4*>(p.out) + r * (D / 8) + sub;
-            const uint4* g = reinterpret_cast<const uint4*>(p.dout) + r * (D / 8) + sub;
-#pragma unroll
-            for (int c = 0; c < S; ++c) {
-                a[i][c] = r < rows ? o[8 * c] : make_uint4(0, 0, 0, 0);
-                b[i][c] = r < rows ? g[8 * c] : make_uint4(0, 0, 0, 0);
-            }
+        for (int c = 0; c < S; ++c) {
+            a[c] = r < rows ? o[8 * c] : make_uint4(0, 0, 0, 0);
+            b[c] = r < rows ? g[8 * c] : make_uint4(0, 0, 0, 0);
         }
+        float acc = 0.f;
 #pragma unroll
-        for (int i = 0; i < kRows; ++i) {
-            const int64_t r = r0 + i * stride;
-            float acc = 0.f;
-#pragma unroll
-            for (int c = 0; c < S; ++c) acc = dot8(a[i][c], b[i][c], acc);
-            acc = sum8(acc);
-            if (r < rows && sub == 0) {
-                const int64_t t = rows >> 31 ? r / p.hq : (int64_t)((uint32_t)r / (uint32_t)p.hq);
-                const int32_t h = (int32_t)(r - t * p.hq);
-                p.dvec[(int64_t)h * p.q_tokens + t] = acc;
-            }
+        for (int c = 0; c < S; ++c) acc = dot8(a[c], b[c], acc);
+        acc = sum8(acc);
+        if (r < rows && sub == 0) {
+            const int64_t t = rows >> 31 ? r / p.hq : (int64_t)((uint32_t)r / (uint32_t)p.hq);
+            const int32_t h = (int32_t)(r - t * p.hq);
+            p.dvec[(int64_t)h * p.q_tokens + t] = acc;
         }
     }
 }
