@@ -481,7 +481,8 @@ pva_status pva_cache_attn(const pva_cache_desc* cache, const pva_cache_batch* ba
  * keys (a source's; rows are beams, or any tokens that answer about it), none of which is
  * the row's own.  A row more than kv_lens counts is no failure, and kv_lens = 0 gives O = 0
  * and LSE = -inf.  A source is read once for its rows and heads of a group, up to 64 of
- * them, so rows of a source belong into one sequence of the batch.  Otherwise as
+ * them (with 4 bits 9 to 16 of them read it twice), so rows of a source belong into one
+ * sequence of the batch.  Otherwise as
  * pva_cache_attn, workspace (pva_cache_attn_bytes) and values too; a slot whose position has
  * no page is left out for all rows.  Weights
  * have 16 bits in the products where out is fp32; where it is bf16 and max_new tokens make
@@ -502,11 +503,12 @@ pva_status pva_cache_cross_attn(const pva_cache_desc* cache, const pva_cache_bat
 
 /* The num_out best continuations of every group.  Row b offers every token t of a logit
  * above -inf with the score scores[b] + x[t] - ln sum_t e^x[t]; a finished row offers itself
- * alone (its end token, at its own score; its logits are not read), and a row whose score is
- * -inf offers nothing.  Candidates are ranked by score * norm of their row, largest first; of
- * equal ones the lower beam comes first, and inside a beam the larger logit, then the lower
- * token.  Where fp32 rounds the score or its product with the norm to -inf there is none.
- * fp32 exponentials, sums and ranks in 64 bits; the result does not depend on timing.
+ * alone (its end token, at its own score), and a row whose score is -inf offers nothing; the
+ * logits of such rows may hold anything.  Candidates are ranked by score * norm of their row,
+ * largest first; of equal ones the lower beam comes first, and inside a beam the larger logit,
+ * then the lower token.  Where fp32 rounds the score or its product with the norm to -inf
+ * there is none.  fp32 exponentials, sums and ranks in 64 bits; the result does not depend on
+ * timing.
  *   logits       DEVICE bf16 or fp32 [num_groups * beams, vocab], rows row_stride elements
  *                apart (0: vocab), any alignment of the type
  *   beams        1 to 64;  num_out 1 to 64

@@ -687,8 +687,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 pair_keys = reinterpret_cast<const uint16_t*>(slice_mask(p.wl, h, slot.s, slot.slice))[r];
         };
         // dQ of a sub-tile goes out after dS of the next one's first key tile, whose scores are there by then:
-        // the MMA warps go on to it before the last dQ MMAs.  (Short pairs, the whole backward: 156.0 -> 154.3 us,
-        // 167.6 -> 161.2 with dynamic dispatch.  After the first half-item 151.5 and 158.3, but with the check in
+        // the MMA warps go on to it before the last dQ MMAs.  (Short pairs, the whole backward, when D came from the kernel before:
+        // 156.0 -> 154.3 us, 167.6 -> 161.2 with dynamic dispatch.  After the first half-item 151.5 and 158.3, but with the check in
         // the innermost loop long documents lose 1 to 3%.)  pend_valid, pend_row: this thread's row of the
         // sub-tile whose dQ is still to be stored.
         bool pend = false, pend_valid = false;

@@ -289,7 +289,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // CROSS: a unit of one sub-tile (one head over its own keys, up to 128 rows) would leave
                 // half of the CTA idle, so its key tiles are dealt to both halves, which meet in the
                 // epilogue.  (77 rows over 1500 keys, 8 heads of 128: 24.9 -> 20.3 us; 64 targets of 100 rows
-                // over 1500 keys each, 16 heads of 64: 126 -> 109 us, of 128: 153 -> 145, near HBM's rate.)
+                // over 1500 keys each, 16 heads of 64: 126 -> 108 us, of 128: 153 -> 143, near HBM's rate.)
                 const bool split = CROSS && u.nsub == 1 && u.ntiles >= 2;
                 if (split) {
                     u.nsub = 2;

@@ -124,7 +124,8 @@ __device__ __forceinline__ void add_exact(float& hi, float& lo, float x, float y
 // candidates go to a list, which is ranked and cut to its k best, and the bound is raised: each run
 // adds about 3 k.
 // (512 rows of 131071 bf16 logits, both kernels: a barrier and a count for each tile 78 us; warps
-// that look through their logits where they find one 55; vectors noted 42; without candidates 28.)
+// that look through their logits where they find one 55; vectors noted 42, 40 since
+// no tile past a row's end is read; without candidates 28.)
 // Should a run hold more than the lists, as ascending logits do, it is read again tile by tile
 // with a better bound.
 // The first bound is the smallest of the largest logits of 8, 16, 32 or 64 groups of threads: as
