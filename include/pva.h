@@ -314,7 +314,7 @@ pva_status pva_build_bwd_plan(const void* worklist_dev, int32_t num_docs,
  *                  every part's call takes the joined ones: its dk and dv are then those of
  *                  its keys, and the parts' dq add up
  *                  (CROSS: where a row's keys in the call lie in one tile and their P sums to
- *                  1 within 2^-17 + 2^-21 |LSE log2 e|, D is the sum of P dP, which is the
+ *                  1 within 2^-18 + 2^-22 |LSE log2 e|, D is the sum of P dP, which is the
  *                  rowsum without O's rounding)
  *   dout           DEVICE bf16 [q_tokens, Hq, head_dim]
  *   dq             DEVICE [q_tokens, Hq, head_dim], dk/dv DEVICE [k_tokens, Hkv,

@@ -748,9 +748,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // is small beside D.  (Sources of 1 to 8 keys: dQ and dK off by 0.0030, so 0.0024; 512 pairs of up to
                     // 120 keys 0.0026, so 0.0024, which is the bf16 dS and result; their backward takes 167 us instead
                     // of 160.)  Elsewhere O and LSE are of more keys (a source attended in parts), and D is the rowsum.
-                    // Rounding: the LSE and its product with log2 e, 2^-24 of |lse2| each, here, in the forward and in
-                    // a few joins; exponentials and the logarithm, 2^-21; two sums of 128 terms.  So only keys outside
-                    // the call whose weights sum to less than that bound go uncounted.
+                    // Rounding: four operations on the LSE, here and in the forward, 2^-24 of |lse2| each, times ln 2; two
+                    // sums with some 20 additions in a row, 2^-24 each; exponentials and a logarithm, 2^-22 each.  So
+                    // only keys outside the call whose weights sum to less than that go uncounted.
                     int32_t lo = 0, hi = valid ? slot.s.k_len : 0;
                     if (slot.s.type == kSlicePackedCross) {
                         lo = pair_keys & 255u;
@@ -806,7 +806,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const float2 other = sums[CROSS ? r : 0];
                         sum_p += other.x;
                         dd += other.y;
-                        if (valid && !(fabsf(sum_p - 1.f) <= 0x1p-17f + 0x1p-21f * fabsf(lse2))) dd = row_dot<D>(p, grow);
+                        if (valid && !(fabsf(sum_p - 1.f) <= 0x1p-18f + 0x1p-22f * fabsf(lse2))) dd = row_dot<D>(p, grow);
                         sums[CROSS ? r : 0].x = dd;
                         __syncwarp();
                         if (lane == 0) mbar_arrive(&d_full[warp & 3]);
